@@ -40,7 +40,7 @@ RLK_GEMM_LINEAR_FWD, RLK_GEMM_LINEAR_DX, RLK_GEMM_LINEAR_DW, RLK_GEMM_FWD_ACCUM 
 STATUS_NAMES = {0: "RLK_OK", 1: "RLK_ERR_NULL", 2: "RLK_ERR_SHAPE", 3: "RLK_ERR_DTYPE",
                 4: "RLK_ERR_ALIGN", 5: "RLK_ERR_WORKSPACE", 6: "RLK_ERR_UNSUPPORTED_DEVICE",
                 7: "RLK_ERR_CUDA", 8: "RLK_ERR_TIMEOUT", 9: "RLK_ERR_BOUNDS",
-                10: "RLK_ERR_NOT_DEBUG_BUILD"}
+                10: "RLK_ERR_NOT_DEBUG_BUILD", 11: "RLK_ERR_VALUE"}
 RLK_DEVERR_TIMEOUT, RLK_DEVERR_BOUNDS = 0x1, 0x2
 TRACE_FIELDS, TRACE_MAX_CTAS = 16, 1024
 
@@ -52,6 +52,7 @@ class RlkError(RuntimeError):
 
 
 _P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_F = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/rlk.h
 SIGNATURES = {
@@ -92,6 +93,14 @@ SIGNATURES = {
     "rlk_linear_logp_backward_workspace_size_for": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64]),
     "rlk_linear_logp_backward": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P,
                                       _P, _I, _I64, _P, _I, _I64, _P, _P, _SZ, _P]),
+    "rlk_linear_distill_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64]),
+    "rlk_linear_distill": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I, _I64,
+                                _I64, _P, _F, _P, _P, _P, _SZ, _P]),
+    "rlk_linear_distill_backward_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64,
+                                                         _I]),
+    "rlk_linear_distill_backward": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I,
+                                         _I64, _I64, _P, _F, _P, _P, _P, _I, _I64, _P, _I, _I64,
+                                         _P, _P, _SZ, _P]),
     "rlk_det_gemm_workspace_size": (_SZ, [_I, _P, _I, _I64, _I64, _I64, _P, _I, _I64, _I64, _I64]),
     "rlk_det_gemm_fwd": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]),
     "rlk_det_gemm_da": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]),
@@ -601,6 +610,156 @@ def linear_logp_trainable(hidden: torch.Tensor, weight: torch.Tensor, target: to
     no gradient.  linear_logp itself stays forward-only and rejects inputs that
     require grad."""
     return _LinearLogpGrad.apply(hidden, weight, bias, target)
+
+
+# ------------------------------------------------------------------ distillation
+def _distill_inputs(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse):
+    """Checked operands of the distillation calls: (hidden, weight, ids, logits as (tensor, ld)
+    pairs, bias, teacher_lse)."""
+    _require_cuda(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
+    if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError("hidden and weight must be bfloat16")
+    if teacher_ids.dtype != torch.int64:
+        raise TypeError("teacher_ids must be int64")
+    if teacher_logits.dtype not in _DT:
+        raise TypeError("teacher_logits must be bfloat16 or float32")
+    if bias is not None and (bias.dtype != torch.float32 or bias.dim() != 1):
+        raise TypeError("bias must be a 1-D float32 tensor")
+    lead, H = hidden.shape[:-1], hidden.size(-1)
+    if teacher_ids.shape != teacher_logits.shape or teacher_ids.shape[:-1] != lead:
+        raise ValueError("teacher_ids and teacher_logits must be [..., K] with hidden's leading shape")
+    K, N = teacher_ids.size(-1), hidden.numel() // H if H else 0
+    h = _matrix(hidden.reshape(-1, H), "hidden")
+    w = _matrix(weight, "weight")
+    if w[0].size(1) != H:
+        raise ValueError("weight must be [V, H] with the hidden size H")
+    ids = _matrix(teacher_ids.reshape(N, K), "teacher_ids")
+    logits = _matrix(teacher_logits.reshape(N, K), "teacher_logits")
+    if bias is not None:
+        bias = bias.contiguous()
+        if bias.numel() != w[0].size(0):
+            raise ValueError("bias must have V entries")
+    if teacher_lse is not None:
+        if teacher_lse.dtype != torch.float32 or teacher_lse.shape != lead:
+            raise ValueError("teacher_lse must be float32 with hidden's leading shape")
+        teacher_lse = teacher_lse.reshape(-1).contiguous()
+    return h, w, ids, logits, bias, teacher_lse
+
+
+def linear_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
+                   teacher_logits: torch.Tensor, bias: torch.Tensor | None = None, *,
+                   temperature: float = 1.0, teacher_lse: torch.Tensor | None = None, stream=None):
+    """loss, lse (FP32, shaped like hidden's leading dims): T^2 KL(teacher || student) over the
+    teacher's top logits, and the student's log-sum-exp at temperature T.
+
+    hidden [..., H] bf16, weight [V, H] bf16, bias [V] fp32 or None; teacher_ids [..., K] int64
+    with the teacher's logits there, teacher_logits [..., K] bf16 or fp32.  A slot whose id is
+    outside [0, V) (pad with -1) or whose logit is -inf is empty; a row without used slots has
+    loss 0.  The teacher's probabilities are normalised over its slots, or by teacher_lse [...]
+    fp32 (its log-sum-exp over its whole vocabulary at this temperature).  Forward only: use
+    linear_distill_trainable for gradients.
+    """
+    if hidden.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad):
+        raise RuntimeError("linear_distill is forward-only: inputs that require grad are rejected")
+    (h, ldh), (w, ldw), (ids, ldi), (tl, ldt), bias, tlse = _distill_inputs(
+        hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
+    N, H, V, K = h.size(0), h.size(1), w.size(0), ids.size(1)
+    dev = hidden.device
+    loss = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        n = lib().rlk_linear_distill_workspace_size(_ptr(h), N, H, ldh, _ptr(w), V, ldw, K)
+        if n == 0:
+            raise RlkError(2, "rlk_linear_distill_workspace_size")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(lib().rlk_linear_distill(
+            _ptr(h), N, H, ldh, _ptr(w), V, ldw, _ptr(bias), _ptr(ids), ldi, _ptr(tl),
+            _DT[tl.dtype], ldt, K, _ptr(tlse), temperature, _ptr(loss), _ptr(lse), _ptr(ws), n,
+            _stream_ptr(stream)), "rlk_linear_distill")
+    lead = hidden.shape[:-1]
+    return loss.reshape(lead), lse.reshape(lead)
+
+
+def linear_distill_backward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
+                            teacher_logits: torch.Tensor, lse: torch.Tensor,
+                            grad_loss: torch.Tensor, bias: torch.Tensor | None = None, *,
+                            temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                            grad_hidden: bool = True, grad_weight: bool = True,
+                            grad_bias: bool | None = None, out_dtype=torch.bfloat16,
+                            return_grad_logits: bool = False, stream=None):
+    """(grad_hidden [..., H], grad_weight [V, H], grad_bias [V] | None) of linear_distill's loss.
+
+    lse is the forward's lse; grad_loss is dL/dloss (one value a row).  With
+    return_grad_logits, also returns G = dL/dz as the BF16 [N, V] view the products read.
+    """
+    (h, ldh), (w, ldw), (ids, ldi), (tl, ldt), bias, tlse = _distill_inputs(
+        hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
+    N, H, V, K = h.size(0), h.size(1), w.size(0), ids.size(1)
+    _require_cuda(lse, grad_loss)
+    l1 = lse.reshape(-1).contiguous().float()
+    g1 = grad_loss.reshape(-1).contiguous().float()
+    if l1.numel() != N or g1.numel() != N:
+        raise ValueError("lse and grad_loss must have one value per hidden row")
+    if grad_bias is None:
+        grad_bias = bias is not None
+    dev = hidden.device
+    gh = torch.empty(N, H, dtype=out_dtype, device=dev) if grad_hidden else None
+    gw = torch.empty(V, H, dtype=out_dtype, device=dev) if grad_weight else None
+    gb = torch.empty(V, dtype=torch.float32, device=dev) if grad_bias else None
+    with torch.cuda.device(dev):
+        n = lib().rlk_linear_distill_backward_workspace_size(_ptr(h), N, H, ldh, _ptr(w), V, ldw, K,
+                                                             int(grad_bias))
+        if n == 0:
+            raise RlkError(2, "rlk_linear_distill_backward_workspace_size")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        dt = _DT[out_dtype]
+        _check(lib().rlk_linear_distill_backward(
+            _ptr(h), N, H, ldh, _ptr(w), V, ldw, _ptr(bias), _ptr(ids), ldi, _ptr(tl),
+            _DT[tl.dtype], ldt, K, _ptr(tlse), temperature, _ptr(l1), _ptr(g1), _ptr(gh), dt, H,
+            _ptr(gw), dt, H, _ptr(gb), _ptr(ws), n, _stream_ptr(stream)),
+            "rlk_linear_distill_backward")
+    out = (None if gh is None else gh.reshape(*hidden.shape[:-1], H), gw, gb)
+    if return_grad_logits:
+        ldG = -(-V // 8) * 8
+        out = out + (ws[:N * ldG * 2].view(torch.bfloat16).view(N, ldG)[:, :V],)
+    return out
+
+
+class _LinearDistillGrad(torch.autograd.Function):
+    """Autograd wiring of rlk_linear_distill and rlk_linear_distill_backward; lse is returned
+    as a constant and the teacher's tensors carry no gradient."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, temperature):
+        loss, lse = linear_distill(hidden.detach(), weight.detach(), teacher_ids, teacher_logits,
+                                   None if bias is None else bias.detach(),
+                                   temperature=temperature, teacher_lse=teacher_lse)
+        ctx.save_for_backward(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, lse)
+        ctx.temperature = temperature
+        ctx.mark_non_differentiable(lse)
+        return loss, lse
+
+    @staticmethod
+    def backward(ctx, grad_loss, _grad_lse):
+        hidden, weight, bias, ids, logits, teacher_lse, lse = ctx.saved_tensors
+        want_h, want_w, want_b = ctx.needs_input_grad[:3]
+        want_b = bool(want_b and bias is not None)
+        if grad_loss is None or not (want_h or want_w or want_b):
+            return (None,) * 7
+        gh, gw, gb = linear_distill_backward(hidden, weight, ids, logits, lse, grad_loss, bias,
+                                             temperature=ctx.temperature, teacher_lse=teacher_lse,
+                                             grad_hidden=want_h, grad_weight=want_w,
+                                             grad_bias=want_b)
+        return gh, gw, gb, None, None, None, None
+
+
+def linear_distill_trainable(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
+                             teacher_logits: torch.Tensor, bias: torch.Tensor | None = None, *,
+                             temperature: float = 1.0, teacher_lse: torch.Tensor | None = None):
+    """loss, lse as linear_distill, differentiable through loss with respect to hidden, weight and
+    bias (BF16 gradients of hidden and weight, FP32 of the bias).  lse carries no gradient."""
+    return _LinearDistillGrad.apply(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse,
+                                    temperature)
 
 
 # ------------------------------------------------------------------ det_gemm

@@ -281,6 +281,7 @@ const char* rlk_status_string(int status) {
       return "RLK_ERR_BOUNDS: a debug-build kernel skipped a store outside its buffer";
     case RLK_ERR_NOT_DEBUG_BUILD:
       return "RLK_ERR_NOT_DEBUG_BUILD: the call needs the debug build of the library";
+    case RLK_ERR_VALUE: return "RLK_ERR_VALUE: a scalar setting is out of range";
     default: return "RLK_ERR_UNKNOWN";
   }
 }
@@ -303,7 +304,7 @@ rlk_status rlk_get_device_error(void* stream, uint32_t* flags) {
     return RLK_ERR_CUDA;
   }
   *flags = rlk::take_error_linear_logp() | rlk::take_error_det_gemm() | rlk::take_error_common() |
-           rlk::take_error_linear_logp_bwd();
+           rlk::take_error_linear_logp_bwd() | rlk::take_error_linear_distill();
   if (*flags & RLK_DEVERR_TIMEOUT) return RLK_ERR_TIMEOUT;
   return *flags ? RLK_ERR_BOUNDS : RLK_OK;
 }

@@ -32,44 +32,13 @@
 #include "rlk_internal.h"
 #include "rlk_pipeline.cuh"
 #include "rlk_solo.cuh"
+#include "rlk_vocab.cuh"
 
 namespace rlk {
 
 __device__ unsigned int g_err_linear_logp = 0;
 
 namespace {
-
-struct LogpSched {
-  Banded order;    // rows = 256-row blocks, cols = this call's vocabulary splits
-  int* counter;    // zeroed unit counter in the workspace (units in order), or null (round-robin)
-  int S;           // vocabulary splits in this call (all S, or a shard's run of them)
-  int vps;         // 256-id tiles per split
-  int vtiles;      // 256-id tiles of the weight rows this call reads
-  int tile0;       // global index of the first of those tiles (0 unless a vocabulary shard)
-  int nkb;         // reduction stages over H (64 or 128 wide)
-  int nkb64;       // 64-wide blocks of H
-  __device__ __forceinline__ int num_units() const { return order.count(); }
-  __device__ __forceinline__ int split_of(int u) const {
-    int rb, j;
-    order.unit(u, rb, j);
-    return j;
-  }
-  __device__ __forceinline__ int rb_of(int u) const {
-    int rb, j;
-    order.unit(u, rb, j);
-    return rb;
-  }
-  __device__ __forceinline__ int first_tile(int u) const { return split_of(u) * vps; }
-  __device__ __forceinline__ int unit_tiles(int u) const {
-    const int t0 = first_tile(u);
-    return min(vps, vtiles - t0);
-  }
-  int rows_per_unit;   // 256 (a CTA pair's rows) or 128 (one CTA's, the one-CTA loop)
-  __device__ __forceinline__ void tile_coords(int u, int i, int& a0, int& b0) const {
-    a0 = rb_of(u) * rows_per_unit;
-    b0 = (first_tile(u) + i) * kBN;
-  }
-};
 
 struct LogpArgs {
   int N, V;                   // V: the whole vocabulary (ids past it are masked)
@@ -87,64 +56,19 @@ struct LogpArgs {
 // target capture and the online (m, s) update.  z values are natural-unit logits;
 // each exponential is 2^((z - m) * log2(e)) with z - m formed first, so the
 // running maximum's own term is exactly 2^0 = 1: s >= 1 always, hence lse >= max
-// logit and logp <= 0 hold exactly in FP32.  Column i's bias comes from the
-// warp's BiasTile (a shuffle: every lane of the warp takes part).
+// logit and logp <= 0 hold exactly in FP32.
 __device__ __forceinline__ void logp_chunk(const uint32_t (&r)[32], int vbase, int V,
                                            bool has_bias, const BiasTile& bias, int c,
                                            int64_t tgt, float& m, float& s, bool& have_zt,
                                            float& zt) {
   float z[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(r[i]);
-  if (has_bias) {
-    if (vbase + 32 <= V) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        z[i] = __fadd_rn(z[i], bias_tile_at(bias, c, i));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float b = bias_tile_at(bias, c, i);
-        if (vbase + i < V) z[i] = __fadd_rn(z[i], b);
-      }
-    }
-  }
-  if (vbase + 32 > V) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (vbase + i >= V) z[i] = -INFINITY;
-  }
+  chunk_logits(r, vbase, V, has_bias, bias, c, z);
   const int64_t d = tgt - vbase;
   if (d >= 0 && d < 32) {
-    // z[d] through a fixed 5-level select tree (keeps z in registers)
-    const int di = (int)d;
-    float t[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = (di & 16) ? z[i + 16] : z[i];
-#pragma unroll
-    for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-      for (int i = 0; i < w; ++i) t[i] = (di & w) ? t[i + w] : t[i];
-    zt = t[0];
+    zt = chunk_at(z, (int)d);
     have_zt = true;
   }
-  // chunk maximum (fixed pairwise tree)
-  float t[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) t[i] = fmaxf(z[2 * i], z[2 * i + 1]);
-#pragma unroll
-  for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-    for (int i = 0; i < w; ++i) t[i] = fmaxf(t[i], t[i + w]);
-  const float mn = fmaxf(m, t[0]);            // finite: vbase < V so z[0] is a real logit
-  const float scale = ex2_approx(__fmul_rn(__fsub_rn(m, mn), kLog2e));   // m = -inf -> 0
-  float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    a[i & 3] = __fadd_rn(a[i & 3], ex2_approx(__fmul_rn(__fsub_rn(z[i], mn), kLog2e)));
-  const float cs = __fadd_rn(__fadd_rn(a[0], a[1]), __fadd_rn(a[2], a[3]));
-  s = __fadd_rn(__fmul_rn(s, scale), cs);
-  m = mn;
+  chunk_fold(z, kLog2e, m, s);
 }
 
 // Epilogue warps (2..5) of both loops: each thread owns one row (TMEM lane) of
@@ -155,7 +79,7 @@ __device__ __forceinline__ void logp_chunk(const uint32_t (&r)[32], int vbase, i
 // the pair, units from the ring, release on rank 0's barrier).  The arithmetic
 // is the same code either way.
 template <bool kSolo>
-__device__ __forceinline__ void logp_epilogue(const LogpSched& sc, const LogpArgs& args,
+__device__ __forceinline__ void logp_epilogue(const VocabSched& sc, const LogpArgs& args,
                                               const PipeSmem& ps, uint32_t tmem) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int q = warp & 3;
@@ -229,7 +153,7 @@ __device__ __forceinline__ void logp_epilogue(const LogpSched& sc, const LogpArg
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_logp_partials_kernel(const __grid_constant__ CUtensorMap tm_hidden,
-                                     const __grid_constant__ CUtensorMap tm_weight, LogpSched sc,
+                                     const __grid_constant__ CUtensorMap tm_weight, VocabSched sc,
                                      LogpArgs args) {
   extern __shared__ uint8_t smem_raw[];
   if (threadIdx.x == 0) {
@@ -249,12 +173,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0)
-      producer_role<THalf, THalf, LogpSched, R>(&tm_hidden, &tm_weight, sc, ps, &g_err_linear_logp);
+      producer_role<THalf, THalf, VocabSched, R>(&tm_hidden, &tm_weight, sc, ps, &g_err_linear_logp);
     if (lane == 1 && ps.rank == 0) scheduler_role(sc, ps, &g_err_linear_logp);
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && ps.rank == 0)
-      mma_role<THalf, THalf, LogpSched, R>(sc, ps, tmem, idesc_bf16_f32(kPairRows, kBN, false, false),
+      mma_role<THalf, THalf, VocabSched, R>(sc, ps, tmem, idesc_bf16_f32(kPairRows, kBN, false, false),
                                            &g_err_linear_logp);
     __syncwarp();
   } else {
@@ -273,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <class R>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_logp_solo_kernel(const __grid_constant__ CUtensorMap tm_hidden,
-                            const __grid_constant__ CUtensorMap tm_weight, LogpSched sc,
+                            const __grid_constant__ CUtensorMap tm_weight, VocabSched sc,
                             LogpArgs args) {
   extern __shared__ uint8_t smem_raw[];
   if (threadIdx.x == 0) {
@@ -307,21 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     RLK_TRACE_CYCLES(7);
     RLK_TRACE(5);
   }
-}
-
-// (m, s) pair merge with explicit roundings, so merge(a, b) == merge(b, a) bitwise.
-__device__ __forceinline__ void merge_ms(float& M, float& s, float m2, float s2) {
-  if (m2 == -INFINITY) return;
-  if (M == -INFINITY) {
-    M = m2;
-    s = s2;
-    return;
-  }
-  const float Mn = fmaxf(M, m2);
-  const float e1 = ex2_approx(__fmul_rn(__fsub_rn(M, Mn), kLog2e));
-  const float e2 = ex2_approx(__fmul_rn(__fsub_rn(m2, Mn), kLog2e));
-  s = __fadd_rn(__fmul_rn(s, e1), __fmul_rn(s2, e2));
-  M = Mn;
 }
 
 // Where the merge reads a row's S partials and its target logit.
@@ -576,7 +485,7 @@ rlk_status launch_partials(const PartialsLaunch& L, const DeviceInfo& dev, cudaS
       !encode_bf16_2d(&tm_w, w_src, L.H, L.w_rows, L.ldw, kBK, solo ? kBN : kHalfRows))
     return RLK_ERR_CUDA;
 
-  LogpSched sc;
+  VocabSched sc;
   const int64_t splits = L.j1 - L.j0;
   sc.order.rows = (int)ceil_div(L.N, kRowsPerUnit);
   sc.order.cols = (int)splits;

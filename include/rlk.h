@@ -23,8 +23,8 @@
  *  - Errors.  Arguments are validated on the host before anything is launched;
  *    on any error nothing is launched and no output is touched.  A launch that
  *    the CUDA runtime rejects returns RLK_ERR_CUDA.  A zero-row call (N == 0 in
- *    rlk_linear_logp, M == 0 in rlk_det_gemm_fwd / _da) is a no-op that
- *    returns RLK_OK.
+ *    rlk_linear_logp, rlk_linear_distill and rlk_sample_logits, M == 0 in
+ *    rlk_det_gemm_fwd / _da) is a no-op that returns RLK_OK.
  *  - Determinism.  For fixed inputs every output bit is identical run to run,
  *    across streams, across leading dimensions and pointer alignment, and -- for
  *    every product whose reduction does not run over the rows (all but dB and
@@ -84,7 +84,8 @@ typedef enum rlk_status {
     RLK_ERR_CUDA = 7,               /* the CUDA runtime rejected a launch or query      */
     RLK_ERR_TIMEOUT = 8,            /* a kernel's bounded wait expired (device error)   */
     RLK_ERR_BOUNDS = 9,             /* debug build: a kernel skipped an out-of-bounds store */
-    RLK_ERR_NOT_DEBUG_BUILD = 10    /* the call exists only in the debug build          */
+    RLK_ERR_NOT_DEBUG_BUILD = 10,   /* the call exists only in the debug build          */
+    RLK_ERR_VALUE = 11              /* a scalar setting (a temperature) is out of range */
 } rlk_status;
 
 typedef enum rlk_dtype {
@@ -470,6 +471,79 @@ RLK_API rlk_status rlk_linear_logp_backward(const void* hidden, int64_t N, int64
                                             int grad_weight_dtype, int64_t ld_grad_weight,
                                             float* grad_bias, void* workspace,
                                             size_t workspace_bytes, void* stream);
+
+/* ===================================================================== *
+ *  Distillation from a teacher's top logits                              *
+ * ===================================================================== */
+
+/*
+ * A linear student (hidden, lm-head weight, optional bias) against the K largest
+ * logits of a teacher at each row, at temperature T, without the [N, V] logits:
+ *   log q_k = t_k / T - L,     L = teacher_lse[r], or log sum_k exp(t_k / T) when NULL
+ *   lse[r]  = log sum_v exp(z[r, v] / T),   z[r, v] = hidden[r] . weight[v] (+ bias[v])
+ *   loss[r] = T^2 * sum_k q_k (log q_k - z[r, id_k] / T + lse[r])
+ * i.e. T^2 KL(q || student) over the teacher's slots: with L from the slots q sums to
+ * one; with the teacher's own log-sum-exp (over its whole vocabulary, at T) q keeps
+ * its probabilities there and the rest of its mass takes no part.
+ *
+ *  hidden, weight, bias   as for rlk_linear_logp
+ *  teacher_ids      int64 [N, K], row pitch ld_ids (>= K): vocabulary ids, in any order;
+ *                   an id named by several slots counts once for each
+ *  teacher_logits   [N, K] in logits_dtype (RLK_BF16 / RLK_FP32), row pitch ld_logits
+ *  K                0 .. RLK_DISTILL_MAX_SLOTS slots per row.  A slot whose id is outside
+ *                   [0, V) or whose logit is -inf is empty (pad lists of unequal length
+ *                   with id -1; what an empty slot's logit holds does not matter).
+ *                   A row without used slots has loss 0 and gradient 0.  A NaN or +inf
+ *                   logit in a used slot makes the row's loss NaN.
+ *  teacher_lse      FP32 [N] or NULL
+ *  temperature      T, 1e-4 .. 1e4 (RLK_ERR_VALUE otherwise)
+ *  loss, lse        FP32 [N] outputs
+ *  workspace        >= rlk_linear_distill_workspace_size(...) bytes, 256-byte aligned
+ *
+ * Arithmetic: the logits, their split over V and the (max, sum) merge are
+ * rlk_linear_logp's, with exponents (z - max) log2(e) / T, so at T = 1 lse has its
+ * bits, and K = 1 gives loss = -logp exactly.  sum q z is added per split in ascending
+ * id order and merged over the splits in the fixed order; the sums over a row's slots
+ * run in a fixed order of the slots.  A row's bits depend on its own inputs, V, H and
+ * K alone.
+ */
+#define RLK_DISTILL_MAX_SLOTS 1024
+RLK_API size_t rlk_linear_distill_workspace_size(const void* hidden, int64_t N, int64_t H,
+                                                 int64_t ld_hidden, const void* weight, int64_t V,
+                                                 int64_t ld_weight, int64_t K);
+RLK_API rlk_status rlk_linear_distill(const void* hidden, int64_t N, int64_t H, int64_t ld_hidden,
+                                      const void* weight, int64_t V, int64_t ld_weight,
+                                      const float* bias, const int64_t* teacher_ids,
+                                      int64_t ld_ids, const void* teacher_logits,
+                                      int logits_dtype, int64_t ld_logits, int64_t K,
+                                      const float* teacher_lse, float temperature, float* loss,
+                                      float* lse, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Backward of rlk_linear_distill for an upstream gradient g = dL/dloss [N]:
+ *   G[r, v]     = g[r] T (Q exp(z[r, v] / T - lse[r]) - sum_{k: id_k = v} q_k),  Q = sum_k q_k
+ *   grad_hidden = G . W,   grad_weight = G^T . hidden,   grad_bias[v] = sum_r G[r, v]
+ * G is formed in FP32 from the recomputed logits and the forward's lse.  The two
+ * products read it rounded to BF16 (nearest even), with FP32 accumulation, as in
+ * rlk_linear_logp_backward (they are rlk_det_gemm_fwd and rlk_det_gemm_db); grad_bias
+ * adds the unrounded G, 32 rows at a time in a fixed tree, those sums in ascending
+ * order.  Outputs, dtypes, pitches and the N == 0 case as for rlk_linear_logp_backward;
+ * any of the three may be NULL.  The workspace (256-byte aligned) begins with G as BF16
+ * [N, 8*ceil(V/8)].
+ */
+RLK_API size_t rlk_linear_distill_backward_workspace_size(const void* hidden, int64_t N, int64_t H,
+                                                          int64_t ld_hidden, const void* weight,
+                                                          int64_t V, int64_t ld_weight, int64_t K,
+                                                          int want_bias);
+RLK_API rlk_status rlk_linear_distill_backward(
+    const void* hidden, int64_t N, int64_t H, int64_t ld_hidden, const void* weight, int64_t V,
+    int64_t ld_weight, const float* bias, const int64_t* teacher_ids, int64_t ld_ids,
+    const void* teacher_logits, int logits_dtype, int64_t ld_logits, int64_t K,
+    const float* teacher_lse, float temperature, const float* lse, const float* grad_loss,
+    void* grad_hidden, int grad_hidden_dtype, int64_t ld_grad_hidden, void* grad_weight,
+    int grad_weight_dtype, int64_t ld_grad_weight, float* grad_bias, void* workspace,
+    size_t workspace_bytes, void* stream);
 
 /* ===================================================================== *
  *  Deterministic GEMM family                                      [P1]  *
