@@ -34,7 +34,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "librlk_debug.so" if os.environ.get("RLK_LIBRA
                         else "librlk.so")
 
 RLK_OK = 0
-RLK_BF16, RLK_FP32 = 0, 1
+RLK_BF16, RLK_FP32, RLK_FP64 = 0, 1, 2
 RLK_GEMM_FWD, RLK_GEMM_DA, RLK_GEMM_DB = 0, 1, 2
 RLK_GEMM_LINEAR_FWD, RLK_GEMM_LINEAR_DX, RLK_GEMM_LINEAR_DW, RLK_GEMM_FWD_ACCUM = 3, 4, 5, 6
 STATUS_NAMES = {0: "RLK_OK", 1: "RLK_ERR_NULL", 2: "RLK_ERR_SHAPE", 3: "RLK_ERR_DTYPE",
@@ -93,6 +93,8 @@ SIGNATURES = {
     "rlk_linear_logp_backward_workspace_size_for": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64]),
     "rlk_linear_logp_backward": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P,
                                       _P, _I, _I64, _P, _I, _I64, _P, _P, _SZ, _P]),
+    "rlk_sample_logits": (_I, [_P, _I, _I64, _I64, _I64, _P, _I, _P, _F, _P, ctypes.c_int32, _P, _F,
+                               _P, _F, _P, _P, _P]),
     "rlk_linear_distill_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64]),
     "rlk_linear_distill": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I, _I64,
                                 _I64, _P, _F, _P, _P, _P, _SZ, _P]),
@@ -610,6 +612,59 @@ def linear_logp_trainable(hidden: torch.Tensor, weight: torch.Tensor, target: to
     no gradient.  linear_logp itself stays forward-only and rejects inputs that
     require grad."""
     return _LinearLogpGrad.apply(hidden, weight, bias, target)
+
+
+# ------------------------------------------------------------------ sampling
+def _per_row(value, name: str, N: int, dtype):
+    """(tensor or None, scalar) of a sampling setting given per row or for all rows."""
+    if not isinstance(value, torch.Tensor):
+        return None, value
+    _require_cuda(value)
+    if value.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor or a number")
+    if value.numel() != N:
+        raise ValueError(f"{name} must have one value per row")
+    return value.reshape(-1).contiguous(), 0
+
+
+def sample_logits(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.0, top_k=0,
+                  top_p=1.0, min_p=0.0, stream=None):
+    """token (int64), logp (FP32), shaped like logits' leading dims: one token a row.
+
+    logits [..., V] bf16 or fp32; uniform [...] fp32 or fp64, one number in [0, 1) a row (fp64
+    reaches all 2^31 steps).  temperature, top_k, top_p and min_p are numbers or per-row tensors
+    (float32; int32 for top_k).  Kept are the top_k largest, of those the smallest leading set
+    whose probability reaches top_p, of those the ids at least min_p times as probable as the
+    likeliest; logp is the token's log-probability among what is kept.  temperature 0 is greedy;
+    top_k <= 0, top_p = 1 and min_p = 0 keep all.  Equal logits are ordered by id.  The token is
+    a function of its row alone, bit for bit.  A row without a distribution (NaN or +inf among
+    its logits or settings, or every id banned with -inf) gives token -1 and logp NaN.
+    """
+    _require_cuda(logits, uniform)
+    if logits.dtype not in _DT:
+        raise TypeError("logits must be bfloat16 or float32")
+    if uniform.dtype not in (torch.float32, torch.float64):
+        raise TypeError("uniform must be float32 or float64")
+    lead, V = logits.shape[:-1], logits.size(-1)
+    if uniform.shape != lead:
+        raise ValueError("uniform must have one number per row of logits")
+    z, ld = _matrix(logits.reshape(-1, V) if logits.dim() != 2 else logits, "logits")
+    N = z.size(0)
+    u = uniform.reshape(-1).contiguous()
+    tau, tau_all = _per_row(temperature, "temperature", N, torch.float32)
+    k, k_all = _per_row(top_k, "top_k", N, torch.int32)
+    p, p_all = _per_row(top_p, "top_p", N, torch.float32)
+    m, m_all = _per_row(min_p, "min_p", N, torch.float32)
+    dev = logits.device
+    token = torch.empty(N, dtype=torch.int64, device=dev)
+    logp = torch.empty(N, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().rlk_sample_logits(
+            _ptr(z), _DT[z.dtype], N, V, ld, _ptr(u),
+            RLK_FP32 if u.dtype == torch.float32 else RLK_FP64, _ptr(tau), tau_all, _ptr(k), k_all,
+            _ptr(p), p_all, _ptr(m), m_all, _ptr(token), _ptr(logp), _stream_ptr(stream)),
+            "rlk_sample_logits")
+    return token.reshape(lead), logp.reshape(lead)
 
 
 # ------------------------------------------------------------------ distillation

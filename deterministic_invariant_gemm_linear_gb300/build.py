@@ -27,7 +27,7 @@ FLAVORS = {"release": (LIB_PATH, []),
            "debug": (os.path.join(PKG_DIR, "librlk_debug.so"), ["-DRLK_DEBUG"])}
 
 SOURCES = ["common.cu", "linear_logp.cu", "linear_logp_bwd.cu", "linear_distill.cu",
-           "det_gemm.cu"]
+           "sample.cu", "det_gemm.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("rlk_device.cuh", "rlk_pipeline.cuh", "rlk_solo.cuh", "rlk_vocab.cuh",
                                              "rlk_internal.h")]
 HEADERS.append(os.path.join(INCLUDE, "rlk.h"))

@@ -304,7 +304,8 @@ rlk_status rlk_get_device_error(void* stream, uint32_t* flags) {
     return RLK_ERR_CUDA;
   }
   *flags = rlk::take_error_linear_logp() | rlk::take_error_det_gemm() | rlk::take_error_common() |
-           rlk::take_error_linear_logp_bwd() | rlk::take_error_linear_distill();
+           rlk::take_error_linear_logp_bwd() | rlk::take_error_linear_distill() |
+           rlk::take_error_sample();
   if (*flags & RLK_DEVERR_TIMEOUT) return RLK_ERR_TIMEOUT;
   return *flags ? RLK_ERR_BOUNDS : RLK_OK;
 }

@@ -148,5 +148,6 @@ uint32_t take_error_det_gemm();
 uint32_t take_error_common();
 uint32_t take_error_linear_logp_bwd();
 uint32_t take_error_linear_distill();
+uint32_t take_error_sample();
 
 }  // namespace rlk

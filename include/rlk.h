@@ -90,7 +90,8 @@ typedef enum rlk_status {
 
 typedef enum rlk_dtype {
     RLK_BF16 = 0,                   /* bfloat16, 2 bytes                                */
-    RLK_FP32 = 1                    /* IEEE binary32, 4 bytes                           */
+    RLK_FP32 = 1,                   /* IEEE binary32, 4 bytes                           */
+    RLK_FP64 = 2                    /* IEEE binary64, 8 bytes (uniform numbers only)    */
 } rlk_dtype;
 
 /* Device error-word bits reported by rlk_get_device_error. */
@@ -471,6 +472,50 @@ RLK_API rlk_status rlk_linear_logp_backward(const void* hidden, int64_t N, int64
                                             int grad_weight_dtype, int64_t ld_grad_weight,
                                             float* grad_bias, void* workspace,
                                             size_t workspace_bytes, void* stream);
+
+/* ===================================================================== *
+ *  Sampling                                                              *
+ * ===================================================================== */
+
+/*
+ * One token per row of logits z [N, V], from one uniform number u per row.  With the
+ * row's maximum m and c = log2(e) / T, the weight of id v is the whole number
+ *   w_v = 2^31 * 2^max((z_v - m) c, -126), rounded to nearest even,
+ * its logits' differences, products and 2^x each rounded in FP32 (2^x: a degree-5
+ * polynomial on [-1/2, 1/2], relative error below 2e-7).  In descending order of z,
+ * equal logits in ascending order of id, id v is kept when
+ *   top-k   fewer than k ids come before it,
+ *   top-p   the weights before it sum to less than max(1, floor(p C_k)), C_k = the
+ *           weight of the ids top-k keeps, p as a multiple of 2^-24,
+ *   min-p   w_v >= min_p * 2^31, min_p as a multiple of 2^-24.
+ * With C = the weight kept, the token is the first id (in ascending order) whose running
+ * sum of kept weights exceeds floor(floor(2^31 u) C / 2^31), and
+ *   logp = (z_token - m) / T - log(C / 2^31),
+ * its log-probability under the distribution drawn from.  All sums are of whole
+ * numbers: the token depends on its own row's inputs alone, whatever the other rows,
+ * their number, the layout and the device do.
+ *
+ *  logits        [N, V] in logits_dtype (RLK_BF16 / RLK_FP32), row pitch ld (>= V); any
+ *                alignment.  -inf (or any very low value) bans an id.
+ *  uniform       [N] in uniform_dtype (RLK_FP32 / RLK_FP64), in [0, 1); 2^31 u is
+ *                rounded down, so FP64 gives all 2^31 steps (values outside are clamped)
+ *  temperature, top_k, top_p, min_p   per-row arrays [N], or NULL for the _all value
+ *                shared by all rows.  T below 1e-6 (0 included) is greedy: the largest
+ *                logit, lowest id, logp 0.  k <= 0 and k >= V keep all; top_p and min_p
+ *                are clamped to [0, 1] (1 and 0 keep all).
+ *  token, logp   int64 [N] and FP32 [N] outputs
+ * A row that defines no distribution -- a NaN or +inf among its logits, no logit above
+ * -inf, a NaN among its settings or u, a negative or infinite T -- gets token -1 and
+ * logp NaN.  Such a value in an _all argument is refused (RLK_ERR_VALUE).
+ * 1 <= V <= RLK_SAMPLE_MAX_VOCAB, 0 <= N < 2^27.  No workspace.
+ */
+#define RLK_SAMPLE_MAX_VOCAB 524288
+RLK_API rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64_t N, int64_t V,
+                                     int64_t ld, const void* uniform, int uniform_dtype,
+                                     const float* temperature, float temperature_all,
+                                     const int32_t* top_k, int32_t top_k_all, const float* top_p,
+                                     float top_p_all, const float* min_p, float min_p_all,
+                                     int64_t* token, float* logp, void* stream);
 
 /* ===================================================================== *
  *  Distillation from a teacher's top logits                              *
