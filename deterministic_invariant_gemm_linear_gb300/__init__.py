@@ -93,8 +93,9 @@ SIGNATURES = {
     "rlk_linear_logp_backward_workspace_size_for": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64]),
     "rlk_linear_logp_backward": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P,
                                       _P, _I, _I64, _P, _I, _I64, _P, _P, _SZ, _P]),
+    "rlk_sample_logits_workspace_size": (_SZ, [_I, _I64, _I64]),
     "rlk_sample_logits": (_I, [_P, _I, _I64, _I64, _I64, _P, _I, _P, _F, _P, ctypes.c_int32, _P, _F,
-                               _P, _F, _P, _P, _P]),
+                               _P, _F, _P, _P, _P, _SZ, _P]),
     "rlk_linear_distill_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64]),
     "rlk_linear_distill": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I, _I64,
                                 _I64, _P, _F, _P, _P, _P, _SZ, _P]),
@@ -658,12 +659,14 @@ def sample_logits(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.
     dev = logits.device
     token = torch.empty(N, dtype=torch.int64, device=dev)
     logp = torch.empty(N, dtype=torch.float32, device=dev)
+    nb = lib().rlk_sample_logits_workspace_size(_DT[z.dtype], N, V)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
     with torch.cuda.device(dev):
         _check(lib().rlk_sample_logits(
             _ptr(z), _DT[z.dtype], N, V, ld, _ptr(u),
             RLK_FP32 if u.dtype == torch.float32 else RLK_FP64, _ptr(tau), tau_all, _ptr(k), k_all,
-            _ptr(p), p_all, _ptr(m), m_all, _ptr(token), _ptr(logp), _stream_ptr(stream)),
-            "rlk_sample_logits")
+            _ptr(p), p_all, _ptr(m), m_all, _ptr(token), _ptr(logp), _ptr(ws), nb,
+            _stream_ptr(stream)), "rlk_sample_logits")
     return token.reshape(lead), logp.reshape(lead)
 
 

@@ -17,14 +17,19 @@
 // of the relative error (below 2e-7), its products and sums rounded one by one.  A weight
 // below 2^-32 of the largest is 0; u's own steps are 2^-31.
 //
-// The row is read once from memory (the bound: V elements) and stays on chip: a cluster of
-// 1 - 16 CTAs holds it in shared memory, each CTA a contiguous run of ids, and passes over
-// it there.  After the maximum, rows with top-k or top-p find where the kept prefix of the
-// sorted order ends without sorting the row: a histogram of x over 16 octaves (counts, and
-// weights for top-p), whose bins are runs of the sorted order, gives the bin the cut falls
-// in.  If what lies up to that bin is at most kList elements, the leading CTA sorts just
-// those and finishes; otherwise the cut is narrowed inside the bin by histograms of the
-// logits' bit patterns to one value, then one id among equal values.
+// A cluster of 1 - 16 CTAs takes a row, each CTA a contiguous run of its ids.  The bound is
+// reading the row once from memory; a row needs one pass for its maximum and at least one
+// more, from shared memory (kOnChip) or from L2.  No row is sorted:
+//  * top-k of few (the usual): a CTA's threads each know their own largest logit, so the
+//    k-th largest of those is a value that at least k of the CTA's logits reach.  What
+//    reaches it goes to the leading CTA, which sorts those few and finishes the row: one
+//    cluster barrier in all.
+//  * otherwise: a histogram of x over the 32 octaves that have weight (counts, and weights
+//    for top-p), whose bins are runs of the sorted order, gives the bin the cut falls in.
+//    If what lies up to that bin is at most kList elements, the leading CTA finishes as
+//    above; else it sorts that bin alone to find the cut, and the cluster draws from what
+//    lies before it.  A bin of more than kList elements (many equal logits) is narrowed by
+//    histograms of the logits' bit patterns to one value, then one id among equal values.
 #include <math.h>
 
 #include <mutex>
@@ -39,18 +44,26 @@ __device__ unsigned int g_err_sample = 0;
 
 namespace {
 
-constexpr int kSampleThreads = 512;
-constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 1024;                  // histogram bins; two per thread in the scan
+constexpr int kMaxSampleWarps = 16;
+constexpr int kBins = 1024;                  // histogram bins
 constexpr int kList = 2048;                  // candidates the leading CTA sorts
 constexpr int kMaxCluster = 16;
 constexpr int64_t kMaxSampleVocab = 524288;
-constexpr float kWindow = 16.f;              // octaves of x per histogram window
-constexpr int kWindows = 2;                  // weights vanish below 2^-32
+constexpr int64_t kMaxSampleRows = int64_t(1) << 20;
+constexpr int64_t kStreamBytes = int64_t(24) << 20;   // logits from which the streaming kernels run
+constexpr float kOctaves = 32.f;             // weights vanish below 2^-32
+constexpr float kNear = 20.f;                // octaves of top-p's first histogram
 constexpr uint32_t kOne = 1u << 31;
 constexpr uint32_t kFull = 0xffffffffu;
 
-static_assert(kBins == 2 * kSampleThreads, "the scan takes two bins per thread");
+// What the streaming kernels know of a row between them.
+enum RowStatus { kDone = 0, kWeigh = 1, kWeighBins = 2, kWeighKept = 3, kGeneral = 4 };
+struct RowState {
+  int status;
+  float m;               // its largest logit
+  float cut;             // kept: z > cut, or z = cut and id <= cut_id
+  int cut_id;
+};
 
 struct SampleArgs {
   const void* logits;
@@ -64,8 +77,10 @@ struct SampleArgs {
   int top_k_all;
   const void* uniform;
   int uniform_fp64;
+  int fp32;
   int64_t* token;
   float* logp;
+  const RowState* state;      // not null: only the rows left for the general search
 };
 
 // ---------------------------------------------------------------- weights
@@ -73,19 +88,71 @@ __device__ __forceinline__ float x_of(float z, float m, float c) {
   return fmaxf(__fmul_rn(__fsub_rn(z, m), c), -126.f);
 }
 
-// 2^(x + 31) rounded to a whole number (nearest even), x in [-126, 0].
+// Two weights, 2^(x + 31) rounded to a whole number (nearest even), from two logits.  The
+// packed operations round each half as the single ones do.  x + 1.5 2^23 rounds x to a
+// whole number n and leaves it in the low bits; the polynomial's coefficients carry the
+// factor 2^31, and n is added to the result's exponent.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ uint64_t both(float a) { return pack_f2(a, a); }
+
+constexpr float kRound = 12582912.f;         // 1.5 * 2^23
+
+__device__ __forceinline__ void weights_of(float x0, float x1, uint32_t& w0, uint32_t& w1) {
+  constexpr float kExp2[6] = {0.0013264727313071489f * 0x1p31f, 0.009671512991189957f * 0x1p31f,
+                              0.05550733581185341f * 0x1p31f, 0.24022242426872253f * 0x1p31f,
+                              0.6931470036506653f * 0x1p31f, 0x1p31f};
+  const uint64_t x = pack_f2(x0, x1);
+  const uint64_t t = add_f2(x, both(kRound));
+  const uint64_t n = add_f2(t, both(-kRound));
+  const uint64_t f = fma_f2(n, both(-1.f), x);     // x - n, exact
+  uint64_t y = both(kExp2[0]);
+#pragma unroll
+  for (int i = 1; i < 6; ++i) y = add_f2(mul_f2(y, f), both(kExp2[i]));
+  float t0, t1, y0, y1;
+  unpack_f2(t, t0, t1);
+  unpack_f2(y, y0, y1);
+  w0 = __float2uint_rn(__int_as_float(__float_as_int(y0) + (__float_as_int(t0) << 23)));
+  w1 = __float2uint_rn(__int_as_float(__float_as_int(y1) + (__float_as_int(t1) << 23)));
+}
+// x of two logits, by the operations of x_of.
+__device__ __forceinline__ void x_pair(float z0, float z1, float m, float c, float& x0, float& x1) {
+  unpack_f2(mul_f2(add_f2(pack_f2(z0, z1), both(-m)), both(c)), x0, x1);
+  x0 = fmaxf(x0, -126.f);
+  x1 = fmaxf(x1, -126.f);
+}
 __device__ __forceinline__ uint32_t weight_of(float x) {
-  constexpr float kRound = 12582912.f;       // 1.5 * 2^23: adding it rounds to a whole number
-  const float t = __fadd_rn(x, kRound);
-  const float f = __fsub_rn(x, __fsub_rn(t, kRound));
-  float y = 0.0013264727313071489f;
-  y = __fadd_rn(__fmul_rn(y, f), 0.009671512991189957f);
-  y = __fadd_rn(__fmul_rn(y, f), 0.05550733581185341f);
-  y = __fadd_rn(__fmul_rn(y, f), 0.24022242426872253f);
-  y = __fadd_rn(__fmul_rn(y, f), 0.6931470036506653f);
-  y = __fadd_rn(__fmul_rn(y, f), 1.f);
-  const int n = __float_as_int(t) - __float_as_int(kRound) + 31;
-  return __float2uint_rn(__int_as_float(__float_as_int(y) + (n << 23)));
+  uint32_t w, unused;
+  weights_of(x, x, w, unused);
+  return w;
+}
+
+// a + b as one multiply-add (a 64-bit addition is two instructions of the busier pipe).
+__device__ __forceinline__ uint64_t add_wide(uint64_t a, uint32_t b) {
+  uint64_t v;
+  asm("mad.wide.u32 %0, %1, 1, %2;" : "=l"(v) : "r"(b), "l"(a));
+  return v;
 }
 
 // Order-preserving bit pattern of a logit (+0 and -0 alike).
@@ -97,11 +164,23 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// Bin of x in the window [-(w + 1) kWindow, -w kWindow): 0 .. kBins - 1 inside, negative
-// above, kBins or more below.  Falls with x, so a bin is a run of the sorted order.
-__device__ __forceinline__ int bin_of(float x, int window) {
-  return __float2int_rd(__fmul_rn(__fsub_rn(-kWindow * window, x), kBins / kWindow));
-}
+// A range of octaves below the top, and the bin of x in it, 0 .. kBins - 1.  The bin falls
+// with x, so a bin is a run of the sorted order.
+struct Window {
+  float from, to, scale, origin;
+  __device__ __forceinline__ Window(float from, float to)
+      : from(from), to(to), scale((kBins - 1) / (to - from)), origin(kRound - from * scale) {}
+  // for x in [-to, -from]
+  __device__ __forceinline__ int at(float x) const {
+    return __float_as_int(__fmaf_rn(x, -scale, origin)) - __float_as_int(kRound);
+  }
+  __device__ __forceinline__ bool has(float x) const { return x > -to && x <= -from; }
+  // -1 above the range, kBins below it
+  __device__ __forceinline__ int bin(float x) const {
+    return x <= -to ? kBins : (x > -from ? -1 : at(x));
+  }
+};
+__device__ __forceinline__ Window all_octaves() { return Window(0.f, kOctaves); }
 
 // floor(a b / 2^31) and floor(a p / 2^24), a < 2^50, b < 2^31, p <= 2^24, exactly.
 __device__ __forceinline__ uint64_t scaled_31(uint64_t a, uint32_t b) {
@@ -111,20 +190,112 @@ __device__ __forceinline__ uint64_t scaled_24(uint64_t a, uint32_t p) {
   return (((a >> 31) * p) << 7) + (((a & (kOne - 1)) * p) >> 24);
 }
 
-// ---------------------------------------------------------------- the row on chip
+// A load that stays where it stands (an ordinary one sinks to its use, behind a condition,
+// and the loads of a batch go out one after another's return).
+__device__ __forceinline__ uint4 load_now(const uint4* p) {
+  uint4 q;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "l"(p));
+  return q;
+}
+
+// ---------------------------------------------------------------- the row
 // The row in 16-byte vectors of its memory: element j of the vectors is id j - lead, where
 // lead (< one vector) is how far the row's start lies past a 16-byte boundary; elements
-// outside the row are -inf.  The CTA of rank r holds vectors [r * per, (r + 1) * per); in
+// outside the row are -inf.  The CTA of rank r has vectors [r * per, (r + 1) * per); in
 // every pass, warp w takes a contiguous part of them, a vector per lane and step, so the
 // order (CTA, warp, step, lane, element) is the order of ids.
-template <bool kFp32>
+template <bool kFp32, bool kOnChip>
 struct Row {
   static constexpr int kElems = kFp32 ? 4 : 8;
-  const uint4* smem;     // this CTA's vectors
+  const uint4* memory;   // the CTA's first vector in global memory
+  uint4* chip;           // and in shared memory
+  const void* start;     // id 0
   int first_id;          // id of the CTA's element 0
-  int v0, v1;            // this warp's vectors
+  int V;
+  int full0, full1;      // the CTA's vectors that lie in the row as a whole
+  int v0, v1;            // this warp's vectors, from the CTA's first
 
-  __device__ __forceinline__ void get(int v, float (&z)[kElems]) const { unpack(smem[v], z); }
+  // Sets all but chip, v0 and v1 for the row's vectors; returns their number.
+  __device__ __forceinline__ int begin(const SampleArgs& a, int row) {
+    const int esize = kFp32 ? 4 : 2;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) + (uintptr_t)(row * a.ld) * esize;
+    const int lead = (int)(at & 15) / esize;
+    memory = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+    chip = nullptr;
+    start = reinterpret_cast<const void*>(at);
+    first_id = -lead;
+    V = a.V;
+    full0 = lead > 0 ? 1 : 0;
+    full1 = (lead + a.V) / kElems;
+    return (lead + a.V + kElems - 1) / kElems;
+  }
+  // Counts vectors from the n-th on.
+  __device__ __forceinline__ void skip(int n) {
+    memory += n;
+    first_id += n * kElems;
+    full0 -= n;
+    full1 -= n;
+  }
+  __device__ __forceinline__ int id_of(int v) const { return first_id + v * kElems; }
+  __device__ __forceinline__ bool whole(int v) const { return v >= full0 && v < full1; }
+  __device__ __forceinline__ uint4 load_part(int v) const {
+    const int id0 = id_of(v);                      // the row's first or last vector
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kFp32) {
+        p[i] = 0xff800000u;
+        if (id0 + i >= 0 && id0 + i < V) p[i] = __ldg(static_cast<const uint32_t*>(start) + id0 + i);
+      } else {
+        uint32_t h[2] = {0xff80u, 0xff80u};
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+          if (id0 + 2 * i + o >= 0 && id0 + 2 * i + o < V)
+            h[o] = __ldg(static_cast<const uint16_t*>(start) + id0 + 2 * i + o);
+        p[i] = h[0] | (h[1] << 16);
+      }
+    }
+    return make_uint4(p[0], p[1], p[2], p[3]);
+  }
+  __device__ __forceinline__ uint4 get(int v) const {
+    if constexpr (kOnChip) return chip[v];
+    return whole(v) ? __ldg(memory + v) : load_part(v);
+  }
+  // Several vectors, all on their way before any is used: the loads are unconditional (of
+  // some whole vector where v is not one), and the row's ends are set right afterwards.
+  template <bool kFromMemory, int kN>
+  __device__ __forceinline__ void get_all(const int (&v)[kN], uint4 (&q)[kN]) const {
+    if constexpr (kOnChip && !kFromMemory) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (v[i] < v1) q[i] = chip[v[i]];
+    } else {
+      if (full1 > full0) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) q[i] = load_now(memory + min(max(v[i], full0), full1 - 1));
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (!whole(v[i]) && v[i] < v1) q[i] = load_part(v[i]);
+    }
+  }
+  // The warp's vectors in order, kN a lane at a time: use(vector, its elements).
+  template <bool kFromMemory, int kN, class F>
+  __device__ __forceinline__ void each(F use) const {
+    for (int base = v0; base < v1; base += 32 * kN) {
+      int v[kN];
+      uint4 q[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = base + 32 * i + (int)(threadIdx.x & 31);
+      get_all<kFromMemory>(v, q);
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (v[i] < v1) use(v[i], q[i]);
+    }
+  }
+  __device__ __forceinline__ void get(int v, float (&z)[kElems]) const { unpack(get(v), z); }
   static __device__ __forceinline__ void unpack(const uint4& q, float (&z)[kElems]) {
     const uint32_t r[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -135,6 +306,26 @@ struct Row {
         z[2 * i] = __uint_as_float(r[i] << 16);
         z[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
       }
+    }
+  }
+  // The largest of a vector's logits; NaN if one of them is.
+  static __device__ __forceinline__ float top_of(const uint4& q) {
+    float a, b;
+    if constexpr (kFp32) {
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(__uint_as_float(q.x)), "f"(__uint_as_float(q.y)));
+      asm("max.NaN.f32 %0, %1, %2, %3;"
+          : "=f"(b)
+          : "f"(__uint_as_float(q.z)), "f"(__uint_as_float(q.w)), "f"(a));
+      return b;
+    } else {
+      uint32_t h, l;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(h) : "r"(q.x), "r"(q.y));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(l) : "r"(q.z), "r"(q.w));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(l));
+      asm("max.NaN.f32 %0, %1, %2;"
+          : "=f"(a)
+          : "f"(__uint_as_float(h << 16)), "f"(__uint_as_float(h & 0xffff0000u)));
+      return a;
     }
   }
 };
@@ -153,15 +344,6 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t atom_add_cluster(uint32_t addr, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;"
-               : "=r"(old)
-               : "r"(addr), "r"(v)
-               : "memory");
-  return old;
-}
-
 // Cluster barrier after code in which a warp's lanes may have parted.
 __device__ __forceinline__ void cluster_join() {
   __syncwarp();
@@ -169,58 +351,85 @@ __device__ __forceinline__ void cluster_join() {
 }
 
 struct Cut {             // where a search ended
-  int bin;               // -1: not in this histogram
+  int bin;               // -1: nowhere in the histogram
   uint32_t before, in;   // elements in the bins before it, and in it
   uint64_t mass;         // weight of the bins before it
 };
 
-// Fixed shared memory; the row's vectors follow.  The candidates take the histogram's
-// place: they are pushed after the second barrier of find_cut, past which no CTA reads
-// another's histogram.
-struct SampleSmem {
+constexpr int kSlots = 10;
+
+// Fixed shared memory; the row's vectors follow (kOnChip).  The list takes the histogram's
+// place: it is filled after the second barrier of find_cut (or before any histogram), when
+// no CTA reads another's histogram.
+struct alignas(16) SampleSmem {
   union {
     struct {
       uint32_t count[kBins], lo[kBins], hi[kBins];   // this CTA's; weights as two halves
     };
-    uint64_t list[kList];                        // candidates (in the leading CTA)
+    uint64_t list[kList];                        // this CTA's candidates; the leading CTA's, all
   };
   uint64_t slice_mass[kBins];                    // merged: this CTA's 1 / C of the bins
   uint32_t slice_count[kBins];
-  uint64_t part[8][kSampleWarps];                // block reductions
-  uint64_t xch[8];                               // a CTA's values for its peers, a slot a step
-  uint64_t xmass[4];
+  // Values pushed here by the CTAs of the cluster, one set per exchange of the row.
+  uint64_t from[kSlots][kMaxCluster];
+  uint64_t part[4][kMaxSampleWarps];              // block reductions and scans
+  uint64_t total[4];
   Cut cut;
-  uint32_t n_list;
+  uint32_t top;                                  // this CTA's largest key
+  uint32_t reached;                              // the least key that k threads' largest reach
+  uint32_t n_list;                               // candidates of this CTA, listed or not
+  uint32_t n_chunks;
   int answer;
 };
 
+static_assert(sizeof(SampleSmem) % 16 == 0, "the row's vectors follow, 16-byte aligned");
+
+template <int kT>
 struct Block {
+  static constexpr int kThreads = kT, kWarps = kT / 32, kPerThread = kList / kT;
   SampleSmem* s;
   int rank, ctas;
   __device__ __forceinline__ uint32_t peer(const void* p, int r) const {
     return mapa_shared(smem_u32(p), (uint32_t)r);
   }
+  // To every CTA of the cluster, this one included: from[slot][rank] = v.  The value of one
+  // thread (warp 0 calls it); read after the next cluster barrier.
+  __device__ __forceinline__ void push(int slot, uint64_t v) const {
+    const int lane = threadIdx.x & 31;
+    if (lane < ctas) st_cluster_u64(peer(&s->from[slot][rank], lane), v);
+  }
+  __device__ __forceinline__ uint64_t max_of(int slot) const {
+    uint64_t v = 0;
+    for (int i = 0; i < ctas; ++i) v = max(v, s->from[slot][i]);
+    return v;
+  }
+  __device__ __forceinline__ uint64_t sum_of(int slot, int n) const {
+    uint64_t v = 0;
+    for (int i = 0; i < n; ++i) v += s->from[slot][i];
+    return v;
+  }
 };
 
-// Sum of v over the block; every thread gets it.  `slot`: one of the part rows, not used
-// again before the next __syncthreads.
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
   return v;
 }
 
-__device__ __forceinline__ uint64_t block_sum(const Block& b, uint64_t v, int slot) {
+// Sum of v over the block, in warp 0 (the others' result is not used).
+template <class B>
+__device__ __forceinline__ uint64_t block_sum(const B& b, uint64_t v, int part) {
   v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) b.s->part[slot][threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) b.s->part[part][threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0;
-  for (int w = 0; w < kSampleWarps; ++w) v += b.s->part[slot][w];
-  return v;
+  if (threadIdx.x < B::kWarps) v = b.s->part[part][threadIdx.x];
+  return threadIdx.x < 32 ? warp_sum(v) : 0;
 }
 
 // Inclusive prefix sums over the block's threads of (count, mass).
-__device__ __forceinline__ void block_scan(const Block& b, uint32_t& n, uint64_t& m) {
+template <class B>
+__device__ __forceinline__ void block_scan(const B& b, uint32_t& n, uint64_t& m) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -233,18 +442,19 @@ __device__ __forceinline__ void block_scan(const Block& b, uint32_t& n, uint64_t
   }
   __syncthreads();
   if (lane == 31) {
-    b.s->part[6][warp] = n;
-    b.s->part[7][warp] = m;
+    b.s->part[2][warp] = n;
+    b.s->part[3][warp] = m;
   }
   __syncthreads();
   for (int w = 0; w < warp; ++w) {
-    n += (uint32_t)b.s->part[6][w];
-    m += b.s->part[7][w];
+    n += (uint32_t)b.s->part[2][w];
+    m += b.s->part[3][w];
   }
 }
 
-__device__ __forceinline__ void clear_bins(const Block& b, bool mass) {
-  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) {
+template <class B>
+__device__ __forceinline__ void clear_bins(const B& b, bool mass) {
+  for (int i = threadIdx.x; i < kBins; i += B::kThreads) {
     b.s->count[i] = 0;
     if (mass) {
       b.s->lo[i] = 0;
@@ -254,23 +464,81 @@ __device__ __forceinline__ void clear_bins(const Block& b, bool mass) {
   __syncthreads();
 }
 
-__device__ __forceinline__ void add_to_bin(const Block& b, int bin, bool mass, uint32_t w) {
+// 64-bit shared atomics are compare-and-swap loops (measured: 2 elements / ns / SM over
+// scattered bins, 0.05 into one), 32-bit ones are not (5.8 and 0.9 for the three below).
+template <class B>
+__device__ __forceinline__ void add_to_bin(const B& b, int bin, bool mass, uint32_t w) {
   atomicAdd(&b.s->count[bin], 1u);
   if (mass) {
-    atomicAdd(&b.s->lo[bin], w & 0xffffu);      // a CTA holds at most 2^15 elements
+    atomicAdd(&b.s->lo[bin], w & 0xffffu);      // a CTA has fewer than 2^16 elements
     atomicAdd(&b.s->hi[bin], w >> 16);
   }
 }
 
+struct Filter {
+  float m, c, tau;
+  uint32_t k;            // elements kept by top-k (V: all)
+  uint32_t p24, least;   // top-p as a multiple of 2^-24; min-p's smallest weight
+  uint32_t u31;
+  bool need_k, need_p;
+  __device__ __forceinline__ uint32_t weight(float z) const { return weight_of(x_of(z, m, c)); }
+  __device__ __forceinline__ uint64_t share(uint64_t mass) const {   // P
+    const uint64_t v = scaled_24(mass, p24);
+    return v < 1 ? 1 : v;
+  }
+};
+
 // The first bin at which the running count reaches want_count, or (by_mass) the running
-// weight reaches want_mass, over the cluster's histograms; *all receives the totals.
-__device__ __forceinline__ Cut find_cut(const Block& b, bool mass, bool by_mass,
+// weight reaches want_mass, over merged bins whose slices the CTAs of the cluster hold, after
+// a barrier; *all_n and *all_mass are the whole count and weight.  s->cut.bin is -1 before.
+template <class B>
+__device__ __forceinline__ Cut scan_cut(const B& b, bool mass, bool by_mass, uint32_t want_count,
+                                        uint64_t want_mass, uint32_t* all_n, uint64_t* all_mass) {
+  SampleSmem* s = b.s;
+  const int per = kBins / b.ctas;
+  constexpr int kMine = kBins / B::kThreads;     // consecutive bins a thread
+  const int bin = kMine * threadIdx.x;
+  uint32_t n[kMine], cn = 0;
+  uint64_t m[kMine], cm = 0;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int owner = (bin + i) / per, at = (bin + i) - owner * per;
+    n[i] = ld_cluster_u32(b.peer(&s->slice_count[at], owner));
+    m[i] = mass ? ld_cluster_u64(b.peer(&s->slice_mass[at], owner)) : 0;
+    cn += n[i];
+    cm += m[i];
+  }
+  uint32_t bn = cn;
+  uint64_t bm = cm;
+  block_scan(b, cn, cm);                         // inclusive, through this thread's bins
+  bn = cn - bn;
+  bm = cm - bm;
+  if (threadIdx.x == B::kThreads - 1) {
+    s->total[0] = cm;
+    s->total[1] = cn;
+  }
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const bool was = by_mass ? bm >= want_mass : bn >= want_count;
+    const bool is = by_mass ? bm + m[i] >= want_mass : bn + n[i] >= want_count;
+    if (!was && is) s->cut = Cut{bin + i, bn, n[i], bm};
+    bn += n[i];
+    bm += m[i];
+  }
+  __syncthreads();
+  *all_mass = s->total[0];
+  *all_n = (uint32_t)s->total[1];
+  return s->cut;
+}
+
+// After a cluster barrier that follows every CTA's histogram: merges them, and scan_cut.
+template <class B>
+__device__ __noinline__ Cut find_cut(B b, bool mass, bool by_mass,
                                         uint32_t want_count, uint64_t want_mass, uint32_t* all_n,
                                         uint64_t* all_mass) {
   SampleSmem* s = b.s;
   const int per = kBins / b.ctas;
-  cluster_join();                                // every CTA's histogram is complete
-  for (int i = threadIdx.x; i < per; i += kSampleThreads) {
+  for (int i = threadIdx.x; i < per; i += B::kThreads) {
     const int bin = b.rank * per + i;
     uint32_t n = 0;
     uint64_t m = 0;
@@ -285,167 +553,68 @@ __device__ __forceinline__ Cut find_cut(const Block& b, bool mass, bool by_mass,
   }
   if (threadIdx.x == 0) s->cut.bin = -1;
   cluster_join();                                // every slice is merged
-  const int bin = 2 * threadIdx.x;
-  const int owner = bin / per, at = bin - owner * per;   // per is even: both bins have one owner
-  uint32_t n[2];
-  uint64_t m[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    n[i] = ld_cluster_u32(b.peer(&s->slice_count[at + i], owner));
-    m[i] = mass ? ld_cluster_u64(b.peer(&s->slice_mass[at + i], owner)) : 0;
-  }
-  uint32_t cn = n[0] + n[1];
-  uint64_t cm = m[0] + m[1];
-  block_scan(b, cn, cm);                         // inclusive, through this thread's two bins
-  uint32_t bn = cn - n[0] - n[1];
-  uint64_t bm = cm - m[0] - m[1];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bool was = by_mass ? bm >= want_mass : bn >= want_count;
-    const bool is = by_mass ? bm + m[i] >= want_mass : bn + n[i] >= want_count;
-    if (!was && is) s->cut = Cut{bin + i, bn, n[i], bm};
-    bn += n[i];
-    bm += m[i];
-  }
-  if (threadIdx.x == kSampleThreads - 1) {
-    s->part[4][0] = cn;
-    s->part[4][1] = cm;
-  }
-  __syncthreads();
-  *all_n = (uint32_t)s->part[4][0];
-  *all_mass = s->part[4][1];
-  return s->cut;
+  return scan_cut(b, mass, by_mass, want_count, want_mass, all_n, all_mass);
 }
 
-// Ascending bitonic sort of n (a power of two) 64-bit values in shared memory.
-__device__ __forceinline__ void block_sort(uint64_t* a, int n) {
-  for (int size = 2; size <= n; size <<= 1)
-    for (int step = size >> 1; step >= 1; step >>= 1) {
-      for (int t = threadIdx.x; t < n / 2; t += kSampleThreads) {
-        const int i = 2 * t - (t & (step - 1)), j = i + step;
-        const uint64_t x = a[i], y = a[j];
-        if ((x > y) == ((i & size) == 0)) {
-          a[i] = y;
-          a[j] = x;
-        }
+// Ascending bitonic sort of n (a power of two, 64 or more) values in shared memory.  A warp
+// does the steps within 64 values in registers; only longer steps go through shared memory.
+__device__ __forceinline__ void order(uint64_t& x, uint64_t& y, bool up) {
+  if ((x > y) == up) {
+    const uint64_t t = x;
+    x = y;
+    y = t;
+  }
+}
+template <class B>
+__device__ __forceinline__ void block_sort(const B&, uint64_t* a, int n) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int size = 64; size <= n; size <<= 1) {
+    for (int step = size >> 1; step >= 64; step >>= 1) {
+      for (int t = threadIdx.x; t < n / 2; t += B::kThreads) {
+        const int i = 2 * t - (t & (step - 1));
+        uint64_t x = a[i], y = a[i + step];
+        order(x, y, (i & size) == 0);
+        a[i] = x;
+        a[i + step] = y;
       }
       __syncthreads();
     }
-}
-
-struct Filter {
-  float m, c, tau;
-  uint32_t k;            // elements kept by top-k (V: all)
-  uint32_t p24, least;   // top-p as a multiple of 2^-24; min-p's smallest weight
-  uint32_t u31;
-  bool need_k, need_p;
-};
-
-__device__ __forceinline__ float logp_of(const Filter& f, float z, uint64_t total) {
-  return __fsub_rn(__fdiv_rn(__fsub_rn(z, f.m), f.tau),
-                   logf(__fmul_rn(__ull2float_rn(total), 0x1p-31f)));
-}
-
-// The leading CTA's end of a row whose cut lies within the n listed candidates (all of the
-// row's elements up to some place in the sorted order): sort them, cut, and take the token.
-__device__ __forceinline__ void finish_list(const Block& b, const Filter& f, const SampleArgs& a,
-                                            int row, int n, uint64_t total_mass) {
-  SampleSmem* s = b.s;
-  int size = 2;
-  while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += kSampleThreads) s->list[i] = ~0ull;
-  __syncthreads();
-  block_sort(s->list, size);
-  // by descending logit: thread t takes the t-th run of `each` candidates
-  const int each = size > kSampleThreads ? size / kSampleThreads : 1;
-  const int i0 = threadIdx.x * each;
-  uint32_t w[kList / kSampleThreads];
-  uint64_t sum = 0;
-  uint32_t zero = 0;
+    for (int base = warp * 64; base < n; base += B::kWarps * 64) {
+      uint64_t x = a[base + lane], y = a[base + 32 + lane];
+      for (int part = size == 64 ? 2 : size; part <= size; part <<= 1) {
 #pragma unroll
-  for (int e = 0; e < kList / kSampleThreads; ++e) {
-    w[e] = 0;
-    if (e < each && i0 + e < n && (uint32_t)(i0 + e) < f.k)
-      w[e] = weight_of(x_of(logit_of(~(uint32_t)(s->list[i0 + e] >> 32)), f.m, f.c));
-    sum += w[e];
-  }
-  uint64_t upto = sum;
-  block_scan(b, zero, upto);
-  if (threadIdx.x == kSampleThreads - 1) s->part[5][0] = upto;
-  __syncthreads();
-  uint64_t most = f.need_k ? s->part[5][0] : total_mass;    // C_k
-  most = scaled_24(most, f.p24);
-  if (most < 1) most = 1;
-  uint64_t before = upto - sum;
-  uint64_t entry[kList / kSampleThreads];
-#pragma unroll
-  for (int e = 0; e < kList / kSampleThreads; ++e) {
-    if (e < each && i0 + e < size) {
-      const uint32_t keep = before < most && w[e] >= f.least ? w[e] : 0;
-      entry[e] = i0 + e < n ? (s->list[i0 + e] << 32) | keep : ~0ull;   // (id, weight)
-    }
-    before += w[e];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < kList / kSampleThreads; ++e)
-    if (e < each && i0 + e < size) s->list[i0 + e] = entry[e];
-  __syncthreads();
-  block_sort(s->list, size);                                // by id
-  sum = 0;
-#pragma unroll
-  for (int e = 0; e < kList / kSampleThreads; ++e) {
-    w[e] = e < each && i0 + e < n ? (uint32_t)s->list[i0 + e] : 0;
-    sum += w[e];
-  }
-  upto = sum;
-  block_scan(b, zero, upto);
-  if (threadIdx.x == kSampleThreads - 1) s->part[5][1] = upto;
-  __syncthreads();
-  const uint64_t total = s->part[5][1];
-  const uint64_t at = scaled_31(total, f.u31);
-  before = upto - sum;
-#pragma unroll
-  for (int e = 0; e < kList / kSampleThreads; ++e) {
-    if (before <= at && at < before + w[e]) {
-      const int id = (int)(s->list[i0 + e] >> 32);
-      if (RLK_STORE_OK(row < a.N && id >= 0 && id < a.V, &g_err_sample)) {
-        a.token[row] = id;
-        s->answer = id;
+        for (int step = 32; step >= 1; step >>= 1) {
+          if (step >= part) continue;
+          if (step == 32) {
+            order(x, y, ((base + lane) & part) == 0);
+          } else {
+            const bool low = (lane & step) == 0;
+            const uint64_t ox = __shfl_xor_sync(kFull, x, step);
+            const uint64_t oy = __shfl_xor_sync(kFull, y, step);
+            const bool upx = ((base + lane) & part) == 0, upy = ((base + 32 + lane) & part) == 0;
+            x = (low == upx) ? min(x, ox) : max(x, ox);
+            y = (low == upy) ? min(y, oy) : max(y, oy);
+          }
+        }
       }
+      a[base + lane] = x;
+      a[base + 32 + lane] = y;
     }
-    before += w[e];
+    __syncthreads();
   }
-  if (threadIdx.x == 0) s->xmass[3] = total;
 }
 
-template <bool kFp32>
-__global__ void __launch_bounds__(kSampleThreads, 2)
-    sample_kernel(SampleArgs a, int per) {
-  using R = Row<kFp32>;
-  constexpr int kE = R::kElems;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  SampleSmem* s = reinterpret_cast<SampleSmem*>(smem_raw);
-  uint4* vecs = reinterpret_cast<uint4*>(smem_raw + sizeof(SampleSmem));
-  Block b;
-  b.s = s;
-  b.rank = (int)cluster_rank();
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(b.ctas));
-  const int row = blockIdx.x / b.ctas;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s->n_list = 0;
-  griddep_wait();
-  if (tid == 0) griddep_launch_dependents();
-
-  // ---- settings of the row
+// The row's settings (f.m is set later); *bad: they define no distribution.
+__device__ __forceinline__ Filter settings_of(const SampleArgs& a, int row, bool* bad) {
   Filter f;
+  f.m = 0.f;
   float tau = a.temperature ? __ldg(a.temperature + row) : a.temperature_all;
   int k = a.top_k ? __ldg(a.top_k + row) : a.top_k_all;
   const float top_p = a.top_p ? __ldg(a.top_p + row) : a.top_p_all;
   const float min_p = a.min_p ? __ldg(a.min_p + row) : a.min_p_all;
   const double u = a.uniform_fp64 ? __ldg(static_cast<const double*>(a.uniform) + row)
                                   : (double)__ldg(static_cast<const float*>(a.uniform) + row);
-  bool bad = !(tau >= 0.f && tau < INFINITY) || top_p != top_p || min_p != min_p || u != u;
+  *bad = !(tau >= 0.f && tau < INFINITY) || top_p != top_p || min_p != min_p || u != u;
   if (tau < 1e-6f) {
     tau = 1.f;
     k = 1;
@@ -458,382 +627,1112 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   f.need_p = f.p24 < (1u << 24);
   f.least = (uint32_t)rintf(__fmul_rn(fminf(fmaxf(min_p, 0.f), 1.f), 16777216.f)) << 7;
   f.u31 = (uint32_t)fmin(fmax(floor(u * 2147483648.0), 0.0), 2147483647.0);
+  return f;
+}
 
-  // ---- the row into shared memory, and its maximum
-  const int esize = kFp32 ? 4 : 2;
-  const uintptr_t start = reinterpret_cast<uintptr_t>(a.logits) + (uintptr_t)(row * a.ld) * esize;
-  const int lead = (int)(start & 15) / esize;
-  const uint4* src = reinterpret_cast<const uint4*>(start & ~(uintptr_t)15);
-  const int vectors = (lead + a.V + kE - 1) / kE;
-  const int cta0 = b.rank * per;
-  const int mine = max(0, min(per, vectors - cta0));
-  R r;
-  r.smem = vecs;
-  r.first_id = cta0 * kE - lead;
-  const int each = (mine + kSampleWarps - 1) / kSampleWarps;
-  r.v0 = min(warp * each, mine);
-  r.v1 = min(r.v0 + each, mine);
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int v = r.v0 + lane; v < r.v1; v += 32) {
-    const int id0 = r.first_id + v * kE;
-    uint4 q;
-    if (id0 >= 0 && id0 + kE <= a.V) {
-      q = __ldg(src + cta0 + v);
-    } else {                                       // the row's first or last vector, in part
-      uint32_t p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (kFp32) {
-          p[i] = 0xff800000u;
-          if (id0 + i >= 0 && id0 + i < a.V)
-            p[i] = __ldg(reinterpret_cast<const uint32_t*>(start) + id0 + i);
-        } else {
-          uint32_t h[2] = {0xff80u, 0xff80u};
-#pragma unroll
-          for (int o = 0; o < 2; ++o)
-            if (id0 + 2 * i + o >= 0 && id0 + 2 * i + o < a.V)
-              h[o] = __ldg(reinterpret_cast<const uint16_t*>(start) + id0 + 2 * i + o);
-          p[i] = h[0] | (h[1] << 16);
-        }
+__device__ __forceinline__ void write_answer(const SampleArgs& a, const Filter& f, int row, int id,
+                                             float z, uint64_t total) {
+  if (RLK_STORE_OK(row < a.N && id >= 0 && id < a.V, &g_err_sample)) {
+    a.token[row] = id;
+    a.logp[row] = __fsub_rn(__fdiv_rn(__fsub_rn(z, f.m), f.tau),
+                            logf(__fmul_rn(__ull2float_rn(total), 0x1p-31f)));
+  }
+}
+
+// Candidate: sorts by descending logit, then by ascending id.
+__device__ __forceinline__ uint64_t entry_of(float z, int id) {
+  return ((uint64_t)~key_of(z) << 32) | (uint32_t)id;
+}
+__device__ __forceinline__ float entry_logit(uint64_t e) { return logit_of(~(uint32_t)(e >> 32)); }
+
+template <class B>
+__device__ __forceinline__ int sort_list(const B& b, int n) {
+  SampleSmem* s = b.s;
+  int size = 64;
+  while (size < n) size <<= 1;
+  if (n <= B::kThreads) {
+    // An entry a thread, which counts those before it: no two are the same.
+    const uint64_t mine = threadIdx.x < n ? s->list[threadIdx.x] : ~0ull;
+    int rank = threadIdx.x;
+    if (threadIdx.x < n) {
+      rank = 0;
+      int j = 0;
+      for (; j + 4 <= n; j += 4) {
+        const ulonglong2 x = reinterpret_cast<const ulonglong2*>(s->list)[j / 2];
+        const ulonglong2 y = reinterpret_cast<const ulonglong2*>(s->list)[j / 2 + 1];
+        rank += (x.x < mine) + (x.y < mine) + (y.x < mine) + (y.y < mine);
       }
-      q = make_uint4(p[0], p[1], p[2], p[3]);
+      for (; j < n; ++j) rank += s->list[j] < mine;
     }
-    vecs[v] = q;
-    float z[kE];
+    __syncthreads();
+    if (threadIdx.x < size) s->list[rank] = mine;
+    __syncthreads();
+    return size;
+  }
+  for (int i = n + threadIdx.x; i < size; i += B::kThreads) s->list[i] = ~0ull;
+  __syncthreads();
+  block_sort(b, s->list, size);
+  return size;
+}
+
+// The end of a row of which the list holds all elements up to some place in the sorted
+// order past the cut, of at most 64 elements of interest (n = the list's, or k): one warp,
+// two elements a lane.
+__device__ __forceinline__ void finish_warp(SampleSmem* s, const Filter& f, const SampleArgs& a,
+                                            int row, int n, uint64_t total_mass) {
+  const int lane = threadIdx.x & 31;
+  float z[2];
+  uint32_t w[2], id[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint64_t x = s->list[2 * lane + e];
+    z[e] = entry_logit(x);
+    id[e] = (uint32_t)x;
+    w[e] = 2 * lane + e < n ? f.weight(z[e]) : 0;
+  }
+  uint64_t upto = (uint64_t)w[0] + w[1];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint64_t o = __shfl_up_sync(kFull, upto, off);
+    if (lane >= off) upto += o;
+  }
+  const uint64_t most = f.share(f.need_k ? __shfl_sync(kFull, upto, 31) : total_mass);
+  const uint64_t before = upto - w[0] - w[1];
+  if (!(before + w[0] < most && w[1] >= f.least)) w[1] = 0;
+  if (!(before < most && w[0] >= f.least)) w[0] = 0;
+  const uint64_t total = warp_sum((uint64_t)w[0] + w[1]);
+  const uint64_t at = scaled_31(total, f.u31);
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) s->list[2 * lane + e] = ((uint64_t)id[e] << 32) | w[e];
+  __syncwarp();
+  uint64_t sum[2] = {0, 0};                        // kept weights of lower ids
+  for (int j = 0; j < min(n, 64); ++j) {
+    const uint64_t o = s->list[j];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if ((uint32_t)(o >> 32) < id[e]) sum[e] += (uint32_t)o;
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (sum[e] <= at && at < sum[e] + w[e]) write_answer(a, f, row, (int)id[e], z[e], total);
+}
+
+// The same for a longer list, by the block: sort by logit, cut, sort by id, take.
+template <class B>
+__device__ __forceinline__ void finish_block(const B& b, const Filter& f, const SampleArgs& a,
+                                             int row, int n, int size, uint64_t total_mass) {
+  SampleSmem* s = b.s;
+  // thread t has the t-th run of `each` elements
+  const int each = size > B::kThreads ? size / B::kThreads : 1;
+  const int i0 = threadIdx.x * each;
+  uint32_t w[B::kPerThread];
+  uint64_t sum = 0;
+  uint32_t unused = 0;
+#pragma unroll
+  for (int e = 0; e < B::kPerThread; ++e) {
+    w[e] = 0;
+    if (e < each && i0 + e < n && (uint32_t)(i0 + e) < f.k)
+      w[e] = f.weight(entry_logit(s->list[i0 + e]));
+    sum += w[e];
+  }
+  uint64_t upto = sum;
+  block_scan(b, unused, upto);
+  if (threadIdx.x == B::kThreads - 1) s->total[0] = upto;
+  __syncthreads();
+  const uint64_t most = f.share(f.need_k ? s->total[0] : total_mass);
+  uint64_t before = upto - sum;
+  uint64_t entry[B::kPerThread];
+#pragma unroll
+  for (int e = 0; e < B::kPerThread; ++e) {
+    if (e < each && i0 + e < size) {
+      const uint32_t keep = before < most && w[e] >= f.least ? w[e] : 0;
+      entry[e] = i0 + e < n ? (s->list[i0 + e] << 32) | keep : ~0ull;   // (id, weight)
+    }
+    before += w[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < B::kPerThread; ++e)
+    if (e < each && i0 + e < size) s->list[i0 + e] = entry[e];
+  __syncthreads();
+  block_sort(b, s->list, size);                             // by id
+  sum = 0;
+#pragma unroll
+  for (int e = 0; e < B::kPerThread; ++e) {
+    w[e] = e < each && i0 + e < n ? (uint32_t)s->list[i0 + e] : 0;
+    sum += w[e];
+  }
+  upto = sum;
+  block_scan(b, unused, upto);
+  if (threadIdx.x == B::kThreads - 1) s->total[1] = upto;
+  __syncthreads();
+  const uint64_t total = s->total[1];
+  const uint64_t at = scaled_31(total, f.u31);
+  before = upto - sum;
+#pragma unroll
+  for (int e = 0; e < B::kPerThread; ++e) {
+    if (before <= at && at < before + w[e]) s->answer = (int)(s->list[i0 + e] >> 32);
+    before += w[e];
+  }
+  __syncthreads();
+}
+
+// The least logit whose bin (below the top m) is at most `bin` < kBins; the warp tries 32
+// places of the range of keys at a time.  Every warp may call it by itself.
+__device__ __noinline__ float least_logit(float m, float c, Window window, int bin) {
+  const int lane = threadIdx.x & 31;
+  uint32_t no = key_of(-INFINITY), yes = key_of(m);
+  while (yes - no > 1) {
+    const uint32_t step = (yes - no) / 33 + 1;
+    const uint32_t at = min(no + step * (lane + 1), yes);
+    const uint32_t ok = __ballot_sync(kFull, window.bin(x_of(logit_of(at), m, c)) <= bin);
+    const int first = ok ? __ffs(ok) - 1 : 32;     // ok is all ones from some lane on
+    const uint32_t hi = first < 32 ? min(no + step * (first + 1), yes) : yes;
+    no = min(no + step * first, yes - 1);
+    yes = hi;
+  }
+  return logit_of(yes);
+}
+
+// Lists the elements of [lo, hi] among those of the warp's threads with `mine` set (the
+// others have none).  Past the list's end they are only counted.  Where few threads have
+// some, the warp shares their vectors out, so that all are on their way at once: a thread's
+// own would be a chain of loads (512 rows of 151,936 from L2: 14 us a CTA for the chain).
+template <class B, class R>
+__device__ __forceinline__ void list_range(const B& b, const R& r, bool mine, float lo, float hi) {
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  const uint32_t who = __ballot_sync(kFull, mine);
+  const int threads = __popc(who);
+  const int steps = (r.v1 - r.v0 + 31) / 32;       // vectors a thread
+  const bool share = threads <= 16;
+  const int at_rank = share ? (int)__fns(who, 0, lane + 1) : lane;   // lane of that rank
+  const int total = (share ? threads : 32) * steps;
+  for (int i0 = 0; i0 < total; i0 += kBatch * 32) {
+    uint4 q[kBatch];
+    int v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = i0 + 32 * i + lane;
+      int step = at >> 5, from = lane;
+      if (share) {
+        const int rank = at / steps;
+        step = at - rank * steps;
+        from = __shfl_sync(kFull, at_rank, rank & 31);
+      }
+      v[i] = at < total ? r.v0 + 32 * step + from : r.v1;
+    }
+    r.template get_all<false>(v, q);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (v[i] >= r.v1 || !(R::top_of(q[i]) >= lo)) continue;
+      float z[R::kElems];
+      R::unpack(q[i], z);
+#pragma unroll
+      for (int e = 0; e < R::kElems; ++e)
+        if (z[e] >= lo && z[e] <= hi) {
+          const uint32_t to = atomicAdd(&b.s->n_list, 1u);
+          if (to < kList) b.s->list[to] = entry_of(z[e], r.id_of(v[i]) + e);
+        }
+    }
+  }
+}
+
+template <class B, class R>
+__device__ __noinline__ void list_range_cold(B b, R r, bool mine, float lo, float hi) {
+  list_range(b, r, mine, lo, hi);
+}
+
+// After list_range: every CTA's count to all (read after the next cluster barrier).
+template <class B>
+__device__ __forceinline__ void push_count(const B& b) {
+  __syncthreads();
+  if (threadIdx.x < 32) b.push(7, b.s->n_list);
+}
+
+// The leading CTA appends the other CTAs' lists to its own; all leave together (the others
+// must not before they have been read).  The sum of the counts is at most kList.
+template <class B>
+__device__ __forceinline__ void gather_lists(const B& b) {
+  if (b.rank == 0) {
+    uint32_t at = (uint32_t)b.s->from[7][0];
+    for (int r = 1; r < b.ctas; ++r) {
+      const uint32_t n = (uint32_t)b.s->from[7][r];
+      for (uint32_t i = threadIdx.x; i < n; i += B::kThreads)
+        b.s->list[at + i] = ld_cluster_u64(b.peer(&b.s->list[i], r));
+      at += n;
+    }
+  }
+  if (b.ctas > 1) cluster_join();
+  __syncthreads();
+}
+
+// The smallest bin such that at least k threads' `bin` (kBins: none) do not exceed it;
+// kBins - 1 where fewer than k threads have one.
+__device__ __forceinline__ int reach_bin(int bin, uint32_t k) {
+  int lo = 0;
+#pragma unroll 1
+  for (int step = kBins / 2; step >= 1; step >>= 1)
+    if ((uint32_t)__syncthreads_count(bin < lo + step) < k) lo += step;
+  return lo;
+}
+
+// Of the leading CTA's n listed candidates for top-k, keeps at least the k first, and few
+// others: the threads' own best give a bin that the k first reach.
+template <class B>
+__device__ __forceinline__ int keep_first(const B& b, const Filter& f, int n) {
+  SampleSmem* s = b.s;
+  uint64_t entry[B::kPerThread];
+  int bin[B::kPerThread], best = kBins;
+#pragma unroll
+  for (int i = 0; i < B::kPerThread; ++i) {
+    const int at = i * B::kThreads + threadIdx.x;
+    entry[i] = at < n ? s->list[at] : ~0ull;
+    bin[i] = at < n ? all_octaves().bin(x_of(entry_logit(entry[i]), f.m, f.c)) : kBins;
+    best = min(best, bin[i]);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s->n_list = 0;
+  const int reach = reach_bin(best, f.k);          // its barriers order these accesses
+#pragma unroll
+  for (int i = 0; i < B::kPerThread; ++i)
+    if (bin[i] <= reach) s->list[atomicAdd(&s->n_list, 1u)] = entry[i];
+  __syncthreads();
+  return (int)s->n_list;
+}
+
+// The leading CTA ends a row from its list of n elements.
+template <class B>
+__device__ __noinline__ void finish(B b, Filter f, const SampleArgs& a, int row, int n,
+                                    uint64_t total_mass) {
+  SampleSmem* s = b.s;
+  if (n > B::kThreads && f.k <= B::kThreads) n = keep_first(b, f, n);
+  const int size = sort_list(b, n);
+  const int of_interest = (int)min((uint32_t)n, f.k);
+  if (of_interest <= 64) {
+    if (threadIdx.x < 32) finish_warp(s, f, a, row, of_interest, total_mass);
+    return;
+  }
+  finish_block(b, f, a, row, n, size, total_mass);
+  if (threadIdx.x == 0) {
+    const int id = s->answer;
+    const int64_t at = row * a.ld + id;
+    const float z = a.fp32 ? __ldg(static_cast<const float*>(a.logits) + at)
+                           : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.logits) +
+                                                             at)
+                                             << 16);
+    write_answer(a, f, row, id, z, s->total[1]);
+  }
+}
+
+// The leading CTA's search inside one bin, whose n elements it has listed: the last entry
+// kept (s->total[2]) and the weight kept with it (s->total[3]).
+template <class B>
+__device__ __noinline__ void cut_in_bin(B b, Filter f, int n, bool by_mass,
+                                           uint32_t keep, uint64_t mass_before,
+                                           uint64_t want_mass) {
+  SampleSmem* s = b.s;
+  const int size = sort_list(b, n);
+  const int each = size > B::kThreads ? size / B::kThreads : 1;
+  const int i0 = threadIdx.x * each;
+  uint32_t w[B::kPerThread];
+  uint64_t sum = 0;
+  uint32_t unused = 0;
+#pragma unroll
+  for (int e = 0; e < B::kPerThread; ++e) {
+    w[e] = e < each && i0 + e < n ? f.weight(entry_logit(s->list[i0 + e])) : 0;
+    sum += w[e];
+  }
+  uint64_t upto = sum;
+  block_scan(b, unused, upto);
+  uint64_t before = mass_before + upto - sum;
+#pragma unroll
+  for (int e = 0; e < B::kPerThread; ++e) {
+    const bool last = by_mass ? before < want_mass && want_mass <= before + w[e]
+                              : (uint32_t)(i0 + e) + 1 == keep;
+    if (e < each && i0 + e < n && last) {
+      s->total[2] = s->list[i0 + e];
+      s->total[3] = before + w[e];
+    }
+    before += w[e];
+  }
+  __syncthreads();
+}
+
+// Adds the window's elements to the CTA's histogram with their weights; returns the weight
+// of the thread's elements, of all of them (whole) or of some that include the window's.
+template <class B, class R>
+__device__ __noinline__ uint64_t weigh(B b, R r, float m, float c, Window window, bool whole) {
+  constexpr int kE = R::kElems;
+  uint64_t sum = 0;
+  r.template each<false, 4>([&](int, const uint4& q) {
+    const bool some = x_of(R::top_of(q), m, c) > -window.to;
+    if (!(whole || some)) return;
+    float z[kE], x[kE];
+    uint32_t w[kE];
     R::unpack(q, z);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      bad |= !(z[e] < INFINITY);                   // NaN or +inf
-      top = fmaxf(top, z[e]);
+    for (int e = 0; e < kE; e += 2) {
+      x_pair(z[e], z[e + 1], m, c, x[e], x[e + 1]);
+      weights_of(x[e], x[e + 1], w[e], w[e + 1]);
     }
-  }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-  bad = __any_sync(kFull, bad);
-  if (lane == 0) s->part[0][warp] = ((uint64_t)bad << 32) | key_of(top);
-  __syncthreads();
+    for (int e = 0; e < kE; ++e) sum = add_wide(sum, w[e]);
+    if (some) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (window.has(x[e])) add_to_bin(b, window.at(x[e]), true, w[e]);
+    }
+  });
+  return sum;
+}
+
+// The same for counts alone.
+template <class B, class R>
+__device__ __noinline__ void count(B b, R r, float m, float c, Window window) {
+  r.template each<false, 4>([&](int, const uint4& q) {
+    if (!(x_of(R::top_of(q), m, c) > -window.to)) return;
+    float z[R::kElems];
+    R::unpack(q, z);
+#pragma unroll
+    for (int e = 0; e < R::kElems; ++e) {
+      const float x = x_of(z[e], m, c);
+      if (window.has(x)) add_to_bin(b, window.at(x), false, 0);
+    }
+  });
+}
+
+// The weight of the thread's elements that are kept: z > cut, or z = cut and id <= cut_id,
+// and a weight of `least` or more.
+template <class R>
+__device__ __noinline__ uint64_t weight_kept(R r, float m, float c, uint32_t least, float cut,
+                                             int cut_id) {
+  constexpr int kE = R::kElems;
+  uint64_t sum = 0;
+  r.template each<false, 4>([&](int v, const uint4& q) {
+    if (!(R::top_of(q) >= cut)) return;
+    float z[kE];
+    uint32_t w[kE];
+    R::unpack(q, z);
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) {
+      float x0, x1;
+      x_pair(z[e], z[e + 1], m, c, x0, x1);
+      weights_of(x0, x1, w[e], w[e + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+      if (w[e] >= least && (z[e] > cut || (z[e] == cut && r.id_of(v) + e <= cut_id)))
+        sum = add_wide(sum, w[e]);
+  });
+  return sum;
+}
+
+// One warp finds the token among its vectors [v0, v1): the kept weights before them sum to
+// `before`, and the running sum of theirs passes `at`.
+template <class R>
+__device__ __noinline__ void take_token(R r, Filter f, const SampleArgs& a, int row, float cut,
+                                        int cut_id, uint64_t before, uint64_t at,
+                                        uint64_t total) {
+  constexpr int kE = R::kElems;
+  const int lane = threadIdx.x & 31;
+  for (int v = r.v0; v < r.v1; v += 32) {
+    float z[kE];
+    uint32_t w[kE];
+    uint64_t n = 0;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) w[e] = 0;
+    if (v + lane < r.v1) {
+      r.get(v + lane, z);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        if (z[e] > cut || (z[e] == cut && r.id_of(v + lane) + e <= cut_id)) {
+          w[e] = f.weight(z[e]);
+          if (w[e] < f.least) w[e] = 0;
+        }
+        n += w[e];
+      }
+    }
+    uint64_t upto = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint64_t o = __shfl_up_sync(kFull, upto, off);
+      if (lane >= off) upto += o;
+    }
+    uint64_t prior = before + upto - n;
+    if (prior <= at && at < before + upto) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        if (prior <= at && at < prior + w[e]) write_answer(a, f, row, r.id_of(v + lane) + e, z[e], total);
+        prior += w[e];
+      }
+    }
+    before += __shfl_sync(kFull, upto, 31);
+    if (before > at) return;
+  }
+}
+
+// Where the kept prefix of the sorted order ends: its last entry (all ones: nowhere), or 0 if
+// the leading CTA finished the row from a list.  `top`: the largest of the thread's logits.
+template <class B, class R>
+__device__ __noinline__ uint64_t search(B b, R r, Filter f, const SampleArgs& a, int row,
+                                        float top) {
+  constexpr int kE = R::kElems;
+  SampleSmem* s = b.s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t last = ~0ull;
+  bool by_mass = !f.need_k;                        // the search under way
+  uint64_t total_mass = 0, want_mass = 0;
+  // at most: by count, by weight instead if that cuts nothing, or by weight after it
+  for (int pass = 0; pass < 2 && (f.need_k || f.need_p); ++pass) {
+    uint32_t before = 0;                           // elements, weight above the range searched
+    uint64_t mass_before = 0;
+    Cut cut;
+    Window window(0.f, f.need_p ? kNear : kOctaves);
+    const float top_x = x_of(top, f.m, f.c);       // of this thread's elements
+    for (;;) {
+      clear_bins(b, f.need_p);
+      if (f.need_p) {
+        const bool whole = total_mass == 0;        // the row's weight is not known yet
+        uint64_t sum = weigh(b, r, f.m, f.c, window, whole);
+        if (whole) {
+          sum = block_sum(b, sum, 0);
+          if (warp == 0) b.push(9, sum);
+        }
+      } else {
+        count(b, r, f.m, f.c, window);
+      }
+      cluster_join();                              // every CTA's histogram is complete
+      if (f.need_p && total_mass == 0) {
+        total_mass = b.sum_of(9, b.ctas);
+        if (by_mass) want_mass = f.share(total_mass);
+      }
+      uint32_t all_n;
+      uint64_t all_mass;
+      cut = find_cut(b, f.need_p, by_mass, f.k - before, want_mass - mass_before, &all_n, &all_mass);
+      if (cut.bin >= 0 || window.to >= kOctaves) break;
+      before += all_n;
+      mass_before += all_mass;
+      window = Window(kNear, kOctaves);
+    }
+    if (cut.bin < 0) {
+      // Only weightless elements are left: top-k cuts nothing that could be drawn.
+      f.need_k = false;
+      if (by_mass || !f.need_p) break;
+      by_mass = true;
+      want_mass = f.share(total_mass);
+      continue;
+    }
+    before += cut.before;
+    mass_before += cut.mass;
+    const bool to_end = f.need_k == !by_mass;      // nothing is left to cut after this search
+    const bool near = window.bin(top_x) <= cut.bin;
+    const float m = f.m, c = f.c;
+    const int bin = cut.bin;
+    if (tid == 0) s->n_list = 0;
+    __syncthreads();
+    if (to_end && before + cut.in <= kList) {
+      list_range_cold(b, r, near, least_logit(m, c, window, bin), INFINITY);
+      push_count(b);
+      cluster_join();
+      gather_lists(b);
+      if (b.rank == 0) finish(b, f, a, row, (int)(before + cut.in), total_mass);
+      return 0;
+    }
+    if (cut.in <= kList) {
+      const float lo = least_logit(m, c, window, bin);
+      // the bin ends below the least logit of the bins before it
+      float hi = m;
+      if (bin > 0 || window.from > 0.f) hi = logit_of(key_of(least_logit(m, c, window, bin - 1)) - 1);
+      list_range_cold(b, r, near, lo, hi);
+      push_count(b);
+      cluster_join();
+      gather_lists(b);
+      if (b.rank == 0) {
+        cut_in_bin(b, f, (int)cut.in, by_mass, f.k - before, mass_before, want_mass);
+        if (warp == 0) {
+          b.push(5, s->total[2]);
+          b.push(6, s->total[3]);
+        }
+      }
+      cluster_join();
+      last = s->from[5][0];
+      mass_before = s->from[6][0];
+    } else {
+      // ---- too many for a sort: the bin's range of keys, ...
+      uint32_t kmin = kFull, kmax = 0;
+      r.template each<false, 4>([&](int, const uint4& q) {
+        float z[kE];
+        R::unpack(q, z);
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+          if (window.bin(x_of(z[e], m, c)) == bin) {
+            kmin = min(kmin, key_of(z[e]));
+            kmax = max(kmax, key_of(z[e]));
+          }
+      });
+      kmin = __reduce_min_sync(kFull, kmin);
+      kmax = __reduce_max_sync(kFull, kmax);
+      if (lane == 0) s->part[0][warp] = ((uint64_t)~kmin << 32) | kmax;
+      __syncthreads();
+      if (warp == 0) {
+        const uint64_t v = lane < B::kWarps ? s->part[0][lane] : 0;
+        b.push(1, ((uint64_t)__reduce_max_sync(kFull, (uint32_t)(v >> 32)) << 32) |
+                      __reduce_max_sync(kFull, (uint32_t)v));
+      }
+      cluster_join();
+      kmin = kmax = 0;
+      for (int i = 0; i < b.ctas; ++i) {
+        kmin = max(kmin, (uint32_t)(s->from[1][i] >> 32));
+        kmax = max(kmax, (uint32_t)s->from[1][i]);
+      }
+      kmin = ~kmin;
+      // ... that range in kBins parts until a part is one key, ...
+      uint32_t in = cut.in;
+      for (int level = 0; kmin != kmax && level < 4; ++level) {   // 32 bits, 10 a level
+        int shift = 0;
+        while (((kmax - kmin) >> shift) >= kBins) ++shift;
+        clear_bins(b, f.need_p);
+        r.template each<false, 4>([&](int, const uint4& q) {
+          float z[kE];
+          R::unpack(q, z);
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const uint32_t key = key_of(z[e]);
+            if (key >= kmin && key <= kmax)
+              add_to_bin(b, (kmax - key) >> shift, f.need_p, f.need_p ? f.weight(z[e]) : 0);
+          }
+        });
+        cluster_join();
+        uint32_t all_n;
+        uint64_t all_mass;
+        const Cut part = find_cut(b, f.need_p, by_mass, f.k - before, want_mass - mass_before,
+                                  &all_n, &all_mass);
+        before += part.before;
+        mass_before += part.mass;
+        in = part.in;
+        const uint32_t hi = kmax - ((uint32_t)part.bin << shift);
+        const uint32_t below = (1u << shift) - 1;
+        kmin = hi - kmin > below ? hi - below : kmin;
+        kmax = hi;
+      }
+      // ... and how many of the equal ones
+      const uint32_t w = f.weight(logit_of(kmax));
+      uint64_t keep = in;
+      if (!by_mass) keep = f.k - before;
+      else if (w) keep = (want_mass - mass_before + w - 1) / w;
+      if (keep > in) keep = in;
+      mass_before += keep * w;
+      uint32_t cut_id = kFull;                     // all of them
+      if (keep < in) {
+        uint32_t ties = 0;
+        r.template each<false, 4>([&](int, const uint4& q) {
+          float z[kE];
+          R::unpack(q, z);
+#pragma unroll
+          for (int e = 0; e < kE; ++e) ties += key_of(z[e]) == kmax;
+        });
+        ties = __reduce_add_sync(kFull, ties);
+        const uint64_t here = block_sum(b, lane == 0 ? ties : 0, 0);
+        if (warp == 0) b.push(2, here);
+        if (tid == 0) s->answer = 0;
+        cluster_join();
+        uint64_t below = b.sum_of(2, b.rank);      // in earlier CTAs, then in earlier warps
+        for (int o = 0; o < warp; ++o) below += s->part[0][o];
+        if (below < keep && keep <= below + ties) {   // uniform in the warp: its part has it
+          for (int v = r.v0; v < r.v1; v += 32) {
+            float z[kE];
+            uint32_t n = 0;
+            if (v + lane < r.v1) {
+              r.get(v + lane, z);
+#pragma unroll
+              for (int e = 0; e < kE; ++e) n += key_of(z[e]) == kmax;
+            }
+            uint32_t upto = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+              const uint32_t o = __shfl_up_sync(kFull, upto, off);
+              if (lane >= off) upto += o;
+            }
+            uint64_t seen = below + upto - n;
+            if (seen < keep && keep <= below + upto) {
+#pragma unroll
+              for (int e = 0; e < kE; ++e)
+                if (key_of(z[e]) == kmax && ++seen == keep) s->answer = r.id_of(v + lane) + e;
+            }
+            below += __shfl_sync(kFull, upto, 31);
+          }
+        }
+        __syncthreads();
+        if (warp == 0) b.push(3, (uint64_t)s->answer);
+        cluster_join();
+        cut_id = (uint32_t)b.max_of(3);
+      }
+      last = ((uint64_t)~kmax << 32) | cut_id;
+    }
+    if (by_mass || !f.need_p) break;
+    by_mass = true;                                // top-p among the k kept
+    want_mass = f.share(mass_before);
+  }
+  return last;
+}
+
+template <bool kFp32, bool kOnChip, int kT>
+__global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_constant__ SampleArgs a,
+                                                                     int per) {
+  using R = Row<kFp32, kOnChip>;
+  using B = Block<kT>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SampleSmem* s = reinterpret_cast<SampleSmem*>(smem_raw);
+  B b;
+  b.s = s;
+  b.rank = (int)cluster_rank();
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(b.ctas));
+  const int row = blockIdx.x / b.ctas;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    uint64_t v = 0;                                // a bad part outranks any logit
-    for (int w = 0; w < kSampleWarps; ++w) v = max(v, s->part[0][w]);
-    s->xch[0] = v;
+    s->n_list = 0;
+    s->top = 0;
+    s->reached = kFull;
+  }
+  __syncthreads();
+  griddep_wait();
+  if (tid == 0) griddep_launch_dependents();
+  if (a.state && a.state[row].status != kGeneral) return;   // all CTAs of the row alike
+
+  bool bad;
+  Filter f = settings_of(a, row, &bad);
+  // ---- the first pass: the largest logit
+  R r;
+  {
+    const int vectors = r.begin(a, row);
+    const int cta0 = b.rank * per;
+    const int mine = max(0, min(per, vectors - cta0));
+    const int each = (mine + B::kWarps - 1) / B::kWarps;
+    r.skip(cta0);
+    r.chip = reinterpret_cast<uint4*>(smem_raw + sizeof(SampleSmem));
+    r.v0 = min(warp * each, mine);
+    r.v1 = min(r.v0 + each, mine);
+  }
+  float top = -INFINITY;
+  r.template each<true, 8>([&](int v, const uint4& q) {
+    if constexpr (kOnChip) r.chip[v] = q;
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(R::top_of(q)));
+  });
+  // A key above all logits marks what no token can be drawn from: NaN, +inf, bad settings.
+  const uint32_t my_top = bad || !(top < INFINITY) ? kFull : key_of(top);
+  const uint32_t warp_top = __reduce_max_sync(kFull, my_top);
+  if (lane == 0) atomicMax(&s->top, warp_top);
+  __syncthreads();
+  const uint32_t cta_top = s->top;
+  if (warp == 0) b.push(0, cta_top);
+
+  // ---- top-k of few: what reaches the k-th largest of the threads' own largest
+  const bool few = f.need_k && f.k <= kT && f.k * b.ctas <= kList / 2;
+  if (few) {
+    // Bins below this CTA's largest; what has no weight beside it has none in the row.
+    const float m = logit_of(cta_top), c = f.c;
+    const int my_bin = cta_top != kFull ? all_octaves().bin(x_of(top, m, c)) : kBins;
+    const int reach = reach_bin(my_bin, f.k);
+    const uint32_t reached = __reduce_min_sync(kFull, my_bin <= reach ? my_top : kFull);
+    if (lane == 0) atomicMin(&s->reached, reached);
+    if ((uint32_t)__syncthreads_count(my_bin <= reach) >= f.k) {
+      const float least = logit_of(s->reached);
+      list_range(b, r, top >= least, least, INFINITY);
+    } else {                                       // fewer have weight than k
+      list_range_cold(b, r, my_bin < kBins, least_logit(m, c, all_octaves(), kBins - 1), INFINITY);
+    }
+    push_count(b);
   }
   cluster_join();
-  {
-    uint64_t v = 0;
-    for (int i = 0; i < b.ctas; ++i) v = max(v, ld_cluster_u64(b.peer(&s->xch[0], i)));
-    f.m = logit_of((uint32_t)v);
-    bad = (v >> 32) != 0 || f.m == -INFINITY;
-  }
-  if (bad) {                                       // nothing to draw from
+  const uint32_t row_top = (uint32_t)b.max_of(0);
+  f.m = logit_of(row_top);
+  if (row_top == kFull || f.m == -INFINITY) {      // nothing to draw from
     if (b.rank == 0 && tid == 0 && RLK_STORE_OK(row < a.N, &g_err_sample)) {
       a.token[row] = -1;
       a.logp[row] = __int_as_float(0x7fc00000);
     }
-    cluster_join();                                // peers may still read this CTA's value
     return;
   }
-
-  // ---- where the kept prefix of the sorted order ends: key > cut_key, or equal and id <= cut_id
-  uint32_t cut_key = 0;
-  int cut_id = a.V;
-  bool by_mass = !f.need_k;                        // the search under way
-  uint64_t total_mass = 0, want_mass = 0;
-  uint32_t want_count = f.k;
-  int slot = 1;
-  // at most: by count, by weight instead if that cuts nothing, or by weight after it
-  for (int pass = 0; pass < 2 && (f.need_k || f.need_p); ++pass) {
-    Cut cut;
-    uint32_t before = 0;                           // elements, weight above the current range
-    uint64_t mass_before = 0;
-    int window = 0;
-    for (; window < kWindows; ++window) {
-      clear_bins(b, f.need_p);
-      uint64_t mass = 0;
-      for (int v = r.v0 + lane; v < r.v1; v += 32) {
-        float z[kE];
-        r.get(v, z);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float x = x_of(z[e], f.m, f.c);
-          const int bin = bin_of(x, window);
-          uint32_t w = 0;
-          if (f.need_p) {
-            w = weight_of(x);
-            mass += w;
-          }
-          if (bin >= 0 && bin < kBins) add_to_bin(b, bin, f.need_p, w);
-        }
-      }
-      if (by_mass && window == 0 && total_mass == 0) {   // C_k is the whole row's weight
-        mass = block_sum(b, mass, 1);
-        if (tid == 0) s->xmass[0] = mass;
-        cluster_join();
-        for (int i = 0; i < b.ctas; ++i) total_mass += ld_cluster_u64(b.peer(&s->xmass[0], i));
-        want_mass = scaled_24(total_mass, f.p24);
-        if (want_mass < 1) want_mass = 1;
-      }
-      uint32_t all_n;
-      uint64_t all_mass;
-      cut = find_cut(b, f.need_p, by_mass, want_count - before, want_mass - mass_before, &all_n,
-                     &all_mass);
-      if (cut.bin >= 0) break;
-      before += all_n;
-      mass_before += all_mass;
-    }
-    if (cut.bin < 0) {
-      // Only weightless elements are left: top-k cuts nothing that could be drawn.
-      if (f.need_k && f.need_p && !by_mass) {
-        f.need_k = false;
-        by_mass = true;
-        continue;
-      }
-      break;
-    }
-    const bool first = f.need_k == !by_mass;       // the search that any list would end
-    before += cut.before;
-    mass_before += cut.mass;
-    if (first && before + cut.in <= kList) {
-      // ---- few candidates: the leading CTA takes them all
-      for (int v = r.v0 + lane; v < r.v1; v += 32) {
-        float z[kE];
-        r.get(v, z);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          if (bin_of(x_of(z[e], f.m, f.c), window) <= cut.bin) {
-            const uint32_t at = atom_add_cluster(b.peer(&s->n_list, 0), 1);
-            if (at < kList)
-              st_cluster_u64(b.peer(&s->list[at], 0),
-                             ((uint64_t)~key_of(z[e]) << 32) | (uint32_t)(r.first_id + v * kE + e));
-          }
-        }
-      }
-      cluster_join();
-      if (b.rank == 0) {
-        const int n = (int)(before + cut.in);
-        finish_list(b, f, a, row, n, total_mass);
-        __syncthreads();
-        if (tid == 0 && RLK_STORE_OK(row < a.N, &g_err_sample)) {
-          const int id = s->answer;
-          const float z =
-              kFp32 ? __ldg(static_cast<const float*>(a.logits) + row * a.ld + id)
-                    : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.logits) +
-                                                      row * a.ld + id)
-                                      << 16);
-          a.logp[row] = logp_of(f, z, s->xmass[3]);
-        }
-      }
+  if (few) {
+    const uint64_t n = b.sum_of(7, b.ctas);
+    if (n <= kList) {
+      gather_lists(b);
+      if (b.rank == 0) finish(b, f, a, row, (int)n, 0);
       return;
     }
-    // ---- narrow the cut inside the bin: first the bin's range of keys ...
-    uint32_t kmin = 0xffffffffu, kmax = 0;
-    for (int v = r.v0 + lane; v < r.v1; v += 32) {
-      float z[kE];
-      r.get(v, z);
+  }
+
+  uint64_t last = ~0ull;                           // the last entry kept
+  if (f.need_k || f.need_p) {
+    last = search(b, r, f, a, row, top);
+    if (last == 0) return;
+  }
+
+  // ---- the weight kept, by warp and CTA: z > cut, or z = cut and id <= cut_id
+  const float cut = last == ~0ull ? -INFINITY : entry_logit(last);
+  const int cut_id = last == ~0ull ? -1 : (int)min((uint32_t)last, (uint32_t)a.V);
+  uint64_t sum = weight_kept(r, f.m, f.c, f.least, cut, cut_id);
+  sum = warp_sum(sum);
+  {
+    const uint64_t here = block_sum(b, lane == 0 ? sum : 0, 1);
+    if (warp == 0) b.push(4, here);
+  }
+  cluster_join();
+  uint64_t before = b.sum_of(4, b.rank);
+  const uint64_t total = b.sum_of(4, b.ctas);
+  for (int o = 0; o < warp; ++o) before += s->part[1][o];
+  const uint64_t at = scaled_31(total, f.u31);
+  if (!(before <= at && at < before + sum)) return;   // uniform in the warp: the token is elsewhere
+  take_token(r, f, a, row, cut, cut_id, before, at, total);
+}
+
+// ---------------------------------------------------------------- streaming kernels
+// Calls of many large rows: every pass over the logits is a kernel of independent warps
+// without a barrier, which streams at memory speed (a pass of weights at 0.5 - 1.0 of it),
+// and what belongs to a row as a whole is a CTA's work between two passes:
+//   tops   the largest logit of every chunk (the 8 vectors a lane of a tile reads)
+//   pick   the row's largest; top-k of at most kChunkTop: the k-th largest of the chunks'
+//          bounds the k first, only the chunks that reach it are read again, and the row
+//          is done
+//   weigh  the other rows' weights by tile, for top-p with their histogram
+//   cut    rows that keep all: the token's tile by a running sum, then the token; top-p: the
+//          cut from the histogram, by a list of what lies up to it (done) or of its bin
+//   weigh  again, the kept weights of the rows cut by their bin; and the token
+// Rows that none of this settles (more equal logits than the list holds, top-k of more, a cut
+// in the last octaves) are left to sample_kernel, one CTA a row.
+constexpr int kTile = 256;                    // vectors of a tile: 8 a lane
+constexpr int kStreamThreads = 256;
+constexpr int kTilesPerCta = 16;              // of the weighing kernels
+constexpr int kChunkTop = 1024;
+
+struct StreamArgs {
+  SampleArgs a;
+  int tiles;                // per row
+  uint32_t* tops;           // [N][tiles * 32] keys
+  uint64_t* mass;           // [N][tiles]
+  uint32_t* bin_count;      // [N][kBins]
+  uint64_t* bin_mass;       // [N][kBins]
+  RowState* state;          // [N]
+};
+
+__device__ __forceinline__ void stream_begin() {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+}
+
+// The warp's vectors of tile t.
+template <class R>
+__device__ __forceinline__ void at_tile(R& r, int vectors, int t) {
+  r.v0 = t * kTile;
+  r.v1 = min(r.v0 + kTile, vectors);
+}
+
+template <bool kFp32>
+__global__ void __launch_bounds__(kStreamThreads) sample_tops_kernel(const __grid_constant__ StreamArgs p,
+                                                                    int per_row) {
+  using R = Row<kFp32, false>;
+  stream_begin();
+  const int row = blockIdx.x / per_row, lane = threadIdx.x & 31;
+  const int t = (blockIdx.x - row * per_row) * (kStreamThreads / 32) + (threadIdx.x >> 5);
+  if (t >= p.tiles) return;
+  R r;
+  at_tile(r, r.begin(p.a, row), t);
+  float top = -INFINITY;
+  r.template each<true, 8>([&](int, const uint4& q) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(R::top_of(q)));
+  });
+  if (RLK_STORE_OK(row < p.a.N && t < p.tiles, &g_err_sample))
+    p.tops[((int64_t)row * p.tiles + t) * 32 + lane] = top < INFINITY ? key_of(top) : kFull;
+}
+
+// The chunks whose largest reaches lo, then their elements of [lo, hi], into the list: the
+// number of elements (more than kList: only counted).  ids: [tiles * 32] in shared memory.
+template <class B, class R>
+__device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* tops, int chunks,
+                                        float lo, float hi, uint16_t* ids) {
+  SampleSmem* s = b.s;
+  const uint32_t least = lo == -INFINITY ? 0u : key_of(lo);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s->n_list = 0;
+    s->n_chunks = 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < chunks; i += B::kThreads)
+    if (tops[i] >= least) ids[atomicAdd(&s->n_chunks, 1u)] = (uint16_t)i;
+  __syncthreads();
+  r.v0 = 0;
+  r.v1 = vectors;
+  const int n = (int)s->n_chunks;
+  for (int i = threadIdx.x; i < n; i += B::kThreads) {
+    const int chunk = ids[i];
+#pragma unroll 1
+    for (int half = 0; half < 8; half += 4) {
+      int v[4];
+      uint4 q[4];
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (bin_of(x_of(z[e], f.m, f.c), window) == cut.bin) {
-          kmin = min(kmin, key_of(z[e]));
-          kmax = max(kmax, key_of(z[e]));
-        }
-    }
-    kmin = __reduce_min_sync(kFull, kmin);
-    kmax = __reduce_max_sync(kFull, kmax);
-    __syncthreads();
-    if (lane == 0) s->part[2][warp] = ((uint64_t)~kmin << 32) | kmax;
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t lo = 0, hi = 0;
-      for (int w = 0; w < kSampleWarps; ++w) {
-        lo = max(lo, (uint32_t)(s->part[2][w] >> 32));
-        hi = max(hi, (uint32_t)s->part[2][w]);
-      }
-      s->xch[slot] = ((uint64_t)lo << 32) | hi;
-    }
-    cluster_join();
-    {
-      uint32_t lo = 0, hi = 0;
-      for (int i = 0; i < b.ctas; ++i) {
-        const uint64_t v = ld_cluster_u64(b.peer(&s->xch[slot], i));
-        lo = max(lo, (uint32_t)(v >> 32));
-        hi = max(hi, (uint32_t)v);
-      }
-      kmin = ~lo;
-      kmax = hi;
-    }
-    ++slot;
-    // ... then that range in kBins parts until a part is one key
-    uint32_t in = cut.in;
-    for (int level = 0; kmin != kmax && level < 4; ++level) {   // 32 bits, 10 a level
-      int shift = 0;
-      while (((kmax - kmin) >> shift) >= kBins) ++shift;
-      clear_bins(b, f.need_p);
-      for (int v = r.v0 + lane; v < r.v1; v += 32) {
-        float z[kE];
-        r.get(v, z);
+      for (int j = 0; j < 4; ++j)
+        v[j] = min((chunk >> 5) * kTile + 32 * (half + j) + (chunk & 31), vectors);
+      r.template get_all<true>(v, q);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const uint32_t key = key_of(z[e]);
-          if (key >= kmin && key <= kmax)
-            add_to_bin(b, (kmax - key) >> shift, f.need_p,
-                       f.need_p ? weight_of(x_of(z[e], f.m, f.c)) : 0);
-        }
+      for (int j = 0; j < 4; ++j) {
+        if (v[j] >= vectors || !(R::top_of(q[j]) >= lo)) continue;
+        float z[R::kElems];
+        R::unpack(q[j], z);
+#pragma unroll
+        for (int e = 0; e < R::kElems; ++e)
+          if (z[e] >= lo && z[e] <= hi) {
+            const uint32_t to = atomicAdd(&s->n_list, 1u);
+            if (to < kList) s->list[to] = entry_of(z[e], r.id_of(v[j]) + e);
+          }
+      }
+    }
+  }
+  __syncthreads();
+  return (int)s->n_list;
+}
+
+template <bool kFp32>
+__global__ void __launch_bounds__(kStreamThreads) sample_pick_kernel(const __grid_constant__ StreamArgs p) {
+  using R = Row<kFp32, false>;
+  using B = Block<kStreamThreads>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  B b;
+  b.s = reinterpret_cast<SampleSmem*>(smem_raw);
+  b.rank = 0;
+  b.ctas = 1;
+  SampleSmem* s = b.s;
+  uint16_t* ids = reinterpret_cast<uint16_t*>(smem_raw + sizeof(SampleSmem));
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) s->top = 0;
+  clear_bins(b, false);
+  stream_begin();
+  bool bad;
+  Filter f = settings_of(p.a, row, &bad);
+  const int chunks = p.tiles * 32;
+  const uint32_t* tops = p.tops + (int64_t)row * chunks;
+  uint32_t top = 0;
+  for (int i = tid; i < chunks; i += kStreamThreads) top = max(top, tops[i]);
+  top = __reduce_max_sync(kFull, top);
+  if (lane == 0) atomicMax(&s->top, top);
+  __syncthreads();
+  top = s->top;
+  f.m = logit_of(top);
+  RowState st;
+  st.status = kDone;
+  st.m = f.m;
+  st.cut = -INFINITY;
+  st.cut_id = -1;
+  if (bad || top == kFull || f.m == -INFINITY) {
+    if (tid == 0 && RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
+      p.a.token[row] = -1;
+      p.a.logp[row] = __int_as_float(0x7fc00000);
+    }
+  } else if (f.need_k) {
+    st.status = kGeneral;
+    if (f.k <= kChunkTop && (int)f.k <= chunks / 2) {
+      for (int i = tid; i < chunks; i += kStreamThreads) {
+        const int bin = all_octaves().bin(x_of(logit_of(tops[i]), f.m, f.c));
+        if (bin < kBins) add_to_bin(b, bin, false, 0);
       }
       uint32_t all_n;
       uint64_t all_mass;
-      cut = find_cut(b, f.need_p, by_mass, want_count - before, want_mass - mass_before, &all_n,
-                     &all_mass);
-      before += cut.before;
-      mass_before += cut.mass;
-      in = cut.in;
-      const uint32_t hi = kmax - ((uint32_t)cut.bin << shift);
-      const uint32_t below = (1u << shift) - 1;
-      kmin = hi - kmin > below ? hi - below : kmin;
-      kmax = hi;
-    }
-    cut_key = kmax;
-    const uint32_t w = weight_of(x_of(logit_of(cut_key), f.m, f.c));
-    uint64_t keep;                                 // how many of the equal ones
-    if (by_mass)
-      keep = w ? (want_mass - mass_before + w - 1) / w : in;
-    else
-      keep = want_count - before;
-    if (keep > in) keep = in;
-    if (!by_mass && f.need_p) {                    // top-p among the k kept
-      total_mass = mass_before + keep * w;
-      want_mass = scaled_24(total_mass, f.p24);
-      if (want_mass < 1) want_mass = 1;
-      by_mass = true;
-      continue;
-    }
-    if (keep < in) {
-      // ---- the id of the keep-th equal logit
-      uint32_t ties = 0;
-      for (int v = r.v0 + lane; v < r.v1; v += 32) {
-        float z[kE];
-        r.get(v, z);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) ties += key_of(z[e]) == cut_key;
-      }
-      ties = __reduce_add_sync(kFull, ties);
-      __syncthreads();
-      if (lane == 0) s->part[3][warp] = ties;
-      __syncthreads();
-      uint64_t below = 0, here = 0;                // ties in earlier CTAs; in this CTA's earlier warps
-      for (int w2 = 0; w2 < kSampleWarps; ++w2) here += s->part[3][w2];
-      if (tid == 0) s->xch[slot] = here;
       cluster_join();
-      for (int i = 0; i < b.rank; ++i) below += ld_cluster_u64(b.peer(&s->xch[slot], i));
-      ++slot;
-      for (int w2 = 0; w2 < warp; ++w2) below += s->part[3][w2];
-      if (tid == 0) s->xch[slot] = 0;
-      __syncthreads();
-      if (below < keep && keep <= below + ties) {  // uniform in the warp: its part holds it
-        for (int v = r.v0; v < r.v1; v += 32) {
-          float z[kE];
-          uint32_t n = 0;
-          if (v + lane < r.v1) {
-            r.get(v + lane, z);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) n += key_of(z[e]) == cut_key;
-          }
-          uint32_t upto = n;
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(kFull, upto, off);
-            if (lane >= off) upto += o;
-          }
-          const uint64_t prior = below + upto - n;
-          if (prior < keep && keep <= below + upto) {
-            uint64_t seen = prior;
-            for (int e = 0; e < kE; ++e)
-              if (key_of(z[e]) == cut_key && ++seen == keep)
-                s->xch[slot] = (uint32_t)(r.first_id + (v + lane) * kE + e) + 1u;
-          }
-          below += __shfl_sync(kFull, upto, 31);
+      const Cut cut = find_cut(b, false, false, f.k, 0, &all_n, &all_mass);
+      // fewer chunks have weight than k: all that has weight
+      const float lo = least_logit(f.m, f.c, all_octaves(), cut.bin >= 0 ? cut.bin : kBins - 1);
+      R r;
+      const int vectors = r.begin(p.a, row);
+      const int n = list_chunks(b, r, vectors, tops, chunks, lo, INFINITY, ids);
+      if (n <= kList) {
+        finish(b, f, p.a, row, n, 0);
+        st.status = kDone;
+      }
+    }
+  } else {
+    st.status = f.need_p ? kWeighBins : kWeigh;
+    if (f.need_p)
+      for (int i = tid; i < kBins; i += kStreamThreads)
+        if (RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
+          p.bin_count[(int64_t)row * kBins + i] = 0;
+          p.bin_mass[(int64_t)row * kBins + i] = 0;
         }
-      }
-      cluster_join();
-      uint64_t id = 0;
-      for (int i = 0; i < b.ctas; ++i) id = max(id, ld_cluster_u64(b.peer(&s->xch[slot], i)));
-      ++slot;
-      cut_id = (int)id - 1;
-    }
-    break;
   }
+  if (tid == 0 && RLK_STORE_OK(row < p.a.N, &g_err_sample)) p.state[row] = st;
+}
 
-  // ---- weights kept, by warp and CTA
-  uint64_t sum = 0;
-  for (int v = r.v0 + lane; v < r.v1; v += 32) {
-    float z[kE];
-    r.get(v, z);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const uint32_t key = key_of(z[e]);
-      if (key > cut_key || (key == cut_key && r.first_id + v * kE + e <= cut_id)) {
-        const uint32_t w = weight_of(x_of(z[e], f.m, f.c));
-        if (w >= f.least) sum += w;
-      }
-    }
+// The weight of tiles: kKept, of what is kept of the rows cut inside a bin; else of the rows
+// that keep all (but what min-p drops) and, with their histogram over the first octaves, of
+// the rows with top-p.
+template <bool kFp32, bool kKept>
+__global__ void __launch_bounds__(kStreamThreads) sample_weigh_kernel(const __grid_constant__ StreamArgs p,
+                                                                     int per_row) {
+  using R = Row<kFp32, false>;
+  constexpr int kE = R::kElems;
+  __shared__ uint32_t count[kKept ? 1 : kBins], lo[kKept ? 1 : kBins], hi[kKept ? 1 : kBins];
+  stream_begin();
+  const int row = blockIdx.x / per_row, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const RowState st = p.state[row];
+  if (kKept ? st.status != kWeighKept : st.status != kWeigh && st.status != kWeighBins) return;
+  const int t0 = (blockIdx.x - row * per_row) * kTilesPerCta;
+  bool bad;
+  const Filter f = settings_of(p.a, row, &bad);
+  const float m = st.m, c = f.c;
+  const bool bins = !kKept && st.status == kWeighBins;
+  const uint32_t least = bins ? 0 : f.least;
+  const Window window(0.f, kNear);
+  if (bins) {
+    for (int i = threadIdx.x; i < kBins; i += kStreamThreads) count[i] = lo[i] = hi[i] = 0;
+    __syncthreads();
   }
-  sum = warp_sum(sum);
-  __syncthreads();
-  if (lane == 0) s->part[0][warp] = sum;
-  __syncthreads();
-  uint64_t here = 0, before = 0, total = 0;
-  for (int w = 0; w < kSampleWarps; ++w) here += s->part[0][w];
-  if (tid == 0) s->xmass[1] = here;
-  cluster_join();
-  for (int i = 0; i < b.ctas; ++i) {
-    const uint64_t v = ld_cluster_u64(b.peer(&s->xmass[1], i));
-    if (i < b.rank) before += v;
-    total += v;
-  }
-  for (int w = 0; w < warp; ++w) before += s->part[0][w];
-  const uint64_t at = scaled_31(total, f.u31);
-  if (before <= at && at < before + sum) {         // uniform in the warp: the token is in its part
-    for (int v = r.v0; v < r.v1; v += 32) {
-      float z[kE];
+  R r;
+  const int vectors = r.begin(p.a, row);
+  for (int t = t0 + warp; t < min(t0 + kTilesPerCta, p.tiles); t += kStreamThreads / 32) {
+    at_tile(r, vectors, t);
+    uint64_t sum = 0;
+    r.template each<true, 4>([&](int v, const uint4& q) {
+      const float top = R::top_of(q);
+      if (kKept && !(top >= st.cut)) return;
+      float z[kE], x[kE];
       uint32_t w[kE];
-      uint64_t n = 0;
+      R::unpack(q, z);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) w[e] = 0;
-      if (v + lane < r.v1) {
-        r.get(v + lane, z);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const uint32_t key = key_of(z[e]);
-          if (key > cut_key || (key == cut_key && r.first_id + (v + lane) * kE + e <= cut_id)) {
-            w[e] = weight_of(x_of(z[e], f.m, f.c));
-            if (w[e] < f.least) w[e] = 0;
-          }
-          n += w[e];
-        }
+      for (int e = 0; e < kE; e += 2) {
+        x_pair(z[e], z[e + 1], m, c, x[e], x[e + 1]);
+        weights_of(x[e], x[e + 1], w[e], w[e + 1]);
       }
-      uint64_t upto = n;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint64_t o = __shfl_up_sync(kFull, upto, off);
-        if (lane >= off) upto += o;
+      for (int e = 0; e < kE; ++e) {
+        const bool keep = !kKept || z[e] > st.cut || (z[e] == st.cut && r.id_of(v) + e <= st.cut_id);
+        if (keep && w[e] >= least) sum = add_wide(sum, w[e]);
       }
-      uint64_t prior = before + upto - n;
-      if (prior <= at && at < before + upto) {
+      if (!kKept) {
+        if (bins && x_of(top, m, c) > -window.to) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          if (prior <= at && at < prior + w[e]) {
-            const int id = r.first_id + (v + lane) * kE + e;
-            if (RLK_STORE_OK(row < a.N && id >= 0 && id < a.V, &g_err_sample)) {
-              a.token[row] = id;
-              a.logp[row] = logp_of(f, z[e], total);
+          for (int e = 0; e < kE; ++e)
+            if (window.has(x[e])) {
+              const int bin = window.at(x[e]);
+              atomicAdd(&count[bin], 1u);
+              atomicAdd(&lo[bin], w[e] & 0xffffu);   // a CTA has at most 2^15 elements
+              atomicAdd(&hi[bin], w[e] >> 16);
             }
-          }
-          prior += w[e];
         }
       }
-      before += __shfl_sync(kFull, upto, 31);
-    }
+    });
+    sum = warp_sum(sum);
+    if (lane == 0 && RLK_STORE_OK(row < p.a.N && t < p.tiles, &g_err_sample))
+      p.mass[(int64_t)row * p.tiles + t] = sum;
   }
-  cluster_join();                                  // peers have read this CTA's sum
+  if (bins) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kStreamThreads)
+      if (count[i] && RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
+        // sums of whole numbers: their order does not matter
+        atomicAdd(&p.bin_count[(int64_t)row * kBins + i], count[i]);
+        atomicAdd(reinterpret_cast<unsigned long long*>(&p.bin_mass[(int64_t)row * kBins + i]),
+                  (unsigned long long)lo[i] + ((unsigned long long)hi[i] << 16));
+      }
+  }
+}
+
+// The token of a row whose tiles' kept weights are known: its tile, then itself.
+template <class B, class R>
+__device__ __forceinline__ void draw(const B& b, const StreamArgs& p, int row, const Filter& f, R r,
+                                     int vectors, float cut, int cut_id) {
+  SampleSmem* s = b.s;
+  const uint64_t* mass = p.mass + (int64_t)row * p.tiles;
+  const int each = (p.tiles + B::kThreads - 1) / B::kThreads;
+  const int t0 = min((int)threadIdx.x * each, p.tiles), t1 = min(t0 + each, p.tiles);
+  uint64_t sum = 0;
+  for (int t = t0; t < t1; ++t) sum += mass[t];
+  uint64_t upto = sum;
+  uint32_t unused = 0;
+  block_scan(b, unused, upto);
+  if (threadIdx.x == B::kThreads - 1) s->total[0] = upto;
+  __syncthreads();
+  const uint64_t total = s->total[0];
+  const uint64_t at = scaled_31(total, f.u31);
+  uint64_t before = upto - sum;
+  if (before <= at && at < upto)                   // one thread's tiles
+    for (int t = t0; t < t1; ++t) {
+      if (at < before + mass[t]) {
+        s->answer = t;
+        s->total[1] = before;
+        break;
+      }
+      before += mass[t];
+    }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    at_tile(r, vectors, s->answer);
+    take_token(r, f, p.a, row, cut, cut_id, s->total[1], at, total);
+  }
+}
+
+template <bool kFp32>
+__global__ void __launch_bounds__(kStreamThreads) sample_cut_kernel(const __grid_constant__ StreamArgs p,
+                                                                   int kept) {
+  using R = Row<kFp32, false>;
+  using B = Block<kStreamThreads>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  B b;
+  b.s = reinterpret_cast<SampleSmem*>(smem_raw);
+  b.rank = 0;
+  b.ctas = 1;
+  SampleSmem* s = b.s;
+  uint16_t* ids = reinterpret_cast<uint16_t*>(smem_raw + sizeof(SampleSmem));
+  const int row = blockIdx.x, tid = threadIdx.x;
+  stream_begin();
+  RowState st = p.state[row];
+  if (kept ? st.status != kWeighKept : st.status != kWeigh && st.status != kWeighBins) return;
+  bool bad;
+  Filter f = settings_of(p.a, row, &bad);
+  f.m = st.m;
+  R r;
+  const int vectors = r.begin(p.a, row);
+  if (st.status != kWeighBins) {
+    draw(b, p, row, f, r, vectors, st.cut, st.cut_id);
+    return;
+  }
+  const int chunks = p.tiles * 32;
+  const uint32_t* tops = p.tops + (int64_t)row * chunks;
+  // the row's weight, its histogram, the cut's bin
+  uint64_t sum = 0;
+  for (int t = tid; t < p.tiles; t += kStreamThreads) sum += p.mass[(int64_t)row * p.tiles + t];
+  sum = block_sum(b, sum, 0);
+  if (tid == 0) {
+    s->total[2] = sum;
+    s->cut.bin = -1;
+  }
+  for (int i = tid; i < kBins; i += kStreamThreads) {
+    s->slice_count[i] = p.bin_count[(int64_t)row * kBins + i];
+    s->slice_mass[i] = p.bin_mass[(int64_t)row * kBins + i];
+  }
+  __syncthreads();
+  const uint64_t total = s->total[2], want = f.share(total);
+  uint32_t all_n;
+  uint64_t all_mass;
+  const Cut cut = scan_cut(b, true, true, 0, want, &all_n, &all_mass);
+  const Window window(0.f, kNear);
+  st.status = kGeneral;
+  if (cut.bin >= 0 && cut.before + cut.in <= kList) {
+    const float lo = least_logit(f.m, f.c, window, cut.bin);
+    const int n = list_chunks(b, r, vectors, tops, chunks, lo, INFINITY, ids);
+    finish(b, f, p.a, row, n, total);
+    st.status = kDone;
+  } else if (cut.bin >= 0 && cut.in <= kList) {
+    const float lo = least_logit(f.m, f.c, window, cut.bin);
+    float hi = f.m;
+    if (cut.bin > 0) hi = logit_of(key_of(least_logit(f.m, f.c, window, cut.bin - 1)) - 1);
+    const int n = list_chunks(b, r, vectors, tops, chunks, lo, hi, ids);
+    cut_in_bin(b, f, n, true, 0, cut.mass, want);
+    st.cut = entry_logit(s->total[2]);
+    st.cut_id = (int)(uint32_t)s->total[2];
+    st.status = kWeighKept;
+  }
+  if (tid == 0 && RLK_STORE_OK(row < p.a.N, &g_err_sample)) p.state[row] = st;
 }
 
 std::mutex g_attr_mutex;
@@ -843,28 +1742,118 @@ cudaError_t ensure_attrs(int dev) {
   std::lock_guard<std::mutex> lock(g_attr_mutex);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (g_attr_set[dev]) return cudaSuccess;
-  for (auto* kernel : {sample_kernel<false>, sample_kernel<true>}) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  cudaError_t e = cudaSuccess;
+  for (auto* kernel : {sample_kernel<false, false, 256>, sample_kernel<false, true, 512>,
+                       sample_kernel<true, false, 256>, sample_kernel<true, true, 512>}) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
   }
-  g_attr_set[dev] = true;
-  return cudaSuccess;
+  for (auto* kernel : {sample_pick_kernel<false>, sample_pick_kernel<true>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  for (auto* kernel : {sample_cut_kernel<false>, sample_cut_kernel<true>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  if (e == cudaSuccess) g_attr_set[dev] = true;
+  return e;
 }
 
 inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
-// CTAs a row: enough that a CTA holds at most 76 KiB of it (two CTAs fit an SM), then
-// doubled while the clusters leave SMs idle and a CTA keeps 2 Ki elements or more.
-int cluster_ctas(int64_t N, int64_t V, int esize, int sms) {
-  int c = 1;
-  while (c < kMaxCluster && ceil_div(V, c) * esize > 77824) c *= 2;
-  while (c < kMaxCluster && N * c * 2 <= sms && V / (2 * c) >= 2048) c *= 2;
-  return c;
+// How a call runs: the streaming kernels, or clusters of CTAs that keep a row in shared
+// memory or read it again from L2.
+struct SamplePlan {
+  bool stream;
+  int ctas;
+  bool on_chip;
+  int tiles;
+  size_t off_mass, off_count, off_bins, off_state, total;   // the streaming kernels' workspace
+};
+
+SamplePlan sample_plan(int64_t N, int64_t V, bool fp32, int sms) {
+  SamplePlan p = {};
+  const int esize = fp32 ? 4 : 2, elems = 16 / esize;
+  p.stream = V >= 16384 && N * V * esize >= kStreamBytes;
+  if (p.stream) {
+    p.tiles = (int)ceil_div(ceil_div(V + elems - 1, elems), kTile);
+    p.off_mass = align_up((size_t)N * p.tiles * 32 * sizeof(uint32_t), 256);
+    p.off_count = align_up(p.off_mass + (size_t)N * p.tiles * sizeof(uint64_t), 256);
+    p.off_bins = align_up(p.off_count + (size_t)N * kBins * sizeof(uint32_t), 256);
+    p.off_state = align_up(p.off_bins + (size_t)N * kBins * sizeof(uint64_t), 256);
+    p.total = align_up(p.off_state + (size_t)N * sizeof(RowState), 256);
+    p.ctas = 1;
+    while (p.ctas < kMaxCluster && ceil_div(V, p.ctas) > 60000) p.ctas *= 2;
+    return p;
+  }
+  p.ctas = 1;
+  // a CTA has fewer than 2^16 elements (its histogram's halves are 32-bit sums)
+  while (p.ctas < kMaxCluster && ceil_div(V, p.ctas) > 60000) p.ctas *= 2;
+  while (p.ctas < kMaxCluster && N * p.ctas * 2 <= sms && V / (2 * p.ctas) >= 2048) p.ctas *= 2;
+  p.on_chip = N * p.ctas <= 2 * sms && ceil_div(V, p.ctas) * esize <= 77824;
+  return p;
+}
+
+// The clusters' kernel over all rows, or (state) those left to it.
+cudaError_t launch_clusters(SampleArgs a, bool fp32, const SamplePlan& plan, const RowState* state,
+                            cudaStream_t stream) {
+  const int elems = fp32 ? 4 : 8;
+  a.state = state;
+  // vectors of a row that starts anywhere in its first vector, dealt evenly
+  const int per = (int)ceil_div(ceil_div((int64_t)a.V + elems - 1, elems), plan.ctas);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.N * plan.ctas));
+  cfg.blockDim = dim3(plan.on_chip ? 512 : 256);
+  cfg.dynamicSmemBytes = sizeof(SampleSmem) + (plan.on_chip ? (size_t)per * 16 : 0);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)plan.ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return fp32 ? (plan.on_chip ? cudaLaunchKernelEx(&cfg, sample_kernel<true, true, 512>, a, per)
+                              : cudaLaunchKernelEx(&cfg, sample_kernel<true, false, 256>, a, per))
+              : (plan.on_chip ? cudaLaunchKernelEx(&cfg, sample_kernel<false, true, 512>, a, per)
+                              : cudaLaunchKernelEx(&cfg, sample_kernel<false, false, 256>, a, per));
+}
+
+template <bool kFp32>
+cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* ws,
+                          cudaStream_t stream) {
+  StreamArgs p;
+  p.a = a;
+  p.tiles = plan.tiles;
+  p.tops = reinterpret_cast<uint32_t*>(ws);
+  p.mass = reinterpret_cast<uint64_t*>(ws + plan.off_mass);
+  p.bin_count = reinterpret_cast<uint32_t*>(ws + plan.off_count);
+  p.bin_mass = reinterpret_cast<uint64_t*>(ws + plan.off_bins);
+  p.state = reinterpret_cast<RowState*>(ws + plan.off_state);
+  const int top_ctas = (int)ceil_div(plan.tiles, kStreamThreads / 32);
+  const int weigh_ctas = (int)ceil_div(plan.tiles, kTilesPerCta);
+  const size_t smem = sizeof(SampleSmem) + align_up((size_t)plan.tiles * 32 * sizeof(uint16_t), 16);
+  const dim3 rows((unsigned)a.N), tops((unsigned)(a.N * top_ctas)), weighs((unsigned)(a.N * weigh_ctas));
+  cudaError_t e;
+  if ((e = launch_overlapped(sample_tops_kernel<kFp32>, tops, kStreamThreads, 0, stream, p,
+                             top_ctas)) != cudaSuccess ||
+      (e = launch_overlapped(sample_pick_kernel<kFp32>, rows, kStreamThreads, smem, stream, p)) !=
+          cudaSuccess ||
+      (e = launch_overlapped(sample_weigh_kernel<kFp32, false>, weighs, kStreamThreads, 0, stream, p,
+                             weigh_ctas)) != cudaSuccess ||
+      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kStreamThreads, smem, stream, p, 0)) !=
+          cudaSuccess ||
+      (e = launch_overlapped(sample_weigh_kernel<kFp32, true>, weighs, kStreamThreads, 0, stream, p,
+                             weigh_ctas)) != cudaSuccess ||
+      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kStreamThreads, smem, stream, p, 1)) !=
+          cudaSuccess)
+    return e;
+  return launch_clusters(a, kFp32, plan, p.state, stream);
 }
 
 }  // namespace
@@ -884,15 +1873,24 @@ uint32_t take_error_sample() {
 
 using namespace rlk;
 
-extern "C" rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64_t N, int64_t V,
+extern "C" {
+
+size_t rlk_sample_logits_workspace_size(int logits_dtype, int64_t N, int64_t V) {
+  if (N < 0 || N >= kMaxSampleRows || V < 1 || V > kMaxSampleVocab ||
+      (logits_dtype != RLK_BF16 && logits_dtype != RLK_FP32))
+    return 0;
+  return sample_plan(N, V, logits_dtype == RLK_FP32, 0).total;
+}
+
+rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64_t N, int64_t V,
                                         int64_t ld, const void* uniform, int uniform_dtype,
                                         const float* temperature, float temperature_all,
                                         const int32_t* top_k, int32_t top_k_all,
                                         const float* top_p, float top_p_all, const float* min_p,
                                         float min_p_all, int64_t* token, float* logp,
-                                        void* stream) {
+                                        void* workspace, size_t workspace_bytes, void* stream) {
   RLK_CALL_RANGE();
-  if (N < 0 || N >= (int64_t(1) << 27) || V < 1 || V > kMaxSampleVocab || ld < V ||
+  if (N < 0 || N >= kMaxSampleRows || V < 1 || V > kMaxSampleVocab || ld < V ||
       ld >= (int64_t(1) << 36))
     return RLK_ERR_SHAPE;
   if ((logits_dtype != RLK_BF16 && logits_dtype != RLK_FP32) ||
@@ -908,6 +1906,9 @@ extern "C" rlk_status rlk_sample_logits(const void* logits, int logits_dtype, in
       !aligned_to(temperature, 4) || !aligned_to(top_k, 4) || !aligned_to(top_p, 4) ||
       !aligned_to(min_p, 4) || !aligned_to(token, 8) || !aligned_to(logp, 4))
     return RLK_ERR_ALIGN;
+  const size_t need = rlk_sample_logits_workspace_size(logits_dtype, N, V);
+  if (need > 0 && (!workspace || !aligned_to(workspace, 256) || workspace_bytes < need))
+    return RLK_ERR_WORKSPACE;
   DeviceInfo dev;
   const rlk_status st = device_ready(&dev);
   if (st != RLK_OK) return st;
@@ -930,31 +1931,21 @@ extern "C" rlk_status rlk_sample_logits(const void* logits, int logits_dtype, in
   a.min_p_all = min_p_all;
   a.uniform = uniform;
   a.uniform_fp64 = uniform_dtype == RLK_FP64;
+  a.fp32 = fp32;
   a.token = token;
   a.logp = logp;
-  const int ctas = cluster_ctas(N, V, fp32 ? 4 : 2, dev.sm_count);
-  const int elems = fp32 ? 4 : 8;
-  // vectors of a row that starts anywhere in its first vector, dealt evenly
-  const int per = (int)ceil_div(ceil_div(V + elems - 1, elems), ctas);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(N * ctas));
-  cfg.blockDim = dim3(kSampleThreads);
-  cfg.dynamicSmemBytes = sizeof(SampleSmem) + (size_t)per * 16;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = fp32 ? cudaLaunchKernelEx(&cfg, sample_kernel<true>, a, per)
-                             : cudaLaunchKernelEx(&cfg, sample_kernel<false>, a, per);
+  a.state = nullptr;
+  const SamplePlan plan = sample_plan(N, V, fp32, dev.sm_count);
+  cudaStream_t q = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const cudaError_t e = !plan.stream ? launch_clusters(a, fp32, plan, nullptr, q)
+                        : fp32       ? launch_stream<true>(a, plan, ws, q)
+                                     : launch_stream<false>(a, plan, ws, q);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return RLK_ERR_CUDA;
   }
   return RLK_OK;
 }
+
+}  // extern "C"

@@ -507,15 +507,19 @@ RLK_API rlk_status rlk_linear_logp_backward(const void* hidden, int64_t N, int64
  * A row that defines no distribution -- a NaN or +inf among its logits, no logit above
  * -inf, a NaN among its settings or u, a negative or infinite T -- gets token -1 and
  * logp NaN.  Such a value in an _all argument is refused (RLK_ERR_VALUE).
- * 1 <= V <= RLK_SAMPLE_MAX_VOCAB, 0 <= N < 2^27.  No workspace.
+ * 1 <= V <= RLK_SAMPLE_MAX_VOCAB, 0 <= N < 2^20.
+ *  workspace     >= rlk_sample_logits_workspace_size(...) bytes, 256-byte aligned (0 bytes,
+ *                and NULL allowed, for calls of little data)
  */
 #define RLK_SAMPLE_MAX_VOCAB 524288
+RLK_API size_t rlk_sample_logits_workspace_size(int logits_dtype, int64_t N, int64_t V);
 RLK_API rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64_t N, int64_t V,
                                      int64_t ld, const void* uniform, int uniform_dtype,
                                      const float* temperature, float temperature_all,
                                      const int32_t* top_k, int32_t top_k_all, const float* top_p,
                                      float top_p_all, const float* min_p, float min_p_all,
-                                     int64_t* token, float* logp, void* stream);
+                                     int64_t* token, float* logp, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /* ===================================================================== *
  *  Distillation from a teacher's top logits                              *

@@ -63,11 +63,70 @@ def test_tokens(N, V, dtype, how):
 
 @pytest.mark.parametrize("N,V,dtype", [(1, 151936, torch.float32), (20, 152064, torch.bfloat16),
                                        (40, 151936, torch.float32), (2, 524288, torch.float32),
-                                       (30, 70001, torch.float32), (160, 20011, torch.bfloat16)])
+                                       (30, 70001, torch.float32), (160, 20011, torch.bfloat16),
+                                       (48, 151936, torch.float32), (90, 152064, torch.bfloat16)])
 @pytest.mark.parametrize("how", [dict(), dict(top_k=50, top_p=0.95), dict(top_p=0.9)])
 def test_large_vocabularies(N, V, dtype, how):
     dev = cuda_or_skip()
     check(dev, logits(N, V, V).to(dtype), uniforms(N, 2), **how)
+
+
+def kinds(N, V, seed):
+    """Rows of every sort: confident, open, flat, equal, few levels, mostly banned, steep, broken."""
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn(N, V, generator=g) * 2
+    for r in range(N):
+        kind = r % 11
+        if kind == 0:
+            z[r, torch.randint(V, (30,), generator=g)] += torch.rand(30, generator=g) * 14
+        elif kind == 1:
+            z[r] *= 0.3
+        elif kind == 2:
+            z[r] = 1.5
+        elif kind == 3:
+            z[r] = torch.randint(4, (V,), generator=g).float()
+        elif kind == 4:
+            z[r, torch.rand(V, generator=g) < 0.999] = -math.inf
+        elif kind == 5:
+            z[r] = -torch.linspace(0, 300, V)
+        elif kind == 6:
+            z[r, torch.rand(V, generator=g) < 0.5] = torch.finfo(torch.float32).min
+        elif kind == 7:
+            z[r, V // 2] = 40
+        elif kind == 8:
+            z[r, 0], z[r, V - 1] = 9, 9
+        elif kind == 9 and r % 2:
+            z[r, (r * 37) % V] = (math.nan, math.inf, -math.inf)[r % 3]
+    return z
+
+
+@pytest.mark.parametrize("N,V,dtype,shift", [(340, 20011, torch.float32, 0), (800, 16384, torch.bfloat16, 0),
+                                             (170, 40007, torch.float32, 3), (330, 40009, torch.bfloat16, 5)])
+def test_many_rows(N, V, dtype, shift):
+    """Calls large enough for the streaming kernels: rows of every sort, settings of every sort, and
+    each row's token and bits those of a call of its own."""
+    dev = cuda_or_skip()
+    wide = torch.full((N, V + 13 if shift else V), 99.0, dtype=dtype, device=dev)
+    z = wide[:, shift:shift + V]
+    z.copy_(kinds(N, V, V).to(dtype))
+    u = uniforms(N, 22)
+    g = torch.Generator().manual_seed(23)
+    def pick(v, dtype):
+        return torch.tensor(v, dtype=dtype)[torch.randint(len(v), (N,), generator=g)]
+    settings = [dict(), dict(top_k=40, top_p=0.9), dict(top_p=0.95), dict(top_p=0.5, min_p=0.01), dict(min_p=0.2),
+                dict(temperature=0.0), dict(top_k=1000), dict(top_k=9000, top_p=0.97),
+                dict(temperature=pick([0.0, 0.5, 1.0, 3.0], torch.float32),
+                     top_k=pick([0, 0, 1, 50, 900, 3000, V - 1], torch.int32),
+                     top_p=pick([0.2, 0.9, 0.999, 1.0, 1.0], torch.float32),
+                     min_p=pick([0.0, 0.0, 0.001, 0.3], torch.float32))]
+    nb = rlk.lib().rlk_sample_logits_workspace_size(rlk._DT[dtype], N, V)
+    assert nb > 0
+    for how in settings:
+        token, logp = check(dev, z, u, **how)
+        for s in (slice(0, 9), slice(40, 75), slice(N - 12, N)):
+            part = {k: v[s].to(dev) if torch.is_tensor(v) else v for k, v in how.items()}
+            a = rlk.sample_logits(z[s], u[s].to(dev), **part)
+            assert torch.equal(a[0], token[s]) and bits_equal(a[1], logp[s])
 
 
 def test_settings_per_row():
@@ -200,6 +259,27 @@ def test_rows_do_not_depend_on_the_call():
         back = torch.arange(N - 1, -1, -1, device=dev)
         a = rlk.sample_logits(z[back], u[back], **how)
         assert torch.equal(a[0][back], token) and bits_equal(a[1][back], logp)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        a = rlk.sample_logits(z, u, stream=side, **how)
+        side.synchronize()
+        assert torch.equal(a[0], token) and bits_equal(a[1], logp)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            a = rlk.sample_logits(z, u, **how)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], token) and bits_equal(a[1], logp)
+
+
+def test_many_rows_on_a_stream_and_in_a_graph():
+    dev = cuda_or_skip()
+    z, u = kinds(400, 20000, 24).to(dev), uniforms(400, 25).to(dev)
+    for how in (dict(top_p=0.9), dict(top_k=60, top_p=0.9), dict(top_k=2000)):
+        token, logp = rlk.sample_logits(z, u, **how)
+        for _ in range(3):
+            a = rlk.sample_logits(z, u, **how)
+            assert torch.equal(a[0], token) and bits_equal(a[1], logp)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         a = rlk.sample_logits(z, u, stream=side, **how)
