@@ -44,26 +44,22 @@ __device__ unsigned int g_err_sample = 0;
 
 namespace {
 
-constexpr int kMaxSampleWarps = 16;
+constexpr int kMaxSampleWarps = 32;
 constexpr int kBins = 1024;                  // histogram bins
 constexpr int kList = 2048;                  // candidates the leading CTA sorts
 constexpr int kMaxCluster = 16;
 constexpr int64_t kMaxSampleVocab = 524288;
 constexpr int64_t kMaxSampleRows = int64_t(1) << 20;
-constexpr int64_t kStreamBytes = int64_t(24) << 20;   // logits from which the streaming kernels run
+// Logits from which the streaming kernels run, for rows of kStreamVocab or more: rows of
+// 151,936 FP32 logits took (us, streaming against clusters) 2 rows 18 / 47 / 17 against
+// 18 / 45 / 15 with top-k and top-p / top-p / neither, 8 rows 19 / 51 / 19 against 23 / 56 /
+// 22, 64 rows 27 / 77 / 31 against 40 / 151 / 74.
+constexpr int64_t kStreamBytes = int64_t(4) << 20;
+constexpr int64_t kStreamVocab = 16384;
 constexpr float kOctaves = 32.f;             // weights vanish below 2^-32
 constexpr float kNear = 20.f;                // octaves of top-p's first histogram
 constexpr uint32_t kOne = 1u << 31;
 constexpr uint32_t kFull = 0xffffffffu;
-
-// What the streaming kernels know of a row between them.
-enum RowStatus { kDone = 0, kWeigh = 1, kWeighBins = 2, kWeighKept = 3, kGeneral = 4 };
-struct RowState {
-  int status;
-  float m;               // its largest logit
-  float cut;             // kept: z > cut, or z = cut and id <= cut_id
-  int cut_id;
-};
 
 struct SampleArgs {
   const void* logits;
@@ -80,7 +76,7 @@ struct SampleArgs {
   int fp32;
   int64_t* token;
   float* logp;
-  const RowState* state;      // not null: only the rows left for the general search
+  const int* left;            // not null: their number and the rows to take, of all
 };
 
 // ---------------------------------------------------------------- weights
@@ -502,9 +498,14 @@ __device__ __forceinline__ Cut scan_cut(const B& b, bool mass, bool by_mass, uin
   uint64_t m[kMine], cm = 0;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int owner = (bin + i) / per, at = (bin + i) - owner * per;
-    n[i] = ld_cluster_u32(b.peer(&s->slice_count[at], owner));
-    m[i] = mass ? ld_cluster_u64(b.peer(&s->slice_mass[at], owner)) : 0;
+    if (b.ctas == 1) {
+      n[i] = s->slice_count[bin + i];
+      m[i] = mass ? s->slice_mass[bin + i] : 0;
+    } else {
+      const int owner = (bin + i) / per, at = (bin + i) - owner * per;
+      n[i] = ld_cluster_u32(b.peer(&s->slice_count[at], owner));
+      m[i] = mass ? ld_cluster_u64(b.peer(&s->slice_mass[at], owner)) : 0;
+    }
     cn += n[i];
     cm += m[i];
   }
@@ -604,6 +605,22 @@ __device__ __forceinline__ void block_sort(const B&, uint64_t* a, int n) {
   }
 }
 
+// floor(u 2^31) of the row's uniform number, within [0, 2^31); all ones for a NaN.  Of an
+// FP64 number by its bits: this GPU's FP64 arithmetic is slow enough to show.
+__device__ __forceinline__ uint32_t uniform_31(const SampleArgs& a, int row) {
+  if (!a.uniform_fp64) {
+    const float u = __ldg(static_cast<const float*>(a.uniform) + row);
+    return u != u ? kFull : min(__float2uint_rd(__fmul_rn(u, 0x1p31f)), kOne - 1);   // saturates
+  }
+  const uint64_t v = __ldg(static_cast<const unsigned long long*>(a.uniform) + row);
+  const int e = (int)((v >> 52) & 0x7ff) - 1023;
+  const uint64_t fraction = v & ((1ull << 52) - 1);
+  if (e == 1024 && fraction) return kFull;
+  if ((v >> 63) || e < -31) return 0;
+  if (e >= 0) return kOne - 1;
+  return (uint32_t)((fraction | (1ull << 52)) >> (21 - e));
+}
+
 // The row's settings (f.m is set later); *bad: they define no distribution.
 __device__ __forceinline__ Filter settings_of(const SampleArgs& a, int row, bool* bad) {
   Filter f;
@@ -612,9 +629,8 @@ __device__ __forceinline__ Filter settings_of(const SampleArgs& a, int row, bool
   int k = a.top_k ? __ldg(a.top_k + row) : a.top_k_all;
   const float top_p = a.top_p ? __ldg(a.top_p + row) : a.top_p_all;
   const float min_p = a.min_p ? __ldg(a.min_p + row) : a.min_p_all;
-  const double u = a.uniform_fp64 ? __ldg(static_cast<const double*>(a.uniform) + row)
-                                  : (double)__ldg(static_cast<const float*>(a.uniform) + row);
-  *bad = !(tau >= 0.f && tau < INFINITY) || top_p != top_p || min_p != min_p || u != u;
+  f.u31 = uniform_31(a, row);
+  *bad = !(tau >= 0.f && tau < INFINITY) || top_p != top_p || min_p != min_p || f.u31 == kFull;
   if (tau < 1e-6f) {
     tau = 1.f;
     k = 1;
@@ -626,7 +642,6 @@ __device__ __forceinline__ Filter settings_of(const SampleArgs& a, int row, bool
   f.p24 = (uint32_t)rintf(__fmul_rn(fminf(fmaxf(top_p, 0.f), 1.f), 16777216.f));
   f.need_p = f.p24 < (1u << 24);
   f.least = (uint32_t)rintf(__fmul_rn(fminf(fmaxf(min_p, 0.f), 1.f), 16777216.f)) << 7;
-  f.u31 = (uint32_t)fmin(fmax(floor(u * 2147483648.0), 0.0), 2147483647.0);
   return f;
 }
 
@@ -676,46 +691,37 @@ __device__ __forceinline__ int sort_list(const B& b, int n) {
 }
 
 // The end of a row of which the list holds all elements up to some place in the sorted
-// order past the cut, of at most 64 elements of interest (n = the list's, or k): one warp,
-// two elements a lane.
-__device__ __forceinline__ void finish_warp(SampleSmem* s, const Filter& f, const SampleArgs& a,
-                                            int row, int n, uint64_t total_mass) {
-  const int lane = threadIdx.x & 31;
-  float z[2];
-  uint32_t w[2], id[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const uint64_t x = s->list[2 * lane + e];
-    z[e] = entry_logit(x);
-    id[e] = (uint32_t)x;
-    w[e] = 2 * lane + e < n ? f.weight(z[e]) : 0;
-  }
-  uint64_t upto = (uint64_t)w[0] + w[1];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const uint64_t o = __shfl_up_sync(kFull, upto, off);
-    if (lane >= off) upto += o;
-  }
-  const uint64_t most = f.share(f.need_k ? __shfl_sync(kFull, upto, 31) : total_mass);
-  const uint64_t before = upto - w[0] - w[1];
-  if (!(before + w[0] < most && w[1] >= f.least)) w[1] = 0;
-  if (!(before < most && w[0] >= f.least)) w[0] = 0;
-  const uint64_t total = warp_sum((uint64_t)w[0] + w[1]);
-  const uint64_t at = scaled_31(total, f.u31);
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < 2; ++e) s->list[2 * lane + e] = ((uint64_t)id[e] << 32) | w[e];
-  __syncwarp();
-  uint64_t sum[2] = {0, 0};                        // kept weights of lower ids
-  for (int j = 0; j < min(n, 64); ++j) {
+// order past the cut, n <= the block's threads, sorted: an element a thread.  One-off code is
+// fetched as it runs, so it is kept short rather than unrolled (unrolled for one warp it took
+// 5 us after a 4 us sort; a token of one row is 15).
+template <class B>
+__device__ __noinline__ void finish_short(B b, Filter f, const SampleArgs& a, int row, int n,
+                                          uint64_t total_mass) {
+  SampleSmem* s = b.s;
+  const int i = threadIdx.x;
+  const uint64_t x = s->list[min(i, n - 1)];
+  const float z = entry_logit(x);
+  const uint32_t id = (uint32_t)x;
+  uint32_t w = i < n && (uint32_t)i < f.k ? f.weight(z) : 0, unused = 0;
+  uint64_t upto = w;
+  block_scan(b, unused, upto);
+  if (i == B::kThreads - 1) s->total[0] = upto;
+  __syncthreads();
+  const uint64_t most = f.share(f.need_k ? s->total[0] : total_mass);
+  if (!(upto - w < most && w >= f.least)) w = 0;
+  const int kept = __syncthreads_count(w > 0);     // the first of the list, all of them
+  if (w) s->list[i] = ((uint64_t)id << 32) | w;
+  __syncthreads();
+  if (i >= kept) return;
+  uint64_t before = 0, total = 0;                  // kept weights of lower ids; of all
+#pragma unroll 2
+  for (int j = 0; j < kept; ++j) {
     const uint64_t o = s->list[j];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if ((uint32_t)(o >> 32) < id[e]) sum[e] += (uint32_t)o;
+    total += (uint32_t)o;
+    if ((uint32_t)(o >> 32) < id) before += (uint32_t)o;
   }
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (sum[e] <= at && at < sum[e] + w[e]) write_answer(a, f, row, (int)id[e], z[e], total);
+  const uint64_t at = scaled_31(total, f.u31);
+  if (before <= at && at < before + w) write_answer(a, f, row, (int)id, z, total);
 }
 
 // The same for a longer list, by the block: sort by logit, cut, sort by id, take.
@@ -756,7 +762,7 @@ __device__ __forceinline__ void finish_block(const B& b, const Filter& f, const 
   for (int e = 0; e < B::kPerThread; ++e)
     if (e < each && i0 + e < size) s->list[i0 + e] = entry[e];
   __syncthreads();
-  block_sort(b, s->list, size);                             // by id
+  sort_list(b, n);                                          // by id
   sum = 0;
 #pragma unroll
   for (int e = 0; e < B::kPerThread; ++e) {
@@ -807,7 +813,10 @@ __device__ __forceinline__ void list_range(const B& b, const R& r, bool mine, fl
   const int threads = __popc(who);
   const int steps = (r.v1 - r.v0 + 31) / 32;       // vectors a thread
   const bool share = threads <= 16;
-  const int at_rank = share ? (int)__fns(who, 0, lane + 1) : lane;   // lane of that rank
+  int at_rank = 0;                                 // the lane of the `lane`-th of them
+#pragma unroll
+  for (int step = 16; step >= 1; step >>= 1)
+    if (__popc(who & ((1u << (at_rank + step)) - 1)) <= lane) at_rank += step;
   const int total = (share ? threads : 32) * steps;
   for (int i0 = 0; i0 < total; i0 += kBatch * 32) {
     uint4 q[kBatch];
@@ -855,13 +864,22 @@ __device__ __forceinline__ void push_count(const B& b) {
 // must not before they have been read).  The sum of the counts is at most kList.
 template <class B>
 __device__ __forceinline__ void gather_lists(const B& b) {
-  if (b.rank == 0) {
-    uint32_t at = (uint32_t)b.s->from[7][0];
-    for (int r = 1; r < b.ctas; ++r) {
-      const uint32_t n = (uint32_t)b.s->from[7][r];
-      for (uint32_t i = threadIdx.x; i < n; i += B::kThreads)
-        b.s->list[at + i] = ld_cluster_u64(b.peer(&b.s->list[i], r));
-      at += n;
+  if (b.rank == 0 && b.ctas > 1) {
+    const int lane = threadIdx.x & 31;
+    int upto = lane < b.ctas ? (int)b.s->from[7][lane] : 0;   // entries of the CTAs up to this lane's
+    const int mine = upto;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(kFull, upto, off);
+      if (lane >= off) upto += o;
+    }
+    const int n = __shfl_sync(kFull, upto, 31);
+    for (int i0 = (int)b.s->from[7][0]; i0 < n; i0 += B::kThreads) {
+      const int i = i0 + threadIdx.x;
+      int r = 0;
+      for (int c = 0; c < b.ctas; ++c) r += i >= __shfl_sync(kFull, upto, c);
+      const int at = i - __shfl_sync(kFull, upto - mine, r & 31);
+      if (i < n) b.s->list[i] = ld_cluster_u64(b.peer(&b.s->list[at], r));
     }
   }
   if (b.ctas > 1) cluster_join();
@@ -907,11 +925,11 @@ template <class B>
 __device__ __noinline__ void finish(B b, Filter f, const SampleArgs& a, int row, int n,
                                     uint64_t total_mass) {
   SampleSmem* s = b.s;
-  if (n > B::kThreads && f.k <= B::kThreads) n = keep_first(b, f, n);
+  // counting places is quadratic: 424 take 8 us, 60 take 1, and keep_first 2
+  if (n > 96 && f.k <= B::kThreads) n = keep_first(b, f, n);
   const int size = sort_list(b, n);
-  const int of_interest = (int)min((uint32_t)n, f.k);
-  if (of_interest <= 64) {
-    if (threadIdx.x < 32) finish_warp(s, f, a, row, of_interest, total_mass);
+  if (n <= B::kThreads) {
+    finish_short(b, f, a, row, n, total_mass);
     return;
   }
   finish_block(b, f, a, row, n, size, total_mass);
@@ -1278,18 +1296,13 @@ __device__ __noinline__ uint64_t search(B b, R r, Filter f, const SampleArgs& a,
   return last;
 }
 
+// A row by its cluster.
 template <bool kFp32, bool kOnChip, int kT>
-__global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_constant__ SampleArgs a,
-                                                                     int per) {
+__device__ __forceinline__ void sample_row(const Block<kT>& b, const SampleArgs& a, int per,
+                                           int row, uint8_t* vectors_at) {
   using R = Row<kFp32, kOnChip>;
   using B = Block<kT>;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  SampleSmem* s = reinterpret_cast<SampleSmem*>(smem_raw);
-  B b;
-  b.s = s;
-  b.rank = (int)cluster_rank();
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(b.ctas));
-  const int row = blockIdx.x / b.ctas;
+  SampleSmem* s = b.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     s->n_list = 0;
@@ -1297,10 +1310,6 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
     s->reached = kFull;
   }
   __syncthreads();
-  griddep_wait();
-  if (tid == 0) griddep_launch_dependents();
-  if (a.state && a.state[row].status != kGeneral) return;   // all CTAs of the row alike
-
   bool bad;
   Filter f = settings_of(a, row, &bad);
   // ---- the first pass: the largest logit
@@ -1311,7 +1320,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
     const int mine = max(0, min(per, vectors - cta0));
     const int each = (mine + B::kWarps - 1) / B::kWarps;
     r.skip(cta0);
-    r.chip = reinterpret_cast<uint4*>(smem_raw + sizeof(SampleSmem));
+    r.chip = reinterpret_cast<uint4*>(vectors_at);
     r.v0 = min(warp * each, mine);
     r.v1 = min(r.v0 + each, mine);
   }
@@ -1388,6 +1397,26 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
   take_token(r, f, a, row, cut, cut_id, before, at, total);
 }
 
+template <bool kFp32, bool kOnChip, int kT>
+__global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_constant__ SampleArgs a,
+                                                               int per) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Block<kT> b;
+  b.s = reinterpret_cast<SampleSmem*>(smem_raw);
+  b.rank = (int)cluster_rank();
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(b.ctas));
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int first = blockIdx.x / b.ctas, clusters = gridDim.x / b.ctas;
+  const int rows = a.left ? *a.left : a.N;         // all: a row each
+  for (int i = first; i < rows; i += clusters) {
+    sample_row<kFp32, kOnChip, kT>(b, a, per, a.left ? a.left[1 + i] : i,
+                                   smem_raw + sizeof(SampleSmem));
+    if (!a.left) return;
+    cluster_join();                                // the shared memory is free again
+  }
+}
+
 // ---------------------------------------------------------------- streaming kernels
 // Calls of many large rows: every pass over the logits is a kernel of independent warps
 // without a barrier, which streams at memory speed (a pass of weights at 0.5 - 1.0 of it),
@@ -1398,14 +1427,28 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
 //          is done
 //   weigh  the other rows' weights by tile, for top-p with their histogram
 //   cut    rows that keep all: the token's tile by a running sum, then the token; top-p: the
-//          cut from the histogram, by a list of what lies up to it (done) or of its bin
-//   weigh  again, the kept weights of the rows cut by their bin; and the token
+//          bin of the cut from the histogram and, if little lies up to it, the token
+//   weigh  again, for the other rows with top-p: the weights above that bin by tile, and its
+//          elements in a list
+//   cut    again: the cut from the sorted list, and the token
 // Rows that none of this settles (more equal logits than the list holds, top-k of more, a cut
 // in the last octaves) are left to sample_kernel, one CTA a row.
 constexpr int kTile = 256;                    // vectors of a tile: 8 a lane
-constexpr int kStreamThreads = 256;
+constexpr int kStreamThreads = 256;           // of the passes
+constexpr int kRowThreads = 512;              // of the row's work between them
 constexpr int kTilesPerCta = 16;              // of the weighing kernels
 constexpr int kChunkTop = 1024;
+
+// What the streaming kernels know of a row between them.
+enum RowStatus { kDone = 0, kWeigh = 1, kWeighBins = 2, kCutBin = 3, kLeft = 4 };
+struct RowState {
+  int status;
+  float m;                  // its largest logit
+  float lo, hi;             // kCutBin: the logits of the bin the cut falls in
+  uint64_t mass_before;     // the weight above the bin, and the weight wanted
+  uint64_t mass_wanted;
+  int listed;               // the bin's elements listed so far
+};
 
 struct StreamArgs {
   SampleArgs a;
@@ -1415,7 +1458,18 @@ struct StreamArgs {
   uint32_t* bin_count;      // [N][kBins]
   uint64_t* bin_mass;       // [N][kBins]
   RowState* state;          // [N]
+  uint64_t* list;           // [N][kList] the elements of the bins the cuts fall in
+  int* left;                // number of rows left to sample_kernel, then the rows
 };
+
+__device__ __forceinline__ void put_state(const StreamArgs& p, int row, const RowState& st) {
+  if (!RLK_STORE_OK(row < p.a.N, &g_err_sample)) return;
+  p.state[row] = st;
+  if (st.status == kLeft) {
+    const int at = atomicAdd(p.left, 1);           // in any order
+    if (RLK_STORE_OK(at < p.a.N, &g_err_sample)) p.left[1 + at] = row;
+  }
+}
 
 __device__ __forceinline__ void stream_begin() {
   griddep_wait();
@@ -1434,6 +1488,7 @@ __global__ void __launch_bounds__(kStreamThreads) sample_tops_kernel(const __gri
                                                                     int per_row) {
   using R = Row<kFp32, false>;
   stream_begin();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.left = 0;
   const int row = blockIdx.x / per_row, lane = threadIdx.x & 31;
   const int t = (blockIdx.x - row * per_row) * (kStreamThreads / 32) + (threadIdx.x >> 5);
   if (t >= p.tiles) return;
@@ -1445,6 +1500,17 @@ __global__ void __launch_bounds__(kStreamThreads) sample_tops_kernel(const __gri
   });
   if (RLK_STORE_OK(row < p.a.N && t < p.tiles, &g_err_sample))
     p.tops[((int64_t)row * p.tiles + t) * 32 + lane] = top < INFINITY ? key_of(top) : kFull;
+}
+
+// A CTA's own histogram as scan_cut takes it.
+template <class B>
+__device__ __forceinline__ void merge_own(const B& b, bool mass) {
+  SampleSmem* s = b.s;
+  for (int i = threadIdx.x; i < kBins; i += B::kThreads) {
+    s->slice_count[i] = s->count[i];
+    if (mass) s->slice_mass[i] = s->lo[i] + ((uint64_t)s->hi[i] << 16);
+  }
+  __syncthreads();
 }
 
 // The chunks whose largest reaches lo, then their elements of [lo, hi], into the list: the
@@ -1460,34 +1526,38 @@ __device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* t
     s->n_chunks = 0;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < chunks; i += B::kThreads)
-    if (tops[i] >= least) ids[atomicAdd(&s->n_chunks, 1u)] = (uint16_t)i;
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 0; i0 < chunks; i0 += B::kThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool has = i < chunks && tops[i] >= least;
+    const uint32_t all = __ballot_sync(kFull, has);
+    uint32_t at = 0;
+    if (lane == 0 && all) at = atomicAdd(&s->n_chunks, (uint32_t)__popc(all));
+    at = __shfl_sync(kFull, at, 0) + __popc(all & ((1u << lane) - 1));
+    if (has) ids[at] = (uint16_t)i;
+  }
   __syncthreads();
   r.v0 = 0;
   r.v1 = vectors;
   const int n = (int)s->n_chunks;
   for (int i = threadIdx.x; i < n; i += B::kThreads) {
     const int chunk = ids[i];
-#pragma unroll 1
-    for (int half = 0; half < 8; half += 4) {
-      int v[4];
-      uint4 q[4];
+    int v[8];
+    uint4 q[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = min((chunk >> 5) * kTile + 32 * (half + j) + (chunk & 31), vectors);
-      r.template get_all<true>(v, q);
+    for (int j = 0; j < 8; ++j) v[j] = min((chunk >> 5) * kTile + 32 * j + (chunk & 31), vectors);
+    r.template get_all<true>(v, q);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (v[j] >= vectors || !(R::top_of(q[j]) >= lo)) continue;
-        float z[R::kElems];
-        R::unpack(q[j], z);
+    for (int j = 0; j < 8; ++j) {
+      if (v[j] >= vectors || !(R::top_of(q[j]) >= lo)) continue;
+      float z[R::kElems];
+      R::unpack(q[j], z);
 #pragma unroll
-        for (int e = 0; e < R::kElems; ++e)
-          if (z[e] >= lo && z[e] <= hi) {
-            const uint32_t to = atomicAdd(&s->n_list, 1u);
-            if (to < kList) s->list[to] = entry_of(z[e], r.id_of(v[j]) + e);
-          }
-      }
+      for (int e = 0; e < R::kElems; ++e)
+        if (z[e] >= lo && z[e] <= hi) {
+          const uint32_t to = atomicAdd(&s->n_list, 1u);
+          if (to < kList) s->list[to] = entry_of(z[e], r.id_of(v[j]) + e);
+        }
     }
   }
   __syncthreads();
@@ -1495,26 +1565,32 @@ __device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* t
 }
 
 template <bool kFp32>
-__global__ void __launch_bounds__(kStreamThreads) sample_pick_kernel(const __grid_constant__ StreamArgs p) {
+__global__ void __launch_bounds__(kRowThreads, 2) sample_pick_kernel(const __grid_constant__ StreamArgs p) {
   using R = Row<kFp32, false>;
-  using B = Block<kStreamThreads>;
+  using B = Block<kRowThreads>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   B b;
   b.s = reinterpret_cast<SampleSmem*>(smem_raw);
   b.rank = 0;
   b.ctas = 1;
   SampleSmem* s = b.s;
-  uint16_t* ids = reinterpret_cast<uint16_t*>(smem_raw + sizeof(SampleSmem));
+  const int chunks = p.tiles * 32;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(smem_raw + sizeof(SampleSmem));
+  uint16_t* ids = reinterpret_cast<uint16_t*>(tops + chunks);
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) s->top = 0;
   clear_bins(b, false);
   stream_begin();
   bool bad;
   Filter f = settings_of(p.a, row, &bad);
-  const int chunks = p.tiles * 32;
-  const uint32_t* tops = p.tops + (int64_t)row * chunks;
+  const uint32_t* src = p.tops + (int64_t)row * chunks;
   uint32_t top = 0;
-  for (int i = tid; i < chunks; i += kStreamThreads) top = max(top, tops[i]);
+#pragma unroll 8
+  for (int i = tid; i < chunks; i += kRowThreads) {
+    const uint32_t key = __ldg(src + i);
+    tops[i] = key;
+    top = max(top, key);
+  }
   top = __reduce_max_sync(kFull, top);
   if (lane == 0) atomicMax(&s->top, top);
   __syncthreads();
@@ -1523,24 +1599,27 @@ __global__ void __launch_bounds__(kStreamThreads) sample_pick_kernel(const __gri
   RowState st;
   st.status = kDone;
   st.m = f.m;
-  st.cut = -INFINITY;
-  st.cut_id = -1;
+  st.lo = st.hi = 0.f;
+  st.mass_before = st.mass_wanted = 0;
+  st.listed = 0;
   if (bad || top == kFull || f.m == -INFINITY) {
     if (tid == 0 && RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
       p.a.token[row] = -1;
       p.a.logp[row] = __int_as_float(0x7fc00000);
     }
   } else if (f.need_k) {
-    st.status = kGeneral;
+    st.status = kLeft;
     if (f.k <= kChunkTop && (int)f.k <= chunks / 2) {
-      for (int i = tid; i < chunks; i += kStreamThreads) {
+      for (int i = tid; i < chunks; i += kRowThreads) {
         const int bin = all_octaves().bin(x_of(logit_of(tops[i]), f.m, f.c));
         if (bin < kBins) add_to_bin(b, bin, false, 0);
       }
       uint32_t all_n;
       uint64_t all_mass;
-      cluster_join();
-      const Cut cut = find_cut(b, false, false, f.k, 0, &all_n, &all_mass);
+      if (tid == 0) s->cut.bin = -1;
+      __syncthreads();
+      merge_own(b, false);
+      const Cut cut = scan_cut(b, false, false, f.k, 0, &all_n, &all_mass);
       // fewer chunks have weight than k: all that has weight
       const float lo = least_logit(f.m, f.c, all_octaves(), cut.bin >= 0 ? cut.bin : kBins - 1);
       R r;
@@ -1554,78 +1633,94 @@ __global__ void __launch_bounds__(kStreamThreads) sample_pick_kernel(const __gri
   } else {
     st.status = f.need_p ? kWeighBins : kWeigh;
     if (f.need_p)
-      for (int i = tid; i < kBins; i += kStreamThreads)
+      for (int i = tid; i < kBins; i += kRowThreads)
         if (RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
           p.bin_count[(int64_t)row * kBins + i] = 0;
           p.bin_mass[(int64_t)row * kBins + i] = 0;
         }
   }
-  if (tid == 0 && RLK_STORE_OK(row < p.a.N, &g_err_sample)) p.state[row] = st;
+  if (tid == 0) put_state(p, row, st);
 }
 
-// The weight of tiles: kKept, of what is kept of the rows cut inside a bin; else of the rows
-// that keep all (but what min-p drops) and, with their histogram over the first octaves, of
-// the rows with top-p.
-template <bool kFp32, bool kKept>
-__global__ void __launch_bounds__(kStreamThreads) sample_weigh_kernel(const __grid_constant__ StreamArgs p,
-                                                                     int per_row) {
+// The weight of tiles: of the rows that keep all (but what min-p drops) and, with their
+// histogram over the first octaves, of the rows with top-p; or (kAbove) of what lies above
+// the bin the cut falls in, with a list of the bin's elements.
+enum WeighWhat { kAll, kAtLeast, kBinned, kAboveBin };
+template <bool kFp32, WeighWhat kWhat>
+__device__ __forceinline__ void weigh_tiles(const StreamArgs& p, int row, int t0, const RowState& st,
+                                            float c, uint32_t least, uint32_t* count, uint32_t* lo,
+                                            uint32_t* hi) {
   using R = Row<kFp32, false>;
   constexpr int kE = R::kElems;
-  __shared__ uint32_t count[kKept ? 1 : kBins], lo[kKept ? 1 : kBins], hi[kKept ? 1 : kBins];
-  stream_begin();
-  const int row = blockIdx.x / per_row, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const RowState st = p.state[row];
-  if (kKept ? st.status != kWeighKept : st.status != kWeigh && st.status != kWeighBins) return;
-  const int t0 = (blockIdx.x - row * per_row) * kTilesPerCta;
-  bool bad;
-  const Filter f = settings_of(p.a, row, &bad);
-  const float m = st.m, c = f.c;
-  const bool bins = !kKept && st.status == kWeighBins;
-  const uint32_t least = bins ? 0 : f.least;
   const Window window(0.f, kNear);
-  if (bins) {
-    for (int i = threadIdx.x; i < kBins; i += kStreamThreads) count[i] = lo[i] = hi[i] = 0;
-    __syncthreads();
-  }
   R r;
   const int vectors = r.begin(p.a, row);
-  for (int t = t0 + warp; t < min(t0 + kTilesPerCta, p.tiles); t += kStreamThreads / 32) {
+  for (int t = t0 + (threadIdx.x >> 5); t < min(t0 + kTilesPerCta, p.tiles); t += kStreamThreads / 32) {
     at_tile(r, vectors, t);
     uint64_t sum = 0;
     r.template each<true, 4>([&](int v, const uint4& q) {
-      const float top = R::top_of(q);
-      if (kKept && !(top >= st.cut)) return;
+      if (kWhat == kAboveBin && !(R::top_of(q) >= st.lo)) return;
       float z[kE], x[kE];
       uint32_t w[kE];
       R::unpack(q, z);
 #pragma unroll
       for (int e = 0; e < kE; e += 2) {
-        x_pair(z[e], z[e + 1], m, c, x[e], x[e + 1]);
+        x_pair(z[e], z[e + 1], st.m, c, x[e], x[e + 1]);
         weights_of(x[e], x[e + 1], w[e], w[e + 1]);
       }
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
-        const bool keep = !kKept || z[e] > st.cut || (z[e] == st.cut && r.id_of(v) + e <= st.cut_id);
-        if (keep && w[e] >= least) sum = add_wide(sum, w[e]);
-      }
-      if (!kKept) {
-        if (bins && x_of(top, m, c) > -window.to) {
-#pragma unroll
-          for (int e = 0; e < kE; ++e)
-            if (window.has(x[e])) {
-              const int bin = window.at(x[e]);
-              atomicAdd(&count[bin], 1u);
-              atomicAdd(&lo[bin], w[e] & 0xffffu);   // a CTA has at most 2^15 elements
-              atomicAdd(&hi[bin], w[e] >> 16);
-            }
+        bool keep = true;
+        if (kWhat == kAtLeast) keep = w[e] >= least;
+        if (kWhat == kAboveBin) {
+          keep = z[e] > st.hi && w[e] >= least;
+          if (z[e] >= st.lo && z[e] <= st.hi) {
+            const int at = atomicAdd(&p.state[row].listed, 1);   // in any order: it is sorted
+            if (at < kList && RLK_STORE_OK(row < p.a.N, &g_err_sample))
+              p.list[(int64_t)row * kList + at] = entry_of(z[e], r.id_of(v) + e);
+          }
         }
+        if (keep) sum = add_wide(sum, w[e]);
+      }
+      if (kWhat == kBinned && x_of(R::top_of(q), st.m, c) > -window.to) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+          if (window.has(x[e])) {
+            const int bin = window.at(x[e]);
+            atomicAdd(&count[bin], 1u);
+            atomicAdd(&lo[bin], w[e] & 0xffffu);   // a CTA has at most 2^15 elements
+            atomicAdd(&hi[bin], w[e] >> 16);
+          }
       }
     });
     sum = warp_sum(sum);
-    if (lane == 0 && RLK_STORE_OK(row < p.a.N && t < p.tiles, &g_err_sample))
+    if ((threadIdx.x & 31) == 0 && RLK_STORE_OK(row < p.a.N && t < p.tiles, &g_err_sample))
       p.mass[(int64_t)row * p.tiles + t] = sum;
   }
-  if (bins) {
+}
+
+template <bool kFp32, bool kAbove>
+__global__ void __launch_bounds__(kStreamThreads) sample_weigh_kernel(const __grid_constant__ StreamArgs p,
+                                                                     int per_row) {
+  __shared__ uint32_t count[kAbove ? 1 : kBins], lo[kAbove ? 1 : kBins], hi[kAbove ? 1 : kBins];
+  stream_begin();
+  const int row = blockIdx.x / per_row;
+  const RowState st = p.state[row];
+  if (kAbove ? st.status != kCutBin : st.status != kWeigh && st.status != kWeighBins) return;
+  const int t0 = (blockIdx.x - row * per_row) * kTilesPerCta;
+  bool bad;
+  const Filter f = settings_of(p.a, row, &bad);
+  if (kAbove) {
+    weigh_tiles<kFp32, kAboveBin>(p, row, t0, st, f.c, f.least, count, lo, hi);
+  } else if (st.status == kWeigh) {
+    if (f.least == 0)
+      weigh_tiles<kFp32, kAll>(p, row, t0, st, f.c, 0, count, lo, hi);
+    else
+      weigh_tiles<kFp32, kAtLeast>(p, row, t0, st, f.c, f.least, count, lo, hi);
+  } else {
+    for (int i = threadIdx.x; i < kBins; i += kStreamThreads) count[i] = lo[i] = hi[i] = 0;
+    __syncthreads();
+    weigh_tiles<kFp32, kBinned>(p, row, t0, st, f.c, 0, count, lo, hi);
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kStreamThreads)
       if (count[i] && RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
@@ -1646,7 +1741,7 @@ __device__ __forceinline__ void draw(const B& b, const StreamArgs& p, int row, c
   const int each = (p.tiles + B::kThreads - 1) / B::kThreads;
   const int t0 = min((int)threadIdx.x * each, p.tiles), t1 = min(t0 + each, p.tiles);
   uint64_t sum = 0;
-  for (int t = t0; t < t1; ++t) sum += mass[t];
+  for (int t = t0; t < t1; ++t) sum += __ldcg(mass + t);   // some just added to
   uint64_t upto = sum;
   uint32_t unused = 0;
   block_scan(b, unused, upto);
@@ -1657,12 +1752,13 @@ __device__ __forceinline__ void draw(const B& b, const StreamArgs& p, int row, c
   uint64_t before = upto - sum;
   if (before <= at && at < upto)                   // one thread's tiles
     for (int t = t0; t < t1; ++t) {
-      if (at < before + mass[t]) {
+      const uint64_t here = __ldcg(mass + t);
+      if (at < before + here) {
         s->answer = t;
         s->total[1] = before;
         break;
       }
-      before += mass[t];
+      before += here;
     }
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -1672,10 +1768,10 @@ __device__ __forceinline__ void draw(const B& b, const StreamArgs& p, int row, c
 }
 
 template <bool kFp32>
-__global__ void __launch_bounds__(kStreamThreads) sample_cut_kernel(const __grid_constant__ StreamArgs p,
-                                                                   int kept) {
+__global__ void __launch_bounds__(kRowThreads, 2) sample_cut_kernel(const __grid_constant__ StreamArgs p,
+                                                                   int again) {
   using R = Row<kFp32, false>;
-  using B = Block<kStreamThreads>;
+  using B = Block<kRowThreads>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   B b;
   b.s = reinterpret_cast<SampleSmem*>(smem_raw);
@@ -1686,27 +1782,70 @@ __global__ void __launch_bounds__(kStreamThreads) sample_cut_kernel(const __grid
   const int row = blockIdx.x, tid = threadIdx.x;
   stream_begin();
   RowState st = p.state[row];
-  if (kept ? st.status != kWeighKept : st.status != kWeigh && st.status != kWeighBins) return;
+  if (again ? st.status != kCutBin : st.status != kWeigh && st.status != kWeighBins) return;
   bool bad;
   Filter f = settings_of(p.a, row, &bad);
   f.m = st.m;
   R r;
   const int vectors = r.begin(p.a, row);
+  float cut = -INFINITY;                           // kept: z > cut, or z = cut and id <= cut_id
+  int cut_id = -1;
+  if (st.status == kCutBin) {
+    const int n = st.listed;
+    const uint64_t* list = p.list + (int64_t)row * kList;
+    // the part of the bin that the cut falls in, and its elements alone sorted
+    const uint32_t high = key_of(st.hi), range = high - key_of(st.lo);
+    const int shift = range < kBins ? 0 : 32 - __clz((int)(range / kBins));
+    clear_bins(b, true);
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint64_t x = __ldg(list + i);
+      add_to_bin(b, (int)((high - ~(uint32_t)(x >> 32)) >> shift), true, f.weight(entry_logit(x)));
+    }
+    if (tid == 0) {
+      s->cut.bin = -1;
+      s->n_list = 0;
+    }
+    __syncthreads();
+    merge_own(b, true);
+    uint32_t all_n;
+    uint64_t all_mass;
+    const Cut part = scan_cut(b, true, true, 0, st.mass_wanted - st.mass_before, &all_n, &all_mass);
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint64_t x = __ldg(list + i);
+      if ((int)((high - ~(uint32_t)(x >> 32)) >> shift) == part.bin)
+        s->list[atomicAdd(&s->n_list, 1u)] = x;
+    }
+    __syncthreads();
+    cut_in_bin(b, f, (int)part.in, true, 0, st.mass_before + part.mass, st.mass_wanted);
+    const uint64_t last = s->total[2];
+    cut = entry_logit(last);
+    cut_id = (int)(uint32_t)last;
+    // the bin's kept elements join their tiles
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint64_t x = __ldg(list + i);
+      const uint32_t w = f.weight(entry_logit(x));
+      const int t = ((int)(uint32_t)x - r.first_id) / R::kElems / kTile;
+      if (x <= last && w >= f.least && RLK_STORE_OK(row < p.a.N && t < p.tiles, &g_err_sample))
+        atomicAdd(reinterpret_cast<unsigned long long*>(&p.mass[(int64_t)row * p.tiles + t]),
+                  (unsigned long long)w);
+    }
+    __syncthreads();
+  }
   if (st.status != kWeighBins) {
-    draw(b, p, row, f, r, vectors, st.cut, st.cut_id);
+    draw(b, p, row, f, r, vectors, cut, cut_id);
     return;
   }
   const int chunks = p.tiles * 32;
   const uint32_t* tops = p.tops + (int64_t)row * chunks;
   // the row's weight, its histogram, the cut's bin
   uint64_t sum = 0;
-  for (int t = tid; t < p.tiles; t += kStreamThreads) sum += p.mass[(int64_t)row * p.tiles + t];
+  for (int t = tid; t < p.tiles; t += kRowThreads) sum += p.mass[(int64_t)row * p.tiles + t];
   sum = block_sum(b, sum, 0);
   if (tid == 0) {
     s->total[2] = sum;
     s->cut.bin = -1;
   }
-  for (int i = tid; i < kBins; i += kStreamThreads) {
+  for (int i = tid; i < kBins; i += kRowThreads) {
     s->slice_count[i] = p.bin_count[(int64_t)row * kBins + i];
     s->slice_mass[i] = p.bin_mass[(int64_t)row * kBins + i];
   }
@@ -1714,25 +1853,23 @@ __global__ void __launch_bounds__(kStreamThreads) sample_cut_kernel(const __grid
   const uint64_t total = s->total[2], want = f.share(total);
   uint32_t all_n;
   uint64_t all_mass;
-  const Cut cut = scan_cut(b, true, true, 0, want, &all_n, &all_mass);
+  const Cut found = scan_cut(b, true, true, 0, want, &all_n, &all_mass);
   const Window window(0.f, kNear);
-  st.status = kGeneral;
-  if (cut.bin >= 0 && cut.before + cut.in <= kList) {
-    const float lo = least_logit(f.m, f.c, window, cut.bin);
+  st.status = kLeft;
+  if (found.bin >= 0 && found.before + found.in <= kRowThreads) {
+    const float lo = least_logit(f.m, f.c, window, found.bin);
     const int n = list_chunks(b, r, vectors, tops, chunks, lo, INFINITY, ids);
     finish(b, f, p.a, row, n, total);
     st.status = kDone;
-  } else if (cut.bin >= 0 && cut.in <= kList) {
-    const float lo = least_logit(f.m, f.c, window, cut.bin);
-    float hi = f.m;
-    if (cut.bin > 0) hi = logit_of(key_of(least_logit(f.m, f.c, window, cut.bin - 1)) - 1);
-    const int n = list_chunks(b, r, vectors, tops, chunks, lo, hi, ids);
-    cut_in_bin(b, f, n, true, 0, cut.mass, want);
-    st.cut = entry_logit(s->total[2]);
-    st.cut_id = (int)(uint32_t)s->total[2];
-    st.status = kWeighKept;
+  } else if (found.bin >= 0 && found.in <= kList) {
+    st.lo = least_logit(f.m, f.c, window, found.bin);
+    st.hi = f.m;
+    if (found.bin > 0) st.hi = logit_of(key_of(least_logit(f.m, f.c, window, found.bin - 1)) - 1);
+    st.mass_before = found.mass;
+    st.mass_wanted = want;
+    st.status = kCutBin;
   }
-  if (tid == 0 && RLK_STORE_OK(row < p.a.N, &g_err_sample)) p.state[row] = st;
+  if (tid == 0) put_state(p, row, st);
 }
 
 std::mutex g_attr_mutex;
@@ -1771,20 +1908,22 @@ struct SamplePlan {
   int ctas;
   bool on_chip;
   int tiles;
-  size_t off_mass, off_count, off_bins, off_state, total;   // the streaming kernels' workspace
+  size_t off_mass, off_count, off_bins, off_state, off_left, off_list, total;   // their workspace
 };
 
 SamplePlan sample_plan(int64_t N, int64_t V, bool fp32, int sms) {
   SamplePlan p = {};
   const int esize = fp32 ? 4 : 2, elems = 16 / esize;
-  p.stream = V >= 16384 && N * V * esize >= kStreamBytes;
+  p.stream = V >= kStreamVocab && N * V * esize >= kStreamBytes;
   if (p.stream) {
     p.tiles = (int)ceil_div(ceil_div(V + elems - 1, elems), kTile);
     p.off_mass = align_up((size_t)N * p.tiles * 32 * sizeof(uint32_t), 256);
     p.off_count = align_up(p.off_mass + (size_t)N * p.tiles * sizeof(uint64_t), 256);
     p.off_bins = align_up(p.off_count + (size_t)N * kBins * sizeof(uint32_t), 256);
     p.off_state = align_up(p.off_bins + (size_t)N * kBins * sizeof(uint64_t), 256);
-    p.total = align_up(p.off_state + (size_t)N * sizeof(RowState), 256);
+    p.off_left = align_up(p.off_state + (size_t)N * sizeof(RowState), 256);
+    p.off_list = align_up(p.off_left + (size_t)(N + 1) * sizeof(int), 256);
+    p.total = align_up(p.off_list + (size_t)N * kList * sizeof(uint64_t), 256);
     p.ctas = 1;
     while (p.ctas < kMaxCluster && ceil_div(V, p.ctas) > 60000) p.ctas *= 2;
     return p;
@@ -1797,15 +1936,17 @@ SamplePlan sample_plan(int64_t N, int64_t V, bool fp32, int sms) {
   return p;
 }
 
-// The clusters' kernel over all rows, or (state) those left to it.
-cudaError_t launch_clusters(SampleArgs a, bool fp32, const SamplePlan& plan, const RowState* state,
-                            cudaStream_t stream) {
+// The clusters' kernel over all rows, or (left) the rows of that list.
+cudaError_t launch_clusters(SampleArgs a, bool fp32, const SamplePlan& plan, const int* left,
+                            int sms, cudaStream_t stream) {
   const int elems = fp32 ? 4 : 8;
-  a.state = state;
+  a.left = left;
+  int64_t clusters = a.N;
+  if (left && clusters * plan.ctas > 4 * sms) clusters = 4 * sms / plan.ctas;
   // vectors of a row that starts anywhere in its first vector, dealt evenly
   const int per = (int)ceil_div(ceil_div((int64_t)a.V + elems - 1, elems), plan.ctas);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.N * plan.ctas));
+  cfg.gridDim = dim3((unsigned)(clusters * plan.ctas));
   cfg.blockDim = dim3(plan.on_chip ? 512 : 256);
   cfg.dynamicSmemBytes = sizeof(SampleSmem) + (plan.on_chip ? (size_t)per * 16 : 0);
   cfg.stream = stream;
@@ -1825,7 +1966,7 @@ cudaError_t launch_clusters(SampleArgs a, bool fp32, const SamplePlan& plan, con
 }
 
 template <bool kFp32>
-cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* ws,
+cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* ws, int sms,
                           cudaStream_t stream) {
   StreamArgs p;
   p.a = a;
@@ -1835,25 +1976,28 @@ cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* 
   p.bin_count = reinterpret_cast<uint32_t*>(ws + plan.off_count);
   p.bin_mass = reinterpret_cast<uint64_t*>(ws + plan.off_bins);
   p.state = reinterpret_cast<RowState*>(ws + plan.off_state);
+  p.left = reinterpret_cast<int*>(ws + plan.off_left);
+  p.list = reinterpret_cast<uint64_t*>(ws + plan.off_list);
   const int top_ctas = (int)ceil_div(plan.tiles, kStreamThreads / 32);
   const int weigh_ctas = (int)ceil_div(plan.tiles, kTilesPerCta);
-  const size_t smem = sizeof(SampleSmem) + align_up((size_t)plan.tiles * 32 * sizeof(uint16_t), 16);
+  const size_t smem_ids = sizeof(SampleSmem) + (size_t)plan.tiles * 32 * sizeof(uint16_t);
+  const size_t smem_pick = smem_ids + (size_t)plan.tiles * 32 * sizeof(uint32_t);
   const dim3 rows((unsigned)a.N), tops((unsigned)(a.N * top_ctas)), weighs((unsigned)(a.N * weigh_ctas));
   cudaError_t e;
   if ((e = launch_overlapped(sample_tops_kernel<kFp32>, tops, kStreamThreads, 0, stream, p,
                              top_ctas)) != cudaSuccess ||
-      (e = launch_overlapped(sample_pick_kernel<kFp32>, rows, kStreamThreads, smem, stream, p)) !=
+      (e = launch_overlapped(sample_pick_kernel<kFp32>, rows, kRowThreads, smem_pick, stream, p)) !=
           cudaSuccess ||
       (e = launch_overlapped(sample_weigh_kernel<kFp32, false>, weighs, kStreamThreads, 0, stream, p,
                              weigh_ctas)) != cudaSuccess ||
-      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kStreamThreads, smem, stream, p, 0)) !=
+      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kRowThreads, smem_ids, stream, p, 0)) !=
           cudaSuccess ||
       (e = launch_overlapped(sample_weigh_kernel<kFp32, true>, weighs, kStreamThreads, 0, stream, p,
                              weigh_ctas)) != cudaSuccess ||
-      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kStreamThreads, smem, stream, p, 1)) !=
+      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kRowThreads, smem_ids, stream, p, 1)) !=
           cudaSuccess)
     return e;
-  return launch_clusters(a, kFp32, plan, p.state, stream);
+  return launch_clusters(a, kFp32, plan, p.left, sms, stream);
 }
 
 }  // namespace
@@ -1934,13 +2078,13 @@ rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64_t N, in
   a.fp32 = fp32;
   a.token = token;
   a.logp = logp;
-  a.state = nullptr;
+  a.left = nullptr;
   const SamplePlan plan = sample_plan(N, V, fp32, dev.sm_count);
   cudaStream_t q = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const cudaError_t e = !plan.stream ? launch_clusters(a, fp32, plan, nullptr, q)
-                        : fp32       ? launch_stream<true>(a, plan, ws, q)
-                                     : launch_stream<false>(a, plan, ws, q);
+  const cudaError_t e = !plan.stream ? launch_clusters(a, fp32, plan, nullptr, dev.sm_count, q)
+                        : fp32       ? launch_stream<true>(a, plan, ws, dev.sm_count, q)
+                                     : launch_stream<false>(a, plan, ws, dev.sm_count, q);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return RLK_ERR_CUDA;

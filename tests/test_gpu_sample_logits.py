@@ -61,7 +61,8 @@ def test_tokens(N, V, dtype, how):
     check(dev, logits(N, V, N * V).to(dtype), uniforms(N, V), **how)
 
 
-@pytest.mark.parametrize("N,V,dtype", [(1, 151936, torch.float32), (20, 152064, torch.bfloat16),
+@pytest.mark.parametrize("N,V,dtype", [(1, 151936, torch.float32), (5, 152064, torch.float32),
+                                       (9, 100003, torch.bfloat16), (20, 152064, torch.bfloat16),
                                        (40, 151936, torch.float32), (2, 524288, torch.float32),
                                        (30, 70001, torch.float32), (160, 20011, torch.bfloat16),
                                        (48, 151936, torch.float32), (90, 152064, torch.bfloat16)])
@@ -100,8 +101,8 @@ def kinds(N, V, seed):
     return z
 
 
-@pytest.mark.parametrize("N,V,dtype,shift", [(340, 20011, torch.float32, 0), (800, 16384, torch.bfloat16, 0),
-                                             (170, 40007, torch.float32, 3), (330, 40009, torch.bfloat16, 5)])
+@pytest.mark.parametrize("N,V,dtype,shift", [(120, 20011, torch.float32, 0), (160, 16384, torch.bfloat16, 0),
+                                             (60, 40007, torch.float32, 3), (110, 40009, torch.bfloat16, 5)])
 def test_many_rows(N, V, dtype, shift):
     """Calls large enough for the streaming kernels: rows of every sort, settings of every sort, and
     each row's token and bits those of a call of its own."""
@@ -274,7 +275,7 @@ def test_rows_do_not_depend_on_the_call():
 
 def test_many_rows_on_a_stream_and_in_a_graph():
     dev = cuda_or_skip()
-    z, u = kinds(400, 20000, 24).to(dev), uniforms(400, 25).to(dev)
+    z, u = kinds(120, 20000, 24).to(dev), uniforms(120, 25).to(dev)
     for how in (dict(top_p=0.9), dict(top_k=60, top_p=0.9), dict(top_k=2000)):
         token, logp = rlk.sample_logits(z, u, **how)
         for _ in range(3):
