@@ -296,9 +296,12 @@ __device__ __forceinline__ void scheduler_role(const Sched& sc, const PipeSmem& 
 }
 
 // Release slot `slot` after reading it (one arrival per consumer).  The arrival
-// carries no data, and the consumer has already used the value it read, so it
-// is relaxed: a release-ordered arrival from a thread with copies in flight
-// would stall that thread until they land.
+// carries no data and is relaxed: a release-ordered arrival from a thread with
+// copies in flight would stall that thread until they land.  So nothing but the
+// caller orders it after the read of the slot: it must be made to depend on the
+// value read.  (Issued before the value came back, behind an epilogue's global
+// stores, the arrival let the scheduler refill the slot first: the warp took the
+// later unit and left the partials of its own unwritten.)
 __device__ __forceinline__ void unit_release(const PipeSmem& ps, int slot) {
   if (ps.rank == 0)
     asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(ps.unit_empty(slot))
@@ -325,7 +328,7 @@ __device__ __forceinline__ int unit_take(const Sched& sc, const PipeSmem& ps, in
   const uint32_t parity = (uint32_t)((k - 1) / kUnitSlots) & 1u;
   if (!mbar_wait_cluster(ps.unit_full(slot), parity, ps.abort_flag(), err)) return kUnitAbort;
   const int u = *reinterpret_cast<volatile int*>(&ps.bars->unit_id[slot]);
-  unit_release(ps, slot);
+  if (u >= kUnitAbort) unit_release(ps, slot);   // always so: waits for the value
   return u;
 }
 
@@ -339,8 +342,8 @@ __device__ __forceinline__ int warp_unit_take(const Sched& sc, const PipeSmem& p
   const bool ok = mbar_wait_cluster(ps.unit_full(slot), parity, ps.abort_flag(), err);
   if (!__all_sync(0xffffffffu, ok)) return kUnitAbort;
   const int u = *reinterpret_cast<volatile int*>(&ps.bars->unit_id[slot]);
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) unit_release(ps, slot);
+  // always so: waits for the value in every lane
+  if (__all_sync(0xffffffffu, u >= kUnitAbort) && (threadIdx.x & 31) == 0) unit_release(ps, slot);
   return u;
 }
 
