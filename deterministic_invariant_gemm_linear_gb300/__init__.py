@@ -22,6 +22,7 @@ Operators (web pages of the RL-Kernel project):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -98,12 +99,12 @@ SIGNATURES = {
                                _P, _F, _P, _P, _P, _SZ, _P]),
     "rlk_linear_distill_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64]),
     "rlk_linear_distill": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I, _I64,
-                                _I64, _P, _F, _P, _P, _P, _SZ, _P]),
+                                _I64, _P, _F, _P, _P, _P, _I64, _P, _SZ, _P]),
     "rlk_linear_distill_backward_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64,
                                                          _I]),
     "rlk_linear_distill_backward": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I,
-                                         _I64, _I64, _P, _F, _P, _P, _P, _I, _I64, _P, _I, _I64,
-                                         _P, _P, _SZ, _P]),
+                                         _I64, _I64, _P, _F, _P, _P, _I64, _P, _P, _I, _I64, _P, _I,
+                                         _I64, _P, _P, _SZ, _P]),
     "rlk_det_gemm_workspace_size": (_SZ, [_I, _P, _I, _I64, _I64, _I64, _P, _I, _I64, _I64, _I64]),
     "rlk_det_gemm_fwd": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]),
     "rlk_det_gemm_da": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]),
@@ -189,14 +190,25 @@ def debug_trace(max_ctas: int = TRACE_MAX_CTAS):
     return out[:n.value]
 
 
+# A small call's time is its host side: addresses pass as plain integers, the current stream
+# and device are asked for without building their Python objects (0.1 us for 2.9, and 0.3 for
+# 1.5 where the device is current already, on the Grace host).
 def _stream_ptr(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device made current for a with block."""
+    return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -282,7 +294,7 @@ def linear_logp(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor
     logp = torch.empty(N, dtype=torch.float32, device=dev)
     lse = torch.empty(N, dtype=torch.float32, device=dev)
     zt = torch.empty(N, dtype=torch.float32, device=dev) if return_target_logit else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         if num_splits is None:
             ws = linear_logp_workspace(h2, w2, ldh, ldw, N, H, V)
             st = lib().rlk_linear_logp(_ptr(h2), N, H, ldh, _ptr(w2), V, ldw, _ptr(bias), _ptr(t1),
@@ -324,7 +336,7 @@ class LinearLogpCall:
         self.logp = torch.empty(self.N, dtype=torch.float32, device=dev)
         self.lse = torch.empty(self.N, dtype=torch.float32, device=dev)
         self.zt = torch.empty(self.N, dtype=torch.float32, device=dev) if target_logit else None
-        with torch.cuda.device(dev):
+        with _on(dev):
             if num_splits is None:
                 self.ws = linear_logp_workspace(self.h, self.w, self.ldh, self.ldw, self.N, self.H,
                                                 self.V)
@@ -403,7 +415,7 @@ def linear_logp_shard_partials(hidden: torch.Tensor, weight_shard: torch.Tensor,
     dev = hidden.device
     partials = torch.empty(N, ld, 2, dtype=torch.float32, device=dev)
     zt = torch.full((N,), float("nan"), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         nb = lib().rlk_linear_logp_shard_workspace_size(_ptr(h2), N, H, ldh, _ptr(w2), V,
                                                         split_begin, split_end, ldw)
         if nb == 0:
@@ -443,7 +455,7 @@ def linear_logp_combine_shards(partials: torch.Tensor, target_logits: torch.Tens
     logp = torch.empty(N, dtype=torch.float32, device=dev)
     lse = torch.empty(N, dtype=torch.float32, device=dev)
     zt = torch.empty(N, dtype=torch.float32, device=dev) if return_target_logit else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().rlk_linear_logp_combine_shards(
             N, V, _ptr(t1), tstride, R, offs, _ptr(partials), ld, N * ld, _ptr(target_logits), N,
             _ptr(logp), _ptr(lse), _ptr(zt), _stream_ptr(stream)), "rlk_linear_logp_combine_shards")
@@ -484,7 +496,7 @@ def sum_partials_ordered(parts: torch.Tensor, out_dtype=torch.float32, *, stream
     parts = parts.contiguous()
     P, rows, cols = parts.shape
     out = torch.empty(rows, cols, dtype=out_dtype, device=parts.device)
-    with torch.cuda.device(parts.device):
+    with _on(parts.device):
         _check(lib().rlk_sum_partials_ordered(_ptr(parts), P, rows, cols, cols, rows * cols,
                                               _ptr(out), _DT[out_dtype], cols, _stream_ptr(stream)),
                "rlk_sum_partials_ordered")
@@ -560,7 +572,7 @@ def linear_logp_backward(hidden: torch.Tensor, weight: torch.Tensor, target: tor
     gh = torch.empty(N, H, dtype=out_dtype, device=dev) if grad_hidden else None
     gw = torch.empty(V, H, dtype=out_dtype, device=dev) if grad_weight else None
     gb = torch.empty(V, dtype=torch.float32, device=dev) if grad_bias else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         n = lib().rlk_linear_logp_backward_workspace_size_for(_ptr(h2), N, H, ldh, _ptr(w2), V, ldw)
         if n == 0:
             raise RlkError(2, "rlk_linear_logp_backward_workspace_size_for")
@@ -661,7 +673,7 @@ def sample_logits(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.
     logp = torch.empty(N, dtype=torch.float32, device=dev)
     nb = lib().rlk_sample_logits_workspace_size(_DT[z.dtype], N, V)
     ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().rlk_sample_logits(
             _ptr(z), _DT[z.dtype], N, V, ld, _ptr(u),
             RLK_FP32 if u.dtype == torch.float32 else RLK_FP64, _ptr(tau), tau_all, _ptr(k), k_all,
@@ -671,42 +683,105 @@ def sample_logits(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.
 
 
 # ------------------------------------------------------------------ distillation
-def _distill_inputs(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse):
-    """Checked operands of the distillation calls: (hidden, weight, ids, logits as (tensor, ld)
-    pairs, bias, teacher_lse)."""
-    _require_cuda(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
-    if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
-        raise TypeError("hidden and weight must be bfloat16")
-    if teacher_ids.dtype != torch.int64:
-        raise TypeError("teacher_ids must be int64")
-    if teacher_logits.dtype not in _DT:
-        raise TypeError("teacher_logits must be bfloat16 or float32")
-    if bias is not None and (bias.dtype != torch.float32 or bias.dim() != 1):
-        raise TypeError("bias must be a 1-D float32 tensor")
-    lead, H = hidden.shape[:-1], hidden.size(-1)
-    if teacher_ids.shape != teacher_logits.shape or teacher_ids.shape[:-1] != lead:
-        raise ValueError("teacher_ids and teacher_logits must be [..., K] with hidden's leading shape")
-    K, N = teacher_ids.size(-1), hidden.numel() // H if H else 0
-    h = _matrix(hidden.reshape(-1, H), "hidden")
-    w = _matrix(weight, "weight")
-    if w[0].size(1) != H:
-        raise ValueError("weight must be [V, H] with the hidden size H")
-    ids = _matrix(teacher_ids.reshape(N, K), "teacher_ids")
-    logits = _matrix(teacher_logits.reshape(N, K), "teacher_logits")
-    if bias is not None:
-        bias = bias.contiguous()
-        if bias.numel() != w[0].size(0):
-            raise ValueError("bias must have V entries")
-    if teacher_lse is not None:
-        if teacher_lse.dtype != torch.float32 or teacher_lse.shape != lead:
-            raise ValueError("teacher_lse must be float32 with hidden's leading shape")
-        teacher_lse = teacher_lse.reshape(-1).contiguous()
-    return h, w, ids, logits, bias, teacher_lse
+class _Distill:
+    """A distillation call's checked operands: tensors with unit column stride, their leading
+    dimensions, sizes and the teacher's settings."""
+
+    __slots__ = ("lead", "h", "ldh", "w", "ldw", "ids", "ldi", "tl", "ldt", "tdt", "bias", "tlse",
+                 "N", "H", "V", "K", "T")
+
+    def __init__(self, hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse, temperature):
+        _require_cuda(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
+        if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+            raise TypeError("hidden and weight must be bfloat16")
+        if teacher_ids.dtype != torch.int64:
+            raise TypeError("teacher_ids must be int64")
+        if teacher_logits.dtype not in _DT:
+            raise TypeError("teacher_logits must be bfloat16 or float32")
+        shape = hidden.shape
+        self.lead = shape[:-1]
+        if teacher_ids.shape != teacher_logits.shape or teacher_ids.shape[:-1] != self.lead:
+            raise ValueError(
+                "teacher_ids and teacher_logits must be [..., K] with hidden's leading shape")
+        self.H, self.K = shape[-1], teacher_ids.shape[-1]
+        if len(shape) != 2:
+            self.N = hidden.numel() // self.H if self.H else 0
+            hidden = hidden.reshape(self.N, self.H)
+            teacher_ids = teacher_ids.reshape(self.N, self.K)
+            teacher_logits = teacher_logits.reshape(self.N, self.K)
+        else:
+            self.N = shape[0]
+        self.h, self.ldh = _matrix(hidden, "hidden")
+        self.w, self.ldw = _matrix(weight, "weight")
+        self.V = weight.shape[0]
+        if weight.shape[1] != self.H:
+            raise ValueError("weight must be [V, H] with the hidden size H")
+        self.ids, self.ldi = _matrix(teacher_ids, "teacher_ids")
+        self.tl, self.ldt = _matrix(teacher_logits, "teacher_logits")
+        self.tdt = _DT[teacher_logits.dtype]
+        if bias is not None:
+            if bias.dtype != torch.float32 or bias.dim() != 1:
+                raise TypeError("bias must be a 1-D float32 tensor")
+            if bias.numel() != self.V:
+                raise ValueError("bias must have V entries")
+            bias = bias.contiguous()
+        self.bias = bias
+        if teacher_lse is not None:
+            if teacher_lse.dtype != torch.float32 or teacher_lse.shape != self.lead:
+                raise ValueError("teacher_lse must be float32 with hidden's leading shape")
+            teacher_lse = teacher_lse.reshape(-1).contiguous()
+        self.tlse, self.T = teacher_lse, temperature
+
+    def forward(self, keep_logits: bool, stream=None):
+        """loss [N], lse [N], logits [N, 4 ceil(V / 4)] or None."""
+        h, w, dev = self.h, self.w, self.h.device
+        N, H, V, K = self.N, self.H, self.V, self.K
+        loss = torch.empty(N, dtype=torch.float32, device=dev)
+        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        ldz = -(-V // 4) * 4
+        logits = torch.empty((N, ldz), dtype=torch.float32, device=dev) if keep_logits else None
+        lib_ = lib()
+        with _on(dev):
+            n = lib_.rlk_linear_distill_workspace_size(_ptr(h), N, H, self.ldh, _ptr(w), V, self.ldw,
+                                                       K)
+            if n == 0:
+                raise RlkError(2, "rlk_linear_distill_workspace_size")
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            _check(lib_.rlk_linear_distill(
+                _ptr(h), N, H, self.ldh, _ptr(w), V, self.ldw, _ptr(self.bias), _ptr(self.ids),
+                self.ldi, _ptr(self.tl), self.tdt, self.ldt, K, _ptr(self.tlse), self.T, _ptr(loss),
+                _ptr(lse), _ptr(logits), ldz, _ptr(ws), n, _stream_ptr(stream)),
+                "rlk_linear_distill")
+        return loss, lse, logits
+
+    def backward(self, lse, grad_loss, logits, want, out_dtype, stream=None):
+        """grad_hidden [N, H], grad_weight, grad_bias (those of `want`, else None), workspace."""
+        h, w, dev = self.h, self.w, self.h.device
+        N, H, V, K = self.N, self.H, self.V, self.K
+        gh = torch.empty((N, H), dtype=out_dtype, device=dev) if want[0] else None
+        gw = torch.empty((V, H), dtype=out_dtype, device=dev) if want[1] else None
+        gb = torch.empty(V, dtype=torch.float32, device=dev) if want[2] else None
+        ldz = 0 if logits is None else logits.stride(0) if N > 1 else -(-V // 4) * 4
+        dt = _DT[out_dtype]
+        lib_ = lib()
+        with _on(dev):
+            n = lib_.rlk_linear_distill_backward_workspace_size(_ptr(h), N, H, self.ldh, _ptr(w), V,
+                                                                self.ldw, K, int(want[2]))
+            if n == 0:
+                raise RlkError(2, "rlk_linear_distill_backward_workspace_size")
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            _check(lib_.rlk_linear_distill_backward(
+                _ptr(h), N, H, self.ldh, _ptr(w), V, self.ldw, _ptr(self.bias), _ptr(self.ids),
+                self.ldi, _ptr(self.tl), self.tdt, self.ldt, K, _ptr(self.tlse), self.T, _ptr(lse),
+                _ptr(logits), ldz, _ptr(grad_loss), _ptr(gh), dt, H, _ptr(gw), dt, H, _ptr(gb),
+                _ptr(ws), n, _stream_ptr(stream)), "rlk_linear_distill_backward")
+        return gh, gw, gb, ws
 
 
 def linear_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
                    teacher_logits: torch.Tensor, bias: torch.Tensor | None = None, *,
-                   temperature: float = 1.0, teacher_lse: torch.Tensor | None = None, stream=None):
+                   temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                   return_logits: bool = False, stream=None):
     """loss, lse (FP32, shaped like hidden's leading dims): T^2 KL(teacher || student) over the
     teacher's top logits, and the student's log-sum-exp at temperature T.
 
@@ -714,73 +789,56 @@ def linear_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torc
     with the teacher's logits there, teacher_logits [..., K] bf16 or fp32.  A slot whose id is
     outside [0, V) (pad with -1) or whose logit is -inf is empty; a row without used slots has
     loss 0.  The teacher's probabilities are normalised over its slots, or by teacher_lse [...]
-    fp32 (its log-sum-exp over its whole vocabulary at this temperature).  Forward only: use
+    fp32 (its log-sum-exp over its whole vocabulary at this temperature).  With return_logits
+    also the student's logits z [N, V] fp32 (bias included, not divided by T), which
+    linear_distill_backward can take in place of forming them again.  Forward only: use
     linear_distill_trainable for gradients.
     """
     if hidden.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad):
         raise RuntimeError("linear_distill is forward-only: inputs that require grad are rejected")
-    (h, ldh), (w, ldw), (ids, ldi), (tl, ldt), bias, tlse = _distill_inputs(
-        hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
-    N, H, V, K = h.size(0), h.size(1), w.size(0), ids.size(1)
-    dev = hidden.device
-    loss = torch.empty(N, dtype=torch.float32, device=dev)
-    lse = torch.empty(N, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        n = lib().rlk_linear_distill_workspace_size(_ptr(h), N, H, ldh, _ptr(w), V, ldw, K)
-        if n == 0:
-            raise RlkError(2, "rlk_linear_distill_workspace_size")
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        _check(lib().rlk_linear_distill(
-            _ptr(h), N, H, ldh, _ptr(w), V, ldw, _ptr(bias), _ptr(ids), ldi, _ptr(tl),
-            _DT[tl.dtype], ldt, K, _ptr(tlse), temperature, _ptr(loss), _ptr(lse), _ptr(ws), n,
-            _stream_ptr(stream)), "rlk_linear_distill")
-    lead = hidden.shape[:-1]
-    return loss.reshape(lead), lse.reshape(lead)
+    d = _Distill(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse, temperature)
+    loss, lse, logits = d.forward(return_logits, stream)
+    if len(d.lead) != 1:
+        loss, lse = loss.reshape(d.lead), lse.reshape(d.lead)
+    return (loss, lse, logits[:, :d.V]) if return_logits else (loss, lse)
 
 
 def linear_distill_backward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
                             teacher_logits: torch.Tensor, lse: torch.Tensor,
                             grad_loss: torch.Tensor, bias: torch.Tensor | None = None, *,
                             temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
-                            grad_hidden: bool = True, grad_weight: bool = True,
-                            grad_bias: bool | None = None, out_dtype=torch.bfloat16,
-                            return_grad_logits: bool = False, stream=None):
+                            logits: torch.Tensor | None = None, grad_hidden: bool = True,
+                            grad_weight: bool = True, grad_bias: bool | None = None,
+                            out_dtype=torch.bfloat16, return_grad_logits: bool = False, stream=None):
     """(grad_hidden [..., H], grad_weight [V, H], grad_bias [V] | None) of linear_distill's loss.
 
-    lse is the forward's lse; grad_loss is dL/dloss (one value a row).  With
+    lse is the forward's lse; grad_loss is dL/dloss (one value a row); logits are those of
+    linear_distill(..., return_logits=True), or None to form them again (the same bits).  With
     return_grad_logits, also returns G = dL/dz as the BF16 [N, V] view the products read.
     """
-    (h, ldh), (w, ldw), (ids, ldi), (tl, ldt), bias, tlse = _distill_inputs(
-        hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
-    N, H, V, K = h.size(0), h.size(1), w.size(0), ids.size(1)
-    _require_cuda(lse, grad_loss)
+    d = _Distill(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse, temperature)
+    _require_cuda(lse, grad_loss, logits)
     l1 = lse.reshape(-1).contiguous().float()
     g1 = grad_loss.reshape(-1).contiguous().float()
-    if l1.numel() != N or g1.numel() != N:
+    if l1.numel() != d.N or g1.numel() != d.N:
         raise ValueError("lse and grad_loss must have one value per hidden row")
+    if logits is not None and (logits.dtype != torch.float32 or tuple(logits.shape) != (d.N, d.V) or
+                               (d.V > 1 and logits.stride(1) != 1)):
+        raise ValueError("logits must be those of linear_distill(..., return_logits=True)")
     if grad_bias is None:
         grad_bias = bias is not None
-    dev = hidden.device
-    gh = torch.empty(N, H, dtype=out_dtype, device=dev) if grad_hidden else None
-    gw = torch.empty(V, H, dtype=out_dtype, device=dev) if grad_weight else None
-    gb = torch.empty(V, dtype=torch.float32, device=dev) if grad_bias else None
-    with torch.cuda.device(dev):
-        n = lib().rlk_linear_distill_backward_workspace_size(_ptr(h), N, H, ldh, _ptr(w), V, ldw, K,
-                                                             int(grad_bias))
-        if n == 0:
-            raise RlkError(2, "rlk_linear_distill_backward_workspace_size")
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        dt = _DT[out_dtype]
-        _check(lib().rlk_linear_distill_backward(
-            _ptr(h), N, H, ldh, _ptr(w), V, ldw, _ptr(bias), _ptr(ids), ldi, _ptr(tl),
-            _DT[tl.dtype], ldt, K, _ptr(tlse), temperature, _ptr(l1), _ptr(g1), _ptr(gh), dt, H,
-            _ptr(gw), dt, H, _ptr(gb), _ptr(ws), n, _stream_ptr(stream)),
-            "rlk_linear_distill_backward")
-    out = (None if gh is None else gh.reshape(*hidden.shape[:-1], H), gw, gb)
+    gh, gw, gb, ws = d.backward(l1, g1, logits, (grad_hidden, grad_weight, grad_bias), out_dtype,
+                                stream)
+    out = (None if gh is None else gh.reshape(*d.lead, d.H), gw, gb)
     if return_grad_logits:
-        ldG = -(-V // 8) * 8
-        out = out + (ws[:N * ldG * 2].view(torch.bfloat16).view(N, ldG)[:, :V],)
+        ldG = -(-d.V // 8) * 8
+        out = out + (ws[:d.N * ldG * 2].view(torch.bfloat16).view(d.N, ldG)[:, :d.V],)
     return out
+
+
+# Most bytes of FP32 logits that linear_distill_trainable keeps from the forward for the
+# backward.  Kept, the backward reads 4 bytes a logit where it would spend 2 H operations.
+KEEP_LOGITS_BYTES = 8 << 30
 
 
 class _LinearDistillGrad(torch.autograd.Function):
@@ -788,36 +846,48 @@ class _LinearDistillGrad(torch.autograd.Function):
     as a constant and the teacher's tensors carry no gradient."""
 
     @staticmethod
-    def forward(ctx, hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, temperature):
-        loss, lse = linear_distill(hidden.detach(), weight.detach(), teacher_ids, teacher_logits,
-                                   None if bias is None else bias.detach(),
-                                   temperature=temperature, teacher_lse=teacher_lse)
+    def forward(ctx, hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, temperature,
+                keep_logits):
+        d = _Distill(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse, temperature)
+        if keep_logits is None:
+            keep_logits = 4 * d.N * d.V <= KEEP_LOGITS_BYTES
+        loss, lse, ctx.logits = d.forward(keep_logits)
         ctx.save_for_backward(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, lse)
-        ctx.temperature = temperature
+        ctx.call, ctx.shape = d, hidden.shape
         ctx.mark_non_differentiable(lse)
+        if len(d.lead) != 1:
+            loss, lse = loss.reshape(d.lead), lse.reshape(d.lead)
+            ctx.mark_non_differentiable(lse)
         return loss, lse
 
     @staticmethod
     def backward(ctx, grad_loss, _grad_lse):
-        hidden, weight, bias, ids, logits, teacher_lse, lse = ctx.saved_tensors
+        lse = ctx.saved_tensors[-1]      # raises if an input was changed in place
         want_h, want_w, want_b = ctx.needs_input_grad[:3]
-        want_b = bool(want_b and bias is not None)
         if grad_loss is None or not (want_h or want_w or want_b):
-            return (None,) * 7
-        gh, gw, gb = linear_distill_backward(hidden, weight, ids, logits, lse, grad_loss, bias,
-                                             temperature=ctx.temperature, teacher_lse=teacher_lse,
-                                             grad_hidden=want_h, grad_weight=want_w,
-                                             grad_bias=want_b)
-        return gh, gw, gb, None, None, None, None
+            return (None,) * 8
+        if grad_loss.dim() != 1 or not grad_loss.is_contiguous():
+            grad_loss = grad_loss.reshape(-1).contiguous()
+        gh, gw, gb, _ = ctx.call.backward(lse, grad_loss, ctx.logits, (want_h, want_w, want_b),
+                                          torch.bfloat16)
+        if gh is not None and len(ctx.shape) != 2:
+            gh = gh.reshape(ctx.shape)
+        return gh, gw, gb, None, None, None, None, None
 
 
 def linear_distill_trainable(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
                              teacher_logits: torch.Tensor, bias: torch.Tensor | None = None, *,
-                             temperature: float = 1.0, teacher_lse: torch.Tensor | None = None):
+                             temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                             keep_logits: bool | None = None):
     """loss, lse as linear_distill, differentiable through loss with respect to hidden, weight and
-    bias (BF16 gradients of hidden and weight, FP32 of the bias).  lse carries no gradient."""
+    bias (BF16 gradients of hidden and weight, FP32 of the bias).  lse carries no gradient.
+
+    keep_logits: hold the logits in FP32 (4 N V bytes) from the forward to the backward, which
+    otherwise forms them again; the gradients' bits are the same.  None: up to
+    KEEP_LOGITS_BYTES.
+    """
     return _LinearDistillGrad.apply(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse,
-                                    temperature)
+                                    temperature, keep_logits)
 
 
 # ------------------------------------------------------------------ det_gemm
@@ -842,7 +912,7 @@ def det_gemm_fwd(A: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat16, *, 
         raise ValueError("A and B disagree on K")
     N = B2.size(1)
     C = torch.empty(M, N, dtype=out_dtype, device=A.device)
-    with torch.cuda.device(A.device):
+    with _on(A.device):
         ws, n = _gemm_ws(RLK_GEMM_FWD, A2, RLK_BF16, lda, B2, RLK_BF16, ldb, A.device)
         _check(lib().rlk_det_gemm_fwd(_ptr(A2), M, K, lda, _ptr(B2), N, ldb, _ptr(C), _DT[out_dtype],
                                       N, _ptr(ws), n, _stream_ptr(stream)), "rlk_det_gemm_fwd")
@@ -860,7 +930,7 @@ def det_gemm_da(dC: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat16, *, 
     if B2.size(1) != N:
         raise ValueError("dC and B disagree on N")
     dA = torch.empty(M, K, dtype=out_dtype, device=dC.device)
-    with torch.cuda.device(dC.device):
+    with _on(dC.device):
         ws, n = _gemm_ws(RLK_GEMM_DA, d2, _DT[d2.dtype], lddc, B2, RLK_BF16, ldb, dC.device)
         _check(lib().rlk_det_gemm_da(_ptr(d2), _DT[d2.dtype], M, N, lddc, _ptr(B2), K, ldb, _ptr(dA),
                                      _DT[out_dtype], K, _ptr(ws), n, _stream_ptr(stream)),
@@ -878,7 +948,7 @@ def det_gemm_db(A: torch.Tensor, dC: torch.Tensor, out_dtype=torch.bfloat16, *, 
         raise ValueError("A and dC disagree on M")
     N = d2.size(1)
     dB = torch.empty(K, N, dtype=out_dtype, device=A.device)
-    with torch.cuda.device(A.device):
+    with _on(A.device):
         ws, n = _gemm_ws(RLK_GEMM_DB, A2, RLK_BF16, lda, d2, _DT[d2.dtype], lddc, A.device)
         _check(lib().rlk_det_gemm_db(_ptr(A2), M, K, lda, _ptr(d2), _DT[d2.dtype], N, lddc, _ptr(dB),
                                      _DT[out_dtype], N, _ptr(ws), n, _stream_ptr(stream)),
@@ -901,7 +971,7 @@ def det_gemm_fwd_accum_fp32_(C: torch.Tensor, A: torch.Tensor, B: torch.Tensor, 
     if B2.size(0) != K or tuple(C.shape) != (M, N):
         raise ValueError("shape mismatch")
     ldc = C.stride(0) if M > 1 else N
-    with torch.cuda.device(A.device):
+    with _on(A.device):
         ws, n = _gemm_ws(RLK_GEMM_FWD_ACCUM, A2, RLK_BF16, lda, B2, RLK_BF16, ldb, A.device)
         _check(lib().rlk_det_gemm_fwd_accum_fp32(_ptr(A2), M, K, lda, _ptr(B2), N, ldb, _ptr(C), ldc,
                                                  _ptr(ws), n, _stream_ptr(stream)),
@@ -920,7 +990,7 @@ def det_linear(X: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16, *, st
     if W2.size(1) != K:
         raise ValueError("W must be [N, K]")
     Y = torch.empty(M, N, dtype=out_dtype, device=X.device)
-    with torch.cuda.device(X.device):
+    with _on(X.device):
         ws, n = _gemm_ws(RLK_GEMM_LINEAR_FWD, X2, RLK_BF16, ldx, W2, RLK_BF16, ldw, X.device)
         _check(lib().rlk_det_linear_fwd(_ptr(X2), M, K, ldx, _ptr(W2), N, ldw, _ptr(Y), _DT[out_dtype],
                                         N, _ptr(ws), n, _stream_ptr(stream)), "rlk_det_linear_fwd")
@@ -938,7 +1008,7 @@ def det_linear_dx(dY: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16, *
     if W2.size(0) != N:
         raise ValueError("W must be [N, K]")
     dX = torch.empty(M, K, dtype=out_dtype, device=dY.device)
-    with torch.cuda.device(dY.device):
+    with _on(dY.device):
         ws, n = _gemm_ws(RLK_GEMM_LINEAR_DX, d2, _DT[d2.dtype], lddy, W2, RLK_BF16, ldw, dY.device)
         _check(lib().rlk_det_linear_dx(_ptr(d2), _DT[d2.dtype], M, N, lddy, _ptr(W2), K, ldw, _ptr(dX),
                                        _DT[out_dtype], K, _ptr(ws), n, _stream_ptr(stream)),
@@ -956,7 +1026,7 @@ def det_linear_dw(dY: torch.Tensor, X: torch.Tensor, out_dtype=torch.bfloat16, *
         raise ValueError("dY and X disagree on the row count")
     K = X2.size(1)
     dW = torch.empty(N, K, dtype=out_dtype, device=dY.device)
-    with torch.cuda.device(dY.device):
+    with _on(dY.device):
         ws, n = _gemm_ws(RLK_GEMM_LINEAR_DW, d2, _DT[d2.dtype], lddy, X2, RLK_BF16, ldx, dY.device)
         _check(lib().rlk_det_linear_dw(_ptr(d2), _DT[d2.dtype], M, N, lddy, _ptr(X2), K, ldx, _ptr(dW),
                                        _DT[out_dtype], K, _ptr(ws), n, _stream_ptr(stream)),
@@ -974,7 +1044,7 @@ def _two_grads(fn, size_fn, g, x, w, out_shapes, out_dtype, want, stream):
     outs = [torch.empty(*shp, dtype=out_dtype, device=dev) if want[i] else None
             for i, shp in enumerate(out_shapes(M, N, K))]
     gdt = _DT[g2.dtype]
-    with torch.cuda.device(dev):
+    with _on(dev):
         n = size_fn(_ptr(g2), gdt, M, N, ldg, _ptr(x2), K, ldx, _ptr(w2), ldw)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
         dt = _DT[out_dtype]

@@ -26,6 +26,8 @@
 //  * distill_grad_kernel: the same loop again; the epilogue forms G in FP32, takes the
 //    32-row column sums for grad_bias from it, and stores it rounded to BF16, the type
 //    in which the two products (det_gemm) read it.
+//  * distill_grad_logits_kernel: the same G, bit for bit, from logits that the forward kept
+//    (4 N V bytes): one pass at memory speed in place of the product's 2 N H V operations.
 #include <limits.h>
 #include <math.h>
 
@@ -214,6 +216,8 @@ struct DistillArgs {
   float2* ws_ms;              // [N][S]: (m, s)
   float* ws_d;                // [N][S]: sum of q z over the split's slots
   int S;
+  float* logits;              // [N][ld_logits] z in FP32, or null; 16-byte aligned rows
+  int64_t ld_logits;
 };
 
 // Epilogue warps (2..5) of both loops; the (m, s) arithmetic is the fused linear-logp's.
@@ -257,6 +261,14 @@ __device__ __forceinline__ void distill_epilogue(const VocabSched& sc, const Dis
         tmem_wait_ld();
         float z[32];
         chunk_logits(r, vbase, a.V, has_bias, bias, c, z);
+        if (a.logits && valid) {
+          float4* dst = reinterpret_cast<float4*>(a.logits + (int64_t)row * a.ld_logits + vbase);
+#pragma unroll
+          for (int g = 0; g < 8; ++g)   // groups past V stay within ld_logits
+            if (vbase + 4 * g < a.V &&
+                RLK_STORE_OK(vbase + 4 * g + 4 <= a.ld_logits, &g_err_linear_distill))
+              dst[g] = make_float4(z[4 * g], z[4 * g + 1], z[4 * g + 2], z[4 * g + 3]);
+        }
         while (__any_sync(0xffffffffu, slot.id < vbase + 32)) {
           if (slot.id < vbase + 32) {
             d = __fadd_rn(d, __fmul_rn(slot.w, chunk_at(z, slot.id - vbase)));
@@ -532,6 +544,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pipe_teardown(tmem);
 }
 
+// G from kept logits: a block takes 32 rows of a 256-id tile, a warp a row at a time, 8
+// columns a lane.  Each element's operations, and the tree of the 32-row column sums, are
+// those of distill_grad_kernel.  Bound by its 4 + 2 bytes an element.
+template <bool kSums>
+__global__ void __launch_bounds__(256)
+    distill_grad_logits_kernel(const float* __restrict__ logits, int64_t ld_logits, int vtiles,
+                               DistillGradArgs a) {
+  __shared__ float sums[kSums ? 32 : 1][kBN];
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int group = blockIdx.x / vtiles, tile = blockIdx.x - group * vtiles;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int v = tile * kBN + 8 * lane;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int in_group = warp + 8 * k, row = group * 32 + in_group;
+    float G[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) G[i] = 0.f;
+    if (row < a.N && v < a.V) {
+      const float* z = logits + (int64_t)row * ld_logits + v;
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(z));
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (v + 4 < a.V) y = __ldcs(reinterpret_cast<const float4*>(z) + 1);
+      const float up = __fmul_rn(__ldg(a.grad + row), a.temperature);
+      const float Q = __ldg(&a.lists.eq[row].y);
+      const float L = __fmul_rn(__ldg(a.lse + row), a.temperature);
+      const float zz[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      if (Q != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          G[i] = __fmul_rn(Q, ex2_approx(__fmul_rn(__fsub_rn(zz[i], L), a.scale)));
+        const uint16_t* f = a.lists.first + (int64_t)row * (a.lists.spans + 1) + tile;
+        for (int at = __ldg(f), end = __ldg(f + 1); at < end; ++at) {
+          const int di = __ldg(a.lists.ids + (int64_t)row * a.lists.K + at) - v;
+          const float w = __ldg(a.lists.q + (int64_t)row * a.lists.K + at);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i == di) G[i] = __fsub_rn(G[i], w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) G[i] = v + i < a.V ? __fmul_rn(up, G[i]) : 0.f;
+      }
+      uint32_t pk[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 b = __floats2bfloat162_rn(G[2 * i], G[2 * i + 1]);
+        pk[i] = *reinterpret_cast<uint32_t*>(&b);
+      }
+      if (RLK_STORE_OK(v + 8 <= a.ldG, &g_err_linear_distill))
+        *reinterpret_cast<uint4*>(a.G + (int64_t)row * a.ldG + v) =
+            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
+    if (kSums) {
+      float4* to = reinterpret_cast<float4*>(&sums[in_group][8 * lane]);
+      to[0] = make_float4(G[0], G[1], G[2], G[3]);
+      to[1] = make_float4(G[4], G[5], G[6], G[7]);
+    }
+  }
+  if (kSums) {
+    __syncthreads();
+    float t[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) t[r] = __fadd_rn(sums[r][threadIdx.x], sums[r + 16][threadIdx.x]);
+#pragma unroll
+    for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+      for (int r = 0; r < w; ++r) t[r] = __fadd_rn(t[r], t[r + w]);
+    const int col = tile * kBN + threadIdx.x;
+    if (col < a.V && RLK_STORE_OK(col < a.ldG, &g_err_linear_distill))
+      a.sums[(int64_t)group * a.ldG + col] = t[0];
+  }
+}
+
 // grad_bias[v] = the 32-row sums of column v, in ascending order.
 __global__ void __launch_bounds__(256)
     distill_bias_kernel(const float* __restrict__ sums, int groups, int V, int64_t ld,
@@ -600,7 +686,7 @@ rlk_status distill_plan(const void* hidden, int64_t N, int64_t H, int64_t ld_hid
   // work units are numbered in ints (the products: their narrower, 128-column tiles)
   const int64_t rb = ceil_div(N, kPairRows), hb = ceil_div(H, kBN / 2);
   if (rb * p->S >= kUnitLimit) return RLK_ERR_SHAPE;
-  if (backward && (rb * p->vtiles >= kUnitLimit || rb * hb >= kUnitLimit ||
+  if (backward && (ceil_div(N, 32) * p->vtiles >= kUnitLimit || rb * hb >= kUnitLimit ||
                    p->vtiles * hb >= kUnitLimit))
     return RLK_ERR_SHAPE;
   p->spans = backward ? p->vtiles : p->S;
@@ -658,6 +744,13 @@ rlk_status check_teacher(const Teacher& t, int64_t N, bool pointers) {
       !aligned_to(t.lse, 4))
     return RLK_ERR_ALIGN;
   return RLK_OK;
+}
+
+// Kept logits: rows of whole 16-byte vectors.
+rlk_status check_logits(const float* logits, int64_t ld, int64_t V) {
+  if (!logits) return RLK_OK;
+  if (ld < ceil_div(V, 4) * 4 || ld % 4 != 0 || ld >= kLdLimit) return RLK_ERR_SHAPE;
+  return aligned_to(logits, 16) ? RLK_OK : RLK_ERR_ALIGN;
 }
 
 Lists lists_at(uint8_t* ws, const DistillPlan& p, int64_t K, int64_t span) {
@@ -718,13 +811,15 @@ rlk_status stage_operands(const void* hidden, int64_t N, int64_t H, int64_t ld_h
 
 rlk_status distill_forward(const void* hidden, int64_t N, int64_t H, int64_t ld_hidden,
                            const void* weight, int64_t V, int64_t ld_weight, const float* bias,
-                           const Teacher& t, float* loss, float* lse, void* workspace,
-                           size_t workspace_bytes, void* stream) {
+                           const Teacher& t, float* loss, float* lse, float* logits,
+                           int64_t ld_out, void* workspace, size_t workspace_bytes,
+                           void* stream) {
   DistillPlan p;
   rlk_status st =
       distill_plan(hidden, N, H, ld_hidden, weight, V, ld_weight, t.K, false, false, &p);
   if (st != RLK_OK) return st;
   if ((st = check_teacher(t, N, false)) != RLK_OK) return st;
+  if ((st = check_logits(logits, ld_out, V)) != RLK_OK) return st;
   if (N == 0) return RLK_OK;
   if (!hidden || !weight || !loss || !lse) return RLK_ERR_NULL;
   if ((st = check_teacher(t, N, true)) != RLK_OK) return st;
@@ -776,6 +871,8 @@ rlk_status distill_forward(const void* hidden, int64_t N, int64_t H, int64_t ld_
   a.ws_ms = reinterpret_cast<float2*>(ws);
   a.ws_d = reinterpret_cast<float*>(ws + p.off_a);
   a.S = (int)p.S;
+  a.logits = logits;
+  a.ld_logits = ld_out;
   const int64_t units = (int64_t)sc.order.rows * sc.S;
   cudaError_t e;
   if (solo) {
@@ -838,12 +935,13 @@ rlk_status rlk_linear_distill(const void* hidden, int64_t N, int64_t H, int64_t 
                               const int64_t* teacher_ids, int64_t ld_ids,
                               const void* teacher_logits, int logits_dtype, int64_t ld_logits,
                               int64_t K, const float* teacher_lse, float temperature, float* loss,
-                              float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+                              float* lse, float* logits, int64_t ld_logits_out, void* workspace,
+                              size_t workspace_bytes, void* stream) {
   RLK_CALL_RANGE();
   const Teacher t = {teacher_ids, ld_ids,      teacher_logits, logits_dtype,
                      ld_logits,   K,           teacher_lse,    temperature};
-  return distill_forward(hidden, N, H, ld_hidden, weight, V, ld_weight, bias, t, loss, lse,
-                         workspace, workspace_bytes, stream);
+  return distill_forward(hidden, N, H, ld_hidden, weight, V, ld_weight, bias, t, loss, lse, logits,
+                         ld_logits_out, workspace, workspace_bytes, stream);
 }
 
 size_t rlk_linear_distill_backward_workspace_size(const void* hidden, int64_t N, int64_t H,
@@ -860,8 +958,8 @@ rlk_status rlk_linear_distill_backward(
     const void* hidden, int64_t N, int64_t H, int64_t ld_hidden, const void* weight, int64_t V,
     int64_t ld_weight, const float* bias, const int64_t* teacher_ids, int64_t ld_ids,
     const void* teacher_logits, int logits_dtype, int64_t ld_logits, int64_t K,
-    const float* teacher_lse, float temperature, const float* lse, const float* grad_loss,
-    void* grad_hidden, int grad_hidden_dtype, int64_t ld_grad_hidden, void* grad_weight,
+    const float* teacher_lse, float temperature, const float* lse, const float* kept_logits,
+    int64_t ld_kept, const float* grad_loss, void* grad_hidden, int grad_hidden_dtype, int64_t ld_grad_hidden, void* grad_weight,
     int grad_weight_dtype, int64_t ld_grad_weight, float* grad_bias, void* workspace,
     size_t workspace_bytes, void* stream) {
   RLK_CALL_RANGE();
@@ -873,6 +971,7 @@ rlk_status rlk_linear_distill_backward(
                                grad_bias != nullptr, &p);
   if (st != RLK_OK) return st;
   if ((st = check_teacher(t, N, false)) != RLK_OK) return st;
+  if ((st = check_logits(kept_logits, ld_kept, V)) != RLK_OK) return st;
   if (grad_hidden && (ld_grad_hidden < H || ld_grad_hidden >= kLdLimit)) return RLK_ERR_SHAPE;
   if (grad_weight && (ld_grad_weight < H || ld_grad_weight >= kLdLimit)) return RLK_ERR_SHAPE;
   if ((grad_hidden && grad_hidden_dtype != RLK_BF16 && grad_hidden_dtype != RLK_FP32) ||
@@ -943,17 +1042,25 @@ rlk_status rlk_linear_distill_backward(
   const int64_t clusters = dev.sm_count / 2;
   const int grid = 2 * (int)(units < clusters ? units : clusters);
   int* counter = reinterpret_cast<int*>(ws + p.off_ctr);
-  if (ordered_units(units, clusters)) {
-    sc.counter = counter;
-    if (cudaMemsetAsync(sc.counter, 0, sizeof(int), s) != cudaSuccess) return cuda_failed();
+  cudaError_t e;
+  if (kept_logits) {
+    const dim3 blocks((unsigned)(ceil_div(N, 32) * p.vtiles));
+    e = a.sums ? launch_overlapped(distill_grad_logits_kernel<true>, blocks, 256, 0, s, kept_logits,
+                                   ld_kept, (int)p.vtiles, a)
+               : launch_overlapped(distill_grad_logits_kernel<false>, blocks, 256, 0, s, kept_logits,
+                                   ld_kept, (int)p.vtiles, a);
+  } else {
+    if (ordered_units(units, clusters)) {
+      sc.counter = counter;
+      if (cudaMemsetAsync(sc.counter, 0, sizeof(int), s) != cudaSuccess) return cuda_failed();
+    }
+    e = stage_k == 128
+            ? launch_overlapped(distill_grad_kernel<128>, grid, kThreads,
+                                PairRingT<kHalfRows, 128>::kSmemBytes, s, tm_h, tm_w, sc, a)
+            : launch_overlapped(distill_grad_kernel<64>, grid, kThreads,
+                                PairRingT<kHalfRows, 64>::kSmemBytes, s, tm_h, tm_w, sc, a);
   }
-  if ((stage_k == 128
-           ? launch_overlapped(distill_grad_kernel<128>, grid, kThreads,
-                               PairRingT<kHalfRows, 128>::kSmemBytes, s, tm_h, tm_w, sc, a)
-           : launch_overlapped(distill_grad_kernel<64>, grid, kThreads,
-                               PairRingT<kHalfRows, 64>::kSmemBytes, s, tm_h, tm_w, sc, a)) !=
-      cudaSuccess)
-    return cuda_failed();
+  if (e != cudaSuccess) return cuda_failed();
 
   // G and the (possibly staged) operands are TMA-ready and every argument of the
   // products was checked above.  One launch or two: the linear-logp backward's rule.

@@ -547,6 +547,10 @@ RLK_API rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64
  *  teacher_lse      FP32 [N] or NULL
  *  temperature      T, 1e-4 .. 1e4 (RLK_ERR_VALUE otherwise)
  *  loss, lse        FP32 [N] outputs
+ *  logits           FP32 [N, V] output or NULL: z (bias included, not divided by T), for a
+ *                   backward that is to read them in place of forming them again; row
+ *                   pitch ld_logits_out (a multiple of 4, >= V), 16-byte aligned (columns
+ *                   V .. 4 ceil(V / 4) - 1 are written too)
  *  workspace        >= rlk_linear_distill_workspace_size(...) bytes, 256-byte aligned
  *
  * Arithmetic: the logits, their split over V and the (max, sum) merge are
@@ -566,14 +570,15 @@ RLK_API rlk_status rlk_linear_distill(const void* hidden, int64_t N, int64_t H, 
                                       int64_t ld_ids, const void* teacher_logits,
                                       int logits_dtype, int64_t ld_logits, int64_t K,
                                       const float* teacher_lse, float temperature, float* loss,
-                                      float* lse, void* workspace, size_t workspace_bytes,
-                                      void* stream);
+                                      float* lse, float* logits, int64_t ld_logits_out,
+                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Backward of rlk_linear_distill for an upstream gradient g = dL/dloss [N]:
  *   G[r, v]     = g[r] T (Q exp(z[r, v] / T - lse[r]) - sum_{k: id_k = v} q_k),  Q = sum_k q_k
  *   grad_hidden = G . W,   grad_weight = G^T . hidden,   grad_bias[v] = sum_r G[r, v]
- * G is formed in FP32 from the recomputed logits and the forward's lse.  The two
+ * G is formed in FP32 from the recomputed logits and the forward's lse, or (kept_logits not
+ * NULL, row pitch ld_kept) from the logits the forward kept, with the same bits.  The two
  * products read it rounded to BF16 (nearest even), with FP32 accumulation, as in
  * rlk_linear_logp_backward (they are rlk_det_gemm_fwd and rlk_det_gemm_db); grad_bias
  * adds the unrounded G, 32 rows at a time in a fixed tree, those sums in ascending
@@ -589,8 +594,8 @@ RLK_API rlk_status rlk_linear_distill_backward(
     const void* hidden, int64_t N, int64_t H, int64_t ld_hidden, const void* weight, int64_t V,
     int64_t ld_weight, const float* bias, const int64_t* teacher_ids, int64_t ld_ids,
     const void* teacher_logits, int logits_dtype, int64_t ld_logits, int64_t K,
-    const float* teacher_lse, float temperature, const float* lse, const float* grad_loss,
-    void* grad_hidden, int grad_hidden_dtype, int64_t ld_grad_hidden, void* grad_weight,
+    const float* teacher_lse, float temperature, const float* lse, const float* kept_logits,
+    int64_t ld_kept, const float* grad_loss, void* grad_hidden, int grad_hidden_dtype, int64_t ld_grad_hidden, void* grad_weight,
     int grad_weight_dtype, int64_t ld_grad_weight, float* grad_bias, void* workspace,
     size_t workspace_bytes, void* stream);
 

@@ -250,6 +250,60 @@ def test_gradients_asked_for_one_by_one():
         assert bits_equal(got[i], every[i])
 
 
+@pytest.mark.parametrize("N,H,V,K,T", [(1, 1, 1, 1, 1.0), (20, 64, 300, 17, 2.0), (130, 72, 1003, 64, 1.0),
+                                       (301, 96, 519, 33, 0.5)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_kept_logits(N, H, V, K, T, bias):
+    """The logits the forward keeps are its own, and a backward that reads them gives the bits of
+    one that forms them again."""
+    dev = cuda_or_skip()
+    h, w, ids, t, b, _ = on(dev, *inputs(N, H, V, K, 15, bias, T=T))
+    ids[::5] = -1
+    ids[1::5, K // 2:] = V
+    loss, lse, z = rlk.linear_distill(h, w, ids, t, b, temperature=T, return_logits=True)
+    plain = rlk.linear_distill(h, w, ids, t, b, temperature=T)
+    assert bits_equal(loss, plain[0]) and bits_equal(lse, plain[1]) and z.shape == (N, V)
+    want = h.cpu().double() @ w.cpu().double().T + (b.cpu().double() if bias else 0.0)
+    assert ((z.cpu().double() - want).abs().amax(1) <=
+            ref.logit_error(h.cpu(), w.cpu(), b.cpu() if bias else None) + 1e-30).all()
+    g = torch.randn(N, device=dev)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        a = rlk.linear_distill_backward(h, w, ids, t, lse, g, b, temperature=T, logits=z,
+                                        out_dtype=out_dtype, return_grad_logits=True)
+        c = rlk.linear_distill_backward(h, w, ids, t, lse, g, b, temperature=T, out_dtype=out_dtype,
+                                        return_grad_logits=True)
+        assert all((x is None and y is None) or bits_equal(x, y) for x, y in zip(a, c))
+    with pytest.raises(ValueError, match="return_logits"):
+        rlk.linear_distill_backward(h, w, ids, t, lse, g, b, logits=z.double())
+    got = []
+    for keep in (True, False):
+        x = [y.clone().requires_grad_() for y in (h, w)]
+        loss, _ = rlk.linear_distill_trainable(x[0], x[1], ids, t, b, temperature=T, keep_logits=keep)
+        got.append(torch.autograd.grad(loss, x, g))
+    assert all(bits_equal(x, y) for x, y in zip(*got))
+
+
+def test_repeated_calls_of_many_units():
+    """Enough units that they are dealt from the counter, and an epilogue whose stores keep the
+    memory pipeline full: every call gives the bits of the call that stores no logits."""
+    dev = cuda_or_skip()
+    N, H, V, K = 2304, 64, 40000, 8
+    g = torch.Generator(device=dev).manual_seed(16)
+    h = torch.randn(N, H, device=dev, generator=g).bfloat16()
+    w = (torch.randn(V, H, device=dev, generator=g) * 0.25).bfloat16()
+    ids = torch.randint(V, (N, K), device=dev, generator=g)
+    t = torch.randn(N, K, device=dev, generator=g)
+    loss, lse = rlk.linear_distill(h, w, ids, t)
+    up = torch.randn(N, device=dev, generator=g)
+    want = rlk.linear_distill_backward(h, w, ids, t, lse, up)
+    for _ in range(40):
+        a, b, z = rlk.linear_distill(h, w, ids, t, return_logits=True)
+        assert bits_equal(a, loss) and bits_equal(b, lse)
+    for kept in (None, z, None, z):
+        got = rlk.linear_distill_backward(h, w, ids, t, lse, up, logits=kept)
+        assert bits_equal(got[0], want[0]) and bits_equal(got[1], want[1])
+
+
 def test_trainable():
     """Autograd gives the backward entry's gradients; shared inputs add up; lse is a constant."""
     dev = cuda_or_skip()

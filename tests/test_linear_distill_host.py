@@ -19,9 +19,9 @@ def lib():
 
 
 FWD = dict(hidden=P, N=4, H=8, ldh=8, weight=P, V=10, ldw=8, bias=None, ids=P, ldi=3, tl=P, dt=1,
-           ldt=3, K=3, tlse=None, T=1.0, loss=P, lse=P, ws=P, n=1 << 20, stream=None)
+           ldt=3, K=3, tlse=None, T=1.0, loss=P, lse=P, z=None, ldz=0, ws=P, n=1 << 20, stream=None)
 BWD = dict(hidden=P, N=4, H=8, ldh=8, weight=P, V=10, ldw=8, bias=None, ids=P, ldi=3, tl=P, dt=1,
-           ldt=3, K=3, tlse=None, T=1.0, lse=P, grad=P, gh=P, ghd=0, ldgh=8, gw=P, gwd=0, ldgw=8,
+           ldt=3, K=3, tlse=None, T=1.0, lse=P, z=None, ldz=0, grad=P, gh=P, ghd=0, ldgh=8, gw=P, gwd=0, ldgw=8,
            gb=None, ws=P, n=1 << 20, stream=None)
 
 REFUSALS = [
@@ -32,7 +32,8 @@ REFUSALS = [
     (dict(weight=None), 1), (dict(ids=None), 1), (dict(tl=None), 1), (dict(lse=None), 1),
     (dict(hidden=ODD), 4), (dict(weight=ODD), 4), (dict(bias=ODD), 4), (dict(ids=ODD), 4),
     (dict(tl=ODD), 4), (dict(tlse=ODD), 4), (dict(lse=ODD), 4), (dict(ws=None), 5), (dict(n=64), 5),
-    (dict(ws=ctypes.c_void_p(0x10010)), 5),
+    (dict(ws=ctypes.c_void_p(0x10010)), 5), (dict(z=P, ldz=11), 2), (dict(z=P, ldz=8), 2),
+    (dict(z=ctypes.c_void_p(0x10008), ldz=12), 4),
 ]
 
 
