@@ -733,12 +733,12 @@ class _Distill:
         self.tlse, self.T = teacher_lse, temperature
 
     def forward(self, keep_logits: bool, stream=None):
-        """loss [N], lse [N], logits [N, 4 ceil(V / 4)] or None."""
+        """loss [N], lse [N], logits [N, 8 ceil(V / 8)] or None."""
         h, w, dev = self.h, self.w, self.h.device
         N, H, V, K = self.N, self.H, self.V, self.K
         loss = torch.empty(N, dtype=torch.float32, device=dev)
         lse = torch.empty(N, dtype=torch.float32, device=dev)
-        ldz = -(-V // 4) * 4
+        ldz = -(-V // 8) * 8
         logits = torch.empty((N, ldz), dtype=torch.float32, device=dev) if keep_logits else None
         lib_ = lib()
         with _on(dev):
@@ -761,7 +761,7 @@ class _Distill:
         gh = torch.empty((N, H), dtype=out_dtype, device=dev) if want[0] else None
         gw = torch.empty((V, H), dtype=out_dtype, device=dev) if want[1] else None
         gb = torch.empty(V, dtype=torch.float32, device=dev) if want[2] else None
-        ldz = 0 if logits is None else logits.stride(0) if N > 1 else -(-V // 4) * 4
+        ldz = 0 if logits is None else logits.stride(0) if N > 1 else -(-V // 8) * 8
         dt = _DT[out_dtype]
         lib_ = lib()
         with _on(dev):

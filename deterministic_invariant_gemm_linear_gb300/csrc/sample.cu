@@ -1519,7 +1519,7 @@ template <class B, class R>
 __device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* tops, int chunks,
                                         float lo, float hi, uint16_t* ids) {
   SampleSmem* s = b.s;
-  const uint32_t least = lo == -INFINITY ? 0u : key_of(lo);
+  const uint32_t least = key_of(lo);
   __syncthreads();
   if (threadIdx.x == 0) {
     s->n_list = 0;
@@ -1527,14 +1527,27 @@ __device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* t
   }
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  for (int i0 = 0; i0 < chunks; i0 += B::kThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool has = i < chunks && tops[i] >= least;
-    const uint32_t all = __ballot_sync(kFull, has);
+  for (int i0 = 0; i0 < chunks; i0 += 8 * B::kThreads) {
+    uint32_t key[8], mine = 0;                     // all eight loads before the first use
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * B::kThreads + threadIdx.x;
+      key[j] = i < chunks ? tops[i] : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine += key[j] >= least && key[j];
+    uint32_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(kFull, upto, off);
+      if (lane >= off) upto += o;
+    }
     uint32_t at = 0;
-    if (lane == 0 && all) at = atomicAdd(&s->n_chunks, (uint32_t)__popc(all));
-    at = __shfl_sync(kFull, at, 0) + __popc(all & ((1u << lane) - 1));
-    if (has) ids[at] = (uint16_t)i;
+    if (lane == 31 && upto) at = atomicAdd(&s->n_chunks, upto);
+    at = __shfl_sync(kFull, at, 31) + upto - mine;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (key[j] >= least && key[j]) ids[at++] = (uint16_t)(i0 + j * B::kThreads + threadIdx.x);
   }
   __syncthreads();
   r.v0 = 0;

@@ -549,8 +549,8 @@ RLK_API rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64
  *  loss, lse        FP32 [N] outputs
  *  logits           FP32 [N, V] output or NULL: z (bias included, not divided by T), for a
  *                   backward that is to read them in place of forming them again; row
- *                   pitch ld_logits_out (a multiple of 4, >= V), 16-byte aligned (columns
- *                   V .. 4 ceil(V / 4) - 1 are written too)
+ *                   pitch ld_logits_out (a multiple of 8, >= V), 32-byte aligned (columns
+ *                   V .. 8 ceil(V / 8) - 1 are written too)
  *  workspace        >= rlk_linear_distill_workspace_size(...) bytes, 256-byte aligned
  *
  * Arithmetic: the logits, their split over V and the (max, sum) merge are

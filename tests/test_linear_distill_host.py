@@ -32,8 +32,8 @@ REFUSALS = [
     (dict(weight=None), 1), (dict(ids=None), 1), (dict(tl=None), 1), (dict(lse=None), 1),
     (dict(hidden=ODD), 4), (dict(weight=ODD), 4), (dict(bias=ODD), 4), (dict(ids=ODD), 4),
     (dict(tl=ODD), 4), (dict(tlse=ODD), 4), (dict(lse=ODD), 4), (dict(ws=None), 5), (dict(n=64), 5),
-    (dict(ws=ctypes.c_void_p(0x10010)), 5), (dict(z=P, ldz=11), 2), (dict(z=P, ldz=8), 2),
-    (dict(z=ctypes.c_void_p(0x10008), ldz=12), 4),
+    (dict(ws=ctypes.c_void_p(0x10010)), 5), (dict(z=P, ldz=12), 2), (dict(z=P, ldz=8), 2),
+    (dict(z=ctypes.c_void_p(0x10010), ldz=16), 4),
 ]
 
 
