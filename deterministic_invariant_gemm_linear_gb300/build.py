@@ -28,8 +28,8 @@ FLAVORS = {"release": (LIB_PATH, []),
 
 SOURCES = ["common.cu", "linear_logp.cu", "linear_logp_bwd.cu", "linear_distill.cu",
            "sample.cu", "det_gemm.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("rlk_device.cuh", "rlk_pipeline.cuh", "rlk_solo.cuh", "rlk_vocab.cuh",
-                                             "rlk_internal.h")]
+HEADERS = [os.path.join(CSRC, h) for h in ("rlk_device.cuh", "rlk_pipeline.cuh", "rlk_solo.cuh",
+                                           "rlk_vocab.cuh", "rlk_sample.cuh", "rlk_internal.h")]
 HEADERS.append(os.path.join(INCLUDE, "rlk.h"))
 
 NVCC_FLAGS = [
