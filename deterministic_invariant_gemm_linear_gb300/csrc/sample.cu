@@ -865,11 +865,13 @@ inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
-// Logits from which the streaming kernels run, for rows of kStreamVocab or more: rows of
-// 151,936 FP32 logits took (us, streaming against clusters) 2 rows 18 / 47 / 17 against
-// 18 / 45 / 15 with top-k and top-p / top-p / neither, 8 rows 19 / 51 / 19 against 23 / 56 /
-// 22, 64 rows 27 / 77 / 31 against 40 / 151 / 74.
-constexpr int64_t kStreamBytes = int64_t(4) << 20;
+// Logits from which the streaming kernels run, for rows of kStreamVocab or more.  Calls over
+// rows of 151,936 FP32 logits took (us with their launches, streaming against clusters, for
+// top-k with top-p / top-p / neither / settings of every kind) 8 rows 37 / 51 / 42 / 56 against
+// 24 / 56 / 23 / 32, 16 rows 37 / 54 / 41 / 58 against 29 / 77 / 38 / 51, 48 rows 38 / 65 / 42 /
+// 60 against 41 / 150 / 72 / 114; in a captured graph, whose launches cost less, 8 rows took
+// 19 / 51 / 19 against 23 / 56 / 22 without the last.
+constexpr int64_t kStreamBytes = int64_t(8) << 20;
 constexpr int64_t kStreamVocab = 16384;
 
 // How a call runs: the streaming kernels, or clusters of CTAs that keep a row in shared
@@ -954,20 +956,24 @@ cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* 
   const size_t smem_ids = sizeof(SampleSmem) + (size_t)plan.tiles * 32 * sizeof(uint16_t);
   const size_t smem_pick = smem_ids + (size_t)plan.tiles * 32 * sizeof(uint32_t);
   const dim3 rows((unsigned)a.N), tops((unsigned)(a.N * top_ctas)), weighs((unsigned)(a.N * weigh_ctas));
-  cudaError_t e;
-  if ((e = launch_overlapped(sample_tops_kernel<kFp32>, tops, kStreamThreads, 0, stream, p,
-                             top_ctas)) != cudaSuccess ||
-      (e = launch_overlapped(sample_pick_kernel<kFp32>, rows, kRowThreads, smem_pick, stream, p)) !=
-          cudaSuccess ||
-      (e = launch_overlapped(sample_weigh_kernel<kFp32, false>, weighs, kStreamThreads, 0, stream, p,
-                             weigh_ctas)) != cudaSuccess ||
-      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kRowThreads, smem_ids, stream, p, 0)) !=
-          cudaSuccess ||
-      (e = launch_overlapped(sample_weigh_kernel<kFp32, true>, weighs, kStreamThreads, 0, stream, p,
-                             weigh_ctas)) != cudaSuccess ||
-      (e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kRowThreads, smem_ids, stream, p, 1)) !=
-          cudaSuccess)
-    return e;
+  // Passes that settings shared by all rows leave nothing to do for are not launched.
+  const bool all_greedy = !a.temperature && a.temperature_all < 1e-6f;
+  const bool all_few = all_greedy || (!a.top_k && a.top_k_all > 0 && a.top_k_all <= kChunkTop &&
+                                      a.top_k_all <= plan.tiles * 16 && a.top_k_all < a.V);
+  const bool any_top_p = !all_few && (a.top_p || a.top_p_all < 1.f);
+  cudaError_t e = launch_overlapped(sample_tops_kernel<kFp32>, tops, kStreamThreads, 0, stream, p,
+                                    top_ctas);
+  if (e == cudaSuccess)
+    e = launch_overlapped(sample_pick_kernel<kFp32>, rows, kRowThreads, smem_pick, stream, p);
+  for (int again = 0; again < (all_few ? 0 : any_top_p ? 2 : 1) && e == cudaSuccess; ++again) {
+    e = again ? launch_overlapped(sample_weigh_kernel<kFp32, true>, weighs, kStreamThreads, 0,
+                                  stream, p, weigh_ctas)
+              : launch_overlapped(sample_weigh_kernel<kFp32, false>, weighs, kStreamThreads, 0,
+                                  stream, p, weigh_ctas);
+    if (e == cudaSuccess)
+      e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kRowThreads, smem_ids, stream, p, again);
+  }
+  if (e != cudaSuccess) return e;
   return launch_clusters(a, kFp32, plan, p.left, sms, stream);
 }
 

@@ -30,7 +30,8 @@ class Guarded:
 
 
 @pytest.mark.parametrize("N,V,dtype", [(1, 1, torch.float32), (3, 1001, torch.bfloat16),
-                                       (70, 20011, torch.float32), (130, 16385, torch.bfloat16)])
+                                       (70, 20011, torch.float32), (130, 16385, torch.bfloat16),
+                                       (110, 20011, torch.float32), (270, 16385, torch.bfloat16)])
 @pytest.mark.parametrize("k,p,m", [(0, 1.0, 0.0), (40, 0.9, 0.0), (0, 0.9, 0.01), (3000, 0.9, 0.0)])
 def test_sampling(N, V, dtype, k, p, m):
     dev = cuda_or_skip()
@@ -41,7 +42,7 @@ def test_sampling(N, V, dtype, k, p, m):
     b = Guarded(dev)
     lib = rlk.lib()
     n = lib.rlk_sample_logits_workspace_size(rlk._DT[dtype], N, V)
-    assert (n > 0) == (N * V * z.element_size() >= 4 << 20)
+    assert (n > 0) == (V >= 16384 and N * V * z.element_size() >= 8 << 20)
     ws = b.take(n)
     token = b.take(8 * N, torch.int64, (N,))
     logp = b.take(4 * N, torch.float32, (N,))
