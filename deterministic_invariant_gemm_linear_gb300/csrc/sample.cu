@@ -386,7 +386,10 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
 // in the last octaves) are left to sample_kernel, which takes them from a list.
 constexpr int kTile = 256;                    // vectors of a tile: 8 a lane
 constexpr int kStreamThreads = 256;           // of the passes
-constexpr int kRowThreads = 512;              // of the row's work between them
+// Of a row's work between them.  The pick's lists want threads (256: 1024 FP32 rows with
+// top-k 247 us in all against 232); the cut waits on short steps, and more rows at a time
+// hide them (512 rows of BF16 with top-p: 181 us at 256, 197 us at 512).
+constexpr int kPickThreads = 512, kCutThreads = 256;
 constexpr int kTilesPerCta = 16;              // of the weighing kernels
 constexpr int kChunkTop = 1024;
 
@@ -529,9 +532,9 @@ __device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* t
 }
 
 template <bool kFp32>
-__global__ void __launch_bounds__(kRowThreads, 2) sample_pick_kernel(const __grid_constant__ StreamArgs p) {
+__global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const __grid_constant__ StreamArgs p) {
   using R = Row<kFp32, false>;
-  using B = Block<kRowThreads>;
+  using B = Block<kPickThreads>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   B b;
   b.s = reinterpret_cast<SampleSmem*>(smem_raw);
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_pick_kernel(const __gri
   const uint32_t* src = p.tops + (int64_t)row * chunks;
   uint32_t top = 0;
 #pragma unroll 8
-  for (int i = tid; i < chunks; i += kRowThreads) {
+  for (int i = tid; i < chunks; i += kPickThreads) {
     const uint32_t key = __ldg(src + i);
     tops[i] = key;
     top = max(top, key);
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_pick_kernel(const __gri
   } else if (f.need_k) {
     st.status = kLeft;
     if (f.k <= kChunkTop && (int)f.k <= chunks / 2) {
-      for (int i = tid; i < chunks; i += kRowThreads) {
+      for (int i = tid; i < chunks; i += kPickThreads) {
         const int bin = all_octaves().bin(x_of(logit_of(tops[i]), f.m, f.c));
         if (bin < kBins) add_to_bin(b, bin, false, 0);
       }
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_pick_kernel(const __gri
   } else {
     st.status = f.need_p ? kWeighBins : kWeigh;
     if (f.need_p)
-      for (int i = tid; i < kBins; i += kRowThreads)
+      for (int i = tid; i < kBins; i += kPickThreads)
         if (RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
           p.bin_count[(int64_t)row * kBins + i] = 0;
           p.bin_mass[(int64_t)row * kBins + i] = 0;
@@ -732,10 +735,10 @@ __device__ __forceinline__ void draw(const B& b, const StreamArgs& p, int row, c
 }
 
 template <bool kFp32>
-__global__ void __launch_bounds__(kRowThreads, 2) sample_cut_kernel(const __grid_constant__ StreamArgs p,
-                                                                   int again) {
+__global__ void __launch_bounds__(kCutThreads, 1024 / kCutThreads)
+    sample_cut_kernel(const __grid_constant__ StreamArgs p, int again) {
   using R = Row<kFp32, false>;
-  using B = Block<kRowThreads>;
+  using B = Block<kCutThreads>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   B b;
   b.s = reinterpret_cast<SampleSmem*>(smem_raw);
@@ -761,7 +764,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_cut_kernel(const __grid
     const uint32_t high = key_of(st.hi), range = high - key_of(st.lo);
     const int shift = range < kBins ? 0 : 32 - __clz((int)(range / kBins));
     clear_bins(b, true);
-    for (int i = tid; i < n; i += kRowThreads) {
+    for (int i = tid; i < n; i += kCutThreads) {
       const uint64_t x = __ldg(list + i);
       add_to_bin(b, (int)((high - ~(uint32_t)(x >> 32)) >> shift), true, f.weight(entry_logit(x)));
     }
@@ -774,7 +777,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_cut_kernel(const __grid
     uint32_t all_n;
     uint64_t all_mass;
     const Cut part = scan_cut(b, true, true, 0, st.mass_wanted - st.mass_before, &all_n, &all_mass);
-    for (int i = tid; i < n; i += kRowThreads) {
+    for (int i = tid; i < n; i += kCutThreads) {
       const uint64_t x = __ldg(list + i);
       if ((int)((high - ~(uint32_t)(x >> 32)) >> shift) == part.bin)
         s->list[atomicAdd(&s->n_list, 1u)] = x;
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_cut_kernel(const __grid
     cut = entry_logit(last);
     cut_id = (int)(uint32_t)last;
     // the bin's kept elements join their tiles
-    for (int i = tid; i < n; i += kRowThreads) {
+    for (int i = tid; i < n; i += kCutThreads) {
       const uint64_t x = __ldg(list + i);
       const uint32_t w = f.weight(entry_logit(x));
       const int t = ((int)(uint32_t)x - r.first_id) / R::kElems / kTile;
@@ -803,13 +806,13 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_cut_kernel(const __grid
   const uint32_t* tops = p.tops + (int64_t)row * chunks;
   // the row's weight, its histogram, the cut's bin
   uint64_t sum = 0;
-  for (int t = tid; t < p.tiles; t += kRowThreads) sum += p.mass[(int64_t)row * p.tiles + t];
+  for (int t = tid; t < p.tiles; t += kCutThreads) sum += p.mass[(int64_t)row * p.tiles + t];
   sum = block_sum(b, sum, 0);
   if (tid == 0) {
     s->total[2] = sum;
     s->cut.bin = -1;
   }
-  for (int i = tid; i < kBins; i += kRowThreads) {
+  for (int i = tid; i < kBins; i += kCutThreads) {
     s->slice_count[i] = p.bin_count[(int64_t)row * kBins + i];
     s->slice_mass[i] = p.bin_mass[(int64_t)row * kBins + i];
   }
@@ -820,7 +823,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_cut_kernel(const __grid
   const Cut found = scan_cut(b, true, true, 0, want, &all_n, &all_mass);
   const Window window(0.f, kNear);
   st.status = kLeft;
-  if (found.bin >= 0 && found.before + found.in <= kRowThreads) {
+  if (found.bin >= 0 && found.before + found.in <= kCutThreads) {
     const float lo = least_logit(f.m, f.c, window, found.bin);
     const int n = list_chunks(b, r, vectors, tops, chunks, lo, INFINITY, ids);
     finish(b, f, p.a, row, n, total);
@@ -964,14 +967,14 @@ cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* 
   cudaError_t e = launch_overlapped(sample_tops_kernel<kFp32>, tops, kStreamThreads, 0, stream, p,
                                     top_ctas);
   if (e == cudaSuccess)
-    e = launch_overlapped(sample_pick_kernel<kFp32>, rows, kRowThreads, smem_pick, stream, p);
+    e = launch_overlapped(sample_pick_kernel<kFp32>, rows, kPickThreads, smem_pick, stream, p);
   for (int again = 0; again < (all_few ? 0 : any_top_p ? 2 : 1) && e == cudaSuccess; ++again) {
     e = again ? launch_overlapped(sample_weigh_kernel<kFp32, true>, weighs, kStreamThreads, 0,
                                   stream, p, weigh_ctas)
               : launch_overlapped(sample_weigh_kernel<kFp32, false>, weighs, kStreamThreads, 0,
                                   stream, p, weigh_ctas);
     if (e == cudaSuccess)
-      e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kRowThreads, smem_ids, stream, p, again);
+      e = launch_overlapped(sample_cut_kernel<kFp32>, rows, kCutThreads, smem_ids, stream, p, again);
   }
   if (e != cudaSuccess) return e;
   return launch_clusters(a, kFp32, plan, p.left, sms, stream);
