@@ -658,7 +658,7 @@ __device__ __forceinline__ int sort_list(const B& b, int n) {
 // The end of a row of which the list holds all elements up to some place in the sorted
 // order past the cut, n <= the block's threads, sorted: an element a thread.  One-off code is
 // fetched as it runs, so it is kept short rather than unrolled (unrolled for one warp it took
-// 5 us after a 4 us sort; a token of one row is 15).
+// 5 us of a one-row call of 20).
 template <class B>
 __device__ __noinline__ void finish_short(B b, Filter f, const SampleArgs& a, int row, int n,
                                           uint64_t total_mass) {
@@ -890,7 +890,7 @@ template <class B>
 __device__ __noinline__ void finish(B b, Filter f, const SampleArgs& a, int row, int n,
                                     uint64_t total_mass) {
   SampleSmem* s = b.s;
-  // counting places is quadratic: 424 take 8 us, 60 take 1, and keep_first 2
+  // counting places is quadratic: 424 entries take 8 us, 60 take 1, and keep_first takes 2
   if (n > 96 && f.k <= B::kThreads) n = keep_first(b, f, n);
   const int size = sort_list(b, n);
   if (n <= B::kThreads) {
