@@ -418,7 +418,6 @@ struct StreamArgs {
   int tiles;                // per row
   uint32_t* tops;           // [N][tiles * 32] keys
   uint64_t* mass;           // [N][tiles]
-  uint32_t* bin_count;      // [N][kBins]
   uint64_t* bin_mass;       // [N][kBins]
   RowState* state;          // [N]
   uint64_t* list;           // [N][kList] the elements of the bins the cuts fall in
@@ -610,12 +609,23 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const __gr
     st.status = f.need_p ? kWeighBins : kWeigh;
     if (f.need_p)
       for (int i = tid; i < kBins; i += kPickThreads)
-        if (RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
-          p.bin_count[(int64_t)row * kBins + i] = 0;
-          p.bin_mass[(int64_t)row * kBins + i] = 0;
-        }
+        if (RLK_STORE_OK(row < p.a.N, &g_err_sample)) p.bin_mass[(int64_t)row * kBins + i] = 0;
   }
   if (tid == 0) put_state(p, row, st);
+}
+
+// A tile CTA's histogram holds weights as two halves whose sums fit 32 bits: it has at most
+// 2^15 elements.  Most weights of an open row have no high part (14 octaves below the top).
+// Shared atomics on scattered bins are what the pass waits for, so elements are not counted:
+// a bin's weights are alike, and its weight bounds their number.
+constexpr int kLowBits = 17;
+constexpr uint32_t kLowPart = (1u << kLowBits) - 1;
+static_assert(kTilesPerCta * kTile * 8 <= 1 << (32 - kLowBits), "sums of low parts fit 32 bits");
+
+// At most so many elements make up the weight of a bin of the first octaves: each lies at
+// most bin + 1/2 steps below the top (2^(1/2 step) is room for rounding).
+__device__ __forceinline__ uint32_t most_in(const Window& window, int bin, uint64_t mass) {
+  return (uint32_t)__fmul_rn(__ull2float_rn(mass), exp2f((bin + 1) / window.scale - 31.f));
 }
 
 // The weight of tiles: of the rows that keep all (but what min-p drops) and, with their
@@ -624,8 +634,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const __gr
 enum WeighWhat { kAll, kAtLeast, kBinned, kAboveBin };
 template <bool kFp32, WeighWhat kWhat>
 __device__ __forceinline__ void weigh_tiles(const StreamArgs& p, int row, int t0, const RowState& st,
-                                            float c, uint32_t least, uint32_t* count, uint32_t* lo,
-                                            uint32_t* hi) {
+                                            float c, uint32_t least, uint32_t* lo, uint32_t* hi) {
   using R = Row<kFp32, false>;
   constexpr int kE = R::kElems;
   const Window window(0.f, kNear);
@@ -661,11 +670,10 @@ __device__ __forceinline__ void weigh_tiles(const StreamArgs& p, int row, int t0
       if (kWhat == kBinned && x_of(R::top_of(q), st.m, c) > -window.to) {
 #pragma unroll
         for (int e = 0; e < kE; ++e)
-          if (window.has(x[e])) {
+          if (x[e] > -window.to) {               // and none lies above the top
             const int bin = window.at(x[e]);
-            atomicAdd(&count[bin], 1u);
-            atomicAdd(&lo[bin], w[e] & 0xffffu);   // a CTA has at most 2^15 elements
-            atomicAdd(&hi[bin], w[e] >> 16);
+            atomicAdd(&lo[bin], w[e] & kLowPart);
+            atomicAdd(&hi[bin], w[e] >> kLowBits);
           }
       }
     });
@@ -678,7 +686,7 @@ __device__ __forceinline__ void weigh_tiles(const StreamArgs& p, int row, int t0
 template <bool kFp32, bool kAbove>
 __global__ void __launch_bounds__(kStreamThreads) sample_weigh_kernel(const __grid_constant__ StreamArgs p,
                                                                      int per_row) {
-  __shared__ uint32_t count[kAbove ? 1 : kBins], lo[kAbove ? 1 : kBins], hi[kAbove ? 1 : kBins];
+  __shared__ uint32_t lo[kAbove ? 1 : kBins], hi[kAbove ? 1 : kBins];
   stream_begin();
   const int row = blockIdx.x / per_row;
   const RowState st = p.state[row];
@@ -687,24 +695,22 @@ __global__ void __launch_bounds__(kStreamThreads) sample_weigh_kernel(const __gr
   bool bad;
   const Filter f = settings_of(p.a, row, &bad);
   if (kAbove) {
-    weigh_tiles<kFp32, kAboveBin>(p, row, t0, st, f.c, f.least, count, lo, hi);
+    weigh_tiles<kFp32, kAboveBin>(p, row, t0, st, f.c, f.least, lo, hi);
   } else if (st.status == kWeigh) {
     if (f.least == 0)
-      weigh_tiles<kFp32, kAll>(p, row, t0, st, f.c, 0, count, lo, hi);
+      weigh_tiles<kFp32, kAll>(p, row, t0, st, f.c, 0, lo, hi);
     else
-      weigh_tiles<kFp32, kAtLeast>(p, row, t0, st, f.c, f.least, count, lo, hi);
+      weigh_tiles<kFp32, kAtLeast>(p, row, t0, st, f.c, f.least, lo, hi);
   } else {
-    for (int i = threadIdx.x; i < kBins; i += kStreamThreads) count[i] = lo[i] = hi[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += kStreamThreads) lo[i] = hi[i] = 0;
     __syncthreads();
-    weigh_tiles<kFp32, kBinned>(p, row, t0, st, f.c, 0, count, lo, hi);
+    weigh_tiles<kFp32, kBinned>(p, row, t0, st, f.c, 0, lo, hi);
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kStreamThreads)
-      if (count[i] && RLK_STORE_OK(row < p.a.N, &g_err_sample)) {
+      if ((lo[i] | hi[i]) && RLK_STORE_OK(row < p.a.N, &g_err_sample))
         // sums of whole numbers: their order does not matter
-        atomicAdd(&p.bin_count[(int64_t)row * kBins + i], count[i]);
         atomicAdd(reinterpret_cast<unsigned long long*>(&p.bin_mass[(int64_t)row * kBins + i]),
-                  (unsigned long long)lo[i] + ((unsigned long long)hi[i] << 16));
-      }
+                  (unsigned long long)lo[i] + ((unsigned long long)hi[i] << kLowBits));
   }
 }
 
@@ -767,7 +773,7 @@ __global__ void __launch_bounds__(kCutThreads, 1024 / kCutThreads)
   float cut = -INFINITY;                           // kept: z > cut, or z = cut and id <= cut_id
   int cut_id = -1;
   if (st.status == kCutBin) {
-    const int n = min(st.listed, kList);           // as many as the histogram counted
+    const int n = min(st.listed, kList);           // no more than the histogram's weight bounds
     const uint64_t* list = p.list + (int64_t)row * kList;
     // the part of the bin that the cut falls in, and its elements alone sorted
     const uint32_t high = key_of(st.hi), range = high - key_of(st.lo);
@@ -821,16 +827,17 @@ __global__ void __launch_bounds__(kCutThreads, 1024 / kCutThreads)
     s->total[2] = sum;
     s->cut.bin = -1;
   }
+  const Window window(0.f, kNear);
   for (int i = tid; i < kBins; i += kCutThreads) {
-    s->slice_count[i] = p.bin_count[(int64_t)row * kBins + i];
-    s->slice_mass[i] = p.bin_mass[(int64_t)row * kBins + i];
+    const uint64_t in = p.bin_mass[(int64_t)row * kBins + i];
+    s->slice_count[i] = most_in(window, i, in);
+    s->slice_mass[i] = in;
   }
   __syncthreads();
   const uint64_t total = s->total[2], want = f.share(total);
   uint32_t all_n;
   uint64_t all_mass;
   const Cut found = scan_cut(b, true, true, 0, want, &all_n, &all_mass);
-  const Window window(0.f, kNear);
   st.status = kLeft;
   if (found.bin >= 0 && found.before + found.in <= kCutThreads) {
     const float lo = least_logit(f.m, f.c, window, found.bin);
@@ -893,7 +900,7 @@ struct SamplePlan {
   int ctas;
   bool on_chip;
   int tiles;
-  size_t off_mass, off_count, off_bins, off_state, off_left, off_list, total;   // their workspace
+  size_t off_mass, off_bins, off_state, off_left, off_list, total;   // their workspace
 };
 
 SamplePlan sample_plan(int64_t N, int64_t V, bool fp32, int sms) {
@@ -903,8 +910,7 @@ SamplePlan sample_plan(int64_t N, int64_t V, bool fp32, int sms) {
   if (p.stream) {
     p.tiles = (int)ceil_div(ceil_div(V + elems - 1, elems), kTile);
     p.off_mass = align_up((size_t)N * p.tiles * 32 * sizeof(uint32_t), 256);
-    p.off_count = align_up(p.off_mass + (size_t)N * p.tiles * sizeof(uint64_t), 256);
-    p.off_bins = align_up(p.off_count + (size_t)N * kBins * sizeof(uint32_t), 256);
+    p.off_bins = align_up(p.off_mass + (size_t)N * p.tiles * sizeof(uint64_t), 256);
     p.off_state = align_up(p.off_bins + (size_t)N * kBins * sizeof(uint64_t), 256);
     p.off_left = align_up(p.off_state + (size_t)N * sizeof(RowState), 256);
     p.off_list = align_up(p.off_left + (size_t)(N + 1) * sizeof(int), 256);
@@ -958,7 +964,6 @@ cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* 
   p.tiles = plan.tiles;
   p.tops = reinterpret_cast<uint32_t*>(ws);
   p.mass = reinterpret_cast<uint64_t*>(ws + plan.off_mass);
-  p.bin_count = reinterpret_cast<uint32_t*>(ws + plan.off_count);
   p.bin_mass = reinterpret_cast<uint64_t*>(ws + plan.off_bins);
   p.state = reinterpret_cast<RowState*>(ws + plan.off_state);
   p.left = reinterpret_cast<int*>(ws + plan.off_left);
