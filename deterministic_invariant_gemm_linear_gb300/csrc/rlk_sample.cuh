@@ -269,6 +269,13 @@ struct Row {
       }
     }
   }
+  // Element t of an array of vectors.
+  static __device__ __forceinline__ float element(const uint4* q, int t) {
+    if constexpr (kFp32)
+      return reinterpret_cast<const float*>(q)[t];
+    else
+      return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(q)[t] << 16);
+  }
   // The largest of a vector's logits; NaN if one of them is.
   static __device__ __forceinline__ float top_of(const uint4& q) {
     float a, b;

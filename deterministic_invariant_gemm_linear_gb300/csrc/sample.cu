@@ -475,17 +475,41 @@ __device__ __forceinline__ void merge_own(const B& b, bool mass) {
   __syncthreads();
 }
 
-// The chunks whose largest reaches lo, then their elements of [lo, hi], into the list: the
-// number of elements (more than kList: only counted).  ids: [tiles * 32] in shared memory.
+// Vectors with an element for the list.
+constexpr int kHits = 512;
+struct alignas(16) Hits {
+  uint4 q[kHits];
+  int id[kHits];            // of the vector's first element
+  uint32_t n;               // kHits and more of them are taken one by one
+};
+
+template <class R>
+__device__ __noinline__ void list_vector(SampleSmem* s, uint4 q, int id, float lo) {
+  float z[R::kElems];
+  R::unpack(q, z);
+#pragma unroll
+  for (int e = 0; e < R::kElems; ++e)
+    if (z[e] >= lo) {
+      const uint32_t to = atomicAdd(&s->n_list, 1u);
+      if (to < kList) s->list[to] = entry_of(z[e], id + e);
+    }
+}
+
+// The chunks whose largest reaches lo, then their elements that do, into the list: the number
+// of elements (more than kList: only counted).  ids: [tiles * 32] in shared memory.  The
+// vectors with such elements are gathered first and dealt out an element a thread: taken by
+// the thread that read them, eight unrolled vectors were 5 us of code run once.
 template <class B, class R>
 __device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* tops, int chunks,
-                                        float lo, float hi, uint16_t* ids) {
+                                        float lo, uint16_t* ids, Hits* hits) {
+  constexpr int kE = R::kElems;
   SampleSmem* s = b.s;
   const uint32_t least = key_of(lo);
   __syncthreads();
   if (threadIdx.x == 0) {
     s->n_list = 0;
     s->n_chunks = 0;
+    hits->n = 0;
   }
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -515,27 +539,40 @@ __device__ __noinline__ int list_chunks(B b, R r, int vectors, const uint32_t* t
   r.v0 = 0;
   r.v1 = vectors;
   const int n = (int)s->n_chunks;
-  for (int i = threadIdx.x; i < n; i += B::kThreads) {
-    const int chunk = ids[i];
-    int v[8];
-    uint4 q[8];
+  for (int i0 = 0; i0 < n; i0 += B::kThreads) {
+    const int i = i0 + threadIdx.x;
+    if (i < n) {
+      const int chunk = ids[i];
+      int v[8];
+      uint4 q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = min((chunk >> 5) * kTile + 32 * j + (chunk & 31), vectors);
-    r.template get_all<true>(v, q);
+      for (int j = 0; j < 8; ++j) v[j] = min((chunk >> 5) * kTile + 32 * j + (chunk & 31), vectors);
+      r.template get_all<true>(v, q);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (v[j] >= vectors || !(R::top_of(q[j]) >= lo)) continue;
-      float z[R::kElems];
-      R::unpack(q[j], z);
-#pragma unroll
-      for (int e = 0; e < R::kElems; ++e)
-        if (z[e] >= lo && z[e] <= hi) {
-          const uint32_t to = atomicAdd(&s->n_list, 1u);
-          if (to < kList) s->list[to] = entry_of(z[e], r.id_of(v[j]) + e);
+      for (int j = 0; j < 8; ++j) {
+        if (v[j] >= vectors || !(R::top_of(q[j]) >= lo)) continue;
+        const uint32_t to = atomicAdd(&hits->n, 1u);
+        if (to < kHits) {
+          hits->q[to] = q[j];
+          hits->id[to] = r.id_of(v[j]);
+        } else {
+          list_vector<R>(s, q[j], r.id_of(v[j]), lo);
         }
+      }
     }
+    __syncthreads();
+    const int elements = kE * (int)min(hits->n, (uint32_t)kHits);
+    for (int t = threadIdx.x; t < elements; t += B::kThreads) {
+      const float z = R::element(hits->q, t);
+      if (z >= lo) {
+        const uint32_t to = atomicAdd(&s->n_list, 1u);
+        if (to < kList) s->list[to] = entry_of(z, hits->id[t / kE] + t % kE);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) hits->n = 0;
+    if (i0 + B::kThreads < n) __syncthreads();
   }
-  __syncthreads();
   return (int)s->n_list;
 }
 
@@ -550,7 +587,8 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const __gr
   b.ctas = 1;
   SampleSmem* s = b.s;
   const int chunks = p.tiles * 32;
-  uint32_t* tops = reinterpret_cast<uint32_t*>(smem_raw + sizeof(SampleSmem));
+  Hits* hits = reinterpret_cast<Hits*>(smem_raw + sizeof(SampleSmem));
+  uint32_t* tops = reinterpret_cast<uint32_t*>(hits + 1);
   uint16_t* ids = reinterpret_cast<uint16_t*>(tops + chunks);
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) s->top = 0;
@@ -599,7 +637,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) sample_pick_kernel(const __gr
       const float lo = least_logit(f.m, f.c, all_octaves(), cut.bin >= 0 ? cut.bin : kBins - 1);
       R r;
       const int vectors = r.begin(p.a, row);
-      const int n = list_chunks(b, r, vectors, tops, chunks, lo, INFINITY, ids);
+      const int n = list_chunks(b, r, vectors, tops, chunks, lo, ids, hits);
       if (n <= kList) {
         finish(b, f, p.a, row, n, 0);
         st.status = kDone;
@@ -760,7 +798,8 @@ __global__ void __launch_bounds__(kCutThreads, 1024 / kCutThreads)
   b.rank = 0;
   b.ctas = 1;
   SampleSmem* s = b.s;
-  uint16_t* ids = reinterpret_cast<uint16_t*>(smem_raw + sizeof(SampleSmem));
+  Hits* hits = reinterpret_cast<Hits*>(smem_raw + sizeof(SampleSmem));
+  uint16_t* ids = reinterpret_cast<uint16_t*>(hits + 1);
   const int row = blockIdx.x, tid = threadIdx.x;
   stream_begin();
   RowState st = p.state[row];
@@ -841,7 +880,7 @@ __global__ void __launch_bounds__(kCutThreads, 1024 / kCutThreads)
   st.status = kLeft;
   if (found.bin >= 0 && found.before + found.in <= kCutThreads) {
     const float lo = least_logit(f.m, f.c, window, found.bin);
-    const int n = list_chunks(b, r, vectors, tops, chunks, lo, INFINITY, ids);
+    const int n = list_chunks(b, r, vectors, tops, chunks, lo, ids, hits);
     finish(b, f, p.a, row, n, total);
     st.status = kDone;
   } else if (found.bin >= 0 && found.in <= kList) {
@@ -970,7 +1009,7 @@ cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* 
   p.list = reinterpret_cast<uint64_t*>(ws + plan.off_list);
   const int top_ctas = (int)ceil_div(plan.tiles, kStreamThreads / 32);
   const int weigh_ctas = (int)ceil_div(plan.tiles, kTilesPerCta);
-  const size_t smem_ids = sizeof(SampleSmem) + (size_t)plan.tiles * 32 * sizeof(uint16_t);
+  const size_t smem_ids = sizeof(SampleSmem) + sizeof(Hits) + (size_t)plan.tiles * 32 * sizeof(uint16_t);
   const size_t smem_pick = smem_ids + (size_t)plan.tiles * 32 * sizeof(uint32_t);
   const dim3 rows((unsigned)a.N), tops((unsigned)(a.N * top_ctas)), weighs((unsigned)(a.N * weigh_ctas));
   // Passes that settings shared by all rows leave nothing to do for are not launched.
