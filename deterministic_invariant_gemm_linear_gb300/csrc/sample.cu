@@ -395,9 +395,10 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
 // in the last octaves) are left to sample_kernel, which takes them from a list.
 constexpr int kTile = 256;                    // vectors of a tile: 8 a lane
 constexpr int kStreamThreads = 256;           // of the passes
-// Of a row's work between them.  The pick's lists want threads (256: 1024 FP32 rows with
-// top-k 247 us in all against 232); the cut waits on short steps, and more rows at a time
-// hide them (512 rows of BF16 with top-p: 181 us at 256, 197 us at 512).
+// Of a row's work between them.  More rows at a time hide the short steps that both wait on,
+// more threads shorten a row's own: the pick took 62.5 / 230 / 174 us of whole calls (64 and
+// 1024 FP32 rows with settings of every kind, 512 BF16 rows with top-p) at 512 threads and 65 /
+// 231 / 171 at 256, the cut 62 / 232 / 197 at 512 and 63 / 233 / 181 at 256 (when each was set).
 constexpr int kPickThreads = 512, kCutThreads = 256;
 constexpr int kTilesPerCta = 16;              // of the weighing kernels
 constexpr int kChunkTop = 1024;

@@ -39,7 +39,7 @@ def test_workspace(lib):
     N, V = 1024, 151936
     tiles = -(-(-(-(V + 3) // 4)) // 256)
     up = lambda x: -(-x // 256) * 256
-    assert f(1, N, V) == up(N * tiles * 128) + up(N * tiles * 8) + N * 4096 + N * 8192 + N * 40 + up(N * 4 + 4) + N * 16384
+    assert f(1, N, V) == up(N * tiles * 128) + up(N * tiles * 8) + N * 8192 + N * 40 + up(N * 4 + 4) + N * 16384
     assert f(2, N, V) == 0 and f(1, -1, V) == 0 and f(1, N, 0) == 0 and f(1, N, 524289) == 0
     big = {**CALL, "N": N, "V": V, "ld": V}
     assert lib.rlk_sample_logits(*big.values()) == 5
