@@ -378,19 +378,19 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
 // (156 MB) and for 1024 rows of 151,936 FP32 logits (622 MB), five in six greedy or with
 // top-k and most of the others with top-p, and what bounds each:
 //   tops   the largest logit of every chunk (the 8 vectors a lane of a tile reads)
-//          [24, 90; memory: 6.5 and 6.9 TB/s]
+//          [25, 90; memory: 6.2 and 6.9 TB/s]
 //   pick   the row's largest; top-k of at most kChunkTop: the k-th largest of the chunks'
 //          bounds the k first, only the chunks that reach it are read again, and the row
-//          is done  [10, 54; latency of the lists and their order]
+//          is done  [10, 49; latency of the lists and their order]
 //   weigh  the other rows' weights by tile, for top-p with their histogram
-//          [76, 43; instructions: some 27 a logit with the histogram (3.1 issued a cycle), 14
-//          without, which alone would take 41 us of the 76]
+//          [72, 41; instructions: the exact weights alone would take 41 of the 72, the
+//          histogram's places and its two shared atomics the rest]
 //   cut    rows that keep all: the token's tile by a running sum, then the token; top-p: the
 //          bin of the cut from the histogram and, if little lies up to it, the token
-//          [24, 20; latency]
+//          [22, 20; latency]
 //   weigh  again, for the other rows with top-p: the weights above that bin by tile, and its
-//          elements in a list  [30, 22; memory]
-//   cut    again: the cut from the sorted list, and the token  [26, 20; latency]
+//          elements in a list  [31, 24; memory]
+//   cut    again: the cut from the sorted list, and the token  [26, 19; latency]
 // Rows that none of this settles (more equal logits than the list holds, top-k of more, a cut
 // in the last octaves) are left to sample_kernel, which takes them from a list.
 constexpr int kTile = 256;                    // vectors of a tile: 8 a lane
