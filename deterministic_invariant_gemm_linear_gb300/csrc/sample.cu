@@ -383,13 +383,13 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
 //          bounds the k first, only the chunks that reach it are read again, and the row
 //          is done  [10, 49; latency of the lists and their order]
 //   weigh  the other rows' weights by tile, for top-p with their histogram
-//          [72, 41; instructions: the exact weights alone would take 41 of the 72, the
+//          [70, 41; instructions: the exact weights alone would take 41 of the 70, the
 //          histogram's places and its two shared atomics the rest]
 //   cut    rows that keep all: the token's tile by a running sum, then the token; top-p: the
 //          bin of the cut from the histogram and, if little lies up to it, the token
 //          [22, 20; latency]
 //   weigh  again, for the other rows with top-p: the weights above that bin by tile, and its
-//          elements in a list  [31, 24; memory]
+//          elements in a list  [28, 23; instructions, of the quarter of the rows left]
 //   cut    again: the cut from the sorted list, and the token  [26, 19; latency]
 // Rows that none of this settles (more equal logits than the list holds, top-k of more, a cut
 // in the last octaves) are left to sample_kernel, which takes them from a list.
@@ -400,7 +400,11 @@ constexpr int kStreamThreads = 256;           // of the passes
 // 1024 FP32 rows with settings of every kind, 512 BF16 rows with top-p) at 512 threads and 65 /
 // 231 / 171 at 256, the cut 62 / 232 / 197 at 512 and 63 / 233 / 181 at 256 (when each was set).
 constexpr int kPickThreads = 512, kCutThreads = 256;
-constexpr int kTilesPerCta = 16;              // of the weighing kernels
+// Tiles a CTA of the weighing kernels: the most, and half of them in calls that then have at
+// most kFewCtas CTAs an SM (us of whole calls, half against the most: with top-p 64 rows of FP32
+// 62 / 65, 128 of BF16 76 / 85, 384 of FP32 168 / 163; 1024 with settings of every kind 239 / 227).
+constexpr int kTilesPerCta = 16;
+constexpr int kFewCtas = 13;
 constexpr int kChunkTop = 1024;
 
 // What the streaming kernels know of a row between them.
@@ -417,6 +421,7 @@ struct RowState {
 struct StreamArgs {
   SampleArgs a;
   int tiles;                // per row
+  int per_cta;              // of the weighing kernels, kTilesPerCta at most
   uint32_t* tops;           // [N][tiles * 32] keys
   uint64_t* mass;           // [N][tiles]
   uint64_t* bin_mass;       // [N][kBins]
@@ -667,19 +672,28 @@ __device__ __forceinline__ uint32_t most_in(const Window& window, int bin, uint6
   return (uint32_t)__fmul_rn(__ull2float_rn(mass), exp2f((bin + 1) / window.scale - 31.f));
 }
 
+// The elements of the cut's bin that a CTA found, at most all of them.  They join the row's
+// list by one addition to its length: one addition an element, each waited for, made the pass
+// 31 us instead of 28 (512 rows of BF16, a quarter of them still under way).
+struct Found {
+  uint64_t entry[kList];
+  uint32_t n, at;
+};
+
 // The weight of tiles: of the rows that keep all (but what min-p drops) and, with their
 // histogram over the first octaves, of the rows with top-p; or (kAbove) of what lies above
 // the bin the cut falls in, with a list of the bin's elements.
 enum WeighWhat { kAll, kAtLeast, kBinned, kAboveBin };
 template <bool kFp32, WeighWhat kWhat>
-__device__ __forceinline__ void weigh_tiles(const StreamArgs& p, int row, int t0, const RowState& st,
-                                            float c, uint32_t least, uint32_t* lo, uint32_t* hi) {
+__device__ __forceinline__ void weigh_tiles(const StreamArgs& p, int row, int t0, int t1,
+                                            const RowState& st, float c, uint32_t least,
+                                            uint32_t* lo, uint32_t* hi, Found* found) {
   using R = Row<kFp32, false>;
   constexpr int kE = R::kElems;
   const Window window(0.f, kNear);
   R r;
   const int vectors = r.begin(p.a, row);
-  for (int t = t0 + (threadIdx.x >> 5); t < min(t0 + kTilesPerCta, p.tiles); t += kStreamThreads / 32) {
+  for (int t = t0 + (threadIdx.x >> 5); t < t1; t += kStreamThreads / 32) {
     at_tile(r, vectors, t);
     uint64_t sum = 0;
     r.template each<true, 4>([&](int v, const uint4& q) {
@@ -699,9 +713,8 @@ __device__ __forceinline__ void weigh_tiles(const StreamArgs& p, int row, int t0
         if (kWhat == kAboveBin) {
           keep = z[e] > st.hi && w[e] >= least;
           if (z[e] >= st.lo && z[e] <= st.hi) {
-            const int at = atomicAdd(&p.state[row].listed, 1);   // in any order: it is sorted
-            if (at < kList && RLK_STORE_OK(row < p.a.N, &g_err_sample))
-              p.list[(int64_t)row * kList + at] = entry_of(z[e], r.id_of(v) + e);
+            const uint32_t at = atomicAdd(&found->n, 1u);        // in any order: it is sorted
+            if (at < kList) found->entry[at] = entry_of(z[e], r.id_of(v) + e);
           }
         }
         if (keep) sum = add_wide(sum, w[e]);
@@ -730,20 +743,31 @@ __global__ void __launch_bounds__(kStreamThreads) sample_weigh_kernel(const __gr
   const int row = blockIdx.x / per_row;
   const RowState st = p.state[row];
   if (kAbove ? st.status != kCutBin : st.status != kWeigh && st.status != kWeighBins) return;
-  const int t0 = (blockIdx.x - row * per_row) * kTilesPerCta;
+  const int t0 = (blockIdx.x - row * per_row) * p.per_cta, t1 = min(t0 + p.per_cta, p.tiles);
   bool bad;
   const Filter f = settings_of(p.a, row, &bad);
   if (kAbove) {
-    weigh_tiles<kFp32, kAboveBin>(p, row, t0, st, f.c, f.least, lo, hi);
+    __shared__ Found found;
+    if (threadIdx.x == 0) found.n = 0;
+    __syncthreads();
+    weigh_tiles<kFp32, kAboveBin>(p, row, t0, t1, st, f.c, f.least, lo, hi, &found);
+    __syncthreads();
+    const int n = (int)min(found.n, (uint32_t)kList);
+    if (n == 0) return;
+    if (threadIdx.x == 0) found.at = (uint32_t)atomicAdd(&p.state[row].listed, n);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kStreamThreads)
+      if (found.at + i < kList && RLK_STORE_OK(row < p.a.N, &g_err_sample))
+        p.list[(int64_t)row * kList + found.at + i] = found.entry[i];
   } else if (st.status == kWeigh) {
     if (f.least == 0)
-      weigh_tiles<kFp32, kAll>(p, row, t0, st, f.c, 0, lo, hi);
+      weigh_tiles<kFp32, kAll>(p, row, t0, t1, st, f.c, 0, lo, hi, nullptr);
     else
-      weigh_tiles<kFp32, kAtLeast>(p, row, t0, st, f.c, f.least, lo, hi);
+      weigh_tiles<kFp32, kAtLeast>(p, row, t0, t1, st, f.c, f.least, lo, hi, nullptr);
   } else {
     for (int i = threadIdx.x; i < kBins; i += kStreamThreads) lo[i] = hi[i] = 0;
     __syncthreads();
-    weigh_tiles<kFp32, kBinned>(p, row, t0, st, f.c, 0, lo, hi);
+    weigh_tiles<kFp32, kBinned>(p, row, t0, t1, st, f.c, 0, lo, hi, nullptr);
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kStreamThreads)
       if ((lo[i] | hi[i]) && RLK_STORE_OK(row < p.a.N, &g_err_sample))
@@ -1009,7 +1033,9 @@ cudaError_t launch_stream(const SampleArgs& a, const SamplePlan& plan, uint8_t* 
   p.left = reinterpret_cast<int*>(ws + plan.off_left);
   p.list = reinterpret_cast<uint64_t*>(ws + plan.off_list);
   const int top_ctas = (int)ceil_div(plan.tiles, kStreamThreads / 32);
-  const int weigh_ctas = (int)ceil_div(plan.tiles, kTilesPerCta);
+  const bool few = a.N * ceil_div(plan.tiles, kTilesPerCta) <= kFewCtas * sms;
+  p.per_cta = few ? kTilesPerCta / 2 : kTilesPerCta;
+  const int weigh_ctas = (int)ceil_div(plan.tiles, p.per_cta);
   const size_t smem_ids = sizeof(SampleSmem) + sizeof(Hits) + (size_t)plan.tiles * 32 * sizeof(uint16_t);
   const size_t smem_pick = smem_ids + (size_t)plan.tiles * 32 * sizeof(uint32_t);
   const dim3 rows((unsigned)a.N), tops((unsigned)(a.N * top_ctas)), weighs((unsigned)(a.N * weigh_ctas));
