@@ -78,6 +78,15 @@ __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
 }
 __device__ __forceinline__ uint64_t both(float a) { return pack_f2(a, a); }
 
+// A product that stays rounded by itself: written as mul.rn.f32x2, the assembler merges it with
+// a sum that follows into one fused operation, rounding once (the single mul.rn.f32 is left
+// alone).  a * b + -0 is the rounded product, signed zeros included; the -0 is read from memory
+// that a host may write, so that nothing can be folded.
+__constant__ float g_minus_zero = -0.f;
+__device__ __forceinline__ uint64_t mul_alone_f2(uint64_t a, uint64_t b, uint64_t minus_zero) {
+  return fma_f2(a, b, minus_zero);
+}
+
 constexpr float kRound = 12582912.f;         // 1.5 * 2^23
 
 __device__ __forceinline__ void weights_of(float x0, float x1, uint32_t& w0, uint32_t& w1) {
@@ -88,9 +97,10 @@ __device__ __forceinline__ void weights_of(float x0, float x1, uint32_t& w0, uin
   const uint64_t t = add_f2(x, both(kRound));
   const uint64_t n = add_f2(t, both(-kRound));
   const uint64_t f = fma_f2(n, both(-1.f), x);     // x - n, exact
+  const uint64_t minus_zero = both(g_minus_zero);
   uint64_t y = both(kExp2[0]);
 #pragma unroll
-  for (int i = 1; i < 6; ++i) y = add_f2(mul_f2(y, f), both(kExp2[i]));
+  for (int i = 1; i < 6; ++i) y = add_f2(mul_alone_f2(y, f, minus_zero), both(kExp2[i]));
   float t0, t1, y0, y1;
   unpack_f2(t, t0, t1);
   unpack_f2(y, y0, y1);
