@@ -686,14 +686,19 @@ __device__ __noinline__ void finish_short(B b, Filter f, const SampleArgs& a, in
   const uint32_t id = (uint32_t)x;
   uint32_t w = i < n && (uint32_t)i < f.k ? f.weight(z) : 0, unused = 0;
   uint64_t upto = w;
+  if (i == 0) s->answer = 0;
   block_scan(b, unused, upto);
   if (i == B::kThreads - 1) s->total[0] = upto;
   __syncthreads();
   const uint64_t most = f.share(f.need_k ? s->total[0] : total_mass);
   if (!(upto - w < most && w >= f.least)) w = 0;
-  const int kept = __syncthreads_count(w > 0);     // the first of the list, all of them
-  if (w) s->list[i] = ((uint64_t)id << 32) | w;
+  // A lower logit can have the larger weight, by a few units: min-p may drop one before another
+  // that it keeps, so the places up to the last kept are taken, the dropped with no weight.
+  if (i < n) s->list[i] = ((uint64_t)id << 32) | w;
+  const int last = __reduce_max_sync(kFull, w ? i + 1 : 0);
+  if ((i & 31) == 0) atomicMax(&s->answer, last);
   __syncthreads();
+  const int kept = s->answer;
   if (i >= kept) return;
   uint64_t before = 0, total = 0;                  // kept weights of lower ids; of all
 #pragma unroll 2
