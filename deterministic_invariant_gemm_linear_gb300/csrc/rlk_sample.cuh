@@ -772,7 +772,8 @@ __device__ __forceinline__ void finish_block(const B& b, const Filter& f, const 
 }
 
 // The least logit whose bin (below the top m) is at most `bin` < kBins; the warp tries 32
-// places of the range of keys at a time.  Every warp may call it by itself.
+// places of the range of keys at a time.  Every warp may call it by itself.  m is a number: from
+// the key above all logits (NaN, +inf) the places would pass 2^32 and the search need not end.
 __device__ __noinline__ float least_logit(float m, float c, Window window, int bin) {
   const int lane = threadIdx.x & 31;
   uint32_t no = key_of(-INFINITY), yes = key_of(m);

@@ -303,7 +303,7 @@ __device__ __forceinline__ void sample_row(const Block<kT>& b, const SampleArgs&
     if ((uint32_t)__syncthreads_count(my_bin <= reach) >= f.k) {
       const float least = logit_of(s->reached);
       list_range(b, r, top >= least, least, INFINITY);
-    } else {                                       // fewer have weight than k
+    } else if (cta_top != kFull) {                 // fewer have weight than k
       list_range_cold(b, r, my_bin < kBins, least_logit(m, c, all_octaves(), kBins - 1), INFINITY);
     }
     push_count(b);
