@@ -770,7 +770,7 @@ class _Distill:
         gh = torch.empty((N, H), dtype=out_dtype, device=dev) if want[0] else None
         gw = torch.empty((V, H), dtype=out_dtype, device=dev) if want[1] else None
         gb = torch.empty(V, dtype=torch.float32, device=dev) if want[2] else None
-        ldz = 0 if logits is None else logits.stride(0) if N > 1 else -(-V // 8) * 8
+        logits, ldz = (None, 0) if logits is None else _kept_logits(logits, N, V)
         dt = _DT[out_dtype]
         lib_ = lib()
         with _on(dev):
@@ -785,6 +785,20 @@ class _Distill:
                 _ptr(logits), ldz, _ptr(grad_loss), _ptr(gh), dt, H, _ptr(gw), dt, H, _ptr(gb),
                 _ptr(ws), n, _stream_ptr(stream)), "rlk_linear_distill_backward")
         return gh, gw, gb, ws
+
+
+def _kept_logits(z: torch.Tensor, N: int, V: int):
+    """(logits, pitch) as the backward reads them: rows of whole 32-byte sectors, 8 ceil(V / 8)
+    readable numbers each.  linear_distill's own are; others are copied into such rows."""
+    width = -(-V // 8) * 8
+    ld = z.stride(0) if N > 1 else width
+    room = z.untyped_storage().nbytes() // 4 - z.storage_offset()
+    if ld >= width and ld % 8 == 0 and z.data_ptr() % 32 == 0 and room >= (N - 1) * ld + width and \
+            (V == 1 or z.stride(1) == 1):
+        return z, ld
+    rows = torch.zeros((N, width), dtype=torch.float32, device=z.device)
+    rows[:, :V] = z[:, :V]
+    return rows, width
 
 
 def linear_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
@@ -831,8 +845,7 @@ def linear_distill_backward(hidden: torch.Tensor, weight: torch.Tensor, teacher_
     g1 = grad_loss.reshape(-1).contiguous().float()
     if l1.numel() != d.N or g1.numel() != d.N:
         raise ValueError("lse and grad_loss must have one value per hidden row")
-    if logits is not None and (logits.dtype != torch.float32 or tuple(logits.shape) != (d.N, d.V) or
-                               (d.V > 1 and logits.stride(1) != 1)):
+    if logits is not None and (logits.dtype != torch.float32 or tuple(logits.shape) != (d.N, d.V)):
         raise ValueError("logits must be those of linear_distill(..., return_logits=True)")
     if grad_bias is None:
         grad_bias = bias is not None
