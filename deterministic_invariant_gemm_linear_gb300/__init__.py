@@ -33,6 +33,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -220,6 +221,33 @@ def _on(device):
     return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
+def _used_by(stream, tensors):
+    """Marks the memory of CUDA tensors as in use by a stream that it was not allocated on."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+
+
+def _streamed(call):
+    """An entry point's stream argument: the whole call, its copies and allocations included, is
+    made with that stream current, so what it makes and drops is ordered and reused there.  The
+    caller orders the stream after the inputs, and its own work after the stream; inputs and
+    outputs may be dropped on either side."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **named):
+        if stream is None:
+            return call(*args, **named)
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            out = call(*args, **named)
+        if stream != here:
+            _used_by(stream, args)
+            _used_by(stream, named.values())
+            _used_by(here, out if isinstance(out, tuple) else (out,))
+        return out
+    return run
+
+
 def _matrix(t: torch.Tensor, name: str):
     """(tensor, leading dimension) for a 2-D row-major operand (unit column stride)."""
     if t.dim() != 2:
@@ -265,6 +293,7 @@ def det_gemm_tile_plan(op: int, out_rows: int, out_cols: int, red: int, sm_count
     return {"tile_cols": t.value, "split_blocks": b.value, "launches": n.value}
 
 
+@_streamed
 def linear_logp(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
                 bias: torch.Tensor | None = None, *, return_target_logit: bool = False,
                 stream=None, num_splits: int | None = None):
@@ -357,9 +386,14 @@ class LinearLogpCall:
                     raise RlkError(2, "rlk_linear_logp_splits_workspace_size")
                 self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
 
+    def _use(self, stream):
+        if stream is not None and stream != torch.cuda.current_stream(stream.device):
+            _used_by(stream, (self.h, self.w, self.t, self.bias, self.logp, self.lse, self.zt, self.ws))
+
     def partials(self, stream=None):
         if self.num_splits is not None:
             raise RuntimeError("the two-stage calls use the V-only split")
+        self._use(stream)
         _check(lib().rlk_linear_logp_partials(
             _ptr(self.h), self.N, self.H, self.ldh, _ptr(self.w), self.V, self.ldw, _ptr(self.bias),
             _ptr(self.t), self.tstride, _ptr(self.ws), self.ws.numel(), _stream_ptr(stream)),
@@ -368,12 +402,14 @@ class LinearLogpCall:
     def combine(self, stream=None):
         if self.num_splits is not None:
             raise RuntimeError("the two-stage calls use the V-only split")
+        self._use(stream)
         _check(lib().rlk_linear_logp_combine(
             self.N, self.V, _ptr(self.t), self.tstride, _ptr(self.logp), _ptr(self.lse),
             _ptr(self.zt), _ptr(self.ws), self.ws.numel(), _stream_ptr(stream)),
             "rlk_linear_logp_combine")
 
     def __call__(self, stream=None):
+        self._use(stream)
         if self.num_splits is None:
             _check(lib().rlk_linear_logp(
                 _ptr(self.h), self.N, self.H, self.ldh, _ptr(self.w), self.V, self.ldw,
@@ -399,6 +435,7 @@ def vocab_shard_range(V: int, num_shards: int, shard: int):
     return tuple(x.value for x in out)
 
 
+@_streamed
 def linear_logp_shard_partials(hidden: torch.Tensor, weight_shard: torch.Tensor,
                                target: torch.Tensor, V: int, split_begin: int, split_end: int,
                                bias_shard: torch.Tensor | None = None, *, ld_partials: int = 0,
@@ -437,6 +474,7 @@ def linear_logp_shard_partials(hidden: torch.Tensor, weight_shard: torch.Tensor,
     return partials, zt
 
 
+@_streamed
 def linear_logp_combine_shards(partials: torch.Tensor, target_logits: torch.Tensor,
                                split_offsets, target: torch.Tensor, V: int, *,
                                return_target_logit: bool = False, stream=None):
@@ -496,6 +534,7 @@ def exchange_shard_partials(partials: torch.Tensor, target_logit: torch.Tensor, 
     return _all_gather(partials, group), _all_gather(target_logit, group)
 
 
+@_streamed
 def sum_partials_ordered(parts: torch.Tensor, out_dtype=torch.float32, *, stream=None):
     """out = parts[0] + parts[1] + ... (FP32, ascending part order) for parts [P, rows, cols]
     fp32, written as out_dtype (bf16 rounds to nearest even)."""
@@ -553,6 +592,7 @@ def vocab_parallel_linear_logp(hidden: torch.Tensor, weight_shard: torch.Tensor,
     return tuple(o.reshape(lead) for o in out)
 
 
+@_streamed
 def linear_logp_backward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
                          lse: torch.Tensor, grad_logp: torch.Tensor, bias: torch.Tensor | None = None,
                          *, grad_hidden: bool = True, grad_weight: bool = True,
@@ -649,6 +689,7 @@ def _per_row(value, name: str, N: int, dtype):
     return value.reshape(-1).contiguous(), 0
 
 
+@_streamed
 def sample_logits(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.0, top_k=0,
                   top_p=1.0, min_p=0.0, stream=None):
     """token (int64), logp (FP32), shaped like logits' leading dims: one token a row.
@@ -801,6 +842,7 @@ def _kept_logits(z: torch.Tensor, N: int, V: int):
     return rows, width
 
 
+@_streamed
 def linear_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
                    teacher_logits: torch.Tensor, bias: torch.Tensor | None = None, *,
                    temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
@@ -826,6 +868,7 @@ def linear_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torc
     return (loss, lse, logits[:, :d.V]) if return_logits else (loss, lse)
 
 
+@_streamed
 def linear_distill_backward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
                             teacher_logits: torch.Tensor, lse: torch.Tensor,
                             grad_loss: torch.Tensor, bias: torch.Tensor | None = None, *,
@@ -926,6 +969,7 @@ def _flatten_rows(t: torch.Tensor) -> torch.Tensor:
     return t.reshape(-1, t.size(-1)) if t.dim() != 2 else t
 
 
+@_streamed
 def det_gemm_fwd(A: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat16, *, stream=None):
     """C = A . B; A [..., M, K] bf16 (leading dims flattened into rows), B [K, N] bf16."""
     _require_cuda(A, B)
@@ -944,6 +988,7 @@ def det_gemm_fwd(A: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat16, *, 
     return C.reshape(*lead, N)
 
 
+@_streamed
 def det_gemm_da(dC: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat16, *, stream=None):
     """dA = dC . B^T; dC [..., M, N] bf16 or fp32 (fp32 is rounded to bf16 first), B [K, N]."""
     _require_cuda(dC, B)
@@ -963,6 +1008,7 @@ def det_gemm_da(dC: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat16, *, 
     return dA.reshape(*lead, K)
 
 
+@_streamed
 def det_gemm_db(A: torch.Tensor, dC: torch.Tensor, out_dtype=torch.bfloat16, *, stream=None):
     """dB = A^T . dC summed over every row; A [..., M, K] bf16, dC [..., M, N] bf16 or fp32."""
     _require_cuda(A, dC)
@@ -981,6 +1027,7 @@ def det_gemm_db(A: torch.Tensor, dC: torch.Tensor, out_dtype=torch.bfloat16, *, 
     return dB
 
 
+@_streamed
 def det_gemm_fwd_accum_fp32_(C: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, stream=None):
     """In place: C (fp32 [M, N]) += A . B, the product formed as by det_gemm_fwd and
     added to C once, after the full K reduction."""
@@ -1004,6 +1051,7 @@ def det_gemm_fwd_accum_fp32_(C: torch.Tensor, A: torch.Tensor, B: torch.Tensor, 
     return C
 
 
+@_streamed
 def det_linear(X: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16, *, stream=None):
     """Y = X . W^T with the weight stored [N, K]; X [..., K] bf16 (leading dims are rows)."""
     _require_cuda(X, W)
@@ -1022,6 +1070,7 @@ def det_linear(X: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16, *, st
     return Y.reshape(*lead, N)
 
 
+@_streamed
 def det_linear_dx(dY: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16, *, stream=None):
     """dX = dY . W for Y = X . W^T; dY [..., N] bf16 or fp32 (fp32 rounded to bf16 first)."""
     _require_cuda(dY, W)
@@ -1041,6 +1090,7 @@ def det_linear_dx(dY: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16, *
     return dX.reshape(*lead, K)
 
 
+@_streamed
 def det_linear_dw(dY: torch.Tensor, X: torch.Tensor, out_dtype=torch.bfloat16, *, stream=None):
     """dW [N, K] = dY^T . X summed over every row; dY [..., N] bf16 or fp32, X [..., K] bf16."""
     _require_cuda(dY, X)
@@ -1080,6 +1130,7 @@ def _two_grads(fn, size_fn, g, x, w, out_shapes, out_dtype, want, stream):
     return tuple(outs)
 
 
+@_streamed
 def det_gemm_backward(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                       out_dtype=torch.bfloat16, *, grad_a: bool = True, grad_b: bool = True,
                       stream=None):
@@ -1093,6 +1144,7 @@ def det_gemm_backward(dC: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                       stream)
 
 
+@_streamed
 def det_linear_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
                         out_dtype=torch.bfloat16, *, grad_x: bool = True, grad_w: bool = True,
                         stream=None):
