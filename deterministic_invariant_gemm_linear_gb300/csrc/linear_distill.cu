@@ -291,7 +291,8 @@ __device__ __forceinline__ void distill_epilogue(const VocabSched& sc, const Dis
         }
         while (__any_sync(0xffffffffu, slot.id < vbase + 32)) {
           if (slot.id < vbase + 32) {
-            d = __fadd_rn(d, __fmul_rn(slot.w, chunk_at(z, slot.id - vbase)));
+            const float zk = chunk_at(z, slot.id - vbase);
+            if (slot.w != 0.f) d = __fadd_rn(d, __fmul_rn(slot.w, zk));   // 0 of a banned id is 0
             slot.next();
           }
         }

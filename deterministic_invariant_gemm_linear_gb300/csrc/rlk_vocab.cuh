@@ -5,6 +5,7 @@
 // explicitly, so all kernels that fold the same logits get the same (m, s) bits.
 #pragma once
 
+#include <float.h>
 #include <math.h>
 
 #include "rlk_device.cuh"
@@ -85,7 +86,10 @@ __device__ __forceinline__ float chunk_at(const float (&z)[32], int di) {
 
 // Folds the chunk into (m, s) with s = sum 2^((z - m) * scale); scale = log2(e), or
 // log2(e) / T for logits at temperature T.  z - m is formed first, so the running
-// maximum's own term is exactly 2^0 = 1: s >= 1 always.  At least one z is finite.
+// maximum's own term is exactly 2^0 = 1: s >= 1 once a logit was above -inf.  m is at
+// least the lowest finite number: a chunk of banned logits (bias -inf) adds 2^-inf = 0
+// each where -inf - -inf would be NaN, and a NaN logit reaches s below a finite m, so
+// that the merge does not take the split for an empty one.
 __device__ __forceinline__ void chunk_fold(const float (&z)[32], float scale, float& m, float& s) {
   // chunk maximum (fixed pairwise tree)
   float t[16];
@@ -95,7 +99,7 @@ __device__ __forceinline__ void chunk_fold(const float (&z)[32], float scale, fl
   for (int w = 8; w >= 1; w >>= 1)
 #pragma unroll
     for (int i = 0; i < w; ++i) t[i] = fmaxf(t[i], t[i + w]);
-  const float mn = fmaxf(m, t[0]);            // finite: vbase < V so z[0] is a real logit
+  const float mn = fmaxf(fmaxf(m, t[0]), -FLT_MAX);
   const float down = ex2_approx(__fmul_rn(__fsub_rn(m, mn), scale));   // m = -inf -> 0
   float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

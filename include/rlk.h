@@ -206,7 +206,8 @@ RLK_API size_t rlk_linear_logp_workspace_size(const void* hidden, int64_t N, int
  *
  *  hidden        BF16 [N, H], leading dimension ld_hidden (>= H)
  *  weight        BF16 [V, H] (the lm-head weight), leading dimension ld_weight (>= H)
- *  bias          FP32 [V] or NULL; added in FP32 after the full H reduction
+ *  bias          FP32 [V] or NULL; added in FP32 after the full H reduction; -inf bans
+ *                an id (a row whose ids are all banned has lse -inf and logp NaN)
  *  target        int64, row r reads target[r * target_stride]; stride 0 means one
  *                id shared by every row (an expanded target)
  *  logp, lse     FP32 [N] outputs
