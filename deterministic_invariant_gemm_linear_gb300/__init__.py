@@ -854,7 +854,7 @@ def linear_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torc
     with the teacher's logits there, teacher_logits [..., K] bf16 or fp32.  A slot whose id is
     outside [0, V) (pad with -1) or whose logit is -inf is empty; a row without used slots has
     loss 0.  The teacher's probabilities are normalised over its slots, or by teacher_lse [...]
-    fp32 (its log-sum-exp over its whole vocabulary at this temperature).  With return_logits
+    fp32 (its log-sum-exp over its whole vocabulary at this temperature, 1e-4 .. 100).  With return_logits
     also the student's logits z [N, V] fp32 (bias included, not divided by T), which
     linear_distill_backward can take in place of forming them again.  Forward only: use
     linear_distill_trainable for gradients.

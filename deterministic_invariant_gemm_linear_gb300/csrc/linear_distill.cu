@@ -6,7 +6,6 @@
 //   log q_k = t_k / T - L,  L = teacher_lse[r], or log sum_k exp(t_k / T) if not given
 //   z[r, v] = hidden[r] . W[v] (+ bias[v]),   lse[r] = log sum_v exp(z[r, v] / T)
 //   loss[r] = T^2 sum_k q_k (log q_k - z[r, id_k] / T + lse[r])
-//           = T^2 ((E - D / T) + Q lse),  E = sum q log q,  D = sum q z,  Q = sum q
 // and, with g[r] = dL/dloss[r],
 //   G[r, v] = dL/dz[r, v] = g[r] T (Q exp(z[r, v] / T - lse[r]) - sum_{k: id_k = v} q_k)
 //   grad_hidden = G . W,  grad_weight = G^T . hidden,  grad_bias = sum_r G.
@@ -14,15 +13,15 @@
 //
 // The work is the product hidden . W^T (2 N H V operations, tensor cores); everything
 // else rides along so that the [N, V] logits need not exist:
-//  * distill_lists_kernel (one block per row): q, E and Q, the used slots sorted by id
+//  * distill_lists_kernel (one block per row): q and its sums, the used slots sorted by id
 //    (rank by counting: K^2 compares over the block, and a stable order whatever the
 //    lists hold), and where each vocabulary split's ids start.
 //  * distill_partials_kernel / distill_solo_kernel: the tcgen05 loops of the fused
 //    linear-logp (2-SM pairs; one CTA for at most 128 rows).  The epilogue thread that
 //    owns a row folds (m, s) as there and walks the row's sorted ids alongside the
 //    columns: an id costs one compare per 32 columns and, when hit, one select tree,
-//    so D is gathered from the accumulators and no row of W is read twice.
-//  * distill_combine_kernel: the fixed-order merge over the splits.
+//    so D = sum q z is gathered from the accumulators and no row of W is read twice.
+//  * distill_combine_kernel: the fixed-order merge over the splits, and the loss.
 //  * distill_grad_kernel: the same loop again; the epilogue forms G in FP32, takes the
 //    32-row column sums for grad_bias from it, and stores it rounded to BF16, the type
 //    in which the two products (det_gemm) read it.
@@ -30,11 +29,14 @@
 //    (4 N V bytes): one pass at memory speed in place of the product's 2 N H V operations.
 //
 // Sums are FP32 and every logit is the tensor core's FP32 sum over H, whose own error at
-// H = 4096 is some 1e-6 of the logit: lse and loss are within 6e-6 (relative, worst of 60
-// random calls at H = 2048 and 4096) of 64 bits.  The one rounding to fewer bits is G's to
-// BF16, the type the products' tensor instructions read: it raises the gradients' error
-// against 64 bits (relative, root mean square) from the 0.0017 of their own BF16 rounding to
-// 0.0024.  grad_bias is summed before it.
+// H = 4096 is some 1e-6 of the logit: lse is within 6e-6 (relative, worst of 60 random calls at
+// H = 2048 and 4096) of 64 bits.  The loss is a difference of parts as large as |z| T and
+// T^2 log V, so its error is absolute: beside the logits' own, about 2e-7 T max|z| and 3e-7
+// max(T^2 Q, loss), measured with exact logits.  At T = 1000 that is as large as the loss of a
+// student close to the teacher, whatever the sums are joined in, so T ends at 100.  The one
+// rounding to fewer bits is G's to BF16, the type the products' tensor instructions read: it
+// raises the gradients' error against 64 bits (relative, root mean square) from the 0.0017 of
+// their own BF16 rounding to 0.0024.  grad_bias is summed before it.
 #include <limits.h>
 #include <math.h>
 
@@ -61,12 +63,13 @@ constexpr int64_t kUnitLimit = int64_t(1) << 31;
 // ---------------------------------------------------------------- teacher lists
 // The teacher's lists as the epilogues read them: row r's used slots in ascending id
 // order at [r * K], their number cut at span boundaries by first[r * (spans + 1) + j]
-// (slots first[j] .. first[j + 1] - 1 have ids in span j), and E, Q of the row.
+// (slots first[j] .. first[j + 1] - 1 have ids in span j), and two sums of the row: E and
+// the norm of q for the forward, Q (second) for the backward.
 struct Lists {
   int* ids;
   float* q;
   uint16_t* first;
-  float2* eq;
+  float2* sums;
   int K, spans;
   int64_t span;      // vocabulary ids per span
 };
@@ -80,6 +83,7 @@ struct ListArgs {
   const float* lse;       // the teacher's own log-sum-exp at this temperature, or null
   float temperature;
   int N, V;
+  bool backward;
 };
 
 // Sum and maximum over the block in a fixed order: every thread's value through a xor
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(256) distill_lists_kernel(ListArgs a, Lists ou
   extern __shared__ int smem_lists[];
   int* key = smem_lists;                                    // [K] id, or INT_MAX when empty
   int* sorted = smem_lists + out.K;                         // [K]
-  float* val = reinterpret_cast<float*>(sorted + out.K);    // [K] t / T, then q
+  float* val = reinterpret_cast<float*>(sorted + out.K);    // [K] t, then q
   __shared__ float warp_out[8];
   __shared__ int used;
   griddep_wait();
@@ -123,43 +127,45 @@ __global__ void __launch_bounds__(256) distill_lists_kernel(ListArgs a, Lists ou
                         ? __ldg(static_cast<const float*>(a.logits) + at)
                         : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.logits) + at)
                                           << 16);
-    const float x = __fdiv_rn(t, a.temperature);
-    const bool on = id >= 0 && id < a.V && x != -INFINITY;
+    const bool on = id >= 0 && id < a.V && t != -INFINITY;
     key[k] = on ? (int)id : INT_MAX;
-    val[k] = on ? x : -INFINITY;
+    val[k] = on ? t : -INFINITY;
     top = fmaxf(top, val[k]);
   }
   if (threadIdx.x == 0) used = 0;
-  float norm;
+  // y = (t - top) / T <= 0 is small where T is large, and so keeps the digits that T^2 needs
+  top = block_fold<true>(top, warp_out);
+  float norm = 1.f, shift = 0.f;                   // q = exp(y - shift) / norm
   if (a.lse) {
-    norm = __ldg(a.lse + row);
-    __syncthreads();
+    shift = __fdiv_rn(__fmaf_rn(__ldg(a.lse + row), a.temperature, -top), a.temperature);
   } else {
-    top = block_fold<true>(top, warp_out);
     float s = 0.f;
     for (int k = threadIdx.x; k < K; k += blockDim.x)
-      if (key[k] != INT_MAX) s = __fadd_rn(s, expf(__fsub_rn(val[k], top)));
-    norm = __fadd_rn(top, logf(block_fold<false>(s, warp_out)));
+      if (key[k] != INT_MAX)
+        s = __fadd_rn(s, expf(__fdiv_rn(__fsub_rn(val[k], top), a.temperature)));
+    norm = block_fold<false>(s, warp_out);
   }
   float e = 0.f, sum = 0.f;
   int n = 0;
   for (int k = threadIdx.x; k < K; k += blockDim.x) {
     float q = 0.f;
     if (key[k] != INT_MAX) {
-      const float lq = __fsub_rn(val[k], norm);
-      q = expf(lq);
-      if (q > 0.f) e = __fadd_rn(e, __fmul_rn(q, lq));
+      const float y = __fdiv_rn(__fsub_rn(val[k], top), a.temperature);
+      q = __fdiv_rn(expf(__fsub_rn(y, shift)), norm);
+      if (q > 0.f) e = __fadd_rn(e, __fmul_rn(q, y));
       sum = __fadd_rn(sum, q);
       ++n;
     }
     val[k] = q;
   }
-  e = block_fold<false>(e, warp_out);
-  sum = block_fold<false>(sum, warp_out);
+  if (a.backward)
+    sum = block_fold<false>(sum, warp_out);
+  else
+    e = block_fold<false>(e, warp_out);
   if (n) atomicAdd(&used, n);      // a whole number: its order does not matter
   __syncthreads();
   if (threadIdx.x == 0 && RLK_STORE_OK(row < a.N, &g_err_linear_distill))
-    out.eq[row] = make_float2(e, sum);
+    out.sums[row] = a.backward ? make_float2(0.f, sum) : make_float2(e, a.lse ? top : norm);
   for (int k = threadIdx.x; k < K; k += blockDim.x) {
     const int id = key[k];
     int rank = 0;
@@ -382,41 +388,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   solo_teardown(tmem);
 }
 
+struct CombineArgs {
+  const float2* ms;
+  const float* d;
+  Lists lists;
+  const float* teacher_lse;
+  int N, S;
+  float temperature, scale;
+  double inv_t;
+  float* loss;
+  float* lse;
+};
+
 // One warp per row: (m, s) and D over the splits, lane l taking splits l, l + 32, ...
-// ascending, then a xor butterfly of symmetric sums (all lanes end with the same bits).
+// ascending, then a xor butterfly of symmetric sums (all lanes end with the same bits); Q over
+// the slots alike.  Then a thread per row: with y = (t - top) / T and L the teacher's norm,
+//   loss = T^2 (sum q y - (D - M Q) / T + Q (log s - L)),  L = log sum exp y, or lse - top / T.
+// T^2 multiplies what the parts lost, and parts of size log V lose 5e-7 each (in FP32, joined
+// from lse, the loss was off by 1e-4 at T = 10 and 1e-2 at T = 100 where it is 0.5): so the two
+// sums of exponentials meet in one logarithm of their ratio, and the parts are joined in FP64.
+// What is left is the error of s, some 2e-7 of T^2.  At T = 1 the rounded lse stands in for
+// M + log s, so that one slot gives -logp exactly.
 // 12 bytes a split and row; latency: 11 us for 4096 rows of 594 splits (29 MB, from L2).
 __global__ void __launch_bounds__(256)
-    distill_combine_kernel(const float2* __restrict__ ms, const float* __restrict__ dz,
-                           const float2* __restrict__ eq, int N, int S, float temperature,
-                           float scale, float* __restrict__ loss, float* __restrict__ lse) {
+    distill_combine_kernel(const __grid_constant__ CombineArgs a) {
+  __shared__ float4 parts[8];                      // M, s, D, Q of the block's rows
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  if (row >= N) return;
-  float M = -INFINITY, s = 0.f, d = 0.f;
-  for (int j = lane; j < S; j += 32) {
-    const float2 v = ms[(int64_t)row * S + j];
-    merge_ms(M, s, v.x, v.y, scale);
-    d = __fadd_rn(d, dz[(int64_t)row * S + j]);
+  int row = blockIdx.x * 8 + threadIdx.x;
+  const bool ends = threadIdx.x < 8 && row < a.N;  // the row that this thread ends: loads go ahead
+  float2 t = make_float2(0.f, 0.f);
+  float teacher = 0.f;
+  if (ends) {
+    t = a.lists.sums[row];
+    if (a.teacher_lse) teacher = a.teacher_lse[row];
   }
+  row = blockIdx.x * 8 + threadIdx.x / 32;
+  if (row < a.N) {
+    float M = -INFINITY, s = 0.f, d = 0.f, Q = 0.f;
+    const float* q = a.lists.q + (int64_t)row * a.lists.K;
+    const float2* ms = a.ms + (int64_t)row * a.S;
+    const float* dz = a.d + (int64_t)row * a.S;
+#pragma unroll 4
+    for (int k = lane; k < a.lists.K; k += 32) Q = __fadd_rn(Q, __ldg(q + k));
+    for (int j0 = lane; j0 < a.S; j0 += 128) {     // four splits' loads before the first merge
+      float2 v[4];
+      float x[4];
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, M, off);
-    const float s2 = __shfl_xor_sync(0xffffffffu, s, off);
-    merge_ms(M, s, m2, s2, scale);
-    d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, off));
+      for (int i = 0; i < 4; ++i) {
+        const int j = min(j0 + 32 * i, a.S - 1);
+        v[i] = __ldg(ms + j);
+        x[i] = __ldg(dz + j);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j0 + 32 * i < a.S) {
+          merge_ms(M, s, v[i].x, v[i].y, a.scale);
+          d = __fadd_rn(d, x[i]);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, M, off);
+      const float s2 = __shfl_xor_sync(0xffffffffu, s, off);
+      merge_ms(M, s, m2, s2, a.scale);
+      d = __fadd_rn(d, __shfl_xor_sync(0xffffffffu, d, off));
+      Q = __fadd_rn(Q, __shfl_xor_sync(0xffffffffu, Q, off));
+    }
+    if (lane == 0) parts[threadIdx.x / 32] = make_float4(M, s, d, Q);
   }
-  if (lane == 0 && RLK_STORE_OK(row >= 0 && row < N, &g_err_linear_distill)) {
-    const float L = __fadd_rn(__fdiv_rn(M, temperature), logf(s));
-    const float2 t = eq[row];
-    float x = 0.f;                   // no used slot, or none with any weight
-    if (t.y != 0.f)
-      x = __fmul_rn(__fmul_rn(temperature, temperature),
-                    __fadd_rn(__fsub_rn(t.x, __fdiv_rn(d, temperature)), __fmul_rn(t.y, L)));
-    lse[row] = L;
-    loss[row] = x;
+  __syncthreads();
+  row = blockIdx.x * 8 + threadIdx.x;
+  if (!ends || !RLK_STORE_OK(row >= 0, &g_err_linear_distill)) return;
+  const float4 r = parts[threadIdx.x];
+  const float M = r.x, s = r.y, Q = r.w, T = a.temperature;
+  const float lse = __fadd_rn(__fdiv_rn(M, T), logf(s));
+  float loss = 0.f;                                // no used slot, or none with any weight
+  if (Q != 0.f) {
+    const double d = r.z - (double)M * Q;
+    double ratio;                                  // log s - L
+    if (a.teacher_lse) {
+      const double norm = teacher - t.y * a.inv_t;
+      const float near = (float)norm;
+      ratio = T == 1.f ? (double)lse - M - norm
+                       : logf(__fmul_rn(s, expf(-near))) - (norm - near);
+    } else {
+      ratio = T == 1.f ? (double)lse - M - logf(t.y) : logf(__fdiv_rn(s, t.y));
+    }
+    loss = (float)((double)T * T * (t.x - d * a.inv_t + Q * ratio));
   }
+  a.lse[row] = lse;
+  a.loss[row] = loss;
 }
 
 // ---------------------------------------------------------------- backward
@@ -512,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float up = 0.f, Q = 0.f, L = 0.f;
       if (valid) {
         up = __fmul_rn(__ldg(a.grad + row), a.temperature);
-        Q = __ldg(&a.lists.eq[row].y);
+        Q = __ldg(&a.lists.sums[row].y);
         L = __fmul_rn(__ldg(a.lse + row), a.temperature);
       }
       const bool has_bias = a.bias != nullptr;
@@ -603,7 +666,7 @@ __global__ void __launch_bounds__(256)
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       if (v + 4 < a.V) y = __ldcs(reinterpret_cast<const float4*>(z) + 1);
       const float up = __fmul_rn(__ldg(a.grad + row), a.temperature);
-      const float Q = __ldg(&a.lists.eq[row].y);
+      const float Q = __ldg(&a.lists.sums[row].y);
       const float L = __fmul_rn(__ldg(a.lse + row), a.temperature);
       const float zz[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
       if (Q != 0.f) {
@@ -705,7 +768,7 @@ struct DistillPlan {
   int64_t S = 0, vps = 0, vtiles = 0, spans = 0, ldG = 0;
   bool stage_h = false, stage_w = false;
   int64_t ldh = 0, ldw = 0;
-  size_t off_a = 0, off_ctr = 0, off_ids = 0, off_q = 0, off_first = 0, off_eq = 0, off_h = 0,
+  size_t off_a = 0, off_ctr = 0, off_ids = 0, off_q = 0, off_first = 0, off_sums = 0, off_h = 0,
          off_w = 0, total = 0;
 };
 
@@ -747,7 +810,7 @@ rlk_status distill_plan(const void* hidden, int64_t N, int64_t H, int64_t ld_hid
   p->off_ids = take((size_t)N * K * sizeof(int));
   p->off_q = take((size_t)N * K * sizeof(float));
   p->off_first = take((size_t)N * (p->spans + 1) * sizeof(uint16_t));
-  p->off_eq = take((size_t)N * sizeof(float2));
+  p->off_sums = take((size_t)N * sizeof(float2));
   p->off_h = take(p->stage_h ? (size_t)N * p->ldh * 2 : 0);
   p->off_w = take(p->stage_w ? (size_t)V * p->ldw * 2 : 0);
   p->total = off;
@@ -771,7 +834,7 @@ rlk_status check_teacher(const Teacher& t, int64_t N, bool pointers) {
         t.ld_ids >= kLdLimit || t.ld_logits >= kLdLimit)
       return RLK_ERR_SHAPE;
     if (t.dtype != RLK_BF16 && t.dtype != RLK_FP32) return RLK_ERR_DTYPE;
-    if (!(t.temperature >= 1e-4f && t.temperature <= 1e4f)) return RLK_ERR_VALUE;
+    if (!(t.temperature >= 1e-4f && t.temperature <= 100.f)) return RLK_ERR_VALUE;
     return RLK_OK;
   }
   if (N > 0 && t.K > 0 && (!t.ids || !t.logits)) return RLK_ERR_NULL;
@@ -793,14 +856,15 @@ Lists lists_at(uint8_t* ws, const DistillPlan& p, int64_t K, int64_t span) {
   l.ids = reinterpret_cast<int*>(ws + p.off_ids);
   l.q = reinterpret_cast<float*>(ws + p.off_q);
   l.first = reinterpret_cast<uint16_t*>(ws + p.off_first);
-  l.eq = reinterpret_cast<float2*>(ws + p.off_eq);
+  l.sums = reinterpret_cast<float2*>(ws + p.off_sums);
   l.K = (int)K;
   l.spans = (int)p.spans;
   l.span = span;
   return l;
 }
 
-cudaError_t launch_lists(const Teacher& t, int64_t N, int64_t V, const Lists& l, cudaStream_t s) {
+cudaError_t launch_lists(const Teacher& t, int64_t N, int64_t V, const Lists& l, bool backward,
+                         cudaStream_t s) {
   ListArgs a;
   a.ids = t.ids;
   a.ld_ids = t.ld_ids;
@@ -811,6 +875,7 @@ cudaError_t launch_lists(const Teacher& t, int64_t N, int64_t V, const Lists& l,
   a.temperature = t.temperature;
   a.N = (int)N;
   a.V = (int)V;
+  a.backward = backward;
   const int threads = t.K <= 64 ? 64 : (t.K <= 128 ? 128 : 256);
   return launch_overlapped(distill_lists_kernel, dim3((unsigned)N), threads, 12 * (size_t)t.K, s, a,
                            l);
@@ -881,7 +946,7 @@ rlk_status distill_forward(const void* hidden, int64_t N, int64_t H, int64_t ld_
       !encode_bf16_2d(&tm_w, w, H, V, p.ldw, kBK, solo ? kBN : kHalfRows))
     return RLK_ERR_CUDA;
   const Lists lists = lists_at(ws, p, t.K, p.vps * kVocabTile);
-  if (launch_lists(t, N, V, lists, s) != cudaSuccess) return cuda_failed();
+  if (launch_lists(t, N, V, lists, false, s) != cudaSuccess) return cuda_failed();
 
   VocabSched sc;
   sc.order.rows = (int)ceil_div(N, rows_per_unit);
@@ -930,9 +995,19 @@ rlk_status distill_forward(const void* hidden, int64_t N, int64_t H, int64_t ld_
                                 PairRingT<kHalfRows, 64>::kSmemBytes, s, tm_h, tm_w, sc, a);
   }
   if (e != cudaSuccess) return cuda_failed();
-  if (launch_overlapped(distill_combine_kernel, (int)ceil_div(N, 8), 256, 0, s, a.ws_ms, a.ws_d,
-                        lists.eq, (int)N, (int)p.S, t.temperature, a.scale, loss, lse) !=
-      cudaSuccess)
+  CombineArgs c;
+  c.ms = a.ws_ms;
+  c.d = a.ws_d;
+  c.lists = lists;
+  c.teacher_lse = t.lse;
+  c.N = (int)N;
+  c.S = (int)p.S;
+  c.temperature = t.temperature;
+  c.scale = a.scale;
+  c.inv_t = 1.0 / t.temperature;
+  c.loss = loss;
+  c.lse = lse;
+  if (launch_overlapped(distill_combine_kernel, (int)ceil_div(N, 8), 256, 0, s, c) != cudaSuccess)
     return cuda_failed();
   return RLK_OK;
 }
@@ -1050,7 +1125,7 @@ rlk_status rlk_linear_distill_backward(
       !encode_bf16_2d(&tm_w, w, H, V, p.ldw, kBK, kHalfRows))
     return RLK_ERR_CUDA;
   const Lists lists = lists_at(ws, p, K, kVocabTile);
-  if (launch_lists(t, N, V, lists, s) != cudaSuccess) return cuda_failed();
+  if (launch_lists(t, N, V, lists, true, s) != cudaSuccess) return cuda_failed();
 
   DistillGradSched sc;
   sc.order.rows = (int)ceil_div(N, kPairRows);

@@ -546,7 +546,7 @@ RLK_API rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64
  *                   A row without used slots has loss 0 and gradient 0.  A NaN or +inf
  *                   logit in a used slot makes the row's loss NaN.
  *  teacher_lse      FP32 [N] or NULL
- *  temperature      T, 1e-4 .. 1e4 (RLK_ERR_VALUE otherwise)
+ *  temperature      T, 1e-4 .. 100 (RLK_ERR_VALUE otherwise)
  *  loss, lse        FP32 [N] outputs
  *  logits           FP32 [N, V] output or NULL: z (bias included, not divided by T), for a
  *                   backward that is to read them in place of forming them again; row
@@ -559,7 +559,9 @@ RLK_API rlk_status rlk_sample_logits(const void* logits, int logits_dtype, int64
  * bits, and K = 1 gives loss = -logp exactly.  sum q z is added per split in ascending
  * id order and merged over the splits in the fixed order; the sums over a row's slots
  * run in a fixed order of the slots.  A row's bits depend on its own inputs, V, H and
- * K alone.
+ * K alone.  The loss is a difference of larger parts: its error is absolute, about
+ * 2e-7 T max|z| + 3e-7 max(T^2 Q, loss) beside what the logits' own error makes of it, so
+ * the loss of a student that equals its teacher may come out slightly below 0.
  */
 #define RLK_DISTILL_MAX_SLOTS 1024
 RLK_API size_t rlk_linear_distill_workspace_size(const void* hidden, int64_t N, int64_t H,
