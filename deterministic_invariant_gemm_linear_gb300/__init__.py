@@ -250,12 +250,15 @@ def _streamed(call):
 
 def _matrix(t: torch.Tensor, name: str):
     """(tensor, leading dimension) for a 2-D row-major operand (unit column stride)."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    if t.stride(1) != 1 or (t.size(0) > 1 and t.stride(0) < t.size(1)):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 or (rows > 1 and ld < cols):
         t = t.contiguous()
-    ld = t.stride(0) if t.size(0) > 1 else max(t.size(1), t.stride(0))
-    return t, ld
+        ld = t.stride(0)
+    return t, ld if rows > 1 or ld > cols else cols
 
 
 def _require_cuda(*ts):
@@ -734,8 +737,8 @@ def sample_logits(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.
 
 # ------------------------------------------------------------------ distillation
 class _Distill:
-    """A distillation call's checked operands: tensors with unit column stride, their leading
-    dimensions, sizes and the teacher's settings."""
+    """A distillation call's sizes and settings, checked, and its operands: tensors with unit
+    column stride and their leading dimensions."""
 
     __slots__ = ("lead", "h", "ldh", "w", "ldw", "ids", "ldi", "tl", "ldt", "tdt", "bias", "tlse",
                  "N", "H", "V", "K", "T")
@@ -754,33 +757,38 @@ class _Distill:
             raise ValueError(
                 "teacher_ids and teacher_logits must be [..., K] with hidden's leading shape")
         self.H, self.K = shape[-1], teacher_ids.shape[-1]
-        if len(shape) != 2:
-            self.N = hidden.numel() // self.H if self.H else 0
-            hidden = hidden.reshape(self.N, self.H)
-            teacher_ids = teacher_ids.reshape(self.N, self.K)
-            teacher_logits = teacher_logits.reshape(self.N, self.K)
-        else:
-            self.N = shape[0]
-        self.h, self.ldh = _matrix(hidden, "hidden")
-        self.w, self.ldw = _matrix(weight, "weight")
-        self.V = weight.shape[0]
-        if weight.shape[1] != self.H:
+        self.N = shape[0] if len(shape) == 2 else hidden.numel() // self.H if self.H else 0
+        if weight.dim() != 2 or weight.shape[1] != self.H:
             raise ValueError("weight must be [V, H] with the hidden size H")
-        self.ids, self.ldi = _matrix(teacher_ids, "teacher_ids")
-        self.tl, self.ldt = _matrix(teacher_logits, "teacher_logits")
-        self.tdt = _DT[teacher_logits.dtype]
+        self.V = weight.shape[0]
         if bias is not None:
             if bias.dtype != torch.float32 or bias.dim() != 1:
                 raise TypeError("bias must be a 1-D float32 tensor")
             if bias.numel() != self.V:
                 raise ValueError("bias must have V entries")
-            bias = bias.contiguous()
-        self.bias = bias
         if teacher_lse is not None:
             if teacher_lse.dtype != torch.float32 or teacher_lse.shape != self.lead:
                 raise ValueError("teacher_lse must be float32 with hidden's leading shape")
-            teacher_lse = teacher_lse.reshape(-1).contiguous()
-        self.tlse, self.T = teacher_lse, temperature
+        self.T = temperature
+        self.tdt = _DT[teacher_logits.dtype]
+        self.hold(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse)
+
+    def hold(self, hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse):
+        """Takes operands of the sizes and types that were checked."""
+        if len(self.lead) != 1:
+            hidden = hidden.reshape(self.N, self.H)
+            teacher_ids = teacher_ids.reshape(self.N, self.K)
+            teacher_logits = teacher_logits.reshape(self.N, self.K)
+        self.h, self.ldh = _matrix(hidden, "hidden")
+        self.w, self.ldw = _matrix(weight, "weight")
+        self.ids, self.ldi = _matrix(teacher_ids, "teacher_ids")
+        self.tl, self.ldt = _matrix(teacher_logits, "teacher_logits")
+        self.bias = None if bias is None else bias.contiguous()
+        self.tlse = None if teacher_lse is None else teacher_lse.reshape(-1).contiguous()
+
+    def drop(self):
+        """Lets go of the operands."""
+        self.h = self.w = self.ids = self.tl = self.bias = self.tlse = None
 
     def forward(self, keep_logits: bool, stream=None):
         """loss [N], lse [N], logits [N, 8 ceil(V / 8)] or None."""
@@ -911,7 +919,8 @@ KEEP_LOGITS_BYTES = 8 << 30
 
 class _LinearDistillGrad(torch.autograd.Function):
     """Autograd wiring of rlk_linear_distill and rlk_linear_distill_backward; lse is returned
-    as a constant and the teacher's tensors carry no gradient."""
+    as a constant and the teacher's tensors carry no gradient.  Whatever the backward needs is
+    saved with autograd, the kept logits too, which frees it after the backward."""
 
     @staticmethod
     def forward(ctx, hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, temperature,
@@ -919,9 +928,11 @@ class _LinearDistillGrad(torch.autograd.Function):
         d = _Distill(hidden, weight, teacher_ids, teacher_logits, bias, teacher_lse, temperature)
         if keep_logits is None:
             keep_logits = 4 * d.N * d.V <= KEEP_LOGITS_BYTES
-        loss, lse, ctx.logits = d.forward(keep_logits)
-        ctx.save_for_backward(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, lse)
-        ctx.call, ctx.shape = d, hidden.shape
+        loss, lse, logits = d.forward(keep_logits)
+        ctx.save_for_backward(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, lse,
+                              logits)
+        d.drop()
+        ctx.call = d
         ctx.mark_non_differentiable(lse)
         if len(d.lead) != 1:
             loss, lse = loss.reshape(d.lead), lse.reshape(d.lead)
@@ -930,16 +941,19 @@ class _LinearDistillGrad(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_loss, _grad_lse):
-        lse = ctx.saved_tensors[-1]      # raises if an input was changed in place
         want_h, want_w, want_b = ctx.needs_input_grad[:3]
         if grad_loss is None or not (want_h or want_w or want_b):
             return (None,) * 8
+        hidden, weight, bias, ids, teacher_logits, teacher_lse, lse, logits = ctx.saved_tensors
+        d = ctx.call
+        d.hold(hidden, weight, ids, teacher_logits, bias, teacher_lse)
         if grad_loss.dim() != 1 or not grad_loss.is_contiguous():
             grad_loss = grad_loss.reshape(-1).contiguous()
-        gh, gw, gb, _ = ctx.call.backward(lse, grad_loss, ctx.logits, (want_h, want_w, want_b),
-                                          torch.bfloat16)
-        if gh is not None and len(ctx.shape) != 2:
-            gh = gh.reshape(ctx.shape)
+        gh, gw, gb, _ = d.backward(lse, grad_loss, logits, (want_h, want_w, want_b),
+                                   torch.bfloat16)
+        d.drop()
+        if gh is not None and hidden.dim() != 2:
+            gh = gh.reshape(hidden.shape)
         return gh, gw, gb, None, None, None, None, None
 
 
@@ -952,8 +966,11 @@ def linear_distill_trainable(hidden: torch.Tensor, weight: torch.Tensor, teacher
 
     keep_logits: hold the logits in FP32 (4 N V bytes) from the forward to the backward, which
     otherwise forms them again; the gradients' bits are the same.  None: up to
-    KEEP_LOGITS_BYTES.
+    KEEP_LOGITS_BYTES.  Where nothing asks for a gradient they are not kept.
     """
+    if not (torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad or
+                                         (bias is not None and bias.requires_grad))):
+        keep_logits = False
     return _LinearDistillGrad.apply(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse,
                                     temperature, keep_logits)
 
