@@ -37,6 +37,7 @@ import functools
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 # RLK_LIBRARY=debug selects the debug build (store checks, phase trace) of the
@@ -658,6 +659,7 @@ class _LinearLogpGrad(torch.autograd.Function):
         return logp, lse
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_logp, _grad_lse):
         hidden, weight, bias, target, lse = ctx.saved_tensors
         want_h, want_w, want_b = ctx.needs_input_grad[:3]
@@ -940,6 +942,7 @@ class _LinearDistillGrad(torch.autograd.Function):
         return loss, lse
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_loss, _grad_lse):
         want_h, want_w, want_b = ctx.needs_input_grad[:3]
         if grad_loss is None or not (want_h or want_w or want_b):
@@ -1188,6 +1191,7 @@ class _DetGemmGrad(torch.autograd.Function):
         return C
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dC):
         A, B = ctx.saved_tensors
         want_a, want_b = ctx.needs_input_grad[:2]
@@ -1209,6 +1213,7 @@ class _DetLinearGrad(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, W = ctx.saved_tensors
         want_x, want_w = ctx.needs_input_grad[:2]
