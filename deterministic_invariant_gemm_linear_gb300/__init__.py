@@ -34,6 +34,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -721,6 +722,8 @@ def sample_logits(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.
     u = uniform.reshape(-1).contiguous()
     tau, tau_all = _per_row(temperature, "temperature", N, torch.float32)
     k, k_all = _per_row(top_k, "top_k", N, torch.int32)
+    if k is None:                         # any whole number: the C call takes 32 bits
+        k_all = max(0, min(operator.index(k_all), V))
     p, p_all = _per_row(top_p, "top_p", N, torch.float32)
     m, m_all = _per_row(min_p, "min_p", N, torch.float32)
     dev = logits.device
