@@ -27,7 +27,8 @@ Operators of a training loop around them (on-policy distillation):
   * ``linear_distill``, ``linear_distill_backward``,
     ``linear_distill_trainable`` — T^2 KL(teacher || student) of hidden . W^T
     over a teacher's top logits without the [N, V] logits of the student, and
-    its gradients.
+    its gradients (the trainable form keeps the FP32 logits between forward and
+    backward where they fit KEEP_LOGITS_BYTES; keep_logits=False does not).
 """
 from __future__ import annotations
 

@@ -105,9 +105,10 @@ __device__ __forceinline__ float block_fold(float v, float* warp_out) {
 }
 
 // Bound by latency: a row's K (id, logit) pairs are read once, and a chain of block-wide steps
-// follows.  Counting ranks costs K^2 shared reads over 256 threads and no barriers: 12 us for
-// 2048 rows of 64 slots (0.02 of the forward it precedes at H = 4096, V = 151936), 5 us for 255
-// rows of 33.
+// follows.  Counting ranks costs K^2 shared reads over 256 threads and no barriers: 12.6 us for
+// 2048 rows of 64 slots (0.01 of the forward it precedes at H = 4096, V = 151936), 5.7 us for 1024
+// rows of 20.  Long lists pay for the square: 2048 rows of 256 slots 44 us, of 1024 slots 560 us
+// (0.3 of the 1.86 ms that this forward then takes, and once more in the backward).
 __global__ void __launch_bounds__(256) distill_lists_kernel(ListArgs a, Lists out) {
   extern __shared__ int smem_lists[];
   int* key = smem_lists;                                    // [K] id, or INT_MAX when empty
@@ -320,10 +321,10 @@ __device__ __forceinline__ void distill_epilogue(const VocabSched& sc, const Dis
 }
 
 // Bound by the tensor cores: the epilogue of one accumulator hides behind the MMAs of the
-// other.  2 N H V operations at N = 4096, H = 4096, V = 151936 in 2.85 ms (with the lists and
-// the merge): 1.79 PFLOP/s, 0.96 of a measured library product's burst rate; at N = 1024,
-// H = 2048, V = 32003 88 us, 1.53 PFLOP/s.  The split of V and the 64 or 128 columns a stage
-// are the fused linear-logp's rules, so lse at T = 1 has its bits.
+// other.  2 N H V operations at N = 4096, H = 4096, V = 151936 in 2.75 - 2.9 ms (with the lists and
+// the merge; the power cap decides): 1.76 - 1.85 PFLOP/s, 0.94 - 0.99 of a measured library
+// product's burst rate; at N = 1024, H = 2048, V = 32003 88 us, 1.52 PFLOP/s.  The split of V and
+// the 64 or 128 columns a stage are the fused linear-logp's rules, so lse at T = 1 has its bits.
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     distill_partials_kernel(const __grid_constant__ CUtensorMap tm_hidden,

@@ -21,7 +21,7 @@
 // contiguous run of its ids.  (Larger calls: see the streaming kernels.)  A row needs one pass
 // for its maximum and at least one more, from shared memory (kOnChip) or from L2; what bounds
 // the kernel is latency, the chain of passes and cluster barriers: a row of 151,936 FP32
-// logits with top-k, top-p and min-p takes 17.6 us, 7 rows of 32,003 in BF16 without any
+// logits with top-k, top-p and min-p takes 17.8 us, 7 rows of 32,003 in BF16 without any
 // 11 us, where their bytes would take 0.1.  No row is sorted:
 //  * top-k of few (the usual): a CTA's threads each know their own largest logit, so the
 //    k-th largest of those is a value that at least k of the CTA's logits reach.  What
@@ -378,19 +378,19 @@ __global__ void __launch_bounds__(kT, 1024 / kT) sample_kernel(const __grid_cons
 // (156 MB) and for 1024 rows of 151,936 FP32 logits (622 MB), five in six greedy or with
 // top-k and most of the others with top-p, and what bounds each:
 //   tops   the largest logit of every chunk (the 8 vectors a lane of a tile reads)
-//          [25, 90; memory: 6.2 and 6.9 TB/s]
+//          [25, 89; memory: 6.2 and 7.0 TB/s]
 //   pick   the row's largest; top-k of at most kChunkTop: the k-th largest of the chunks'
 //          bounds the k first, only the chunks that reach it are read again, and the row
-//          is done  [10, 49; latency of the lists and their order]
+//          is done  [10, 54; latency of the lists and their order]
 //   weigh  the other rows' weights by tile, for top-p with their histogram
-//          [70, 41; instructions: the exact weights alone would take 41 of the 70, the
-//          histogram's places and its two shared atomics the rest]
+//          [80, 38; instructions: the exact weights alone take 55 of the 80 (the same rows
+//          without top-p), the histogram's places and its two shared atomics the rest]
 //   cut    rows that keep all: the token's tile by a running sum, then the token; top-p: the
 //          bin of the cut from the histogram and, if little lies up to it, the token
-//          [22, 20; latency]
+//          [24, 21; latency]
 //   weigh  again, for the other rows with top-p: the weights above that bin by tile, and its
-//          elements in a list  [28, 23; instructions, of the quarter of the rows left]
-//   cut    again: the cut from the sorted list, and the token  [26, 19; latency]
+//          elements in a list  [27, 21; instructions, of the quarter of the rows left]
+//   cut    again: the cut from the sorted list, and the token  [25, 20; latency]
 // Rows that none of this settles (more equal logits than the list holds, top-k of more, a cut
 // in the last octaves) are left to sample_kernel, which takes them from a list.
 constexpr int kTile = 256;                    // vectors of a tile: 8 a lane
@@ -400,9 +400,10 @@ constexpr int kStreamThreads = 256;           // of the passes
 // 1024 FP32 rows with settings of every kind, 512 BF16 rows with top-p) at 512 threads and 65 /
 // 231 / 171 at 256, the cut 62 / 232 / 197 at 512 and 63 / 233 / 181 at 256 (when each was set).
 constexpr int kPickThreads = 512, kCutThreads = 256;
-// Tiles a CTA of the weighing kernels: the most, and half of them in calls that then have at
-// most kFewCtas CTAs an SM (us of whole calls, half against the most: with top-p 64 rows of FP32
-// 62 / 65, 128 of BF16 76 / 85, 384 of FP32 168 / 163; 1024 with settings of every kind 239 / 227).
+// Tiles a CTA of the weighing kernels: the most, and half of them in calls that have at most
+// kFewCtas CTAs an SM with the most (us of whole calls, half against the most: with top-p 64 rows
+// of FP32 64 / 69, 128 of BF16 82 / 90, 256 of BF16 119 / 126, 384 of FP32 171 / 168; settings of
+// every kind, FP32, 64 rows 60 / 65, 1024 rows 238 / 229).
 constexpr int kTilesPerCta = 16;
 constexpr int kFewCtas = 13;
 constexpr int kChunkTop = 1024;
@@ -948,12 +949,22 @@ inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
-// Logits from which the streaming kernels run, for rows of kStreamVocab or more.  Calls over
-// rows of 151,936 FP32 logits took (us with their launches, streaming against clusters, for
-// top-k with top-p / top-p / neither / settings of every kind) 8 rows 37 / 51 / 42 / 56 against
-// 24 / 56 / 23 / 32, 16 rows 37 / 54 / 41 / 58 against 29 / 77 / 38 / 51, 48 rows 38 / 65 / 42 /
-// 60 against 41 / 150 / 72 / 114; in a captured graph, whose launches cost less, 8 rows took
-// 19 / 51 / 19 against 23 / 56 / 22 without the last.
+// Logits from which the streaming kernels run, for rows of kStreamVocab or more.  The size alone
+// decides, so that it decides the workspace too; the settings do not agree where to change over.
+// us of calls over rows of 151,936 FP32 logits, streaming against clusters, with settings for the
+// call (top-k and top-p / top-p / neither) and of every kind:
+//    8 rows  34 / 44 / 40 / 55   against  26 /  56 / 26 /  33     (4.6 MiB)
+//   12 rows  34 / 45 / 40 / 53   against  26 /  77 / 34 /  51
+//   16 rows  32 / 46 / 40 / 55   against  29 /  79 / 38 /  53     (9.3 MiB)
+//   24 rows  33 / 49 / 39 / 53   against  31 / 126 / 63 /  79
+//   48 rows  33 / 62 / 38 / 58   against  42 / 149 / 73 / 112
+// so at the change-over top-k loses 10% where top-p gains 40%.  In captured graphs, whose launches
+// cost less, 8 rows take 15 / 42 / 17 / 23 against 23 / 56 / 23 / 32.  1024 rows of BF16 (8 MiB
+// from 4096 ids on), by vocabulary:
+//   12,000   41 /  86 / 43 / 117  against  38 /  97 /  53 /  79
+//   16,000   44 /  91 / 48 / 126  against  41 / 136 /  61 / 114
+//   24,000   47 / 110 / 57 / 135  against  52 / 167 /  86 / 109
+//   32,000   50 / 122 / 64 / 105  against  57 / 187 / 103 / 131
 constexpr int64_t kStreamBytes = int64_t(8) << 20;
 constexpr int64_t kStreamVocab = 16384;
 
