@@ -82,6 +82,7 @@ struct ListArgs {
   int logits_fp32;
   const float* lse;       // the teacher's own log-sum-exp at this temperature, or null
   float temperature;
+  double inv_t;
   int N, V;
   bool backward;
 };
@@ -136,9 +137,13 @@ __global__ void __launch_bounds__(256) distill_lists_kernel(ListArgs a, Lists ou
   if (threadIdx.x == 0) used = 0;
   // y = (t - top) / T <= 0 is small where T is large, and so keeps the digits that T^2 needs
   top = block_fold<true>(top, warp_out);
-  float norm = 1.f, shift = 0.f;                   // q = exp(y - shift) / norm
+  float norm;                                      // q = exp(y) / norm
   if (a.lse) {
-    shift = __fdiv_rn(__fmaf_rn(__ldg(a.lse + row), a.temperature, -top), a.temperature);
+    // exp(lse - top / T), the exponent in two parts: rounded to one it would move every q by
+    // 5e-7 of itself, and the loss with them
+    const double x = __ldg(a.lse + row) - top * a.inv_t;
+    const float near = (float)x;
+    norm = __fmul_rn(expf(near), __fadd_rn(1.f, (float)(x - near)));
   } else {
     float s = 0.f;
     for (int k = threadIdx.x; k < K; k += blockDim.x)
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(256) distill_lists_kernel(ListArgs a, Lists ou
     float q = 0.f;
     if (key[k] != INT_MAX) {
       const float y = __fdiv_rn(__fsub_rn(val[k], top), a.temperature);
-      q = __fdiv_rn(expf(__fsub_rn(y, shift)), norm);
+      q = __fdiv_rn(expf(y), norm);
       if (q > 0.f) e = __fadd_rn(e, __fmul_rn(q, y));
       sum = __fadd_rn(sum, q);
       ++n;
@@ -234,6 +239,15 @@ __device__ __forceinline__ void store_sector(float* p, const float* z) {
                : "memory");
 }
 
+// sum += x, and what the rounding lost to `lost` (the sum of two numbers is exact in two; NaN
+// where an infinity came in).  Hundreds of slots of one vocabulary split, added plainly, were off
+// by 4e-5 at logits of 13.
+__device__ __forceinline__ void sum_exactly(float x, float& sum, float& lost) {
+  const float to = __fadd_rn(sum, x), of_x = __fsub_rn(to, sum);
+  lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(sum, __fsub_rn(to, of_x)), __fsub_rn(x, of_x)));
+  sum = to;
+}
+
 struct DistillArgs {
   int N, V;
   float scale;                // log2(e) / T
@@ -266,7 +280,7 @@ __device__ __forceinline__ void distill_epilogue(const VocabSched& sc, const Dis
     const bool valid = row < a.N;
     SlotWalk slot;
     slot.start(a.lists, row, j, valid);
-    float m = -INFINITY, s = 0.f, d = 0.f;
+    float m = -INFINITY, s = 0.f, d = 0.f, d_lost = 0.f;
     const int t0 = sc.first_tile(u), nt = sc.unit_tiles(u);
     const bool has_bias = a.bias != nullptr;
     for (int i = 0; i < nt; ++i) {
@@ -299,7 +313,7 @@ __device__ __forceinline__ void distill_epilogue(const VocabSched& sc, const Dis
         while (__any_sync(0xffffffffu, slot.id < vbase + 32)) {
           if (slot.id < vbase + 32) {
             const float zk = chunk_at(z, slot.id - vbase);
-            if (slot.w != 0.f) d = __fadd_rn(d, __fmul_rn(slot.w, zk));   // 0 of a banned id is 0
+            if (slot.w != 0.f) sum_exactly(__fmul_rn(slot.w, zk), d, d_lost);   // 0 of a banned id is 0
             slot.next();
           }
         }
@@ -315,7 +329,7 @@ __device__ __forceinline__ void distill_epilogue(const VocabSched& sc, const Dis
     if (!run) break;
     if (valid && RLK_STORE_OK(row >= 0 && j >= 0 && j < a.S, &g_err_linear_distill)) {
       a.ws_ms[(int64_t)row * a.S + j] = make_float2(m, s);
-      a.ws_d[(int64_t)row * a.S + j] = d;
+      a.ws_d[(int64_t)row * a.S + j] = d_lost == d_lost ? __fadd_rn(d, d_lost) : d;
     }
   }
 }
@@ -874,6 +888,7 @@ cudaError_t launch_lists(const Teacher& t, int64_t N, int64_t V, const Lists& l,
   a.logits_fp32 = t.dtype == RLK_FP32;
   a.lse = t.lse;
   a.temperature = t.temperature;
+  a.inv_t = 1.0 / t.temperature;
   a.N = (int)N;
   a.V = (int)V;
   a.backward = backward;
