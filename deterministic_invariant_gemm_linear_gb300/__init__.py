@@ -29,6 +29,17 @@ Operators of a training loop around them (on-policy distillation):
     over a teacher's top logits without the [N, V] logits of the student, and
     its gradients (the trainable form keeps the FP32 logits between forward and
     backward where they fit KEEP_LOGITS_BYTES; keep_logits=False does not).
+
+Operators of the trunk in front of the head:
+  * ``embedding``, ``embedding_backward``, ``embedding_grad_accum_fp32_``,
+    ``embedding_trainable`` — rows of a table, scaled, and the table's gradient by
+    sorted ids: a table row's bits depend on its own rows alone.
+  * ``gated_linear``, ``gated_linear_backward``, ``gated_linear_trainable`` — the
+    gated block of a feed-forward layer, act(X Wg^T) * (X Wu^T), in one kernel, and
+    its gradients.
+  * ``pack_int8``, ``unpack_int8`` — activations in blocks of 8 bits, and
+    ``checkpoint="int8"`` of ``gated_linear_trainable`` and ``det_linear_trainable``,
+    which hold what waits for the backward so.
 """
 from __future__ import annotations
 
@@ -118,6 +129,18 @@ SIGNATURES = {
     "rlk_linear_distill_backward": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _I,
                                          _I64, _I64, _P, _F, _P, _P, _I64, _P, _P, _I, _I64, _P, _I,
                                          _I64, _P, _P, _SZ, _P]),
+    "rlk_embedding": (_I, [_P, _I64, _I64, _P, _I, _I64, _I64, _I64, _F, _P, _I, _I64, _P]),
+    "rlk_embedding_backward_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "rlk_embedding_backward": (_I, [_P, _I64, _I64, _P, _I, _I64, _I64, _F, _P, _I, _I64, _I64, _I,
+                                    _P, _SZ, _P]),
+    "rlk_pack_int8": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "rlk_unpack_int8": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I, _I64, _P]),
+    "rlk_gated_linear_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64]),
+    "rlk_gated_linear": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I, _P, _I, _I64, _I, _P, _P, _P,
+                              _SZ, _P]),
+    "rlk_gated_linear_backward_workspace_size": (_SZ, [_P, _I64, _I64, _I64, _P, _I64, _I64]),
+    "rlk_gated_linear_backward": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I, _I,
+                                       _P, _P, _P, _I, _I64, _P, _I, _I64, _P, _SZ, _P]),
     "rlk_det_gemm_workspace_size": (_SZ, [_I, _P, _I, _I64, _I64, _I64, _P, _I, _I64, _I64, _I64]),
     "rlk_det_gemm_fwd": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]),
     "rlk_det_gemm_da": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]),
@@ -1181,6 +1204,380 @@ def det_linear_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
                       stream)
 
 
+# ------------------------------------------------------------------ embedding
+def _ids(ids: torch.Tensor):
+    """(flat int64 ids, stride, number)"""
+    if ids.dtype != torch.int64:
+        raise TypeError("ids must be int64")
+    flat = ids if ids.dim() == 1 else ids.reshape(-1)
+    n = flat.numel()
+    return flat, flat.stride(0) if n > 1 else 1, n
+
+
+def _refuse_grad(what: str, *tensors):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise RuntimeError(f"{what} is forward-only: use {what}_trainable for inputs that require grad")
+
+
+@_streamed
+def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, *, out_dtype=None,
+              stream=None):
+    """scale * weight[ids], rounded once: [..., H] in out_dtype (weight's dtype by default).
+
+    ids [...] int64 (any strides), weight [V, H] bf16 or fp32.  An id outside [0, V) (padding)
+    gives a row of zeros.  Forward only: use embedding_trainable for gradients.
+    """
+    _refuse_grad("embedding", weight)
+    _require_cuda(ids, weight)
+    if weight.dtype not in _DT:
+        raise TypeError("weight must be bfloat16 or float32")
+    flat, step, N = _ids(ids)
+    w, ldw = _matrix(weight, "weight")
+    V, H = w.shape
+    dt = weight.dtype if out_dtype is None else out_dtype
+    out = torch.empty((N, H), dtype=dt, device=weight.device)
+    with _on(weight.device):
+        _check(lib().rlk_embedding(_ptr(flat), step, N, _ptr(w), _DT[w.dtype], V, H, ldw, scale,
+                                   _ptr(out), _DT[dt], H, _stream_ptr(stream)), "rlk_embedding")
+    return out if ids.dim() == 1 else out.reshape(*ids.shape, H)
+
+
+def _embedding_backward(grad, ids, V, scale, out, ld_out, accumulate, stream):
+    _require_cuda(grad, ids, out)
+    if grad.dtype not in _DT:
+        raise TypeError("grad must be bfloat16 or float32")
+    if grad.shape[:-1] != ids.shape:
+        raise ValueError("grad must be [..., H] with ids' shape")
+    flat, step, N = _ids(ids)
+    H = grad.size(-1)
+    g, ldg = _matrix(grad.reshape(N, H) if grad.dim() != 2 else grad, "grad")
+    dev = out.device
+    n = lib().rlk_embedding_backward_workspace_size(N, V, H)
+    if n == 0:
+        raise RlkError(2, "rlk_embedding_backward_workspace_size")
+    with _on(dev):
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(lib().rlk_embedding_backward(
+            _ptr(flat), step, N, _ptr(g), _DT[g.dtype], H, ldg, scale, _ptr(out), _DT[out.dtype], V,
+            ld_out, accumulate, _ptr(ws), n, _stream_ptr(stream)), "rlk_embedding_backward")
+    return out
+
+
+@_streamed
+def embedding_backward(grad: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
+                       out_dtype=torch.bfloat16, *, stream=None):
+    """grad_weight [V, H] of embedding(ids, weight, scale) for grad = dL/dout [..., H] (bf16 or
+    fp32): scale times the sum of each id's rows of grad, in ascending order, in FP32."""
+    out = torch.empty((V, grad.size(-1)), dtype=out_dtype, device=grad.device)
+    return _embedding_backward(grad, ids, V, scale, out, grad.size(-1), 0, stream)
+
+
+@_streamed
+def embedding_grad_accum_fp32_(grad_weight: torch.Tensor, grad: torch.Tensor, ids: torch.Tensor,
+                               scale: float = 1.0, *, stream=None):
+    """In place: grad_weight (fp32 [V, H]) += embedding_backward(grad, ids, V, scale) in FP32; rows
+    that no id names are not touched (nor read), so a small batch costs its own rows only."""
+    if grad_weight.dtype != torch.float32:
+        raise TypeError("grad_weight must be float32")
+    if grad_weight.dim() != 2 or (grad_weight.size(1) > 1 and grad_weight.stride(1) != 1) or \
+            (grad_weight.size(0) > 1 and grad_weight.stride(0) < grad_weight.size(1)):
+        raise ValueError("grad_weight must be a 2-D row-major tensor (it is updated in place)")
+    V, H = grad_weight.shape
+    if grad.size(-1) != H:
+        raise ValueError("grad and grad_weight disagree on H")
+    ld = grad_weight.stride(0) if V > 1 else H
+    return _embedding_backward(grad, ids, V, scale, grad_weight, ld, 1, stream)
+
+
+class _EmbeddingGrad(torch.autograd.Function):
+    """Autograd wiring of rlk_embedding and rlk_embedding_backward (a dense gradient in the
+    weight's dtype)."""
+
+    @staticmethod
+    def forward(ctx, weight, ids, scale):
+        out = embedding(ids, weight.detach(), scale)
+        ctx.save_for_backward(ids)
+        ctx.of = weight.size(0), weight.dtype, scale
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        (ids,) = ctx.saved_tensors
+        V, dtype, scale = ctx.of
+        return embedding_backward(grad, ids, V, scale, dtype), None, None
+
+
+def embedding_trainable(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0):
+    """embedding(ids, weight, scale) differentiable with respect to weight."""
+    return _EmbeddingGrad.apply(weight, ids, scale)
+
+
+# ------------------------------------------------------------------ activations in 8 bits
+INT8_BLOCK = 32
+
+
+@_streamed
+def pack_int8(x: torch.Tensor, *, stream=None):
+    """(values int8 [..., K], exponents uint8 [..., ceil(K / 32)]) of x [..., K], bf16 or fp32.
+
+    Blocks of 32 columns of a row share a power of two 2^(e - 127) with e = max(1,
+    floor(log2 max|x|) + 121) and hold x / 2^(e - 127) rounded to whole numbers -127 .. 127; what they
+    stand for is exact in bf16.  A block with a NaN or an infinity reads back as NaN.
+    """
+    _require_cuda(x)
+    if x.dtype not in _DT:
+        raise TypeError("x must be bfloat16 or float32")
+    lead, K = x.shape[:-1], x.size(-1)
+    m, ld = _matrix(x.reshape(-1, K) if x.dim() != 2 else x, "x")
+    rows, blocks = m.size(0), -(-K // INT8_BLOCK)
+    wide = blocks * INT8_BLOCK
+    values = torch.empty((rows, wide), dtype=torch.int8, device=x.device)
+    exponents = torch.empty((rows, blocks), dtype=torch.uint8, device=x.device)
+    with _on(x.device):
+        _check(lib().rlk_pack_int8(_ptr(m), _DT[m.dtype], rows, K, ld, _ptr(values), wide,
+                                   _ptr(exponents), blocks, _stream_ptr(stream)), "rlk_pack_int8")
+    if len(lead) != 1:
+        values, exponents = values.reshape(*lead, wide), exponents.reshape(*lead, blocks)
+    return (values if wide == K else values[..., :K]), exponents
+
+
+def _int8_rows(values: torch.Tensor):
+    """(values, pitch) as the kernels read them: rows of whole blocks from a 16-byte boundary.
+    pack_int8's own are; others are copied into such rows."""
+    rows, K = values.shape
+    wide = -(-K // INT8_BLOCK) * INT8_BLOCK
+    ld = values.stride(0) if rows > 1 else wide
+    room = values.untyped_storage().nbytes() - values.storage_offset()
+    if ld >= wide and ld % 16 == 0 and values.data_ptr() % 16 == 0 and \
+            room >= (rows - 1) * ld + wide and (K == 1 or values.stride(1) == 1):
+        return values, ld
+    own = torch.zeros((rows, wide), dtype=torch.int8, device=values.device)
+    own[:, :K] = values
+    return own, wide
+
+
+@_streamed
+def unpack_int8(values: torch.Tensor, exponents: torch.Tensor, out_dtype=torch.bfloat16, *,
+                stream=None):
+    """What pack_int8's blocks stand for: [..., K] in out_dtype (exact in bf16 and fp32)."""
+    _require_cuda(values, exponents)
+    if values.dtype != torch.int8 or exponents.dtype != torch.uint8:
+        raise TypeError("values must be int8 and exponents uint8")
+    lead, K = values.shape[:-1], values.size(-1)
+    blocks = -(-K // INT8_BLOCK)
+    if exponents.shape != (*lead, blocks):
+        raise ValueError("exponents must have one value per block of 32 columns")
+    if len(lead) != 1:
+        # pack_int8's padded rows stay in place where the leading dimensions fold into one
+        values, exponents = values.flatten(0, -2) if lead else values[None], exponents.reshape(-1, blocks)
+    v, ldv = _int8_rows(values)
+    e, lde = _matrix(exponents, "exponents")
+    rows = v.size(0)
+    out = torch.empty((rows, K), dtype=out_dtype, device=values.device)
+    with _on(values.device):
+        _check(lib().rlk_unpack_int8(_ptr(v), rows, K, ldv, _ptr(e), lde, _ptr(out),
+                                     _DT[out_dtype], K, _stream_ptr(stream)), "rlk_unpack_int8")
+    return out if len(lead) == 1 else out.reshape(*lead, K)
+
+
+# ------------------------------------------------------------------ gated linear block
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+RLK_KEEP_NONE, RLK_KEEP_FP32, RLK_KEEP_INT8 = 0, 1, 2
+
+
+class _Gated:
+    """A gated block's sizes and settings, checked, and its operands."""
+
+    __slots__ = ("lead", "x", "ldx", "w", "ldw", "act", "M", "K", "F")
+
+    def __init__(self, X, W, activation):
+        _require_cuda(X, W)
+        if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+            raise TypeError("X and W must be bfloat16")
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+        self.act = ACTIVATIONS[activation]
+        self.lead, self.K = X.shape[:-1], X.size(-1)
+        if W.dim() != 2 or W.size(1) != self.K or W.size(0) % 2:
+            raise ValueError("W must be [2 F, K]: F rows of the gate, then F rows of the other projection")
+        self.F = W.size(0) // 2
+        self.x, self.ldx = _matrix(_flatten_rows(X), "X")
+        self.w, self.ldw = _matrix(W, "W")
+        self.M = self.x.size(0)
+
+
+def _kept_parts(kept, M: int, F: int):
+    """(keep, tensor, exponents) of what gated_linear kept, checked."""
+    if kept is None:
+        return RLK_KEEP_NONE, None, None
+    blocks = -(-F // INT8_BLOCK)
+    values, exponents = (kept, None) if isinstance(kept, torch.Tensor) else kept
+    ok = values.shape == (M, 2, blocks * INT8_BLOCK) and values.is_contiguous()
+    if exponents is None:
+        ok = ok and values.dtype == torch.float32
+    else:
+        ok = ok and values.dtype == torch.int8 and exponents.dtype == torch.uint8 and \
+            exponents.shape == (M, 2, blocks) and exponents.is_contiguous()
+    if not ok:
+        raise ValueError("kept must be what gated_linear(..., keep=) returned for these rows")
+    return (RLK_KEEP_FP32 if exponents is None else RLK_KEEP_INT8), values, exponents
+
+
+@_streamed
+def gated_linear(X: torch.Tensor, W: torch.Tensor, activation: str = "silu", out_dtype=torch.bfloat16,
+                 *, keep: str | None = None, stream=None):
+    """H [..., F] = act(X Wg^T) * (X Wu^T), rounded once, in one kernel.
+
+    X [..., K] bf16 (leading dims are rows), W [2 F, K] bf16: the F rows of Wg, then those of Wu.
+    activation: "silu" or "gelu_tanh".  A row's bits depend on its own row of X alone, and the
+    projections have the bits of det_linear(X, W, torch.float32).
+    keep: also return them for gated_linear_backward, "fp32" as a float32 tensor [rows, 2, Fp] or
+    "int8" as (values int8 [rows, 2, Fp], exponents uint8 [rows, 2, Fp / 32]) in pack_int8's
+    blocks, Fp = F rounded up to 32.  Forward only: use gated_linear_trainable for gradients.
+    """
+    _refuse_grad("gated_linear", X, W)
+    g = _Gated(X, W, activation)
+    if keep not in (None, "fp32", "int8"):
+        raise ValueError('keep must be None, "fp32" or "int8"')
+    dev, M, F = X.device, g.M, g.F
+    H = torch.empty((M, F), dtype=out_dtype, device=dev)
+    kept = exponents = None
+    if keep is not None:
+        blocks = -(-F // INT8_BLOCK)
+        kept = torch.empty((M, 2, blocks * INT8_BLOCK),
+                           dtype=torch.float32 if keep == "fp32" else torch.int8, device=dev)
+        if keep == "int8":
+            exponents = torch.empty((M, 2, blocks), dtype=torch.uint8, device=dev)
+    lib_ = lib()
+    with _on(dev):
+        n = lib_.rlk_gated_linear_workspace_size(_ptr(g.x), M, g.K, g.ldx, _ptr(g.w), F, g.ldw)
+        if n == 0:
+            raise RlkError(2, "rlk_gated_linear_workspace_size")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(lib_.rlk_gated_linear(
+            _ptr(g.x), M, g.K, g.ldx, _ptr(g.w), F, g.ldw, g.act, _ptr(H), _DT[out_dtype], F,
+            RLK_KEEP_NONE if keep is None else RLK_KEEP_FP32 if keep == "fp32" else RLK_KEEP_INT8,
+            _ptr(kept), _ptr(exponents), _ptr(ws), n, _stream_ptr(stream)), "rlk_gated_linear")
+    if len(g.lead) != 1:
+        H = H.reshape(*g.lead, F)
+    if keep is None:
+        return H
+    return H, (kept if exponents is None else (kept, exponents))
+
+
+@_streamed
+def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
+                          activation: str = "silu", *, kept=None, grad_x: bool = True,
+                          grad_w: bool = True, out_dtype=torch.bfloat16,
+                          return_grad_projections: bool = False, stream=None):
+    """(dX [..., K], dW [2 F, K]) of gated_linear for dH = dL/dH [..., F] (bf16 or fp32).
+
+    kept: what gated_linear(..., keep=) returned for these rows, or None to form the projections
+    again (the same bits as keep="fp32").  dX and dW are det_linear_backward's products of the
+    projections' gradient rounded to bf16; with return_grad_projections that is returned too,
+    as the [rows, 2 F] view that the products read.
+    """
+    g = _Gated(X, W, activation)
+    _require_cuda(dH)
+    if dH.dtype not in _DT:
+        raise TypeError("dH must be bfloat16 or float32")
+    if dH.shape != (*g.lead, g.F):
+        raise ValueError("dH must be [..., F] with X's leading shape")
+    d, ldd = _matrix(_flatten_rows(dH), "dH")
+    M, K, F, dev = g.M, g.K, g.F, X.device
+    keep, values, exponents = _kept_parts(kept, M, F)
+    _require_cuda(values, exponents)
+    dX = torch.empty((M, K), dtype=out_dtype, device=dev) if grad_x else None
+    dW = torch.empty((2 * F, K), dtype=out_dtype, device=dev) if grad_w else None
+    lib_ = lib()
+    dt = _DT[out_dtype]
+    with _on(dev):
+        n = lib_.rlk_gated_linear_backward_workspace_size(_ptr(g.x), M, K, g.ldx, _ptr(g.w), F, g.ldw)
+        if n == 0:
+            raise RlkError(2, "rlk_gated_linear_backward_workspace_size")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(lib_.rlk_gated_linear_backward(
+            _ptr(d), _DT[d.dtype], M, F, ldd, _ptr(g.x), K, g.ldx, _ptr(g.w), g.ldw, g.act, keep,
+            _ptr(values), _ptr(exponents), _ptr(dX), dt, K, _ptr(dW), dt, K, _ptr(ws), n,
+            _stream_ptr(stream)), "rlk_gated_linear_backward")
+    out = (None if dX is None else dX if X.dim() == 2 else dX.reshape(X.shape), dW)
+    if return_grad_projections:
+        ldG = -(-2 * F // 8) * 8
+        out = out + (ws[:M * ldG * 2].view(torch.bfloat16).view(M, ldG)[:, :2 * F],)
+    return out
+
+
+# Most bytes of FP32 projections that gated_linear_trainable keeps from the forward for the
+# backward of one block (checkpoint=None).
+KEEP_PROJECTIONS_BYTES = 2 << 30
+
+CHECKPOINTS = (None, "fp32", "int8", "again")
+
+
+class _GatedLinearGrad(torch.autograd.Function):
+    """Autograd wiring of rlk_gated_linear and rlk_gated_linear_backward.  Whatever the backward
+    needs is saved with autograd."""
+
+    @staticmethod
+    def forward(ctx, X, W, activation, checkpoint):
+        ctx.of = activation, checkpoint, X.shape
+        if checkpoint == "again":
+            H = gated_linear(X.detach(), W.detach(), activation)
+            ctx.save_for_backward(X, W)
+            return H
+        H, kept = gated_linear(X.detach(), W.detach(), activation, keep=checkpoint)
+        if checkpoint == "int8":             # X is read for dW alone
+            x = pack_int8(_flatten_rows(X.detach())) if ctx.needs_input_grad[1] else ()
+            ctx.save_for_backward(W, *kept, *x)
+        else:
+            ctx.save_for_backward(X, W, kept)
+        return H
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dH):
+        activation, checkpoint, shape = ctx.of
+        want_x, want_w = ctx.needs_input_grad[:2]
+        if not (want_x or want_w):
+            return None, None, None, None
+        kept = None
+        if checkpoint == "int8":
+            W, values, exponents, *x = ctx.saved_tensors
+            kept = values, exponents
+            if x:
+                X = unpack_int8(*x).view(shape)
+            else:                            # nothing reads it: its shape alone counts
+                X = torch.empty(shape, dtype=torch.bfloat16, device=W.device)
+        elif checkpoint == "fp32":
+            X, W, kept = ctx.saved_tensors
+        else:
+            X, W = ctx.saved_tensors
+        dX, dW = gated_linear_backward(dH, X, W, activation, kept=kept, grad_x=want_x, grad_w=want_w)
+        return dX, dW, None, None
+
+
+def gated_linear_trainable(X: torch.Tensor, W: torch.Tensor, activation: str = "silu", *,
+                           checkpoint: str | None = None):
+    """gated_linear(X, W, activation) differentiable with respect to X and W (BF16 gradients).
+
+    checkpoint says what waits for the backward beside W: "fp32" X and both projections in FP32
+    (8 F bytes a row), "int8" X and both projections in 8 bits (about K + 2 F bytes; the gradients
+    are those of the stored values), "again" X alone (the projections are formed again, the same
+    bits as "fp32").  None: "fp32" up to KEEP_PROJECTIONS_BYTES, else "again".  Where nothing asks
+    for a gradient nothing is kept.
+    """
+    if checkpoint not in CHECKPOINTS:
+        raise ValueError('checkpoint must be None, "fp32", "int8" or "again"')
+    if not (torch.is_grad_enabled() and (X.requires_grad or W.requires_grad)):
+        checkpoint = "again"
+    elif checkpoint is None:
+        wide = -(-W.size(0) // 2 // INT8_BLOCK) * INT8_BLOCK
+        rows = X.numel() // max(1, X.size(-1))
+        checkpoint = "fp32" if 8 * rows * wide <= KEEP_PROJECTIONS_BYTES else "again"
+    return _GatedLinearGrad.apply(X, W, activation, checkpoint)
+
+
 # ------------------------------------------------------------------ autograd wiring
 class _DetGemmGrad(torch.autograd.Function):
     """C = A . B under autograd: det_gemm_fwd forward; det_gemm_backward for the
@@ -1207,24 +1604,31 @@ class _DetGemmGrad(torch.autograd.Function):
 
 class _DetLinearGrad(torch.autograd.Function):
     """Y = X . W^T (W stored [N, K]) under autograd: det_linear forward,
-    det_linear_backward for dX and dW."""
+    det_linear_backward for dX and dW; with int8 the X that dW reads waits in 8 bits."""
 
     @staticmethod
-    def forward(ctx, X, W, out_dtype):
+    def forward(ctx, X, W, out_dtype, int8):
         with torch.no_grad():
             Y = det_linear(X.detach(), W.detach(), out_dtype)
-        ctx.save_for_backward(X, W)
+            held = (X,)
+            if int8:                             # X is read for dW alone
+                held = pack_int8(_flatten_rows(X.detach())) if ctx.needs_input_grad[1] else ()
+        ctx.save_for_backward(W, *held)
+        ctx.shape = X.shape
         return Y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        X, W = ctx.saved_tensors
+        W, *held = ctx.saved_tensors
         want_x, want_w = ctx.needs_input_grad[:2]
         if not (want_x or want_w):
-            return None, None, None
+            return None, None, None, None
+        if not held:
+            return det_linear_dx(dY, W).reshape(ctx.shape), None, None, None
+        X = unpack_int8(*held).view(ctx.shape) if len(held) == 2 else held[0]
         dX, dW = det_linear_backward(dY, X, W, grad_x=want_x, grad_w=want_w)
-        return (None if dX is None else dX.reshape(X.shape)), dW, None
+        return (None if dX is None else dX.reshape(X.shape)), dW, None, None
 
 
 def det_gemm_trainable(A: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat16):
@@ -1233,7 +1637,12 @@ def det_gemm_trainable(A: torch.Tensor, B: torch.Tensor, out_dtype=torch.bfloat1
     return _DetGemmGrad.apply(A, B, out_dtype)
 
 
-def det_linear_trainable(X: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16):
+def det_linear_trainable(X: torch.Tensor, W: torch.Tensor, out_dtype=torch.bfloat16, *,
+                         checkpoint: str | None = None):
     """det_linear(X, W) differentiable with respect to X and W: a deterministic,
-    batch-invariant stand-in for a bias-free nn.Linear forward and backward."""
-    return _DetLinearGrad.apply(X, W, out_dtype)
+    batch-invariant stand-in for a bias-free nn.Linear forward and backward.
+    checkpoint="int8" holds X for the backward in pack_int8's blocks (half its bytes): dW is then
+    the gradient for the stored values; the output and dX are the same bits."""
+    if checkpoint not in (None, "int8"):
+        raise ValueError('checkpoint must be None or "int8"')
+    return _DetLinearGrad.apply(X, W, out_dtype, checkpoint == "int8")

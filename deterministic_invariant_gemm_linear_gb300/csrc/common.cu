@@ -83,6 +83,21 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t
   return r == CUDA_SUCCESS;
 }
 
+bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                    uint64_t planes, uint64_t ld, uint64_t plane_stride, uint32_t box_inner,
+                    uint32_t box_outer, uint32_t box_planes) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {inner, outer, planes};
+  cuuint64_t strides[2] = {ld * 2, plane_stride * 2};
+  cuuint32_t box[3] = {box_inner, box_outer, box_planes};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- staging kernels
 namespace {
 
@@ -305,7 +320,8 @@ rlk_status rlk_get_device_error(void* stream, uint32_t* flags) {
   }
   *flags = rlk::take_error_linear_logp() | rlk::take_error_det_gemm() | rlk::take_error_common() |
            rlk::take_error_linear_logp_bwd() | rlk::take_error_linear_distill() |
-           rlk::take_error_sample();
+           rlk::take_error_sample() | rlk::take_error_embedding() | rlk::take_error_int8() |
+           rlk::take_error_gated_linear();
   if (*flags & RLK_DEVERR_TIMEOUT) return RLK_ERR_TIMEOUT;
   return *flags ? RLK_ERR_BOUNDS : RLK_OK;
 }

@@ -1,0 +1,459 @@
+// Embedding lookup and its gradient on sm_103a.
+//
+//   out[r, :] = s W[id_r, :]           dW[v, :] = s sum_{r: id_r = v} d[r, :]
+//
+// Both are bound by HBM.  The lookup reads N rows and writes N rows.  The gradient writes the
+// whole table (V H elements, most of the bytes) and reads the N rows of d once.
+//
+// The gradient's order is fixed without atomics on numbers: the rows are sorted by id, rows of
+// one id in ascending order, and each table row adds its own rows in that order (groups of 64,
+// then the groups' sums), so its bits depend on its own rows of d alone.
+//  * embed_sort_kernel: the whole sort in one launch, with no exchange between CTAs.  CTA j owns
+//    1024 ids and reads all N ids: how many are smaller says where its part of the order begins;
+//    its warps, each over its own stretch of the rows, count its ids and then place their rows
+//    (equal ids of a warp's 32 rows are ranked by match_any).  N ids are read by V / 1024 CTAs
+//    from L2, which for N rows of H elements of d is less than reading d.
+//  * embed_groups_kernel: ids with more than 64 rows (a padding or a common token can have most
+//    of them) are cut into groups of 64 that any CTA can add; their sums wait in the workspace.
+//  * embed_rows_kernel: every table row: zeros, its rows' sum, or its groups' sum.
+#include <math.h>
+
+#include <mutex>
+
+#include "rlk.h"
+#include "rlk_internal.h"
+#include "rlk_rows.cuh"
+
+namespace rlk {
+
+__device__ unsigned int g_err_embedding = 0;
+
+namespace {
+
+// ---------------------------------------------------------------- lookup
+template <bool kWFp32, bool kOutFp32>
+__global__ void __launch_bounds__(kRowThreads)
+    embed_kernel(const int64_t* __restrict__ ids, int64_t ids_stride, int64_t N,
+                 const void* __restrict__ weight, int64_t V, int H, int64_t ldw, int vec_w,
+                 float scale, void* __restrict__ out, int64_t ldo, int vec_o, RowLanes lanes) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int64_t r = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
+  if (r >= N) return;
+  const int64_t id = __ldg(ids + r * ids_stride);
+  const bool known = id >= 0 && id < V;
+  for (int c = lanes.col(); c < H; c += lanes.step()) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    if (known) {
+      load8<kWFp32>(weight, id * ldw, c, H, vec_w, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], scale);
+    }
+    if (RLK_STORE_OK(r < N && min(c + 8, H) <= ldo, &g_err_embedding))
+      store8<kOutFp32>(out, r * ldo, c, H, vec_o, v);
+  }
+}
+
+// ---------------------------------------------------------------- gradient: the sort
+constexpr int kSortIds = 1024;        // ids a CTA owns, one a thread
+constexpr int kSortWarps = kSortIds / 32;
+constexpr int kSortSmem = kSortWarps * kSortIds * 4;    // a count for each warp and id
+constexpr int kGroup = RLK_EMBED_GROUP;
+
+struct Order {
+  int* start;        // [V + 1]: the rows of id v are rows[start[v] .. start[v + 1] - 1]
+  int* rows;         // [N], ascending within an id
+  int* group_base;   // [V]: first group of an id with more than kGroup rows
+  int2* groups;      // {first place in rows, number of rows}
+  int* group_count;
+  float* sums;       // [groups, ld_sums]
+  int64_t ld_sums;
+};
+
+// Sum over the block and this thread's exclusive prefix, of one int a thread.
+__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  return x - v + (warp ? warp_sums[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kSortIds)
+    embed_sort_kernel(const int64_t* __restrict__ ids, int64_t ids_stride, int N, int V,
+                      Order o, int max_groups) {
+  extern __shared__ int count[];      // [kSortWarps][kSortIds]
+  __shared__ int warp_sums[32];
+  __shared__ int2 heavy[kSortIds];    // {id - lo, first group}
+  __shared__ int n_heavy;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int lo = blockIdx.x * kSortIds;
+  const int hi = min(lo + kSortIds, V);
+#pragma unroll 8
+  for (int w = 0; w < kSortWarps; ++w) count[w * kSortIds + t] = 0;
+  if (t == 0) n_heavy = 0;
+  __syncthreads();
+  griddep_wait();
+  if (t == 0) griddep_launch_dependents();
+  // each warp takes one stretch of the rows, a multiple of 32 long
+  const int per = (int)((((int64_t)N + kSortIds - 1) / kSortIds) * 32);
+  const int64_t n0 = (int64_t)warp * per;
+  const int n1 = (int)(n0 + per < N ? n0 + per : N);
+  int below = 0;
+  int* mine = count + warp * kSortIds;
+#pragma unroll 4
+  for (int64_t n = n0 + lane; n < n1; n += 32) {
+    const int64_t id = __ldg(ids + n * ids_stride);
+    below += id >= 0 && id < lo;
+    if (id >= lo && id < hi) atomicAdd(mine + (int)(id - lo), 1);
+  }
+  int before, total, rows = 0;
+  block_prefix(below, warp_sums, &before);      // rows with smaller ids; also a barrier
+#pragma unroll 8
+  for (int w = 0; w < kSortWarps; ++w) rows += count[w * kSortIds + t];
+  int at = before + block_prefix(rows, warp_sums, &total);
+  if (lo + t < V && RLK_STORE_OK(lo + t < V, &g_err_embedding)) {
+    o.start[lo + t] = at;
+    if (lo + t == V - 1) o.start[V] = at + rows;
+    if (rows > kGroup) {
+      const int base = atomicAdd(o.group_count, (rows + kGroup - 1) / kGroup);
+      o.group_base[lo + t] = base;
+      heavy[atomicAdd(&n_heavy, 1)] = make_int2(t, base);
+    }
+  }
+  const int first = at;
+#pragma unroll 8
+  for (int w = 0; w < kSortWarps; ++w) {        // where each warp's rows of this id begin
+    const int c = count[w * kSortIds + t];
+    count[w * kSortIds + t] = at;
+    at += c;
+  }
+  __syncthreads();
+  // place the rows, in order within a warp
+  for (int64_t n = n0 + lane; n - lane < n1; n += 32) {
+    const int64_t id = n < n1 ? __ldg(ids + n * ids_stride) : -1;
+    const bool own = id >= lo && id < hi;
+    if (!__ballot_sync(0xffffffffu, own)) continue;
+    const int key = own ? (int)(id - lo) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (own) {
+      const int place = mine[key] + rank;
+      if (RLK_STORE_OK(place >= 0 && place < N, &g_err_embedding)) o.rows[place] = (int)n;
+    }
+    __syncwarp();
+    if (own && rank == 0) mine[key] += __popc(same);
+    __syncwarp();
+  }
+  // the groups of the ids with many rows: `first` of an id is what its thread computed
+  __syncthreads();
+  int* first_of = count;              // reused: every place was taken above
+  int* rows_of = count + kSortIds;
+  first_of[t] = first;
+  rows_of[t] = rows;
+  __syncthreads();
+  for (int h = 0; h < n_heavy; ++h) {
+    const int k = heavy[h].x, base = heavy[h].y;
+    const int f = first_of[k], n = rows_of[k];
+    for (int g = t; g * kGroup < n; g += kSortIds)
+      if (RLK_STORE_OK(base + g < max_groups, &g_err_embedding))
+        o.groups[base + g] = make_int2(f + g * kGroup, min(kGroup, n - g * kGroup));
+  }
+}
+
+// ---------------------------------------------------------------- gradient: the sums
+// acc = the rows rows[at .. at + n - 1] of d at columns c .. c + 7, added in that order.
+template <bool kFp32>
+__device__ __forceinline__ void add_rows(const void* __restrict__ d, int64_t ldd, int vec,
+                                         const int* __restrict__ rows, int at, int n, int c, int H,
+                                         float (&acc)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  int k = 0;
+  for (; k + 4 <= n; k += 4) {
+    float v[4][8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      load8<kFp32>(d, (int64_t)__ldg(rows + at + k + j) * ldd, c, H, vec, v[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[j][i]);
+  }
+  for (; k < n; ++k) {
+    float v[8];
+    load8<kFp32>(d, (int64_t)__ldg(rows + at + k) * ldd, c, H, vec, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[i]);
+  }
+}
+
+template <bool kDFp32>
+__global__ void __launch_bounds__(kRowThreads)
+    embed_groups_kernel(const void* __restrict__ d, int64_t ldd, int vec_d, int H, Order o,
+                        int max_groups, RowLanes lanes) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int n = min(*o.group_count, max_groups);
+  for (int g = (int)blockIdx.x * lanes.rows() + lanes.row(); g < n;
+       g += (int)gridDim.x * lanes.rows()) {
+    const int2 what = o.groups[g];
+    for (int c = (int)blockIdx.y * lanes.step() + lanes.col(); c < H;
+         c += (int)gridDim.y * lanes.step()) {
+      float acc[8];
+      add_rows<kDFp32>(d, ldd, vec_d, o.rows, what.x, what.y, c, H, acc);
+      if (RLK_STORE_OK(c + 8 <= o.ld_sums, &g_err_embedding))
+        store8<true>(o.sums, g * o.ld_sums, c, (int)o.ld_sums, true, acc);
+    }
+  }
+}
+
+template <bool kDFp32, bool kOutFp32, bool kAccumulate>
+__global__ void __launch_bounds__(kRowThreads)
+    embed_rows_kernel(const void* __restrict__ d, int64_t ldd, int vec_d, int H, int V, Order o,
+                      float scale, void* __restrict__ dw, int64_t ldw, int vec_w, RowLanes lanes) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int64_t v = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
+  if (v >= V) return;
+  const int at = __ldg(o.start + v), n = __ldg(o.start + v + 1) - at;
+  if (kAccumulate && n == 0) return;
+  for (int c = lanes.col(); c < H; c += lanes.step()) {
+    float acc[8];
+    if (n <= kGroup) {
+      add_rows<kDFp32>(d, ldd, vec_d, o.rows, at, n, c, H, acc);
+    } else {
+      const int groups = (n + kGroup - 1) / kGroup;
+      const float* s = o.sums + (int64_t)__ldg(o.group_base + v) * o.ld_sums;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 4
+      for (int g = 0; g < groups; ++g) {
+        float x[8];
+        load8<true>(s, g * o.ld_sums, c, (int)o.ld_sums, true, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], x[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = __fmul_rn(acc[i], scale);
+    if (kAccumulate) {
+      float x[8];
+      const float* p = static_cast<const float*>(dw) + v * ldw;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = c + i < H ? p[c + i] : 0.f;
+        acc[i] = __fadd_rn(x[i], acc[i]);
+      }
+    }
+    if (RLK_STORE_OK(v < V && min(c + 8, H) <= ldw, &g_err_embedding))
+      store8<kOutFp32>(dw, v * ldw, c, H, vec_w, acc);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+constexpr int64_t kMaxTable = int64_t(1) << 30;    // ids of a gradient: a sorting CTA's last + 1 fits an int
+
+// Most groups that the ids with more than kGroup of N rows can make: ceil(c / 64) <= 2 c / 65
+// for every c > 64.
+inline int64_t most_groups(int64_t N) { return 2 * N / (kGroup + 1); }
+
+struct EmbedPlan {
+  int64_t groups = 0, ld_sums = 0;
+  size_t off_base = 0, off_rows = 0, off_groups = 0, off_count = 0, off_sums = 0, total = 0;
+};
+
+bool embed_plan(int64_t N, int64_t V, int64_t H, EmbedPlan* p) {
+  if (N < 0 || N >= kMaxExtent || V < 1 || V >= kMaxTable || H < 1 || H >= kMaxWidth) return false;
+  p->groups = most_groups(N);
+  p->ld_sums = ceil_div(H, 8) * 8;
+  size_t off = align_up((size_t)(V + 1) * 4, 256);
+  p->off_base = off;
+  off = align_up(off + (size_t)V * 4, 256);
+  p->off_rows = off;
+  off = align_up(off + (size_t)N * 4, 256);
+  p->off_groups = off;
+  off = align_up(off + (size_t)p->groups * 8, 256);
+  p->off_count = off;
+  off += 256;
+  p->off_sums = off;
+  p->total = align_up(off + (size_t)p->groups * p->ld_sums * 4, 256);
+  return true;
+}
+
+std::mutex g_attr_mutex;
+bool g_attr_set[64];
+
+cudaError_t ensure_attrs(int dev) {
+  std::lock_guard<std::mutex> lock(g_attr_mutex);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!g_attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e != cudaSuccess) return e;
+    g_attr_set[dev] = true;
+  }
+  return cudaSuccess;
+}
+
+rlk_status cuda_failed() {
+  cudaGetLastError();
+  return RLK_ERR_CUDA;
+}
+
+}  // namespace
+
+uint32_t take_error_embedding() {
+  unsigned int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_embedding, sizeof v) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaMemcpyToSymbol(g_err_embedding, &zero, sizeof zero);
+  cudaGetLastError();
+  return v;
+}
+
+}  // namespace rlk
+
+using namespace rlk;
+
+extern "C" {
+
+rlk_status rlk_embedding(const int64_t* ids, int64_t ids_stride, int64_t N, const void* weight,
+                         int weight_dtype, int64_t V, int64_t H, int64_t ld_weight, float scale,
+                         void* out, int out_dtype, int64_t ld_out, void* stream) {
+  RLK_CALL_RANGE();
+  if (!known_dtype(weight_dtype) || !known_dtype(out_dtype)) return RLK_ERR_DTYPE;
+  if (N < 0 || N >= kMaxExtent || V < 1 || V >= kMaxExtent || H < 1 || H >= kMaxWidth ||
+      ids_stride < 0 || ids_stride >= kPitchLimit || ld_weight < H || ld_weight >= kPitchLimit || ld_out < H ||
+      ld_out >= kPitchLimit)
+    return RLK_ERR_SHAPE;
+  if (!isfinite(scale)) return RLK_ERR_VALUE;
+  if (N == 0) return RLK_OK;
+  if (!ids || !weight || !out) return RLK_ERR_NULL;
+  if (!is_aligned(ids, 8) || !is_aligned(weight, dtype_bytes(weight_dtype)) ||
+      !is_aligned(out, dtype_bytes(out_dtype)))
+    return RLK_ERR_ALIGN;
+  DeviceInfo dev;
+  const rlk_status st = device_ready(&dev);
+  if (st != RLK_OK) return st;
+  const RowLanes lanes = row_lanes(H);
+  const dim3 grid((unsigned)ceil_div(N, lanes.rows()));
+  const int vw = rows_vec(weight, ld_weight, dtype_bytes(weight_dtype));
+  const int vo = rows_vec(out, ld_out, dtype_bytes(out_dtype));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = by_dtypes(weight_dtype, out_dtype, [&](auto w32, auto o32) {
+    return launch_overlapped(embed_kernel<decltype(w32)::value, decltype(o32)::value>, grid,
+                             kRowThreads, 0, s, ids, ids_stride, N, weight, V, (int)H, ld_weight,
+                             vw, scale, out, ld_out, vo, lanes);
+  });
+  return e == cudaSuccess ? RLK_OK : cuda_failed();
+}
+
+size_t rlk_embedding_backward_workspace_size(int64_t N, int64_t V, int64_t H) {
+  EmbedPlan p;
+  return embed_plan(N, V, H, &p) ? p.total : 0;
+}
+
+rlk_status rlk_embedding_backward(const int64_t* ids, int64_t ids_stride, int64_t N,
+                                  const void* grad, int grad_dtype, int64_t H, int64_t ld_grad,
+                                  float scale, void* grad_weight, int grad_weight_dtype, int64_t V,
+                                  int64_t ld_grad_weight, int accumulate, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  RLK_CALL_RANGE();
+  if (!known_dtype(grad_dtype) || !known_dtype(grad_weight_dtype) ||
+      (accumulate && grad_weight_dtype != RLK_FP32))
+    return RLK_ERR_DTYPE;
+  EmbedPlan p;
+  if (!embed_plan(N, V, H, &p) || ids_stride < 0 || ids_stride >= kPitchLimit || ld_grad < H || ld_grad >= kPitchLimit ||
+      ld_grad_weight < H || ld_grad_weight >= kPitchLimit)
+    return RLK_ERR_SHAPE;
+  if (!isfinite(scale)) return RLK_ERR_VALUE;
+  if (N == 0 && accumulate) return RLK_OK;
+  if (!grad_weight || (N > 0 && (!ids || !grad))) return RLK_ERR_NULL;
+  const size_t esize = dtype_bytes(grad_weight_dtype);
+  if (!is_aligned(ids, 8) || !is_aligned(grad, dtype_bytes(grad_dtype)) ||
+      !is_aligned(grad_weight, esize))
+    return RLK_ERR_ALIGN;
+  if (N > 0 && (!workspace || !is_aligned(workspace, 256) || workspace_bytes < p.total))
+    return RLK_ERR_WORKSPACE;
+  DeviceInfo dev;
+  const rlk_status st = device_ready(&dev);
+  if (st != RLK_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0)
+    return cudaMemset2DAsync(grad_weight, ld_grad_weight * esize, 0, H * esize, V, s) == cudaSuccess
+               ? RLK_OK
+               : cuda_failed();
+  if (ensure_attrs(dev.device) != cudaSuccess) return cuda_failed();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Order o;
+  o.start = reinterpret_cast<int*>(ws);
+  o.group_base = reinterpret_cast<int*>(ws + p.off_base);
+  o.rows = reinterpret_cast<int*>(ws + p.off_rows);
+  o.groups = reinterpret_cast<int2*>(ws + p.off_groups);
+  o.group_count = reinterpret_cast<int*>(ws + p.off_count);
+  o.sums = reinterpret_cast<float*>(ws + p.off_sums);
+  o.ld_sums = p.ld_sums;
+  const bool heavy = N > kGroup;       // fewer rows cannot make an id of many
+  if (heavy && cudaMemsetAsync(o.group_count, 0, sizeof(int), s) != cudaSuccess)
+    return cuda_failed();
+  if (launch_overlapped(embed_sort_kernel, dim3((unsigned)ceil_div(V, kSortIds)), kSortIds,
+                        kSortSmem, s, ids, ids_stride, (int)N, (int)V, o,
+                        (int)p.groups) != cudaSuccess)
+    return cuda_failed();
+  const RowLanes lanes = row_lanes(H);
+  const int vg = rows_vec(grad, ld_grad, dtype_bytes(grad_dtype));
+  const int vw = rows_vec(grad_weight, ld_grad_weight, esize);
+  const int64_t col_blocks = ceil_div(H, lanes.step());
+  if (heavy) {
+    // groups by columns: four blocks an SM, or all there can be
+    int64_t gx = ceil_div(4 * (int64_t)dev.sm_count, col_blocks);
+    const int64_t all = ceil_div(p.groups, lanes.rows());
+    gx = gx < all ? gx : all;
+    const dim3 grid((unsigned)(gx < 1 ? 1 : gx), (unsigned)col_blocks);
+    const cudaError_t e =
+        grad_dtype == RLK_FP32
+            ? launch_overlapped(embed_groups_kernel<true>, grid, kRowThreads, 0, s, grad, ld_grad,
+                                vg, (int)H, o, (int)p.groups, lanes)
+            : launch_overlapped(embed_groups_kernel<false>, grid, kRowThreads, 0, s, grad, ld_grad,
+                                vg, (int)H, o, (int)p.groups, lanes);
+    if (e != cudaSuccess) return cuda_failed();
+  }
+  const dim3 grid((unsigned)ceil_div(V, lanes.rows()));
+  const cudaError_t e = by_dtypes(grad_dtype, grad_weight_dtype, [&](auto d32, auto o32) {
+    constexpr bool kD = decltype(d32)::value, kO = decltype(o32)::value;
+    if constexpr (kO)
+      if (accumulate)
+        return launch_overlapped(embed_rows_kernel<kD, true, true>, grid, kRowThreads, 0, s, grad,
+                                 ld_grad, vg, (int)H, (int)V, o, scale, grad_weight,
+                                 ld_grad_weight, vw, lanes);
+    return launch_overlapped(embed_rows_kernel<kD, kO, false>, grid, kRowThreads, 0, s, grad,
+                             ld_grad, vg, (int)H, (int)V, o, scale, grad_weight, ld_grad_weight,
+                             vw, lanes);
+  });
+  return e == cudaSuccess ? RLK_OK : cuda_failed();
+}
+
+}  // extern "C"

@@ -1,0 +1,875 @@
+// The gated linear block on sm_103a: both projections, the gate's activation and the product in
+// one kernel, and its backward.
+//
+//   g = X . Wg^T,  u = X . Wu^T,  h = act(g) u        act(g) = g s,  s = sigmoid(a(g))
+//   SiLU: a(g) = g;  GELU in its tanh form: a(g) = 2 sqrt(2/pi) (g + 0.044715 g^3)
+//   act'(g) = s + g s (1 - s) a'(g)
+//   G = dL/d[g, u] = [d u act'(g), d act(g)],  dX = G . W,  dW = G^T . X        W = [Wg; Wu]
+//
+// The forward is 4 M K F operations on the tensor cores.  A tile of 256 rows holds 128 columns of g
+// and the same 128 of u side by side in one accumulator (MMA N = 256): the right operand's tile is
+// 128 rows of Wg followed by 128 of Wu, read by one 3-D tensor map {K, F, 2}.  So the loops are
+// the library's (rlk_pipeline.cuh, rlk_solo.cuh), each accumulator is the sum that det_linear
+// forms, and the epilogue thread that owns a row finds g and u of a column 128 accumulator columns
+// apart: the [M, 2 F] projections need not exist.
+// The backward forms G (the same loop again, or one pass over kept g and u), rounds it to BF16,
+// the type in which the two products read it, and runs them as det_linear's backward.
+#include <math.h>
+
+#include <mutex>
+
+#include <cuda_bf16.h>
+
+#include "rlk.h"
+#include "rlk_int8.cuh"
+#include "rlk_internal.h"
+#include "rlk_pipeline.cuh"
+#include "rlk_rows.cuh"
+#include "rlk_solo.cuh"
+
+namespace rlk {
+
+__device__ unsigned int g_err_gated_linear = 0;
+
+namespace {
+
+constexpr int kGateCols = kBN / 2;     // columns of g (and of u) in a 256-wide accumulator
+
+// ---------------------------------------------------------------- the activation
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kTanhSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kTanhCube = 0.044715f;
+
+// s = sigmoid(a(g)) and s (1 - s), from e = exp(-|a|) so that neither overflows.
+template <int kAct>
+__device__ __forceinline__ void gate(float g, float& s, float& both) {
+  float a = g;
+  if constexpr (kAct == RLK_ACT_GELU_TANH)
+    a = kTanhSlope * __fmaf_rn(kTanhCube * g * g, g, g);
+  const float e = ex2_approx(-fabsf(a) * kLog2e);
+  const float r = rcp_approx(1.f + e);
+  s = a < 0.f ? e * r : r;
+  both = e * r * r;
+}
+
+template <int kAct>
+__device__ __forceinline__ float gate_value(float g) {
+  float s, both;
+  gate<kAct>(g, s, both);
+  return g * s;
+}
+
+// act(g) and act'(g).
+template <int kAct>
+__device__ __forceinline__ void gate_slope(float g, float& value, float& slope) {
+  float s, both;
+  gate<kAct>(g, s, both);
+  value = g * s;
+  float da = 1.f;
+  if constexpr (kAct == RLK_ACT_GELU_TANH)
+    da = kTanhSlope * __fmaf_rn(3.f * kTanhCube * g, g, 1.f);
+  slope = both == 0.f ? s : __fmaf_rn(g * both, da, s);   // a flat end, however large a'(g)
+}
+
+// ---------------------------------------------------------------- operands and schedule
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar, int32_t c0, int32_t c1,
+                                                 int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// The right operand of the 2-SM loop.  The loop asks for rows [row0, row0 + 128) of tiles of 256:
+// tile t is columns [128 t, 128 t + 128) of g, whose weight rows rank 0 stages, and the same of
+// u, whose rows rank 1 stages.  K-major, laid out as OperandTile<false, 128>.
+template <int kStageK>
+struct GateUpHalf {
+  using Layout = OperandTile<false, kGateCols, kStageK>;
+  static constexpr int kK = kStageK;
+  static constexpr uint32_t kBytes = Layout::kBytes;
+  template <bool kPair>
+  static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                              int32_t row0, int32_t k0) {
+    const int32_t f0 = row0 / (2 * kGateCols) * kGateCols, plane = row0 / kGateCols & 1;
+#pragma unroll
+    for (int i = 0; i < kStageK / 64; ++i)
+      tma_load_3d_pair(dst + i * (kGateCols * 128), map, bar, k0 + 64 * i, f0, plane);
+  }
+  static __device__ __forceinline__ uint64_t desc(uint32_t base, int kstep) {
+    return Layout::desc(base, kstep);
+  }
+};
+
+// The right operand of the one-CTA loop: kCols rows of Wg, then the same of Wu, in one copy.
+template <int kCols>
+struct GateUpBoth {
+  using Layout = OperandTile<false, 2 * kCols>;
+  static constexpr uint32_t kBytes = Layout::kBytes;
+  static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                              int32_t row0, int32_t k0) {
+    tma_load_3d(dst, map, bar, k0, row0 / 2, 0);
+  }
+  static __device__ __forceinline__ uint64_t desc(uint32_t base, int kstep) {
+    return Layout::desc(base, kstep);
+  }
+};
+
+struct GatedSched {
+  Banded order;     // rows = blocks of 256 rows (one CTA pair) or the only one of 128, cols = tiles
+  int* counter;     // zeroed unit counter in the workspace, or null (round-robin)
+  int nkb, nkb64;   // reduction stages over K, and its 64-wide blocks
+  int tile_rows;    // right-operand rows per tile: 256, or 2 w in the one-CTA loop
+  __device__ __forceinline__ int num_units() const { return order.count(); }
+  __device__ __forceinline__ int unit_tiles(int) const { return 1; }
+  __device__ __forceinline__ void tile_coords(int u, int, int& a0, int& b0) const {
+    int rb, ct;
+    order.unit(u, rb, ct);
+    a0 = rb * kPairRows;
+    b0 = ct * tile_rows;
+  }
+};
+
+// ---------------------------------------------------------------- rows of 32 columns
+// The widest vector (16, 8 or 4 bytes; 0: elements) that addresses `base + 32 c` of every row allow.
+inline int run_width(const void* base, int64_t ld, int64_t esize) {
+  for (int w = 16; w >= 4; w /= 2)
+    if (reinterpret_cast<uintptr_t>(base) % w == 0 && (ld * esize) % w == 0) return w;
+  return 0;
+}
+
+// x[0 .. n) to BF16 or FP32 at dst (n = 32 for whole runs, which use vectors of `width` bytes).
+__device__ __forceinline__ void store_run_bf16(uint16_t* dst, const float (&x)[32], int n,
+                                               int width) {
+  if (n >= 32 && width != 0) {
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    if (width == 16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4*>(dst)[i] =
+            make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+    } else if (width == 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<uint2*>(dst)[i] = make_uint2(p[2 * i], p[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(dst)[i] = p[i];
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < n) reinterpret_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(x[i]);
+}
+
+__device__ __forceinline__ void store_run_fp32(float* dst, const float (&x)[32], int n, int width) {
+  if (n >= 32 && width == 16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      reinterpret_cast<float4*>(dst)[i] =
+          make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < n) dst[i] = x[i];
+}
+
+// x[0 .. 32) = n elements at src, the rest 0.
+__device__ __forceinline__ void load_run(const void* src, int64_t at, int fp32, int n, int width,
+                                         float (&x)[32]) {
+  if (n >= 32 && width == 16) {
+    if (fp32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 v = __ldg(p + i);
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+      }
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = __ldg(p + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+          x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    x[i] = 0.f;
+    if (i < n)
+      x[i] = fp32 ? __ldg(static_cast<const float*>(src) + at + i)
+                  : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(src) + at + i)
+                                    << 16);
+  }
+}
+
+// ---------------------------------------------------------------- forward
+struct GatedOut {
+  int M, F;
+  int act;
+  void* H;
+  int64_t ldh;
+  int h_fp32, h_width;
+  int keep;
+  void* kept;            // [M, 2, Fp] FP32 or int8
+  uint8_t* exponents;    // [M, 2, Fp / 32]
+  int Fp;                // 32 ceil(F / 32)
+};
+
+// One projection's 32 columns from column f of row `row` as they are kept (plane 0: g, 1: u).
+__device__ __forceinline__ void keep_run(const GatedOut& o, int row, int f, int plane,
+                                         const uint32_t (&z)[32]) {
+  if (!RLK_STORE_OK(row < o.M && f + 32 <= o.Fp, &g_err_gated_linear)) return;
+  const int64_t at = ((int64_t)row * 2 + plane) * o.Fp + f;
+  if (o.keep == RLK_KEEP_FP32) {
+    uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(o.kept) + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      d[i] = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+    return;
+  }
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) most = max(most, z[i] & 0x7fffffffu);
+  const uint32_t e = int8_exponent(most);
+  const float inverse = int8_inverse(e);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = 0;
+    if (e != 255u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[i] |= int8_value(__uint_as_float(z[4 * i + j]), inverse) << (8 * j);
+    }
+  }
+  uint4* d = reinterpret_cast<uint4*>(static_cast<int8_t*>(o.kept) + at);
+  d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  o.exponents[at / kInt8Block] = (uint8_t)e;
+}
+
+template <int kAct>
+__device__ __forceinline__ void value_run(const uint32_t (&g)[32], const uint32_t (&u)[32],
+                                          float (&h)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    h[i] = gate_value<kAct>(__uint_as_float(g[i])) * __uint_as_float(u[i]);
+}
+
+// A tile's epilogue in one warp: accumulator columns [0, kCols) hold g and [kCols, 2 kCols) u of
+// columns f0 .. f0 + kCols - 1; the thread's row is `row`.
+template <int kCols>
+__device__ __forceinline__ void gated_tile(const GatedOut& o, uint32_t taddr, int row, int f0) {
+#pragma unroll 1
+  for (int c = 0; c < kCols / 32; ++c) {
+    const int f = f0 + 32 * c;
+    if (f >= o.F) break;                    // uniform: depends on the tile only
+    uint32_t g[32], u[32];
+    __syncwarp();
+    tmem_ld32(taddr + 32 * c, g);
+    tmem_ld32(taddr + kCols + 32 * c, u);
+    tmem_wait_ld();
+    if (row >= o.M) continue;
+    float h[32];
+    if (o.act == RLK_ACT_SILU)
+      value_run<RLK_ACT_SILU>(g, u, h);
+    else
+      value_run<RLK_ACT_GELU_TANH>(g, u, h);
+    const int n = min(32, o.F - f);
+    const int64_t at = (int64_t)row * o.ldh + f;
+    if (RLK_STORE_OK(row < o.M && f + n <= o.ldh, &g_err_gated_linear)) {
+      if (o.h_fp32)
+        store_run_fp32(static_cast<float*>(o.H) + at, h, n, o.h_width);
+      else
+        store_run_bf16(static_cast<uint16_t*>(o.H) + at, h, n, o.h_width);
+    }
+    if (o.keep != RLK_KEEP_NONE) {
+      keep_run(o, row, f, 0, g);
+      keep_run(o, row, f, 1, u);
+    }
+  }
+}
+
+template <int kK>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gated_linear_kernel(const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_w, GatedSched sc, GatedOut o) {
+  extern __shared__ uint8_t smem_raw[];
+  const PipeSmem ps = pipe_smem(smem_raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w);
+  }
+  const uint32_t tmem = pipe_setup(ps);
+  using TA = OperandTile<false, kHalfRows, kK>;
+  using TB = GateUpHalf<kK>;
+  using R = PairRingT<kHalfRows, kK>;
+  if (warp == 0) {
+    if (lane == 0)
+      producer_role<TA, TB, GatedSched, R>(&tm_x, &tm_w, sc, ps, &g_err_gated_linear);
+    if (lane == 1 && ps.rank == 0) scheduler_role(sc, ps, &g_err_gated_linear);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && ps.rank == 0)
+      mma_role<TA, TB, GatedSched, R>(sc, ps, tmem, idesc_bf16_f32(kPairRows, kBN, false, false),
+                                      &g_err_gated_linear);
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int k = 0;; ++k) {
+      const int u = warp_unit_take(sc, ps, k, &g_err_gated_linear);
+      if (u < 0) break;
+      if (!epilogue_acquire(ps, acc, acc_phase, &g_err_gated_linear)) break;
+      int r0, b0;
+      sc.tile_coords(u, 0, r0, b0);
+      gated_tile<kGateCols>(o, tmem + acc * kAccCols + lane_off,
+                            r0 + (int)ps.rank * kHalfRows + q * 32 + lane, b0 / 2);
+      epilogue_release(ps, acc);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  pipe_teardown(tmem);
+}
+
+// At most 128 rows: the weight is streamed once, a CTA to a tile of kCols columns.
+template <int kARows, int kCols>
+__global__ void __launch_bounds__(kThreads, 1)
+    gated_linear_solo_kernel(const __grid_constant__ CUtensorMap tm_x,
+                             const __grid_constant__ CUtensorMap tm_w, GatedSched sc, GatedOut o) {
+  extern __shared__ uint8_t smem_raw[];
+  const PipeSmem ps = pipe_smem(smem_raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w);
+  }
+  const uint32_t tmem = solo_setup(ps);
+  using R = SoloRing<kARows, 2 * kCols>;
+  using TA = OperandTile<false, kARows>;
+  using TB = GateUpBoth<kCols>;
+  if (warp == 0) {
+    if (lane == 0) solo_producer<TA, TB, R>(&tm_x, &tm_w, sc, ps, &g_err_gated_linear);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0)
+      solo_mma<TA, TB, R>(sc, ps, tmem, idesc_bf16_f32(kHalfRows, 2 * kCols, false, false),
+                          &g_err_gated_linear);
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int k = 0;; ++k) {
+      const int u = solo_unit(sc, k);
+      if (u < 0) break;
+      if (!epilogue_acquire(ps, acc, acc_phase, &g_err_gated_linear)) break;
+      int r0, b0;
+      sc.tile_coords(u, 0, r0, b0);
+      if (32 * q < o.M)
+        gated_tile<kCols>(o, tmem + acc * kAccCols + lane_off, q * 32 + lane, b0 / 2);
+      solo_release(ps, acc);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  solo_teardown(tmem);
+}
+
+// ---------------------------------------------------------------- backward: G
+struct GradOut {
+  int M, F;
+  int act;
+  const void* dH;
+  int64_t lddh;
+  int dh_fp32, dh_width;
+  uint16_t* G;           // [M, ldG] BF16: dL/dg in columns [0, F), dL/du in [F, 2 F)
+  int64_t ldG;
+  int up_width;          // vectors that column F + 32 c of a row allows
+};
+
+template <int kAct>
+__device__ __forceinline__ void slope_run(float (&d)[32], const uint32_t (&g)[32],
+                                          const uint32_t (&u)[32], float (&dg)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float value, slope;
+    gate_slope<kAct>(__uint_as_float(g[i]), value, slope);
+    dg[i] = d[i] * __uint_as_float(u[i]) * slope;
+    d[i] *= value;
+  }
+}
+
+// G from projections formed again: the forward's loop, with another epilogue.
+template <int kK>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gated_grad_kernel(const __grid_constant__ CUtensorMap tm_x,
+                      const __grid_constant__ CUtensorMap tm_w, GatedSched sc, GradOut o) {
+  extern __shared__ uint8_t smem_raw[];
+  const PipeSmem ps = pipe_smem(smem_raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_w);
+  }
+  const uint32_t tmem = pipe_setup(ps);
+  using TA = OperandTile<false, kHalfRows, kK>;
+  using TB = GateUpHalf<kK>;
+  using R = PairRingT<kHalfRows, kK>;
+  if (warp == 0) {
+    if (lane == 0)
+      producer_role<TA, TB, GatedSched, R>(&tm_x, &tm_w, sc, ps, &g_err_gated_linear);
+    if (lane == 1 && ps.rank == 0) scheduler_role(sc, ps, &g_err_gated_linear);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && ps.rank == 0)
+      mma_role<TA, TB, GatedSched, R>(sc, ps, tmem, idesc_bf16_f32(kPairRows, kBN, false, false),
+                                      &g_err_gated_linear);
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int k = 0;; ++k) {
+      const int unit = warp_unit_take(sc, ps, k, &g_err_gated_linear);
+      if (unit < 0) break;
+      if (!epilogue_acquire(ps, acc, acc_phase, &g_err_gated_linear)) break;
+      int r0, b0;
+      sc.tile_coords(unit, 0, r0, b0);
+      const int row = r0 + (int)ps.rank * kHalfRows + q * 32 + lane;
+      const int f0 = b0 / 2;
+      const uint32_t taddr = tmem + acc * kAccCols + lane_off;
+#pragma unroll 1
+      for (int c = 0; c < kGateCols / 32; ++c) {
+        const int f = f0 + 32 * c;
+        if (f >= o.F) break;
+        const int n = min(32, o.F - f);
+        float d[32];
+        if (row < o.M)
+          load_run(o.dH, (int64_t)row * o.lddh + f, o.dh_fp32, n, o.dh_width, d);
+        uint32_t g[32], u[32];
+        __syncwarp();
+        tmem_ld32(taddr + 32 * c, g);
+        tmem_ld32(taddr + kGateCols + 32 * c, u);
+        tmem_wait_ld();
+        if (row >= o.M) continue;
+        float dg[32];
+        if (o.act == RLK_ACT_SILU)
+          slope_run<RLK_ACT_SILU>(d, g, u, dg);
+        else
+          slope_run<RLK_ACT_GELU_TANH>(d, g, u, dg);
+        if (!RLK_STORE_OK(row < o.M && o.F + f + n <= o.ldG, &g_err_gated_linear)) continue;
+        uint16_t* to = o.G + (int64_t)row * o.ldG + f;
+        store_run_bf16(to, dg, n, 16);
+        store_run_bf16(to + o.F, d, n, o.up_width);
+      }
+      epilogue_release(ps, acc);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  pipe_teardown(tmem);
+}
+
+// G from kept projections, eight columns a thread: one pass at memory speed.
+template <bool kInt8, bool kDFp32, int kAct>
+__global__ void __launch_bounds__(kRowThreads)
+    gated_grad_kept_kernel(const void* __restrict__ kept, const uint8_t* __restrict__ exponents,
+                           int Fp, GradOut o, int vec_d, RowLanes lanes) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int64_t row = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
+  if (row >= o.M) return;
+  const bool vec_up = o.up_width == 16;
+  for (int f = lanes.col(); f < o.F; f += lanes.step()) {
+    float d[8], g[8], u[8];
+    load8<kDFp32>(o.dH, row * o.lddh, f, o.F, vec_d, d);
+    const int64_t at = row * 2 * Fp + f;
+    if constexpr (kInt8) {
+      const int8_t* q = static_cast<const int8_t*>(kept) + at;
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(q));
+      const uint2 b = __ldg(reinterpret_cast<const uint2*>(q + Fp));
+      const float sa = int8_step(__ldg(exponents + at / kInt8Block));
+      const float sb = int8_step(__ldg(exponents + (at + Fp) / kInt8Block));
+      int8_floats(a.x, sa, g);
+      int8_floats(a.y, sa, g + 4);
+      int8_floats(b.x, sb, u);
+      int8_floats(b.y, sb, u + 4);
+    } else {
+      load8<true>(kept, at, 0, 8, true, g);
+      load8<true>(kept, at + Fp, 0, 8, true, u);
+    }
+    float dg[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float value, slope;
+      gate_slope<kAct>(g[i], value, slope);
+      dg[i] = d[i] * u[i] * slope;
+      d[i] *= value;
+    }
+    if (!RLK_STORE_OK(row < o.M && o.F + min(f + 8, o.F) <= o.ldG, &g_err_gated_linear)) continue;
+    store8<false>(o.G, row * o.ldG, f, o.F, true, dg);
+    store8<false>(o.G, row * o.ldG + o.F, f, o.F, vec_up, d);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int64_t kMaxInner = (int64_t(1) << 30) - 256;
+constexpr int64_t kMaxReduction = int64_t(1) << 20;
+constexpr int64_t kUnitLimit = int64_t(1) << 31;
+
+std::mutex g_attr_mutex;
+bool g_attr_set[64];
+
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+cudaError_t ensure_attrs(int dev) {
+  std::lock_guard<std::mutex> lock(g_attr_mutex);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (g_attr_set[dev]) return cudaSuccess;
+  constexpr int kDeep = PairRingT<kHalfRows, 64>::kSmemBytes;
+  constexpr int kWide = PairRingT<kHalfRows, 128>::kSmemBytes;
+  cudaError_t e;
+  if ((e = allow_smem(gated_linear_kernel<64>, kDeep)) != cudaSuccess ||
+      (e = allow_smem(gated_linear_kernel<128>, kWide)) != cudaSuccess ||
+      (e = allow_smem(gated_grad_kernel<64>, kDeep)) != cudaSuccess ||
+      (e = allow_smem(gated_grad_kernel<128>, kWide)) != cudaSuccess ||
+      (e = allow_smem(gated_linear_solo_kernel<32, 128>, SoloRing<32, 256>::kSmemBytes)) !=
+          cudaSuccess ||
+      (e = allow_smem(gated_linear_solo_kernel<128, 128>, SoloRing<128, 256>::kSmemBytes)) !=
+          cudaSuccess)
+    return e;
+  g_attr_set[dev] = true;
+  return cudaSuccess;
+}
+
+rlk_status cuda_failed() {
+  cudaGetLastError();
+  return RLK_ERR_CUDA;
+}
+
+// [G (backward)][unit counter, 256 bytes][padded copy of X][padded copy of W], each region
+// 256-byte aligned; copies only of operands that TMA cannot read in place.
+struct GatedPlan {
+  int64_t ldG = 0;
+  bool stage_x = false, stage_w = false;
+  int64_t ldx = 0, ldw = 0;
+  size_t off_ctr = 0, off_x = 0, off_w = 0, total = 0;
+};
+
+rlk_status gated_plan(bool backward, const void* X, int64_t M, int64_t K, int64_t ldx,
+                      const void* W, int64_t F, int64_t ldw, GatedPlan* p) {
+  if (M < 0 || M >= kMaxExtent || K < 1 || K >= kMaxReduction || F < 1 || F >= kMaxInner ||
+      ldx < K || ldw < K || ldx >= kPitchLimit || ldw >= kPitchLimit)
+    return RLK_ERR_SHAPE;
+  // work units are numbered in ints, here and in the backward's products (128-column tiles)
+  const int64_t rb = ceil_div(M, kPairRows), kb = ceil_div(K, kBN / 2);
+  if (rb * ceil_div(F, kGateCols) >= kUnitLimit || rb * kb >= kUnitLimit ||
+      ceil_div(2 * F, kPairRows) * kb >= kUnitLimit)
+    return RLK_ERR_SHAPE;
+  p->ldG = ceil_div(2 * F, 8) * 8;
+  p->stage_x = M > 0 && !tma_ready(X, ldx);
+  p->stage_w = M > 0 && !tma_ready(W, ldw);
+  p->ldx = p->stage_x ? staged_ld(K) : ldx;
+  p->ldw = p->stage_w ? staged_ld(K) : ldw;
+  size_t off = backward ? align_up((size_t)M * p->ldG * 2, 256) : 0;
+  p->off_ctr = off;
+  off += 256;
+  p->off_x = off;
+  if (p->stage_x) off = align_up(off + (size_t)M * p->ldx * 2, 256);
+  p->off_w = off;
+  if (p->stage_w) off = align_up(off + (size_t)(2 * F) * p->ldw * 2, 256);
+  p->total = off;
+  return RLK_OK;
+}
+
+// The operands as the kernels read them: in place, or the workspace's copies (made by stage()).
+struct Operands {
+  const void *x, *w;
+};
+Operands operands_of(const GatedPlan& p, const void* X, const void* W, uint8_t* ws) {
+  return {p.stage_x ? ws + p.off_x : X, p.stage_w ? ws + p.off_w : W};
+}
+cudaError_t stage(const GatedPlan& p, bool x_used, bool w_used, const void* X, int64_t M, int64_t K,
+                  int64_t ldx, const void* W, int64_t F, int64_t ldw, uint8_t* ws, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (x_used && p.stage_x)
+    e = launch_stage_bf16(static_cast<const uint16_t*>(X), M, K, ldx,
+                          reinterpret_cast<uint16_t*>(ws + p.off_x), p.ldx, s);
+  if (e == cudaSuccess && w_used && p.stage_w)
+    e = launch_stage_bf16(static_cast<const uint16_t*>(W), 2 * F, K, ldw,
+                          reinterpret_cast<uint16_t*>(ws + p.off_w), p.ldw, s);
+  return e;
+}
+
+bool encode_x(CUtensorMap* map, const GatedPlan& p, const void* x, int64_t M, int64_t K, int rows) {
+  return encode_bf16_2d(map, x, K, M, p.ldx, kBK, rows);
+}
+bool encode_w(CUtensorMap* map, const GatedPlan& p, const void* w, int64_t K, int64_t F, int rows,
+              int planes) {
+  return encode_bf16_3d(map, w, K, F, 2, p.ldw, (uint64_t)F * p.ldw, kBK, rows, planes);
+}
+
+// The 2-SM loop's schedule; zeroes the unit counter where one is used.
+cudaError_t pair_sched(int64_t M, int64_t K, int64_t F, int stage_k, int64_t clusters, int* counter,
+                       cudaStream_t s, GatedSched* sc, int* grid) {
+  sc->order.rows = (int)ceil_div(M, kPairRows);
+  sc->order.cols = (int)ceil_div(F, kGateCols);
+  sc->order.band = band_rows(sc->order.rows, K, kPairRows);
+  sc->nkb = (int)ceil_div(K, stage_k);
+  sc->nkb64 = (int)ceil_div(K, kBK);
+  sc->tile_rows = kBN;
+  sc->counter = nullptr;
+  const int64_t units = (int64_t)sc->order.rows * sc->order.cols;
+  *grid = 2 * (int)(units < clusters ? units : clusters);
+  if (!ordered_units(units, clusters)) return cudaSuccess;
+  sc->counter = counter;
+  return cudaMemsetAsync(counter, 0, sizeof(int), s);
+}
+
+bool known_activation(int a) { return a == RLK_ACT_SILU || a == RLK_ACT_GELU_TANH; }
+
+rlk_status check_kept(int keep, const void* kept, const uint8_t* exponents) {
+  if (keep == RLK_KEEP_NONE) return RLK_OK;
+  if (!kept || (keep == RLK_KEEP_INT8 && !exponents)) return RLK_ERR_NULL;
+  return is_aligned(kept, 32) ? RLK_OK : RLK_ERR_ALIGN;
+}
+
+}  // namespace
+
+uint32_t take_error_gated_linear() {
+  unsigned int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_gated_linear, sizeof v) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaMemcpyToSymbol(g_err_gated_linear, &zero, sizeof zero);
+  cudaGetLastError();
+  return v;
+}
+
+}  // namespace rlk
+
+using namespace rlk;
+
+extern "C" {
+
+size_t rlk_gated_linear_workspace_size(const void* X, int64_t M, int64_t K, int64_t ldx,
+                                       const void* W, int64_t F, int64_t ldw) {
+  GatedPlan p;
+  return gated_plan(false, X, M, K, ldx, W, F, ldw, &p) == RLK_OK ? p.total : 0;
+}
+
+rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, const void* W,
+                            int64_t F, int64_t ldw, int activation, void* H, int h_dtype,
+                            int64_t ldh, int keep, void* kept, uint8_t* kept_exponents,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  RLK_CALL_RANGE();
+  GatedPlan p;
+  rlk_status st = gated_plan(false, X, M, K, ldx, W, F, ldw, &p);
+  if (st != RLK_OK) return st;
+  if (ldh < F || ldh >= kPitchLimit) return RLK_ERR_SHAPE;
+  if (!known_dtype(h_dtype)) return RLK_ERR_DTYPE;
+  if (!known_activation(activation) || keep < RLK_KEEP_NONE || keep > RLK_KEEP_INT8)
+    return RLK_ERR_VALUE;
+  if (M == 0) return RLK_OK;
+  if (!X || !W || !H) return RLK_ERR_NULL;
+  if (!is_aligned(X, 2) || !is_aligned(W, 2) || !is_aligned(H, dtype_bytes(h_dtype)))
+    return RLK_ERR_ALIGN;
+  if ((st = check_kept(keep, kept, kept_exponents)) != RLK_OK) return st;
+  if (!workspace || !is_aligned(workspace, 256) || workspace_bytes < p.total)
+    return RLK_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if ((st = device_ready(&dev)) != RLK_OK) return st;
+  if (ensure_attrs(dev.device) != cudaSuccess) return cuda_failed();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Operands in = operands_of(p, X, W, ws);
+  const bool solo = M <= kHalfRows;
+  const int x_rows = M <= 32 ? 32 : kHalfRows;
+  CUtensorMap tm_x, tm_w;
+  if (!encode_x(&tm_x, p, in.x, M, K, x_rows) ||
+      !encode_w(&tm_w, p, in.w, K, F, kGateCols, solo ? 2 : 1))
+    return RLK_ERR_CUDA;
+  if (stage(p, true, true, X, M, K, ldx, W, F, ldw, ws, s) != cudaSuccess) return cuda_failed();
+  GatedOut o;
+  o.M = (int)M;
+  o.F = (int)F;
+  o.act = activation;
+  o.H = H;
+  o.ldh = ldh;
+  o.h_fp32 = h_dtype == RLK_FP32;
+  o.h_width = run_width(H, ldh, dtype_bytes(h_dtype));
+  o.keep = keep;
+  o.kept = kept;
+  o.exponents = kept_exponents;
+  o.Fp = (int)(ceil_div(F, kInt8Block) * kInt8Block);
+  GatedSched sc;
+  cudaError_t e;
+  if (solo) {
+    sc.order.rows = 1;
+    sc.order.cols = (int)ceil_div(F, kGateCols);
+    sc.order.band = 1;
+    sc.counter = nullptr;
+    sc.nkb = sc.nkb64 = (int)ceil_div(K, kBK);
+    sc.tile_rows = kBN;
+    const int grid = sc.order.cols < dev.sm_count ? sc.order.cols : dev.sm_count;
+    e = x_rows == 32 ? launch_overlapped(gated_linear_solo_kernel<32, 128>, grid, kThreads,
+                                         SoloRing<32, 256>::kSmemBytes, s, tm_x, tm_w, sc, o)
+                     : launch_overlapped(gated_linear_solo_kernel<128, 128>, grid, kThreads,
+                                         SoloRing<128, 256>::kSmemBytes, s, tm_x, tm_w, sc, o);
+  } else {
+    const int stage_k = M > kWideStageRows ? 128 : 64;
+    int grid;
+    e = pair_sched(M, K, F, stage_k, dev.sm_count / 2, reinterpret_cast<int*>(ws + p.off_ctr), s,
+                   &sc, &grid);
+    if (e == cudaSuccess)
+      e = stage_k == 128 ? launch_overlapped(gated_linear_kernel<128>, grid, kThreads,
+                                             PairRingT<kHalfRows, 128>::kSmemBytes, s, tm_x, tm_w,
+                                             sc, o)
+                         : launch_overlapped(gated_linear_kernel<64>, grid, kThreads,
+                                             PairRingT<kHalfRows, 64>::kSmemBytes, s, tm_x, tm_w,
+                                             sc, o);
+  }
+  return e == cudaSuccess ? RLK_OK : cuda_failed();
+}
+
+size_t rlk_gated_linear_backward_workspace_size(const void* X, int64_t M, int64_t K, int64_t ldx,
+                                                const void* W, int64_t F, int64_t ldw) {
+  GatedPlan p;
+  return gated_plan(true, X, M, K, ldx, W, F, ldw, &p) == RLK_OK ? p.total : 0;
+}
+
+rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, int64_t F,
+                                     int64_t lddh, const void* X, int64_t K, int64_t ldx,
+                                     const void* W, int64_t ldw, int activation, int keep,
+                                     const void* kept, const uint8_t* kept_exponents, void* dX,
+                                     int dx_dtype, int64_t lddx, void* dW, int dw_dtype,
+                                     int64_t lddw, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  RLK_CALL_RANGE();
+  // ---- every check, including those of the products below, before the first launch
+  GatedPlan p;
+  rlk_status st = gated_plan(true, X, M, K, ldx, W, F, ldw, &p);
+  if (st != RLK_OK) return st;
+  if (lddh < F || lddh >= kPitchLimit || (dX && (lddx < K || lddx >= kPitchLimit)) ||
+      (dW && (lddw < K || lddw >= kPitchLimit)))
+    return RLK_ERR_SHAPE;
+  if (!known_dtype(dh_dtype) || (dX && !known_dtype(dx_dtype)) || (dW && !known_dtype(dw_dtype)))
+    return RLK_ERR_DTYPE;
+  if (!known_activation(activation) || keep < RLK_KEEP_NONE || keep > RLK_KEEP_INT8)
+    return RLK_ERR_VALUE;
+  if (!dX && !dW) return RLK_OK;
+  if ((dX && !is_aligned(dX, dtype_bytes(dx_dtype))) ||
+      (dW && !is_aligned(dW, dtype_bytes(dw_dtype))))
+    return RLK_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  if (M == 0) {
+    if (!dW) return RLK_OK;
+    if ((st = device_ready(&dev)) != RLK_OK) return st;
+    const size_t es = dtype_bytes(dw_dtype);
+    return cudaMemset2DAsync(dW, lddw * es, 0, K * es, 2 * F, s) == cudaSuccess ? RLK_OK
+                                                                                : cuda_failed();
+  }
+  const bool x_used = dW || keep == RLK_KEEP_NONE, w_used = dX || keep == RLK_KEEP_NONE;
+  if (!dH || (x_used && !X) || (w_used && !W)) return RLK_ERR_NULL;
+  if (!is_aligned(dH, dtype_bytes(dh_dtype)) || !is_aligned(X, 2) || !is_aligned(W, 2))
+    return RLK_ERR_ALIGN;
+  if ((st = check_kept(keep, kept, kept_exponents)) != RLK_OK) return st;
+  if (!workspace || !is_aligned(workspace, 256) || workspace_bytes < p.total)
+    return RLK_ERR_WORKSPACE;
+  if ((st = device_ready(&dev)) != RLK_OK) return st;
+  if (ensure_attrs(dev.device) != cudaSuccess) return cuda_failed();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const Operands in = operands_of(p, X, W, ws);
+  CUtensorMap tm_x, tm_w;
+  if (keep == RLK_KEEP_NONE && (!encode_x(&tm_x, p, in.x, M, K, kHalfRows) ||
+                                !encode_w(&tm_w, p, in.w, K, F, kGateCols, 1)))
+    return RLK_ERR_CUDA;
+  if (stage(p, x_used, w_used, X, M, K, ldx, W, F, ldw, ws, s) != cudaSuccess) return cuda_failed();
+
+  GradOut o;
+  o.M = (int)M;
+  o.F = (int)F;
+  o.act = activation;
+  o.dH = dH;
+  o.lddh = lddh;
+  o.dh_fp32 = dh_dtype == RLK_FP32;
+  o.dh_width = run_width(dH, lddh, dtype_bytes(dh_dtype));
+  o.G = reinterpret_cast<uint16_t*>(ws);
+  o.ldG = p.ldG;
+  o.up_width = run_width(o.G + F, p.ldG, 2);
+  int* counter = reinterpret_cast<int*>(ws + p.off_ctr);
+  cudaError_t e;
+  if (keep == RLK_KEEP_NONE) {
+    const int stage_k = M > kWideStageRows ? 128 : 64;
+    GatedSched sc;
+    int grid;
+    e = pair_sched(M, K, F, stage_k, dev.sm_count / 2, counter, s, &sc, &grid);
+    if (e == cudaSuccess)
+      e = stage_k == 128 ? launch_overlapped(gated_grad_kernel<128>, grid, kThreads,
+                                             PairRingT<kHalfRows, 128>::kSmemBytes, s, tm_x, tm_w,
+                                             sc, o)
+                         : launch_overlapped(gated_grad_kernel<64>, grid, kThreads,
+                                             PairRingT<kHalfRows, 64>::kSmemBytes, s, tm_x, tm_w,
+                                             sc, o);
+  } else {
+    const int Fp = (int)(ceil_div(F, kInt8Block) * kInt8Block);
+    const RowLanes lanes = row_lanes(F);
+    const dim3 grid((unsigned)ceil_div(M, lanes.rows()));
+    const int vec_d = o.dh_width == 16;
+    e = by_dtypes(keep == RLK_KEEP_INT8 ? RLK_FP32 : RLK_BF16, dh_dtype, [&](auto q8, auto d32) {
+      constexpr bool kQ = decltype(q8)::value, kD = decltype(d32)::value;
+      return activation == RLK_ACT_SILU
+                 ? launch_overlapped(gated_grad_kept_kernel<kQ, kD, RLK_ACT_SILU>, grid,
+                                     kRowThreads, 0, s, kept, kept_exponents, Fp, o, vec_d, lanes)
+                 : launch_overlapped(gated_grad_kept_kernel<kQ, kD, RLK_ACT_GELU_TANH>, grid,
+                                     kRowThreads, 0, s, kept, kept_exponents, Fp, o, vec_d, lanes);
+    });
+  }
+  if (e != cudaSuccess) return cuda_failed();
+  // The products read G and the (possibly copied) operands, all TMA-ready: the counter is all the
+  // workspace they need, and every argument that they check was checked above.
+  return rlk_det_linear_backward(o.G, RLK_BF16, M, 2 * F, p.ldG, in.x, K, p.ldx, in.w, p.ldw, dX,
+                                 dx_dtype, dX ? lddx : K, dW, dw_dtype, dW ? lddw : K,
+                                 ws + p.off_ctr, 256, stream);
+}
+
+}  // extern "C"

@@ -37,6 +37,11 @@ rlk_status device_ready(DeviceInfo* info);
 bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t ld, uint32_t box_inner, uint32_t box_outer);
 
+// 3-D form: `planes` such matrices, plane_stride elements apart (a multiple of 8).
+bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                    uint64_t planes, uint64_t ld, uint64_t plane_stride, uint32_t box_inner,
+                    uint32_t box_outer, uint32_t box_planes);
+
 // Launches `kernel` with programmatic stream serialisation: it may begin while
 // the previous kernel in the stream is finishing, and must call griddep_wait()
 // (rlk_device.cuh) before it touches global memory that kernel may use.
@@ -149,5 +154,8 @@ uint32_t take_error_common();
 uint32_t take_error_linear_logp_bwd();
 uint32_t take_error_linear_distill();
 uint32_t take_error_sample();
+uint32_t take_error_embedding();
+uint32_t take_error_int8();
+uint32_t take_error_gated_linear();
 
 }  // namespace rlk

@@ -21,17 +21,18 @@
 namespace rlk {
 
 // Stage ring: kARows rows of the left operand (32 when every row of the call
-// lies in the first 32, else 128) and the 256-row right-operand tile, 64
-// reduction columns each; left-operand blocks of all stages first, then the
+// lies in the first 32, else 128) and the right-operand tile (256 rows, or fewer
+// for outputs of few columns), 64 reduction columns each; left-operand blocks of all stages first, then the
 // right-operand blocks.  The MMA always reads 128 left rows: with the thin ring
 // the rows past the 32 staged ones hold other data (the next stages' blocks),
 // which reaches only accumulator rows that nothing reads (row i of a product
 // depends on row i of the left operand alone).
-template <int kARows_>
+template <int kARows_, int kBRows_ = kBN>
 struct SoloRing {
   static constexpr int kARows = kARows_;
+  static constexpr int kBRows = kBRows_;
   static constexpr int kABytes = kARows * kBK * 2;                 // 4 or 16 KiB
-  static constexpr int kBBytes = kBN * kBK * 2;                    // 32 KiB
+  static constexpr int kBBytes = kBRows * kBK * 2;                 // 32 KiB for 256 rows
   static constexpr int kStages =
       (kSmemLimit - 1024 - kBarrierBlockBytes) / (kABytes + kBBytes) < kMaxStages
           ? (kSmemLimit - 1024 - kBarrierBlockBytes) / (kABytes + kBBytes)

@@ -23,8 +23,8 @@
  *  - Errors.  Arguments are validated on the host before anything is launched;
  *    on any error nothing is launched and no output is touched.  A launch that
  *    the CUDA runtime rejects returns RLK_ERR_CUDA.  A zero-row call (N == 0 in
- *    rlk_linear_logp, rlk_linear_distill and rlk_sample_logits, M == 0 in
- *    rlk_det_gemm_fwd / _da) is a no-op that returns RLK_OK.
+ *    rlk_linear_logp, rlk_linear_distill, rlk_sample_logits and rlk_embedding, M == 0 in
+ *    rlk_det_gemm_fwd / _da and rlk_gated_linear) is a no-op that returns RLK_OK.
  *  - Determinism.  For fixed inputs every output bit is identical run to run,
  *    across streams, across leading dimensions and pointer alignment, and -- for
  *    every product whose reduction does not run over the rows (all but dB and
@@ -85,7 +85,7 @@ typedef enum rlk_status {
     RLK_ERR_TIMEOUT = 8,            /* a kernel's bounded wait expired (device error)   */
     RLK_ERR_BOUNDS = 9,             /* debug build: a kernel skipped an out-of-bounds store */
     RLK_ERR_NOT_DEBUG_BUILD = 10,   /* the call exists only in the debug build          */
-    RLK_ERR_VALUE = 11              /* a scalar setting (a temperature) is out of range */
+    RLK_ERR_VALUE = 11              /* a scalar setting (a temperature, an activation) is out of range */
 } rlk_status;
 
 typedef enum rlk_dtype {
@@ -601,6 +601,144 @@ RLK_API rlk_status rlk_linear_distill_backward(
     int64_t ld_kept, const float* grad_loss, void* grad_hidden, int grad_hidden_dtype, int64_t ld_grad_hidden, void* grad_weight,
     int grad_weight_dtype, int64_t ld_grad_weight, float* grad_bias, void* workspace,
     size_t workspace_bytes, void* stream);
+
+/* ===================================================================== *
+ *  Embedding                                                             *
+ * ===================================================================== */
+
+/*
+ * out[r, :] = scale * weight[ids[r], :], rounded once.
+ *  ids           int64, row r reads ids[r * ids_stride] (0: one id shared by every row);
+ *                an id outside [0, V) gives a row of zeros (nothing is read for it)
+ *  weight        [V, H] in weight_dtype (RLK_BF16 / RLK_FP32), row pitch ld_weight (>= H)
+ *  scale         finite (RLK_ERR_VALUE otherwise); scale * weight is formed in FP32
+ *  out           [N, H] in out_dtype, row pitch ld_out (>= H)
+ * 0 <= N < 2^31 - 256, 1 <= V < 2^31 - 256, 1 <= H < 2^20; any alignment of the element
+ * size.  N == 0 is a no-op.
+ */
+RLK_API rlk_status rlk_embedding(const int64_t* ids, int64_t ids_stride, int64_t N,
+                                 const void* weight, int weight_dtype, int64_t V, int64_t H,
+                                 int64_t ld_weight, float scale, void* out, int out_dtype,
+                                 int64_t ld_out, void* stream);
+
+/*
+ * The table's gradient for an upstream gradient d = dL/dout [N, H]:
+ *   grad_weight[v, :] = scale * sum over the rows r with ids[r] == v of d[r, :]
+ * Ids outside [0, V) take no part.  The rows of an id are added in FP32 in ascending
+ * order of r, RLK_EMBED_GROUP at a time, and those sums in ascending order; scale is
+ * applied to the whole sum and the result rounded once.  A table row's bits depend on its
+ * own rows of d alone, however the other ids lie.
+ *  grad          [N, H] in grad_dtype (RLK_BF16 / RLK_FP32), row pitch ld_grad (>= H)
+ *  grad_weight   [V, H] in grad_weight_dtype, row pitch ld_grad_weight (>= H).  Every row
+ *                is written (zeros where no row of d belongs to it); with accumulate != 0
+ *                (RLK_FP32 only) the sums are added to what is there and rows without any
+ *                are left alone.  Must not overlap grad.
+ *  workspace     >= rlk_embedding_backward_workspace_size(N, V, H) bytes, 256-byte aligned
+ * 0 <= N < 2^31 - 256, 1 <= V < 2^30, 1 <= H < 2^20.  N == 0 writes zeros (accumulate: a
+ * no-op).
+ */
+#define RLK_EMBED_GROUP 64
+RLK_API size_t rlk_embedding_backward_workspace_size(int64_t N, int64_t V, int64_t H);
+RLK_API rlk_status rlk_embedding_backward(const int64_t* ids, int64_t ids_stride, int64_t N,
+                                          const void* grad, int grad_dtype, int64_t H,
+                                          int64_t ld_grad, float scale, void* grad_weight,
+                                          int grad_weight_dtype, int64_t V,
+                                          int64_t ld_grad_weight, int accumulate,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ===================================================================== *
+ *  Activations in 8 bits                                                 *
+ * ===================================================================== */
+
+/*
+ * Blocks of RLK_INT8_BLOCK = 32 consecutive columns of a row (the first at column 0, the
+ * last of a row may be shorter) share a power of two 2^(e - 127),
+ *   e = max(1, floor(log2 max|x|) + 121),   q = x / 2^(e - 127) rounded to nearest even,
+ * held to -127 .. 127.  A value q 2^(e - 127) has at most 7 significant bits, so it is
+ * exact in BF16: a tensor-core operand made of it is the stored value.  It is within half a
+ * step of x, at most 2^-7 max|x| (2^-127 where that is less); an FP32 x beyond 127.5 steps,
+ * held to 127, within a step, at most 2^-7 max|x| too.  A block with a NaN or an infinity
+ * has e = 255 and q = 0 and reads back as NaN.
+ *  x             [rows, cols] in x_dtype (RLK_BF16 / RLK_FP32), row pitch ldx (>= cols)
+ *  q             int8 [rows, 32 ceil(cols / 32)], row pitch ldq (a multiple of 16), 16-byte
+ *                aligned; columns past cols are written with 0
+ *  exponents     uint8 [rows, ceil(cols / 32)], row pitch ld_exponents
+ *  out           [rows, cols] in out_dtype, row pitch ld_out (>= cols)
+ * 0 <= rows < 2^31 - 256, 1 <= cols < 2^30.  rows == 0 is a no-op.
+ */
+#define RLK_INT8_BLOCK 32
+RLK_API rlk_status rlk_pack_int8(const void* x, int x_dtype, int64_t rows, int64_t cols,
+                                 int64_t ldx, int8_t* q, int64_t ldq, uint8_t* exponents,
+                                 int64_t ld_exponents, void* stream);
+RLK_API rlk_status rlk_unpack_int8(const int8_t* q, int64_t rows, int64_t cols, int64_t ldq,
+                                   const uint8_t* exponents, int64_t ld_exponents, void* out,
+                                   int out_dtype, int64_t ld_out, void* stream);
+
+/* ===================================================================== *
+ *  Gated linear block                                                    *
+ * ===================================================================== */
+
+/*
+ * The first half of a gated feed-forward block: two projections of the same rows, the
+ * gate's activation and the product, in one kernel:
+ *   g = X . Wg^T,  u = X . Wu^T,  H = act(g) u,   W = [Wg; Wu]
+ * with act(g) = g sigmoid(a(g)) and
+ *   RLK_ACT_SILU       a(g) = g
+ *   RLK_ACT_GELU_TANH  a(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3)
+ *                      (GELU in its tanh form, g (1 + tanh(a / 2)) / 2)
+ * g and u are the FP32 accumulators: the bits of rlk_det_linear_fwd with an FP32 output.
+ *  X             BF16 [M, K], row pitch ldx (>= K)
+ *  W             BF16 [2 F, K], row pitch ldw (>= K): rows 0 .. F - 1 are Wg, the others Wu
+ *  H             [M, F] in h_dtype (RLK_BF16 / RLK_FP32), row pitch ldh (>= F)
+ *  keep          what is kept of g and u for a backward that does not form them again:
+ *                RLK_KEEP_NONE, RLK_KEEP_FP32 (FP32 [M, 2, Fp]) or RLK_KEEP_INT8 (q int8
+ *                [M, 2, Fp] and exponents [M, 2, Fp / 32] as in rlk_pack_int8), with
+ *                Fp = 32 ceil(F / 32), g first, columns past F written with 0
+ *  kept          32-byte aligned; kept_exponents any alignment (RLK_KEEP_INT8 only)
+ *  workspace     >= rlk_gated_linear_workspace_size(...) bytes, 256-byte aligned: 256 bytes
+ *                and padded copies of misaligned operands
+ * Shapes: 0 <= M < 2^31 - 256, 1 <= K < 2^20, 1 <= F < 2^30 - 256.  A row's bits depend on
+ * its own row of X alone.  M == 0 is a no-op.
+ */
+#define RLK_ACT_SILU 0
+#define RLK_ACT_GELU_TANH 1
+#define RLK_KEEP_NONE 0
+#define RLK_KEEP_FP32 1
+#define RLK_KEEP_INT8 2
+RLK_API size_t rlk_gated_linear_workspace_size(const void* X, int64_t M, int64_t K, int64_t ldx,
+                                               const void* W, int64_t F, int64_t ldw);
+RLK_API rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx,
+                                    const void* W, int64_t F, int64_t ldw, int activation,
+                                    void* H, int h_dtype, int64_t ldh, int keep, void* kept,
+                                    uint8_t* kept_exponents, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of rlk_gated_linear for an upstream gradient d = dL/dH:
+ *   G = [d u act'(g), d act(g)]   [M, 2 F],    dX = G . W,    dW = G^T . X
+ * G is formed in FP32 from g and u and rounded to BF16 (nearest even), the type the two
+ * products read (they are rlk_det_linear_dx and rlk_det_linear_dw of G).  g and u are
+ * formed again on the tensor cores (RLK_KEEP_NONE) or read from what the forward kept;
+ * with RLK_KEEP_FP32 the bits are the same.  With RLK_KEEP_INT8 they are the stored
+ * values, and X is commonly the stored values of rlk_unpack_int8 too.
+ *  dH            [M, F] in dh_dtype (RLK_BF16 / RLK_FP32), row pitch lddh (>= F)
+ *  dX            [M, K] in dx_dtype, row pitch lddx (>= K), or NULL
+ *  dW            [2 F, K] in dw_dtype, row pitch lddw (>= K), or NULL
+ *  workspace     >= rlk_gated_linear_backward_workspace_size(...) bytes, 256-byte aligned;
+ *                begins with G, row pitch 8 ceil(2 F / 8)
+ * X may be NULL when dW is NULL and keep is not RLK_KEEP_NONE; W may be NULL when dX is
+ * NULL and keep is not RLK_KEEP_NONE.  M == 0 writes zeros to dW.
+ */
+RLK_API size_t rlk_gated_linear_backward_workspace_size(const void* X, int64_t M, int64_t K,
+                                                        int64_t ldx, const void* W, int64_t F,
+                                                        int64_t ldw);
+RLK_API rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, int64_t F,
+                                             int64_t lddh, const void* X, int64_t K, int64_t ldx,
+                                             const void* W, int64_t ldw, int activation, int keep,
+                                             const void* kept, const uint8_t* kept_exponents,
+                                             void* dX, int dx_dtype, int64_t lddx, void* dW,
+                                             int dw_dtype, int64_t lddw, void* workspace,
+                                             size_t workspace_bytes, void* stream);
 
 /* ===================================================================== *
  *  Deterministic GEMM family                                      [P1]  *
