@@ -22,6 +22,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 
 std::mutex g_mutex;
 EncodeTiledFn g_encode = nullptr;
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+CtxGetCurrentFn g_ctx_current = nullptr;
 constexpr int kMaxDevices = 64;
 int g_dev_state[kMaxDevices];      // 0 unknown, 1 ready, -1 unsupported
 int g_dev_sms[kMaxDevices];
@@ -37,6 +39,34 @@ EncodeTiledFn get_encode() {
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   }
   return g_encode;
+}
+
+// Makes the device's context current in a host thread that has none yet (its first CUDA call may
+// be one of ours: torch's autograd thread with tensors from the allocator's cache).  The
+// runtime does so by itself in its own calls, but cuTensorMapEncodeTiled is the driver's and
+// refuses without one.  A context that is current, whoever made it, stays.
+bool bind_context(int dev) {
+  CtxGetCurrentFn current;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!g_ctx_current) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 12000, cudaEnableDefault, &q) !=
+              cudaSuccess ||
+          q != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return false;
+      }
+      g_ctx_current = reinterpret_cast<CtxGetCurrentFn>(fn);
+    }
+    current = g_ctx_current;
+  }
+  CUcontext ctx = nullptr;
+  if (current(&ctx) == CUDA_SUCCESS && ctx != nullptr) return true;
+  if (cudaSetDevice(dev) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
 }
 
 }  // namespace
@@ -65,7 +95,7 @@ rlk_status device_ready(DeviceInfo* info) {
     info->device = dev;
     info->sm_count = g_dev_sms[dev];
   }
-  if (!get_encode()) return RLK_ERR_CUDA;
+  if (!get_encode() || !bind_context(dev)) return RLK_ERR_CUDA;
   return RLK_OK;
 }
 
