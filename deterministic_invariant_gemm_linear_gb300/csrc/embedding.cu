@@ -31,35 +31,39 @@ __device__ unsigned int g_err_embedding = 0;
 namespace {
 
 // ---------------------------------------------------------------- lookup
-template <bool kWFp32, bool kOutFp32>
+template <bool kWFp32, bool kOutFp32, int kRun>
 __global__ void __launch_bounds__(kRowThreads)
     embed_kernel(const int64_t* __restrict__ ids, int64_t ids_stride, int64_t N,
-                 const void* __restrict__ weight, int64_t V, int H, int64_t ldw, int vec_w,
-                 float scale, void* __restrict__ out, int64_t ldo, int vec_o, RowLanes lanes) {
+                 const void* __restrict__ weight, int64_t V, int H, int64_t ldw, float scale,
+                 void* __restrict__ out, int64_t ldo, RowLanes<kRun> lanes) {
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int64_t r = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
   if (r >= N) return;
   const int64_t id = __ldg(ids + r * ids_stride);
   const bool known = id >= 0 && id < V;
+  const int gap = lanes.gap();
   for (int c = lanes.col(); c < H; c += lanes.step()) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.f;
     if (known) {
-      load8<kWFp32>(weight, id * ldw, c, H, vec_w, v);
+      load8<kWFp32, kRun>(weight, id * ldw, c, gap, H, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], scale);
     }
-    if (RLK_STORE_OK(r < N && min(c + 8, H) <= ldo, &g_err_embedding))
-      store8<kOutFp32>(out, r * ldo, c, H, vec_o, v);
+    if (RLK_STORE_OK(r < N && min(c + run_at<kRun>(7, gap) + 1, H) <= ldo, &g_err_embedding))
+      store8<kOutFp32, kRun>(out, r * ldo, c, gap, H, v);
   }
 }
 
 // ---------------------------------------------------------------- gradient: the sort
 constexpr int kSortIds = 1024;        // ids a CTA owns, one a thread
 constexpr int kSortWarps = kSortIds / 32;
-constexpr int kSortSmem = kSortWarps * kSortIds * 4;    // a count for each warp and id
+constexpr int kSortCounts = kSortWarps * kSortIds * 4;  // bytes: a count for each warp and id
+constexpr int kSortKeys = 32768;      // rows whose id - lo (kNoKey: another CTA's) waits in shared memory
+constexpr uint16_t kNoKey = 0xffff;
+inline int sort_smem(int64_t N) { return kSortCounts + (N <= kSortKeys ? 2 * (int)align_up(N, 32) : 0); }
 constexpr int kGroup = RLK_EMBED_GROUP;
 
 struct Order {
@@ -98,16 +102,18 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
   return x - v + (warp ? warp_sums[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kSortIds)
+__global__ void __launch_bounds__(kSortIds, 1)
     embed_sort_kernel(const int64_t* __restrict__ ids, int64_t ids_stride, int N, int V,
                       Order o, int max_groups) {
-  extern __shared__ int count[];      // [kSortWarps][kSortIds]
+  extern __shared__ int count[];      // [kSortWarps][kSortIds], then the keys of at most kSortKeys rows
   __shared__ int warp_sums[32];
   __shared__ int2 heavy[kSortIds];    // {id - lo, first group}
   __shared__ int n_heavy;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int lo = blockIdx.x * kSortIds;
   const int hi = min(lo + kSortIds, V);
+  uint16_t* keys = reinterpret_cast<uint16_t*>(count + kSortWarps * kSortIds);
+  const bool kept = N <= kSortKeys;
 #pragma unroll 8
   for (int w = 0; w < kSortWarps; ++w) count[w * kSortIds + t] = 0;
   if (t == 0) n_heavy = 0;
@@ -120,11 +126,13 @@ __global__ void __launch_bounds__(kSortIds)
   const int n1 = (int)(n0 + per < N ? n0 + per : N);
   int below = 0;
   int* mine = count + warp * kSortIds;
-#pragma unroll 4
+#pragma unroll 8
   for (int64_t n = n0 + lane; n < n1; n += 32) {
     const int64_t id = __ldg(ids + n * ids_stride);
+    const bool own = id >= lo && id < hi;
     below += id >= 0 && id < lo;
-    if (id >= lo && id < hi) atomicAdd(mine + (int)(id - lo), 1);
+    if (kept) keys[n] = own ? (uint16_t)(id - lo) : kNoKey;
+    if (own) atomicAdd(mine + (int)(id - lo), 1);
   }
   int before, total, rows = 0;
   block_prefix(below, warp_sums, &before);      // rows with smaller ids; also a barrier
@@ -150,10 +158,17 @@ __global__ void __launch_bounds__(kSortIds)
   __syncthreads();
   // place the rows, in order within a warp
   for (int64_t n = n0 + lane; n - lane < n1; n += 32) {
-    const int64_t id = n < n1 ? __ldg(ids + n * ids_stride) : -1;
-    const bool own = id >= lo && id < hi;
+    int key = -1;
+    if (n < n1) {
+      if (kept) {
+        key = keys[n] == kNoKey ? -1 : keys[n];
+      } else {
+        const int64_t id = __ldg(ids + n * ids_stride);
+        key = id >= lo && id < hi ? (int)(id - lo) : -1;
+      }
+    }
+    const bool own = key >= 0;
     if (!__ballot_sync(0xffffffffu, own)) continue;
-    const int key = own ? (int)(id - lo) : -1;
     const unsigned same = __match_any_sync(0xffffffffu, key);
     const int rank = __popc(same & ((1u << lane) - 1u));
     if (own) {
@@ -181,92 +196,109 @@ __global__ void __launch_bounds__(kSortIds)
 }
 
 // ---------------------------------------------------------------- gradient: the sums
-// acc = the rows rows[at .. at + n - 1] of d at columns c .. c + 7, added in that order.
-template <bool kFp32>
-__device__ __forceinline__ void add_rows(const void* __restrict__ d, int64_t ldd, int vec,
-                                         const int* __restrict__ rows, int at, int n, int c, int H,
-                                         float (&acc)[8]) {
+// acc = the rows rows[at .. at + n - 1] of d at columns c + i * gap, added in that order, kDepth
+// rows' loads in flight.
+template <bool kFp32, int kRun, int kDepth>
+__device__ __forceinline__ void add_rows(const void* __restrict__ d, int64_t ldd,
+                                         const int* __restrict__ rows, int at, int n, int c,
+                                         int gap, int H, float (&acc)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   int k = 0;
-  for (; k + 4 <= n; k += 4) {
-    float v[4][8];
+  for (; k + kDepth <= n; k += kDepth) {
+    float v[kDepth][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      load8<kFp32>(d, (int64_t)__ldg(rows + at + k + j) * ldd, c, H, vec, v[j]);
+    for (int j = 0; j < kDepth; ++j)
+      load8<kFp32, kRun>(d, (int64_t)__ldg(rows + at + k + j) * ldd, c, gap, H, v[j]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kDepth; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[j][i]);
   }
+#pragma unroll 2
   for (; k < n; ++k) {
     float v[8];
-    load8<kFp32>(d, (int64_t)__ldg(rows + at + k) * ldd, c, H, vec, v);
+    load8<kFp32, kRun>(d, (int64_t)__ldg(rows + at + k) * ldd, c, gap, H, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[i]);
   }
 }
 
-template <bool kDFp32>
-__global__ void __launch_bounds__(kRowThreads)
-    embed_groups_kernel(const void* __restrict__ d, int64_t ldd, int vec_d, int H, Order o,
-                        int max_groups, RowLanes lanes) {
+template <bool kDFp32, int kRun>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    embed_groups_kernel(const void* __restrict__ d, int64_t ldd, int H, Order o, int max_groups,
+                        RowLanes<kRun> lanes) {
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int n = min(*o.group_count, max_groups);
+  const int gap = lanes.gap();
   for (int g = (int)blockIdx.x * lanes.rows() + lanes.row(); g < n;
        g += (int)gridDim.x * lanes.rows()) {
     const int2 what = o.groups[g];
     for (int c = (int)blockIdx.y * lanes.step() + lanes.col(); c < H;
          c += (int)gridDim.y * lanes.step()) {
       float acc[8];
-      add_rows<kDFp32>(d, ldd, vec_d, o.rows, what.x, what.y, c, H, acc);
-      if (RLK_STORE_OK(c + 8 <= o.ld_sums, &g_err_embedding))
-        store8<true>(o.sums, g * o.ld_sums, c, (int)o.ld_sums, true, acc);
+      add_rows<kDFp32, kRun, kRun == 1 ? 4 : kDFp32 ? 8 : 16>(d, ldd, o.rows, what.x, what.y, c, gap, H, acc);
+      if (RLK_STORE_OK(g < max_groups && min(c + run_at<kRun>(7, gap) + 1, H) <= o.ld_sums, &g_err_embedding))
+        store8<true, kRun>(o.sums, g * o.ld_sums, c, gap, H, acc);
     }
   }
 }
 
-template <bool kDFp32, bool kOutFp32, bool kAccumulate>
-__global__ void __launch_bounds__(kRowThreads)
-    embed_rows_kernel(const void* __restrict__ d, int64_t ldd, int vec_d, int H, int V, Order o,
-                      float scale, void* __restrict__ dw, int64_t ldw, int vec_w, RowLanes lanes) {
+// Threads of a row take `turns` (at most kRowsInTurn) consecutive table rows, most of them rows of zeros: how many
+// rows of d each has is read for all of them at once, and the zeros wait for nothing.
+constexpr int kRowsInTurn = 16;
+
+template <bool kDFp32, bool kOutFp32, bool kAccumulate, int kRun>
+__global__ void __launch_bounds__(kRowThreads, 4)
+    embed_rows_kernel(const void* __restrict__ d, int64_t ldd, int H, int V, Order o, float scale,
+                      void* __restrict__ dw, int64_t ldw, int turns, RowLanes<kRun> lanes) {
+  __shared__ int start[kRowThreads / 4 * kRowsInTurn + 1];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int64_t v = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
-  if (v >= V) return;
-  const int at = __ldg(o.start + v), n = __ldg(o.start + v + 1) - at;
-  if (kAccumulate && n == 0) return;
-  for (int c = lanes.col(); c < H; c += lanes.step()) {
-    float acc[8];
-    if (n <= kGroup) {
-      add_rows<kDFp32>(d, ldd, vec_d, o.rows, at, n, c, H, acc);
-    } else {
-      const int groups = (n + kGroup - 1) / kGroup;
-      const float* s = o.sums + (int64_t)__ldg(o.group_base + v) * o.ld_sums;
+  const int per_block = lanes.rows() * turns;
+  const int64_t first = (int64_t)blockIdx.x * per_block;
+  for (int i = threadIdx.x; i <= per_block; i += kRowThreads)
+    start[i] = __ldg(o.start + (first + i < V ? first + i : V));
+  __syncthreads();
+  const int gap = lanes.gap();
+#pragma unroll 1
+  for (int k = 0; k < turns; ++k) {
+    const int mine = lanes.row() * turns + k;
+    const int64_t v = first + mine;
+    if (v >= V) break;
+    const int at = start[mine], n = start[mine + 1] - at;
+    if (kAccumulate && n == 0) continue;
+    for (int c = lanes.col(); c < H; c += lanes.step()) {
+      float acc[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+      if (n > 0) {
+        if (n <= kGroup) {
+          add_rows<kDFp32, kRun, kRun == 1 ? 2 : 4>(d, ldd, o.rows, at, n, c, gap, H, acc);
+        } else {
+          const int groups = (n + kGroup - 1) / kGroup;
+          const float* s = o.sums + (int64_t)__ldg(o.group_base + v) * o.ld_sums;
 #pragma unroll 4
-      for (int g = 0; g < groups; ++g) {
-        float x[8];
-        load8<true>(s, g * o.ld_sums, c, (int)o.ld_sums, true, x);
+          for (int g = 0; g < groups; ++g) {
+            float x[8];
+            load8<true, kRun>(s, g * o.ld_sums, c, gap, H, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], x[i]);
+            for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], x[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __fmul_rn(acc[i], scale);
       }
-    }
+      if (kAccumulate) {
+        const float* p = static_cast<const float*>(dw) + v * ldw;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = __fmul_rn(acc[i], scale);
-    if (kAccumulate) {
-      float x[8];
-      const float* p = static_cast<const float*>(dw) + v * ldw;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = c + i < H ? p[c + i] : 0.f;
-        acc[i] = __fadd_rn(x[i], acc[i]);
+        for (int i = 0; i < 8; ++i)
+          if (c + run_at<kRun>(i, gap) < H) acc[i] = __fadd_rn(p[c + run_at<kRun>(i, gap)], acc[i]);
       }
+      if (RLK_STORE_OK(v < V && min(c + run_at<kRun>(7, gap) + 1, H) <= ldw, &g_err_embedding))
+        store8<kOutFp32, kRun>(dw, v * ldw, c, gap, H, acc);
     }
-    if (RLK_STORE_OK(v < V && min(c + 8, H) <= ldw, &g_err_embedding))
-      store8<kOutFp32>(dw, v * ldw, c, H, vec_w, acc);
   }
 }
 
@@ -301,6 +333,20 @@ bool embed_plan(int64_t N, int64_t V, int64_t H, EmbedPlan* p) {
   return true;
 }
 
+// The run length (see RowLanes) that both matrices of a pass allow: by the output's type, or 1.
+int embed_run(int64_t H, const void* in, int in_dtype, int64_t ld_in, const void* out,
+              int out_dtype, int64_t ld_out) {
+  const int n = out_dtype == RLK_FP32 ? 4 : 8;
+  return rows_vec(in, ld_in, dtype_bytes(in_dtype), H, n) &&
+                 rows_vec(out, ld_out, dtype_bytes(out_dtype), H, n)
+             ? n
+             : 1;
+}
+template <class Out32, class F>
+cudaError_t by_run(int run, Out32, F f) {
+  return run == 1 ? f(Const<1>()) : f(Const<Out32::value ? 4 : 8>());
+}
+
 std::mutex g_attr_mutex;
 bool g_attr_set[64];
 
@@ -309,7 +355,7 @@ cudaError_t ensure_attrs(int dev) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!g_attr_set[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+        embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem(kSortKeys));
     if (e != cudaSuccess) return e;
     g_attr_set[dev] = true;
   }
@@ -358,15 +404,17 @@ rlk_status rlk_embedding(const int64_t* ids, int64_t ids_stride, int64_t N, cons
   DeviceInfo dev;
   const rlk_status st = device_ready(&dev);
   if (st != RLK_OK) return st;
-  const RowLanes lanes = row_lanes(H);
-  const dim3 grid((unsigned)ceil_div(N, lanes.rows()));
-  const int vw = rows_vec(weight, ld_weight, dtype_bytes(weight_dtype));
-  const int vo = rows_vec(out, ld_out, dtype_bytes(out_dtype));
+  const int run = embed_run(H, weight, weight_dtype, ld_weight, out, out_dtype, ld_out);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = by_dtypes(weight_dtype, out_dtype, [&](auto w32, auto o32) {
-    return launch_overlapped(embed_kernel<decltype(w32)::value, decltype(o32)::value>, grid,
-                             kRowThreads, 0, s, ids, ids_stride, N, weight, V, (int)H, ld_weight,
-                             vw, scale, out, ld_out, vo, lanes);
+    return by_run(run, o32, [&](auto r) {
+      constexpr int kRun = decltype(r)::value;
+      const RowLanes<kRun> lanes = row_lanes<kRun>(H);
+      const dim3 grid((unsigned)ceil_div(N, lanes.rows()));
+      return launch_overlapped(embed_kernel<decltype(w32)::value, decltype(o32)::value, kRun>, grid,
+                               kRowThreads, 0, s, ids, ids_stride, N, weight, V, (int)H, ld_weight,
+                               scale, out, ld_out, lanes);
+    });
   });
   return e == cudaSuccess ? RLK_OK : cuda_failed();
 }
@@ -420,38 +468,40 @@ rlk_status rlk_embedding_backward(const int64_t* ids, int64_t ids_stride, int64_
   if (heavy && cudaMemsetAsync(o.group_count, 0, sizeof(int), s) != cudaSuccess)
     return cuda_failed();
   if (launch_overlapped(embed_sort_kernel, dim3((unsigned)ceil_div(V, kSortIds)), kSortIds,
-                        kSortSmem, s, ids, ids_stride, (int)N, (int)V, o,
+                        sort_smem(N), s, ids, ids_stride, (int)N, (int)V, o,
                         (int)p.groups) != cudaSuccess)
     return cuda_failed();
-  const RowLanes lanes = row_lanes(H);
-  const int vg = rows_vec(grad, ld_grad, dtype_bytes(grad_dtype));
-  const int vw = rows_vec(grad_weight, ld_grad_weight, esize);
-  const int64_t col_blocks = ceil_div(H, lanes.step());
-  if (heavy) {
-    // groups by columns: four blocks an SM, or all there can be
-    int64_t gx = ceil_div(4 * (int64_t)dev.sm_count, col_blocks);
-    const int64_t all = ceil_div(p.groups, lanes.rows());
-    gx = gx < all ? gx : all;
-    const dim3 grid((unsigned)(gx < 1 ? 1 : gx), (unsigned)col_blocks);
-    const cudaError_t e =
-        grad_dtype == RLK_FP32
-            ? launch_overlapped(embed_groups_kernel<true>, grid, kRowThreads, 0, s, grad, ld_grad,
-                                vg, (int)H, o, (int)p.groups, lanes)
-            : launch_overlapped(embed_groups_kernel<false>, grid, kRowThreads, 0, s, grad, ld_grad,
-                                vg, (int)H, o, (int)p.groups, lanes);
-    if (e != cudaSuccess) return cuda_failed();
-  }
-  const dim3 grid((unsigned)ceil_div(V, lanes.rows()));
+  const int run = embed_run(H, grad, grad_dtype, ld_grad, grad_weight, grad_weight_dtype,
+                            ld_grad_weight);
   const cudaError_t e = by_dtypes(grad_dtype, grad_weight_dtype, [&](auto d32, auto o32) {
-    constexpr bool kD = decltype(d32)::value, kO = decltype(o32)::value;
-    if constexpr (kO)
-      if (accumulate)
-        return launch_overlapped(embed_rows_kernel<kD, true, true>, grid, kRowThreads, 0, s, grad,
-                                 ld_grad, vg, (int)H, (int)V, o, scale, grad_weight,
-                                 ld_grad_weight, vw, lanes);
-    return launch_overlapped(embed_rows_kernel<kD, kO, false>, grid, kRowThreads, 0, s, grad,
-                             ld_grad, vg, (int)H, (int)V, o, scale, grad_weight, ld_grad_weight,
-                             vw, lanes);
+    return by_run(run, o32, [&](auto r) {
+      constexpr bool kD = decltype(d32)::value, kO = decltype(o32)::value;
+      constexpr int kRun = decltype(r)::value;
+      const RowLanes<kRun> lanes = row_lanes<kRun>(H);
+      if (heavy) {
+        // groups by columns: four blocks an SM, or all there can be
+        const int64_t col_blocks = ceil_div(H, lanes.step());
+        int64_t gx = ceil_div(4 * (int64_t)dev.sm_count, col_blocks);
+        const int64_t all = ceil_div(p.groups, lanes.rows());
+        gx = gx < all ? gx : all;
+        const cudaError_t err = launch_overlapped(
+            embed_groups_kernel<kD, kRun>, dim3((unsigned)(gx < 1 ? 1 : gx), (unsigned)col_blocks),
+            kRowThreads, 0, s, grad, ld_grad, (int)H, o, (int)p.groups, lanes);
+        if (err != cudaSuccess) return err;
+      }
+      // 16 table rows in turn a row of threads, fewer where that leaves under 16 blocks an SM
+      int turns = kRowsInTurn;
+      while (turns > 1 && ceil_div(V, lanes.rows() * turns) < 16 * dev.sm_count) turns /= 2;
+      const dim3 grid((unsigned)ceil_div(V, lanes.rows() * turns));
+      if constexpr (kO)
+        if (accumulate)
+          return launch_overlapped(embed_rows_kernel<kD, true, true, kRun>, grid, kRowThreads, 0, s,
+                                   grad, ld_grad, (int)H, (int)V, o, scale, grad_weight,
+                                   ld_grad_weight, turns, lanes);
+      return launch_overlapped(embed_rows_kernel<kD, kO, false, kRun>, grid, kRowThreads, 0, s,
+                               grad, ld_grad, (int)H, (int)V, o, scale, grad_weight,
+                               ld_grad_weight, turns, lanes);
+    });
   });
   return e == cudaSuccess ? RLK_OK : cuda_failed();
 }

@@ -146,87 +146,124 @@ struct GatedSched {
 };
 
 // ---------------------------------------------------------------- rows of 32 columns
-// The widest vector (16, 8 or 4 bytes; 0: elements) that addresses `base + 32 c` of every row allow.
-inline int run_width(const void* base, int64_t ld, int64_t esize) {
-  for (int w = 16; w >= 4; w /= 2)
-    if (reinterpret_cast<uintptr_t>(base) % w == 0 && (ld * esize) % w == 0) return w;
-  return 0;
+// An epilogue thread holds 32 columns of its own row.  Where a matrix allows 16-byte vectors it
+// writes (or reads) them itself, four neighbouring vectors of one row after another.  Else the
+// warp turns its 32 x 32 block by shuffles, so that a lane holds a column, and each row goes out
+// as one run of 32 elements: with an odd width every thread would write 32 single elements in a
+// row of its own, 32 sectors an instruction in place of two or three (2000 x 2048 -> 5461: 140 us,
+// turned 61, as for 5464; G of the backward with them formed again 280 and 193 with its products).
+
+// Element i of lane l <- element (l mod n) of lane l - l mod n + i, n = 32 or 16.
+template <int n, class T>
+__device__ __forceinline__ void turn_block(T (&x)[n]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = n / 2; s >= 1; s >>= 1) {
+    const bool high = lane & s;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if (i & s) continue;
+      const T got = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i | s], s);
+      if (high)
+        x[i] = got;
+      else
+        x[i | s] = got;
+    }
+  }
 }
 
-// x[0 .. n) to BF16 or FP32 at dst (n = 32 for whole runs, which use vectors of `width` bytes).
-__device__ __forceinline__ void store_run_bf16(uint16_t* dst, const float (&x)[32], int n,
-                                               int width) {
-  if (n >= 32 && width != 0) {
-    uint32_t p[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-    if (width == 16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<uint4*>(dst)[i] =
-            make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-    } else if (width == 8) {
+// Columns c .. c + n - 1 (n <= 32) of the warp's rows r0 .. r0 + 31 below M; the whole warp takes part,
+// and x, the thread's row, is used up.  vec: whole rows of 32 are 16-byte vectors.  BF16 is turned
+// in pairs, columns i and i + 16 in one register: 32 shuffles in place of 80, and a store then
+// covers half a row of each half of the block.
+template <bool kFp32>
+__device__ __forceinline__ void store_block(void* base, int64_t ld, int r0, int M, int c, int n,
+                                            bool vec, float (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (vec && n == 32) {
+    if (r0 + lane >= M) return;
+    const int64_t at = (int64_t)(r0 + lane) * ld + c;
+    if constexpr (kFp32) {
+      float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint2*>(dst)[i] = make_uint2(p[2 * i], p[2 * i + 1]);
+        d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     } else {
+      uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(dst)[i] = p[i];
+      for (int i = 0; i < 4; ++i)
+        d[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                          pack_bf16(x[8 * i + 4], x[8 * i + 5]),
+                          pack_bf16(x[8 * i + 6], x[8 * i + 7]));
     }
     return;
   }
+  if constexpr (kFp32) {
+    turn_block(x);
+    float* d = static_cast<float*>(base) + (int64_t)r0 * ld + c + lane;
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < n) reinterpret_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(x[i]);
-}
-
-__device__ __forceinline__ void store_run_fp32(float* dst, const float (&x)[32], int n, int width) {
-  if (n >= 32 && width == 16) {
+    for (int i = 0; i < 32; ++i)
+      if (r0 + i < M && lane < n) d[i * ld] = x[i];
+  } else {
+    uint32_t p[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      reinterpret_cast<float4*>(dst)[i] =
-          make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    return;
-  }
+    for (int i = 0; i < 16; ++i) p[i] = pack_bf16(x[i], x[i + 16]);
+    turn_block(p);
+    const int r = r0 + (lane & 16), col = lane & 15;
+    uint16_t* d = static_cast<uint16_t*>(base) + (int64_t)r * ld + c + col;
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < n) dst[i] = x[i];
-}
-
-// x[0 .. 32) = n elements at src, the rest 0.
-__device__ __forceinline__ void load_run(const void* src, int64_t at, int fp32, int n, int width,
-                                         float (&x)[32]) {
-  if (n >= 32 && width == 16) {
-    if (fp32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v = __ldg(p + i);
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-      }
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = __ldg(p + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-          x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-      }
+    for (int i = 0; i < 16; ++i) {
+      if (r + i < M && col < n) d[i * ld] = (uint16_t)p[i];
+      if (r + i < M && col + 16 < n) d[i * ld + 16] = (uint16_t)(p[i] >> 16);
     }
-    return;
+  }
+}
+
+// The same block read: x is the thread's row, 0 past column n and past row M.  The turned loads
+// take the block's nearest element where there is none, so that none hangs on a branch.
+template <bool kFp32>
+__device__ __forceinline__ void load_block(const void* base, int64_t ld, int r0, int M, int c,
+                                           int n, bool vec, float (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+  const bool in = r0 + lane < M;
+  if (vec && n == 32) {
+    const int64_t at = (int64_t)(in ? r0 + lane : M - 1) * ld + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float y[8];
+      load8<kFp32, 8>(base, at, 8 * i, 0, 32, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[8 * i + j] = y[j];
+    }
+  } else if constexpr (kFp32) {
+    const float* s = static_cast<const float*>(base) + c + min(lane, n - 1);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __ldg(s + (int64_t)min(r0 + i, M - 1) * ld);
+    turn_block(x);
+  } else {
+    uint32_t p[16];
+    const int r = r0 + (lane & 16), col = lane & 15;
+    const uint16_t* s = static_cast<const uint16_t*>(base) + c;
+    const int lo = min(col, n - 1), hi = min(col + 16, n - 1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint16_t* row = s + (int64_t)min(r + i, M - 1) * ld;
+      p[i] = (uint32_t)__ldg(row + lo) | (uint32_t)__ldg(row + hi) << 16;
+    }
+    turn_block(p);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = __uint_as_float(p[i] << 16);
+      x[i + 16] = __uint_as_float(p[i] & 0xffff0000u);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    x[i] = 0.f;
-    if (i < n)
-      x[i] = fp32 ? __ldg(static_cast<const float*>(src) + at + i)
-                  : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(src) + at + i)
-                                    << 16);
-  }
+  for (int i = 0; i < 32; ++i)
+    if (!in || i >= n) x[i] = 0.f;
+}
+
+inline bool block_vec(const void* base, int64_t ld, int64_t esize) {
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (ld * esize) % 16 == 0;
 }
 
 // ---------------------------------------------------------------- forward
@@ -235,7 +272,7 @@ struct GatedOut {
   int act;
   void* H;
   int64_t ldh;
-  int h_fp32, h_width;
+  bool h_fp32, h_vec;
   int keep;
   void* kept;            // [M, 2, Fp] FP32 or int8
   uint8_t* exponents;    // [M, 2, Fp / 32]
@@ -254,20 +291,17 @@ __device__ __forceinline__ void keep_run(const GatedOut& o, int row, int f, int 
       d[i] = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
     return;
   }
-  uint32_t most = 0;
+  float most = fabsf(__uint_as_float(z[0]));
 #pragma unroll
-  for (int i = 0; i < 32; ++i) most = max(most, z[i] & 0x7fffffffu);
+  for (int i = 1; i < 32; ++i) most = max_magnitude(most, __uint_as_float(z[i]));
   const uint32_t e = int8_exponent(most);
   const float inverse = int8_inverse(e);
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    w[i] = 0;
-    if (e != 255u) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[i] |= int8_value(__uint_as_float(z[4 * i + j]), inverse) << (8 * j);
-    }
+    const float x[4] = {__uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1]),
+                        __uint_as_float(z[4 * i + 2]), __uint_as_float(z[4 * i + 3])};
+    w[i] = e == 255u ? 0u : int8_word(x, inverse);
   }
   uint4* d = reinterpret_cast<uint4*>(static_cast<int8_t*>(o.kept) + at);
   d[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -284,9 +318,10 @@ __device__ __forceinline__ void value_run(const uint32_t (&g)[32], const uint32_
 }
 
 // A tile's epilogue in one warp: accumulator columns [0, kCols) hold g and [kCols, 2 kCols) u of
-// columns f0 .. f0 + kCols - 1; the thread's row is `row`.
+// columns f0 .. f0 + kCols - 1 of the warp's rows r0 .. r0 + 31.
 template <int kCols>
-__device__ __forceinline__ void gated_tile(const GatedOut& o, uint32_t taddr, int row, int f0) {
+__device__ __forceinline__ void gated_tile(const GatedOut& o, uint32_t taddr, int r0, int f0) {
+  const int row = r0 + (threadIdx.x & 31);
 #pragma unroll 1
   for (int c = 0; c < kCols / 32; ++c) {
     const int f = f0 + 32 * c;
@@ -296,21 +331,19 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, uint32_t taddr, in
     tmem_ld32(taddr + 32 * c, g);
     tmem_ld32(taddr + kCols + 32 * c, u);
     tmem_wait_ld();
-    if (row >= o.M) continue;
     float h[32];
     if (o.act == RLK_ACT_SILU)
       value_run<RLK_ACT_SILU>(g, u, h);
     else
       value_run<RLK_ACT_GELU_TANH>(g, u, h);
     const int n = min(32, o.F - f);
-    const int64_t at = (int64_t)row * o.ldh + f;
-    if (RLK_STORE_OK(row < o.M && f + n <= o.ldh, &g_err_gated_linear)) {
+    if (RLK_STORE_OK(f + n <= o.ldh, &g_err_gated_linear)) {
       if (o.h_fp32)
-        store_run_fp32(static_cast<float*>(o.H) + at, h, n, o.h_width);
+        store_block<true>(o.H, o.ldh, r0, o.M, f, n, o.h_vec, h);
       else
-        store_run_bf16(static_cast<uint16_t*>(o.H) + at, h, n, o.h_width);
+        store_block<false>(o.H, o.ldh, r0, o.M, f, n, o.h_vec, h);
     }
-    if (o.keep != RLK_KEEP_NONE) {
+    if (o.keep != RLK_KEEP_NONE && row < o.M) {
       keep_run(o, row, f, 0, g);
       keep_run(o, row, f, 1, u);
     }
@@ -354,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int r0, b0;
       sc.tile_coords(u, 0, r0, b0);
       gated_tile<kGateCols>(o, tmem + acc * kAccCols + lane_off,
-                            r0 + (int)ps.rank * kHalfRows + q * 32 + lane, b0 / 2);
+                            r0 + (int)ps.rank * kHalfRows + q * 32, b0 / 2);
       epilogue_release(ps, acc);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -399,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int r0, b0;
       sc.tile_coords(u, 0, r0, b0);
       if (32 * q < o.M)
-        gated_tile<kCols>(o, tmem + acc * kAccCols + lane_off, q * 32 + lane, b0 / 2);
+        gated_tile<kCols>(o, tmem + acc * kAccCols + lane_off, q * 32, b0 / 2);
       solo_release(ps, acc);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -414,10 +447,10 @@ struct GradOut {
   int act;
   const void* dH;
   int64_t lddh;
-  int dh_fp32, dh_width;
+  bool dh_fp32, dh_vec;
   uint16_t* G;           // [M, ldG] BF16: dL/dg in columns [0, F), dL/du in [F, 2 F)
   int64_t ldG;
-  int up_width;          // vectors that column F + 32 c of a row allows
+  bool up_vec;           // column F of every row is on 16 bytes
 };
 
 template <int kAct>
@@ -469,32 +502,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!epilogue_acquire(ps, acc, acc_phase, &g_err_gated_linear)) break;
       int r0, b0;
       sc.tile_coords(unit, 0, r0, b0);
-      const int row = r0 + (int)ps.rank * kHalfRows + q * 32 + lane;
+      const int row0 = r0 + (int)ps.rank * kHalfRows + q * 32;
       const int f0 = b0 / 2;
       const uint32_t taddr = tmem + acc * kAccCols + lane_off;
 #pragma unroll 1
       for (int c = 0; c < kGateCols / 32; ++c) {
         const int f = f0 + 32 * c;
-        if (f >= o.F) break;
+        if (f >= o.F) break;                    // uniform: depends on the tile only
         const int n = min(32, o.F - f);
-        float d[32];
-        if (row < o.M)
-          load_run(o.dH, (int64_t)row * o.lddh + f, o.dh_fp32, n, o.dh_width, d);
+        float d[32], dg[32];
+        if (o.dh_fp32)
+          load_block<true>(o.dH, o.lddh, row0, o.M, f, n, o.dh_vec, d);
+        else
+          load_block<false>(o.dH, o.lddh, row0, o.M, f, n, o.dh_vec, d);
         uint32_t g[32], u[32];
         __syncwarp();
         tmem_ld32(taddr + 32 * c, g);
         tmem_ld32(taddr + kGateCols + 32 * c, u);
         tmem_wait_ld();
-        if (row >= o.M) continue;
-        float dg[32];
         if (o.act == RLK_ACT_SILU)
           slope_run<RLK_ACT_SILU>(d, g, u, dg);
         else
           slope_run<RLK_ACT_GELU_TANH>(d, g, u, dg);
-        if (!RLK_STORE_OK(row < o.M && o.F + f + n <= o.ldG, &g_err_gated_linear)) continue;
-        uint16_t* to = o.G + (int64_t)row * o.ldG + f;
-        store_run_bf16(to, dg, n, 16);
-        store_run_bf16(to + o.F, d, n, o.up_width);
+        if (!RLK_STORE_OK(o.F + f + n <= o.ldG, &g_err_gated_linear)) continue;
+        store_block<false>(o.G, o.ldG, row0, o.M, f, n, true, dg);
+        store_block<false>(o.G + o.F, o.ldG, row0, o.M, f, n, o.up_vec, d);
       }
       epilogue_release(ps, acc);
       acc ^= 1;
@@ -504,33 +536,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pipe_teardown(tmem);
 }
 
-// G from kept projections, eight columns a thread: one pass at memory speed.
-template <bool kInt8, bool kDFp32, int kAct>
+// G from kept projections, eight columns a thread: one pass at memory speed.  kVec: dH and both
+// halves of G's rows allow 16-byte vectors; else they pass through shared memory (RowStage).
+template <bool kInt8, bool kDFp32, int kAct, bool kVec>
 __global__ void __launch_bounds__(kRowThreads)
     gated_grad_kept_kernel(const void* __restrict__ kept, const uint8_t* __restrict__ exponents,
-                           int Fp, GradOut o, int vec_d, RowLanes lanes) {
+                           int Fp, GradOut o, RowLanes<8> lanes) {
+  __shared__ __align__(16) float staged[kVec ? 1 : kRowThreads / 32][256];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int64_t row = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
-  if (row >= o.M) return;
-  const bool vec_up = o.up_width == 16;
-  for (int f = lanes.col(); f < o.F; f += lanes.step()) {
+  const bool in = row < o.M && RLK_STORE_OK(2 * (int64_t)o.F <= o.ldG, &g_err_gated_linear);
+  const int64_t at = row * 2 * Fp;         // plane 0 of this row's kept projections
+  const int64_t to = row * o.ldG;
+  for (int f0 = (int)blockIdx.y * lanes.step(); f0 < o.F; f0 += (int)gridDim.y * lanes.step()) {
+    const int f = f0 + lanes.col();
     float d[8], g[8], u[8];
-    load8<kDFp32>(o.dH, row * o.lddh, f, o.F, vec_d, d);
-    const int64_t at = row * 2 * Fp + f;
-    if constexpr (kInt8) {
-      const int8_t* q = static_cast<const int8_t*>(kept) + at;
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(q));
-      const uint2 b = __ldg(reinterpret_cast<const uint2*>(q + Fp));
-      const float sa = int8_step(__ldg(exponents + at / kInt8Block));
-      const float sb = int8_step(__ldg(exponents + (at + Fp) / kInt8Block));
-      int8_floats(a.x, sa, g);
-      int8_floats(a.y, sa, g + 4);
-      int8_floats(b.x, sb, u);
-      int8_floats(b.y, sb, u + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = g[i] = u[i] = 0.f;
+    if constexpr (kVec) {
+      if (in) load8<kDFp32, 8>(o.dH, row * o.lddh, f, 0, o.F, d);
     } else {
-      load8<true>(kept, at, 0, 8, true, g);
-      load8<true>(kept, at + Fp, 0, 8, true, u);
+      RowStage(staged).load<kDFp32>(o.dH, row * o.lddh, f, o.F, in, d);
+    }
+    if (in && f < o.F) {
+      if constexpr (kInt8) {
+        const int8_t* q = static_cast<const int8_t*>(kept) + at;
+        const uint8_t* e = exponents + at / kInt8Block;
+        load_int8(q, e, f, g);
+        load_int8(q + Fp, e + Fp / kInt8Block, f, u);
+      } else {
+        load8<true, 8>(kept, at, f, 0, Fp, g);
+        load8<true, 8>(kept, at + Fp, f, 0, Fp, u);
+      }
     }
     float dg[8];
 #pragma unroll
@@ -540,9 +578,14 @@ __global__ void __launch_bounds__(kRowThreads)
       dg[i] = d[i] * u[i] * slope;
       d[i] *= value;
     }
-    if (!RLK_STORE_OK(row < o.M && o.F + min(f + 8, o.F) <= o.ldG, &g_err_gated_linear)) continue;
-    store8<false>(o.G, row * o.ldG, f, o.F, true, dg);
-    store8<false>(o.G, row * o.ldG + o.F, f, o.F, vec_up, d);
+    if constexpr (kVec) {
+      if (!in) continue;
+      store8<false, 8>(o.G, to, f, 0, o.F, dg);
+      store8<false, 8>(o.G, to + o.F, f, 0, o.F, d);
+    } else {
+      RowStage(staged).store<false>(o.G, to, f, o.F, in, dg);
+      RowStage(staged).store<false>(o.G, to + o.F, f, o.F, in, d);
+    }
   }
 }
 
@@ -735,7 +778,7 @@ rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, co
   o.H = H;
   o.ldh = ldh;
   o.h_fp32 = h_dtype == RLK_FP32;
-  o.h_width = run_width(H, ldh, dtype_bytes(h_dtype));
+  o.h_vec = block_vec(H, ldh, dtype_bytes(h_dtype));
   o.keep = keep;
   o.kept = kept;
   o.exponents = kept_exponents;
@@ -832,10 +875,10 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
   o.dH = dH;
   o.lddh = lddh;
   o.dh_fp32 = dh_dtype == RLK_FP32;
-  o.dh_width = run_width(dH, lddh, dtype_bytes(dh_dtype));
+  o.dh_vec = block_vec(dH, lddh, dtype_bytes(dh_dtype));
   o.G = reinterpret_cast<uint16_t*>(ws);
   o.ldG = p.ldG;
-  o.up_width = run_width(o.G + F, p.ldG, 2);
+  o.up_vec = block_vec(o.G + F, p.ldG, 2);
   int* counter = reinterpret_cast<int*>(ws + p.off_ctr);
   cudaError_t e;
   if (keep == RLK_KEEP_NONE) {
@@ -852,21 +895,32 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
                                              sc, o);
   } else {
     const int Fp = (int)(ceil_div(F, kInt8Block) * kInt8Block);
-    const RowLanes lanes = row_lanes(F);
-    const dim3 grid((unsigned)ceil_div(M, lanes.rows()));
-    const int vec_d = o.dh_width == 16;
-    e = by_dtypes(keep == RLK_KEEP_INT8 ? RLK_FP32 : RLK_BF16, dh_dtype, [&](auto q8, auto d32) {
+    const auto launch = [&](auto q8, auto d32, auto v) {
       constexpr bool kQ = decltype(q8)::value, kD = decltype(d32)::value;
+      constexpr bool kVec = decltype(v)::value;
+      const RowLanes<8> lanes = row_lanes<8>(F, kVec ? 2 : 5);
+      const int64_t steps = ceil_div(F, lanes.step());
+      const dim3 grid((unsigned)ceil_div(M, lanes.rows()), (unsigned)(steps < 65535 ? steps : 65535));
       return activation == RLK_ACT_SILU
-                 ? launch_overlapped(gated_grad_kept_kernel<kQ, kD, RLK_ACT_SILU>, grid,
-                                     kRowThreads, 0, s, kept, kept_exponents, Fp, o, vec_d, lanes)
-                 : launch_overlapped(gated_grad_kept_kernel<kQ, kD, RLK_ACT_GELU_TANH>, grid,
-                                     kRowThreads, 0, s, kept, kept_exponents, Fp, o, vec_d, lanes);
+                 ? launch_overlapped(gated_grad_kept_kernel<kQ, kD, RLK_ACT_SILU, kVec>, grid,
+                                     kRowThreads, 0, s, kept, kept_exponents, Fp, o, lanes)
+                 : launch_overlapped(gated_grad_kept_kernel<kQ, kD, RLK_ACT_GELU_TANH, kVec>, grid,
+                                     kRowThreads, 0, s, kept, kept_exponents, Fp, o, lanes);
+    };
+    const bool vec = o.dh_vec && o.up_vec && F % 8 == 0;
+    e = by_dtypes(keep == RLK_KEEP_INT8 ? RLK_FP32 : RLK_BF16, dh_dtype, [&](auto q8, auto d32) {
+      return vec ? launch(q8, d32, Const<true>()) : launch(q8, d32, Const<false>());
     });
   }
   if (e != cudaSuccess) return cuda_failed();
   // The products read G and the (possibly copied) operands, all TMA-ready: the counter is all the
-  // workspace they need, and every argument that they check was checked above.
+  // workspace they need, and every argument that they check was checked above.  Both wanted and the
+  // longer reduction's 256 x 256 tiles fill at most half of the SM pairs: one launch over both
+  // products' tiles, the linear-logp backward's rule (the same bits); else det_linear's.
+  const int64_t long_tiles = ceil_div(2 * F >= M ? M : 2 * F, kPairRows) * ceil_div(K, kBN);
+  if (dX && dW && 2 * long_tiles <= dev.sm_count / 2)
+    return launch_fwd_and_db(o.G, M, 2 * F, p.ldG, in.w, K, p.ldw, dX, dx_dtype, lddx, in.x, p.ldx,
+                             dW, dw_dtype, lddw, counter, s);
   return rlk_det_linear_backward(o.G, RLK_BF16, M, 2 * F, p.ldG, in.x, K, p.ldx, in.w, p.ldw, dX,
                                  dx_dtype, dX ? lddx : K, dW, dw_dtype, dW ? lddw : K,
                                  ws + p.off_ctr, 256, stream);

@@ -15,61 +15,105 @@ __device__ unsigned int g_err_int8 = 0;
 
 namespace {
 
-template <bool kFp32>
+// kRowsAThread rows a thread, their loads issued together.  Rows that rule vectors out (kVec false)
+// pass through shared memory (RowStage).  Packing is bound by instructions as much as by HBM.
+constexpr int kRowsAThread = 2;
+
+template <bool kFp32, bool kVec>
 __global__ void __launch_bounds__(kRowThreads)
-    pack_int8_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ldx, int vec,
+    pack_int8_kernel(const void* __restrict__ x, int64_t rows, int cols, int64_t ldx,
                      int8_t* __restrict__ q, int64_t ldq, uint8_t* __restrict__ exponents,
-                     int64_t lde, RowLanes lanes) {
+                     int64_t lde, RowLanes<8> lanes) {
+  __shared__ __align__(16) float staged[kVec ? 1 : kRowThreads / 32][256];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int64_t r = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
+  const int64_t r0 = (int64_t)blockIdx.x * (kRowsAThread * lanes.rows()) + lanes.row();
   const int wide = (cols + kInt8Block - 1) / kInt8Block * kInt8Block;
-  // whole warps stay in the loop together: the four lanes of a block exchange maxima
-  for (int c0 = 0; c0 < wide; c0 += lanes.step()) {
+  // whole warps stay in the loop together: a block's four lanes exchange their largest magnitude
+  for (int c0 = (int)blockIdx.y * lanes.step(); c0 < wide; c0 += (int)gridDim.y * lanes.step()) {
     const int c = c0 + lanes.col();
-    const bool in = r < rows && c < wide;
-    float v[8];
+    float v[kRowsAThread][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (in) load8<kFp32>(x, r * ldx, c, cols, vec, v);
-    uint32_t most = 0;
+    for (int k = 0; k < kRowsAThread; ++k) {
+      const int64_t r = r0 + k * lanes.rows();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    if (!in) continue;
-    const uint32_t e = int8_exponent(most);
-    const float inverse = int8_inverse(e);
-    uint32_t w[2] = {0, 0};
-    if (e != 255u) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i >> 2] |= int8_value(v[i], inverse) << (8 * (i & 3));
+      for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+      if constexpr (kVec) {
+        if (r < rows) load8<kFp32, 8>(x, r * ldx, c, 0, cols, v[k]);
+      } else {
+        RowStage(staged).load<kFp32>(x, r * ldx, c, cols, r < rows, v[k]);
+      }
     }
-    if (RLK_STORE_OK(c + 8 <= ldq, &g_err_int8))
-      *reinterpret_cast<uint2*>(q + r * ldq + c) = make_uint2(w[0], w[1]);
-    if ((c & (kInt8Block - 1)) == 0 && RLK_STORE_OK(c / kInt8Block < lde, &g_err_int8))
-      exponents[r * lde + c / kInt8Block] = (uint8_t)e;
+#pragma unroll
+    for (int k = 0; k < kRowsAThread; ++k) {
+      const int64_t r = r0 + k * lanes.rows();
+      float most = fabsf(v[k][0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) most = max_magnitude(most, v[k][i]);
+      most = max_magnitude(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max_magnitude(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      if (r >= rows || c >= wide || !RLK_STORE_OK(c + 8 <= ldq && c / kInt8Block < lde, &g_err_int8))
+        continue;
+      const uint32_t e = int8_exponent(most);
+      const float inverse = int8_inverse(e);
+      uint2 w = make_uint2(int8_word(v[k], inverse), int8_word(v[k] + 4, inverse));
+      if (e == 255u) w = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(q + r * ldq + c) = w;
+      if ((c & (kInt8Block - 1)) == 0) exponents[r * lde + c / kInt8Block] = (uint8_t)e;
+    }
   }
 }
 
-template <bool kFp32>
+// kRun 8: BF16 in vectors, 4: FP32 in vectors, 1: by way of shared memory.
+template <bool kFp32, int kRun>
 __global__ void __launch_bounds__(kRowThreads)
     unpack_int8_kernel(const int8_t* __restrict__ q, int64_t rows, int cols, int64_t ldq,
                        const uint8_t* __restrict__ exponents, int64_t lde, void* __restrict__ out,
-                       int64_t ldo, int vec, RowLanes lanes) {
+                       int64_t ldo, RowLanes<kRun == 4 ? 4 : 8> lanes) {
+  __shared__ __align__(16) float staged[kRun == 1 ? kRowThreads / 32 : 1][256];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int64_t r = (int64_t)blockIdx.x * lanes.rows() + lanes.row();
-  if (r >= rows) return;
-  for (int c = lanes.col(); c < cols; c += lanes.step()) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + r * ldq + c));
-    const float step = int8_step(__ldg(exponents + r * lde + c / kInt8Block));
-    float v[8];
-    int8_floats(w.x, step, v);
-    int8_floats(w.y, step, v + 4);
-    if (RLK_STORE_OK(min(c + 8, cols) <= ldo, &g_err_int8))
-      store8<kFp32>(out, r * ldo, c, cols, vec, v);
+  const int64_t r0 = (int64_t)blockIdx.x * (kRowsAThread * lanes.rows()) + lanes.row();
+  const int gap = lanes.gap();
+  for (int c0 = (int)blockIdx.y * lanes.step(); c0 < cols; c0 += (int)gridDim.y * lanes.step()) {
+    const int c = c0 + lanes.col();
+    float v[kRowsAThread][8];
+#pragma unroll
+    for (int k = 0; k < kRowsAThread; ++k) {
+      const int64_t r = r0 + k * lanes.rows();
+      if (r >= rows) continue;
+      const int8_t* values = q + r * ldq;
+      const uint8_t* e = exponents + r * lde;
+      if constexpr (kRun == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int at = c + h * gap;
+          if (at < cols)
+            int8_floats(__ldg(reinterpret_cast<const uint32_t*>(values + at)),
+                        int8_step(__ldg(e + at / kInt8Block)), v[k] + 4 * h);
+        }
+      } else if (c < cols) {
+        load_int8(values, e, c, v[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsAThread; ++k) {
+      const int64_t r = r0 + k * lanes.rows();
+      const bool in = r < rows && RLK_STORE_OK(cols <= ldo, &g_err_int8);
+      if constexpr (kRun == 1)
+        RowStage(staged).store<kFp32>(out, r * ldo, c, cols, in, v[k]);
+      else if (in)
+        store8<kFp32, kRun>(out, r * ldo, c, gap, cols, v[k]);
+    }
   }
+}
+
+// Rows to blocks, and their column steps too (the y dimension's limit aside).
+template <int kRun>
+dim3 int8_grid(int64_t rows, int64_t cols, const RowLanes<kRun>& lanes) {
+  const int64_t steps = ceil_div(cols, lanes.step());
+  return dim3((unsigned)ceil_div(rows, kRowsAThread * lanes.rows()),
+              (unsigned)(steps < 65535 ? steps : 65535));
 }
 
 // Column extents stay below 2^30: a thread's column index plus a step must fit an int.
@@ -82,6 +126,11 @@ rlk_status check_int8(int dtype, int64_t rows, int64_t cols, int64_t ld, int64_t
       ldq >= kPitchLimit || lde < ceil_div(cols, kInt8Block) || lde >= kPitchLimit)
     return RLK_ERR_SHAPE;
   return RLK_OK;
+}
+
+rlk_status cuda_failed() {
+  cudaGetLastError();
+  return RLK_ERR_CUDA;
 }
 
 }  // namespace
@@ -114,19 +163,21 @@ rlk_status rlk_pack_int8(const void* x, int x_dtype, int64_t rows, int64_t cols,
   if (!is_aligned(x, dtype_bytes(x_dtype)) || !is_aligned(q, 16)) return RLK_ERR_ALIGN;
   DeviceInfo dev;
   if ((st = device_ready(&dev)) != RLK_OK) return st;
-  const RowLanes lanes = row_lanes(cols);
-  const dim3 grid((unsigned)ceil_div(rows, lanes.rows()));
-  const int vec = rows_vec(x, ldx, dtype_bytes(x_dtype));
+  const bool vec = rows_vec(x, ldx, dtype_bytes(x_dtype), cols, 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((x_dtype == RLK_FP32
-           ? launch_overlapped(pack_int8_kernel<true>, grid, kRowThreads, 0, s, x, rows, (int)cols,
-                               ldx, vec, q, ldq, exponents, ld_exponents, lanes)
-           : launch_overlapped(pack_int8_kernel<false>, grid, kRowThreads, 0, s, x, rows, (int)cols,
-                               ldx, vec, q, ldq, exponents, ld_exponents, lanes)) != cudaSuccess) {
-    cudaGetLastError();
-    return RLK_ERR_CUDA;
-  }
-  return RLK_OK;
+  const auto launch = [&](auto x32, auto v) {
+    constexpr bool kVec = decltype(v)::value;
+    const RowLanes<8> lanes = row_lanes<8>(cols, kVec ? 2 : 5);
+    return launch_overlapped(pack_int8_kernel<decltype(x32)::value, kVec>,
+                             int8_grid(rows, cols, lanes), kRowThreads, 0, s, x, rows, (int)cols,
+                             ldx, q, ldq, exponents, ld_exponents, lanes);
+  };
+  const auto by_vec = [&](auto x32) {
+    return vec ? launch(x32, Const<true>()) : launch(x32, Const<false>());
+  };
+  return (x_dtype == RLK_FP32 ? by_vec(Const<true>()) : by_vec(Const<false>())) == cudaSuccess
+             ? RLK_OK
+             : cuda_failed();
 }
 
 rlk_status rlk_unpack_int8(const int8_t* q, int64_t rows, int64_t cols, int64_t ldq,
@@ -140,20 +191,21 @@ rlk_status rlk_unpack_int8(const int8_t* q, int64_t rows, int64_t cols, int64_t 
   if (!is_aligned(out, dtype_bytes(out_dtype)) || !is_aligned(q, 16)) return RLK_ERR_ALIGN;
   DeviceInfo dev;
   if ((st = device_ready(&dev)) != RLK_OK) return st;
-  const RowLanes lanes = row_lanes(cols);
-  const dim3 grid((unsigned)ceil_div(rows, lanes.rows()));
-  const int vec = rows_vec(out, ld_out, dtype_bytes(out_dtype));
+  const bool fp32 = out_dtype == RLK_FP32;
+  const bool vec = rows_vec(out, ld_out, dtype_bytes(out_dtype), cols, fp32 ? 4 : 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((out_dtype == RLK_FP32
-           ? launch_overlapped(unpack_int8_kernel<true>, grid, kRowThreads, 0, s, q, rows,
-                               (int)cols, ldq, exponents, ld_exponents, out, ld_out, vec, lanes)
-           : launch_overlapped(unpack_int8_kernel<false>, grid, kRowThreads, 0, s, q, rows,
-                               (int)cols, ldq, exponents, ld_exponents, out, ld_out, vec,
-                               lanes)) != cudaSuccess) {
-    cudaGetLastError();
-    return RLK_ERR_CUDA;
-  }
-  return RLK_OK;
+  const auto launch = [&](auto o32, auto run) {
+    constexpr int kRun = decltype(run)::value;
+    const auto lanes = row_lanes<kRun == 4 ? 4 : 8>(cols, kRun == 1 ? 5 : 2);
+    return launch_overlapped(unpack_int8_kernel<decltype(o32)::value, kRun>,
+                             int8_grid(rows, cols, lanes), kRowThreads, 0, s, q, rows, (int)cols,
+                             ldq, exponents, ld_exponents, out, ld_out, lanes);
+  };
+  const cudaError_t e =
+      fp32 ? vec ? launch(Const<true>(), Const<4>()) : launch(Const<true>(), Const<1>())
+      : vec ? launch(Const<false>(), Const<8>())
+            : launch(Const<false>(), Const<1>());
+  return e == cudaSuccess ? RLK_OK : cuda_failed();
 }
 
 }  // extern "C"

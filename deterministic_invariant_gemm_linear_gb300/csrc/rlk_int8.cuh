@@ -14,10 +14,16 @@ namespace rlk {
 
 constexpr int kInt8Block = 32;
 
-// The exponent byte from the largest of the block's |x| as FP32 bit patterns (integer order,
-// which puts NaN above infinity above every number).
-__device__ __forceinline__ uint32_t int8_exponent(uint32_t most_bits) {
-  const int E = (int)(most_bits >> 23);
+// The larger magnitude; NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return m;
+}
+
+// The exponent byte from the block's largest magnitude.
+__device__ __forceinline__ uint32_t int8_exponent(float most) {
+  const int E = (int)(__float_as_uint(most) >> 23 & 255u);
   return E == 255 ? 255u : (uint32_t)max(E - 6, 1);
 }
 // 2^(127 - e), exact for every e of a finite block (1 .. 248); 0 for e = 255.
@@ -26,10 +32,27 @@ __device__ __forceinline__ float int8_inverse(uint32_t e) {
 }
 __device__ __forceinline__ float int8_step(uint32_t e) { return __uint_as_float(e << 23); }
 
-// x / step, rounded to nearest even and held to -127 .. 127 (the product is exact).
-__device__ __forceinline__ uint32_t int8_value(float x, float inverse) {
-  const float q = fminf(fmaxf(__fmul_rn(x, inverse), -127.f), 127.f);
-  return (uint32_t)__float2int_rn(q) & 255u;
+// Four x / step as bytes, rounded to nearest even and held to -127 .. 127.  x / step + 1.5 2^23 is
+// rounded to a whole number by the addition (the product is exact), whose low byte it is: one
+// fused operation where a conversion would run at a quarter of the rate.  |x / step| is below
+// 128, so only +-128 has to be held, which is rare and shows as a byte of 0x80.
+__device__ __forceinline__ uint32_t int8_word(const float* x, float inverse) {
+  constexpr float kOffset = 12582912.f;
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = __fmaf_rn(x[i], inverse, kOffset);
+  const auto bytes = [&]() {
+    return __byte_perm(__byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040),
+                       __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040), 0x5410);
+  };
+  uint32_t w = bytes();
+  const uint32_t t = w ^ 0x80808080u;
+  if ((t - 0x01010101u) & ~t & 0x80808080u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fminf(fmaxf(y[i], kOffset - 127.f), kOffset + 127.f);
+    w = bytes();
+  }
+  return w;
 }
 
 // Four values of a word as FP32: q + 2^23 + 128 built by bytes (q with its sign bit flipped is
@@ -41,6 +64,15 @@ __device__ __forceinline__ void int8_floats(uint32_t word, float step, float* x)
     const float v = __uint_as_float(__byte_perm(word, 0x4b000000u, 0x7540 + i));
     x[i] = __fmul_rn(__fsub_rn(v, 8388736.f), step);
   }
+}
+
+// Eight values from column c (a multiple of 8) of a row of blocks as FP32; the row begins on 8 bytes.
+__device__ __forceinline__ void load_int8(const int8_t* q, const uint8_t* exponents, int c,
+                                          float (&x)[8]) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + c));
+  const float step = int8_step(__ldg(exponents + c / kInt8Block));
+  int8_floats(w.x, step, x);
+  int8_floats(w.y, step, x + 4);
 }
 
 }  // namespace rlk

@@ -11,58 +11,86 @@ namespace rlk {
 
 // A block of kRowThreads threads takes `rows()` rows at a time, 1 << shift threads a row (a
 // power of two, so that no index is divided), each eight columns and then the ones 8 << shift
-// further on.
+// further on.  The eight are runs of kRun consecutive columns (element i at column c + at(i)),
+// each run next to the neighbouring lane's, so that a warp's access is one stretch:
+//   8   BF16 or 8-bit results, 16-byte vectors
+//   4   FP32 results, 16-byte vectors (two of a lane side by side would write half sectors:
+//       a 32003 x 2048 table's gradient took 67 us so and takes 40)
+//   1   bases, pitches or widths that rule vectors out: single elements
+// kRun is a constant of each kernel: a branch around every load would keep the loads of
+// several rows from being issued together.
 constexpr int kRowThreads = 256;
+template <int kRun>
 struct RowLanes {
   int shift;
   __host__ __device__ __forceinline__ int rows() const { return kRowThreads >> shift; }
-  __device__ __forceinline__ int row() const { return (int)threadIdx.x >> shift; }
-  __device__ __forceinline__ int col() const { return ((int)threadIdx.x & ((1 << shift) - 1)) * 8; }
   __host__ __device__ __forceinline__ int step() const { return 8 << shift; }
+  __device__ __forceinline__ int row() const { return (int)threadIdx.x >> shift; }
+  // columns from one run of a lane to its next
+  __device__ __forceinline__ int gap() const { return kRun << (shift < 5 ? shift : 5); }
+  __device__ __forceinline__ int col() const {
+    const int l = (int)threadIdx.x & ((1 << shift) - 1);
+    const int in = l & ((1 << (shift < 5 ? shift : 5)) - 1);
+    return 8 * (l - in) + kRun * in;
+  }
 };
-inline RowLanes row_lanes(int64_t cols) {
-  RowLanes l{2};
+template <int kRun>
+inline RowLanes<kRun> row_lanes(int64_t cols, int least_shift = 2) {
+  RowLanes<kRun> l{least_shift};
   while (l.shift < 8 && (int64_t(8) << l.shift) < cols) ++l.shift;
   return l;
 }
-
-// Whether rows of `esize`-byte elements can be read or written eight at a time with 16-byte
-// vectors: base and pitch are multiples of 16 bytes.
-inline bool rows_vec(const void* p, int64_t ld, int64_t esize) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * esize) % 16 == 0;
+// Column offset of element i.
+template <int kRun>
+__device__ __forceinline__ int run_at(int i, int gap) {
+  return i / kRun * gap + i % kRun;
 }
 
-// Elements c .. c + 7 of a row whose first element is element `at` of p; those at or past
-// column n are 0.
-template <bool kFp32>
-__device__ __forceinline__ void load8(const void* p, int64_t at, int c, int n, bool vec,
+// Whether every row of `esize`-byte elements can be accessed in vectors of n: base, pitch and
+// width are whole vectors.
+inline bool rows_vec(const void* p, int64_t ld, int64_t esize, int64_t cols, int64_t n) {
+  return reinterpret_cast<uintptr_t>(p) % (n * esize < 16 ? n * esize : 16) == 0 &&
+         (ld * esize) % (n * esize < 16 ? n * esize : 16) == 0 && cols % n == 0;
+}
+
+// The eight elements from column c on (see RowLanes) of a row whose first element is element `at`
+// of p; those at or past column n are 0.
+template <bool kFp32, int kRun>
+__device__ __forceinline__ void load8(const void* p, int64_t at, int c, int gap, int n,
                                       float (&x)[8]) {
-  if (vec && c + 8 <= n) {
-    if constexpr (kFp32) {
-      const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + c);
-      const float4 a = __ldg(s), b = __ldg(s + 1);
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-      const uint4 a =
-          __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at + c));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
-    return;
-  }
+  for (int q = 0; q < 8 / kRun; ++q) {
+    const int k = c + q * gap;
+    float* y = x + q * kRun;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = 0.f;
-    if (c + i < n) {
+    for (int j = 0; j < kRun; ++j) y[j] = 0.f;
+    if (k >= n) continue;
+    if constexpr (kRun == 1) {
       if constexpr (kFp32)
-        x[i] = __ldg(static_cast<const float*>(p) + at + c + i);
+        y[0] = __ldg(static_cast<const float*>(p) + at + k);
       else
-        x[i] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + at + c + i) << 16);
+        y[0] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + at + k) << 16);
+    } else if constexpr (kFp32) {
+#pragma unroll
+      for (int j = 0; j < kRun; j += 4) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + k + j));
+        y[j] = a.x; y[j + 1] = a.y; y[j + 2] = a.z; y[j + 3] = a.w;
+      }
+    } else {
+      uint32_t w[kRun / 2];
+      const uint16_t* s = static_cast<const uint16_t*>(p) + at + k;
+      if constexpr (kRun == 8) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(s));
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(s));
+        w[0] = a.x; w[1] = a.y;
+      }
+#pragma unroll
+      for (int j = 0; j < kRun / 2; ++j) {
+        y[2 * j] = __uint_as_float(w[j] << 16);
+        y[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
     }
   }
 }
@@ -72,41 +100,99 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Stores x to elements c .. c + 7 of the row (those before column n).
-template <bool kFp32>
-__device__ __forceinline__ void store8(void* p, int64_t at, int c, int n, bool vec,
+// Stores x to the eight columns from c on (those before column n).
+template <bool kFp32, int kRun>
+__device__ __forceinline__ void store8(void* p, int64_t at, int c, int gap, int n,
                                        const float (&x)[8]) {
-  if (vec && c + 8 <= n) {
-    if constexpr (kFp32) {
-      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at + c);
-      d[0] = make_float4(x[0], x[1], x[2], x[3]);
-      d[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at + c) =
-          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                     pack_bf16(x[6], x[7]));
-    }
-    return;
-  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < n) {
+  for (int q = 0; q < 8 / kRun; ++q) {
+    const int k = c + q * gap;
+    const float* y = x + q * kRun;
+    if (k >= n) continue;
+    if constexpr (kRun == 1) {
       if constexpr (kFp32)
-        static_cast<float*>(p)[at + c + i] = x[i];
+        static_cast<float*>(p)[at + k] = y[0];
       else
-        static_cast<__nv_bfloat16*>(p)[at + c + i] = __float2bfloat16_rn(x[i]);
+        static_cast<__nv_bfloat16*>(p)[at + k] = __float2bfloat16_rn(y[0]);
+    } else if constexpr (kFp32) {
+#pragma unroll
+      for (int j = 0; j < kRun; j += 4)
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + at + k + j) =
+            make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+    } else {
+      uint16_t* d = static_cast<uint16_t*>(p) + at + k;
+      if constexpr (kRun == 8)
+        *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                  pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+      else
+        *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
     }
+  }
 }
 
-// f(a, b) with a::value, b::value: whether each dtype is FP32, as constants.
-template <bool kValue>
-struct BoolC {
-  static constexpr bool value = kValue;
+// Eight consecutive columns a lane (c = those of RowLanes<8>, a whole warp on one row) of rows that
+// rule vectors out: the warp reads or writes whole runs of single elements, and the lanes'
+// eights change hands through 1 KB of shared memory a warp.  All lanes take part; `in` says
+// whether the warp's row exists.
+struct RowStage {
+  float* buf;                         // this warp's 256 floats
+  __device__ __forceinline__ explicit RowStage(float (*all)[256]) : buf(all[threadIdx.x >> 5]) {}
+  template <bool kFp32>
+  __device__ __forceinline__ void load(const void* p, int64_t at, int c, int n, bool in,
+                                       float (&x)[8]) const {
+    const int lane = threadIdx.x & 31, c0 = c - 8 * lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = c0 + 32 * i + lane;
+      float v = 0.f;
+      if (in && k < n) {
+        if constexpr (kFp32)
+          v = __ldg(static_cast<const float*>(p) + at + k);
+        else
+          v = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + at + k) << 16);
+      }
+      x[i] = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) buf[32 * i + lane] = x[i];
+    __syncwarp();
+    const float4 a = reinterpret_cast<const float4*>(buf)[2 * lane];
+    const float4 b = reinterpret_cast<const float4*>(buf)[2 * lane + 1];
+    __syncwarp();
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  template <bool kFp32>
+  __device__ __forceinline__ void store(void* p, int64_t at, int c, int n, bool in,
+                                        const float (&x)[8]) const {
+    const int lane = threadIdx.x & 31, c0 = c - 8 * lane;
+    reinterpret_cast<float4*>(buf)[2 * lane] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(buf)[2 * lane + 1] = make_float4(x[4], x[5], x[6], x[7]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = c0 + 32 * i + lane;
+      if (in && k < n) {
+        if constexpr (kFp32)
+          static_cast<float*>(p)[at + k] = buf[32 * i + lane];
+        else
+          static_cast<__nv_bfloat16*>(p)[at + k] = __float2bfloat16_rn(buf[32 * i + lane]);
+      }
+    }
+    __syncwarp();
+  }
+};
+
+// f(d1, d2, run) with ::value: whether each dtype is FP32, and the run length, as constants.
+template <auto kValue>
+struct Const {
+  static constexpr auto value = kValue;
 };
 template <class F>
 inline cudaError_t by_dtypes(int d1, int d2, F f) {
-  if (d1 == RLK_FP32) return d2 == RLK_FP32 ? f(BoolC<true>(), BoolC<true>()) : f(BoolC<true>(), BoolC<false>());
-  return d2 == RLK_FP32 ? f(BoolC<false>(), BoolC<true>()) : f(BoolC<false>(), BoolC<false>());
+  if (d1 == RLK_FP32)
+    return d2 == RLK_FP32 ? f(Const<true>(), Const<true>()) : f(Const<true>(), Const<false>());
+  return d2 == RLK_FP32 ? f(Const<false>(), Const<true>()) : f(Const<false>(), Const<false>());
 }
 
 inline bool known_dtype(int d) { return d == RLK_BF16 || d == RLK_FP32; }
