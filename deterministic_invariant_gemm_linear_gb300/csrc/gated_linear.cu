@@ -34,6 +34,8 @@ __device__ unsigned int g_err_gated_linear = 0;
 namespace {
 
 constexpr int kGateCols = kBN / 2;     // columns of g (and of u) in a 256-wide accumulator
+constexpr int kSlotBytes = 4096;       // a block of 32 x 32 FP32 on its way out (see StoreSlots)
+constexpr int kStoreBytes = 4 * 2 * kSlotBytes;     // the four epilogue warps' two slots each
 
 // ---------------------------------------------------------------- the activation
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -129,6 +131,11 @@ struct GateUpBoth {
     return Layout::desc(base, kstep);
   }
 };
+
+// The 2-SM loop's ring, with room for the epilogue's store slots after it (3 stages of 128 reduction
+// elements, or 6 of 64).
+template <int kK>
+using GatedRing = PairRingT<kHalfRows, kK, kStoreBytes>;
 
 struct GatedSched {
   Banded order;     // rows = blocks of 256 rows (one CTA pair) or the only one of 128, cols = tiles
@@ -266,6 +273,74 @@ inline bool block_vec(const void* base, int64_t ld, int64_t esize) {
   return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (ld * esize) % 16 == 0;
 }
 
+// Blocks of 32 rows and 32 columns on their way out by TMA.  A warp has two slots of 4 KB after the
+// ring's stages; each thread writes its row into one (16-byte pieces swizzled as the tensor map
+// says, so that no two lanes of a phase share a bank), lane 0 starts the copy and the warp goes
+// on; a slot is taken again once its last copy has been read.  The copies write whole rows of
+// 32, 64 or 128 bytes and end at the matrix's last row by themselves.  (Not at its last column: a
+// box that the width cuts is written in units of 16 bytes, so a run of fewer than 32 columns
+// goes out from the threads.)  With stores from
+// the threads, 16 bytes in each of 32 rows an instruction, the epilogue of a tile with FP32
+// projections kept took 9.9 us (4096 rows, K = 64 -> 16384).
+struct StoreSlots {
+  uint32_t base;      // this warp's two slots, or 0 (no slots: stores from the threads)
+  int turn = 0;
+  __device__ __forceinline__ explicit StoreSlots(uint32_t at) : base(at) {}
+  // The next slot, free to be written.
+  __device__ __forceinline__ uint32_t take() {
+    if ((threadIdx.x & 31) == 0)
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    return base + (turn & 1) * kSlotBytes;
+  }
+  // Sends it to columns c .. c + 31 of rows r .. r + 31.
+  __device__ __forceinline__ void send(const CUtensorMap* map, int c, int r) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      asm volatile(
+          "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+              reinterpret_cast<uint64_t>(map)),
+          "r"(base + (turn & 1) * kSlotBytes), "r"(c), "r"(r)
+          : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    ++turn;
+  }
+  // Every copy has been written (before the CTA gives up its shared memory).
+  __device__ __forceinline__ void finish() {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+};
+
+__device__ __forceinline__ void put16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+// Row `lane` of a slot: 32 FP32 patterns, 32 numbers as BF16, or 32 bytes.
+__device__ __forceinline__ void put_fp32(uint32_t slot, const uint32_t (&x)[32]) {
+  const uint32_t r = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    put16(slot + 128 * r + 16 * (i ^ (r & 7)), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+__device__ __forceinline__ void put_bf16(uint32_t slot, const float (&x)[32]) {
+  const uint32_t r = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    put16(slot + 64 * r + 16 * (i ^ (r >> 1 & 3)), pack_bf16(x[8 * i], x[8 * i + 1]),
+          pack_bf16(x[8 * i + 2], x[8 * i + 3]), pack_bf16(x[8 * i + 4], x[8 * i + 5]),
+          pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+}
+__device__ __forceinline__ void put_bytes(uint32_t slot, const uint32_t (&w)[8]) {
+  const uint32_t r = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    put16(slot + 32 * r + 16 * (i ^ (r >> 2 & 1)), w[4 * i], w[4 * i + 1], w[4 * i + 2],
+          w[4 * i + 3]);
+}
+
 // ---------------------------------------------------------------- forward
 struct GatedOut {
   int M, F;
@@ -279,34 +354,62 @@ struct GatedOut {
   int Fp;                // 32 ceil(F / 32)
 };
 
-// One projection's 32 columns from column f of row `row` as they are kept (plane 0: g, 1: u).
-__device__ __forceinline__ void keep_run(const GatedOut& o, int row, int f, int plane,
+// One projection's 32 columns from column f of rows r0 .. r0 + 31 as they are kept (plane 0: g, 1: u).
+template <bool kSlots>
+__device__ __forceinline__ void keep_run(const GatedOut& o, const CUtensorMap* map,
+                                         StoreSlots& slots, int r0, int f, int plane,
                                          const uint32_t (&z)[32]) {
-  if (!RLK_STORE_OK(row < o.M && f + 32 <= o.Fp, &g_err_gated_linear)) return;
+  const int row = r0 + (threadIdx.x & 31);
+  const bool in = row < o.M;
+  if (!RLK_STORE_OK(f + 32 <= o.Fp, &g_err_gated_linear)) return;
   const int64_t at = ((int64_t)row * 2 + plane) * o.Fp + f;
   if (o.keep == RLK_KEEP_FP32) {
-    uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(o.kept) + at);
+    if constexpr (kSlots) {
+      put_fp32(slots.take(), z);
+      slots.send(map, plane * o.Fp + f, r0);
+    } else if (in) {
+      uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(o.kept) + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      d[i] = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+      for (int i = 0; i < 8; ++i)
+        d[i] = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+    }
     return;
   }
-  float most = fabsf(__uint_as_float(z[0]));
+  float m[16];
 #pragma unroll
-  for (int i = 1; i < 32; ++i) most = max_magnitude(most, __uint_as_float(z[i]));
-  const uint32_t e = int8_exponent(most);
+  for (int i = 0; i < 16; ++i)
+    m[i] = max_magnitude(__uint_as_float(z[i]), __uint_as_float(z[i + 16]));
+#pragma unroll
+  for (int s = 8; s >= 1; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < s; ++i) m[i] = max_magnitude(m[i], m[i + s]);
+  const uint32_t e = int8_exponent(m[0]);
   const float inverse = int8_inverse(e);
   uint32_t w[8];
+  const auto words = [&](bool hold) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x[4] = {__uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1]),
-                        __uint_as_float(z[4 * i + 2]), __uint_as_float(z[4 * i + 3])};
-    w[i] = e == 255u ? 0u : int8_word(x, inverse);
+    for (int i = 0; i < 8; ++i) {
+      const float x[4] = {__uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1]),
+                          __uint_as_float(z[4 * i + 2]), __uint_as_float(z[4 * i + 3])};
+      w[i] = int8_word(x, inverse, hold);
+    }
+  };
+  if (int8_holds(m[0], inverse))
+    words(true);
+  else
+    words(false);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (e == 255u) w[i] = 0u;
+  if constexpr (kSlots) {
+    put_bytes(slots.take(), w);
+    slots.send(map, plane * o.Fp + f, r0);
+  } else if (in) {
+    uint4* d = reinterpret_cast<uint4*>(static_cast<int8_t*>(o.kept) + at);
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  uint4* d = reinterpret_cast<uint4*>(static_cast<int8_t*>(o.kept) + at);
-  d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  o.exponents[at / kInt8Block] = (uint8_t)e;
+  if (in) o.exponents[at / kInt8Block] = (uint8_t)e;
 }
 
 template <int kAct>
@@ -318,10 +421,12 @@ __device__ __forceinline__ void value_run(const uint32_t (&g)[32], const uint32_
 }
 
 // A tile's epilogue in one warp: accumulator columns [0, kCols) hold g and [kCols, 2 kCols) u of
-// columns f0 .. f0 + kCols - 1 of the warp's rows r0 .. r0 + 31.
-template <int kCols>
-__device__ __forceinline__ void gated_tile(const GatedOut& o, uint32_t taddr, int r0, int f0) {
-  const int row = r0 + (threadIdx.x & 31);
+// columns f0 .. f0 + kCols - 1 of the warp's rows r0 .. r0 + 31.  kSlots: the warp has store slots.
+template <int kCols, bool kSlots>
+__device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap* tm_h,
+                                           const CUtensorMap* tm_kept, StoreSlots& slots,
+                                           uint32_t taddr, int r0, int f0) {
+  if (r0 >= o.M) return;                    // uniform: depends on the warp's rows only
 #pragma unroll 1
   for (int c = 0; c < kCols / 32; ++c) {
     const int f = f0 + 32 * c;
@@ -338,14 +443,22 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, uint32_t taddr, in
       value_run<RLK_ACT_GELU_TANH>(g, u, h);
     const int n = min(32, o.F - f);
     if (RLK_STORE_OK(f + n <= o.ldh, &g_err_gated_linear)) {
-      if (o.h_fp32)
+      if (kSlots && o.h_vec && n == 32) {
+        const uint32_t slot = slots.take();
+        if (o.h_fp32)
+          put_fp32(slot, reinterpret_cast<const uint32_t(&)[32]>(h));
+        else
+          put_bf16(slot, h);
+        slots.send(tm_h, f, r0);
+      } else if (o.h_fp32) {
         store_block<true>(o.H, o.ldh, r0, o.M, f, n, o.h_vec, h);
-      else
+      } else {
         store_block<false>(o.H, o.ldh, r0, o.M, f, n, o.h_vec, h);
+      }
     }
-    if (o.keep != RLK_KEEP_NONE && row < o.M) {
-      keep_run(o, row, f, 0, g);
-      keep_run(o, row, f, 1, u);
+    if (o.keep != RLK_KEEP_NONE) {
+      keep_run<kSlots>(o, tm_kept, slots, r0, f, 0, g);
+      keep_run<kSlots>(o, tm_kept, slots, r0, f, 1, u);
     }
   }
 }
@@ -353,7 +466,9 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, uint32_t taddr, in
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gated_linear_kernel(const __grid_constant__ CUtensorMap tm_x,
-                        const __grid_constant__ CUtensorMap tm_w, GatedSched sc, GatedOut o) {
+                        const __grid_constant__ CUtensorMap tm_w,
+                        const __grid_constant__ CUtensorMap tm_h,
+                        const __grid_constant__ CUtensorMap tm_kept, GatedSched sc, GatedOut o) {
   extern __shared__ uint8_t smem_raw[];
   const PipeSmem ps = pipe_smem(smem_raw);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -364,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = pipe_setup(ps);
   using TA = OperandTile<false, kHalfRows, kK>;
   using TB = GateUpHalf<kK>;
-  using R = PairRingT<kHalfRows, kK>;
+  using R = GatedRing<kK>;
   if (warp == 0) {
     if (lane == 0)
       producer_role<TA, TB, GatedSched, R>(&tm_x, &tm_w, sc, ps, &g_err_gated_linear);
@@ -378,6 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     const int q = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    StoreSlots slots(R::reserve(ps.stages) + q * 2 * kSlotBytes);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int k = 0;; ++k) {
@@ -386,12 +502,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!epilogue_acquire(ps, acc, acc_phase, &g_err_gated_linear)) break;
       int r0, b0;
       sc.tile_coords(u, 0, r0, b0);
-      gated_tile<kGateCols>(o, tmem + acc * kAccCols + lane_off,
-                            r0 + (int)ps.rank * kHalfRows + q * 32, b0 / 2);
+      gated_tile<kGateCols, true>(o, &tm_h, &tm_kept, slots, tmem + acc * kAccCols + lane_off,
+                                  r0 + (int)ps.rank * kHalfRows + q * 32, b0 / 2);
       epilogue_release(ps, acc);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    slots.finish();
   }
   pipe_teardown(tmem);
 }
@@ -423,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int q = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    StoreSlots slots(0);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int k = 0;; ++k) {
@@ -431,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!epilogue_acquire(ps, acc, acc_phase, &g_err_gated_linear)) break;
       int r0, b0;
       sc.tile_coords(u, 0, r0, b0);
-      if (32 * q < o.M)
-        gated_tile<kCols>(o, tmem + acc * kAccCols + lane_off, q * 32, b0 / 2);
+      gated_tile<kCols, false>(o, nullptr, nullptr, slots, tmem + acc * kAccCols + lane_off, q * 32,
+                               b0 / 2);
       solo_release(ps, acc);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -469,7 +587,9 @@ __device__ __forceinline__ void slope_run(float (&d)[32], const uint32_t (&g)[32
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gated_grad_kernel(const __grid_constant__ CUtensorMap tm_x,
-                      const __grid_constant__ CUtensorMap tm_w, GatedSched sc, GradOut o) {
+                      const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_gate,
+                      const __grid_constant__ CUtensorMap tm_up, GatedSched sc, GradOut o) {
   extern __shared__ uint8_t smem_raw[];
   const PipeSmem ps = pipe_smem(smem_raw);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -480,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = pipe_setup(ps);
   using TA = OperandTile<false, kHalfRows, kK>;
   using TB = GateUpHalf<kK>;
-  using R = PairRingT<kHalfRows, kK>;
+  using R = GatedRing<kK>;
   if (warp == 0) {
     if (lane == 0)
       producer_role<TA, TB, GatedSched, R>(&tm_x, &tm_w, sc, ps, &g_err_gated_linear);
@@ -494,6 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     const int q = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    StoreSlots slots(R::reserve(ps.stages) + q * 2 * kSlotBytes);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int k = 0;; ++k) {
@@ -508,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < kGateCols / 32; ++c) {
         const int f = f0 + 32 * c;
-        if (f >= o.F) break;                    // uniform: depends on the tile only
+        if (f >= o.F || row0 >= o.M) break;     // uniform: depends on the tile and the warp only
         const int n = min(32, o.F - f);
         float d[32], dg[32];
         if (o.dh_fp32)
@@ -525,13 +646,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         else
           slope_run<RLK_ACT_GELU_TANH>(d, g, u, dg);
         if (!RLK_STORE_OK(o.F + f + n <= o.ldG, &g_err_gated_linear)) continue;
-        store_block<false>(o.G, o.ldG, row0, o.M, f, n, true, dg);
-        store_block<false>(o.G + o.F, o.ldG, row0, o.M, f, n, o.up_vec, d);
+        if (n == 32) {
+          put_bf16(slots.take(), dg);
+          slots.send(&tm_gate, f, row0);
+        } else {
+          store_block<false>(o.G, o.ldG, row0, o.M, f, n, true, dg);
+        }
+        if (o.up_vec && n == 32) {
+          put_bf16(slots.take(), d);
+          slots.send(&tm_up, f, row0);
+        } else {
+          store_block<false>(o.G + o.F, o.ldG, row0, o.M, f, n, o.up_vec, d);
+        }
       }
       epilogue_release(ps, acc);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    slots.finish();
   }
   pipe_teardown(tmem);
 }
@@ -606,8 +738,8 @@ cudaError_t ensure_attrs(int dev) {
   std::lock_guard<std::mutex> lock(g_attr_mutex);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (g_attr_set[dev]) return cudaSuccess;
-  constexpr int kDeep = PairRingT<kHalfRows, 64>::kSmemBytes;
-  constexpr int kWide = PairRingT<kHalfRows, 128>::kSmemBytes;
+  constexpr int kDeep = GatedRing<64>::kSmemBytes;
+  constexpr int kWide = GatedRing<128>::kSmemBytes;
   cudaError_t e;
   if ((e = allow_smem(gated_linear_kernel<64>, kDeep)) != cudaSuccess ||
       (e = allow_smem(gated_linear_kernel<128>, kWide)) != cudaSuccess ||
@@ -770,7 +902,6 @@ rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, co
   if (!encode_x(&tm_x, p, in.x, M, K, x_rows) ||
       !encode_w(&tm_w, p, in.w, K, F, kGateCols, solo ? 2 : 1))
     return RLK_ERR_CUDA;
-  if (stage(p, true, true, X, M, K, ldx, W, F, ldw, ws, s) != cudaSuccess) return cuda_failed();
   GatedOut o;
   o.M = (int)M;
   o.F = (int)F;
@@ -783,6 +914,14 @@ rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, co
   o.kept = kept;
   o.exponents = kept_exponents;
   o.Fp = (int)(ceil_div(F, kInt8Block) * kInt8Block);
+  // the maps of what the 2-SM loop stores by TMA (see StoreSlots)
+  CUtensorMap tm_h = {}, tm_kept = {};
+  if (!solo &&
+      ((o.h_vec && !encode_store_2d(&tm_h, H, dtype_bytes(h_dtype), F, M, ldh)) ||
+       (keep != RLK_KEEP_NONE && !encode_store_2d(&tm_kept, kept, keep == RLK_KEEP_FP32 ? 4 : 1,
+                                                  2 * (uint64_t)o.Fp, M, 2 * (uint64_t)o.Fp))))
+    return RLK_ERR_CUDA;
+  if (stage(p, true, true, X, M, K, ldx, W, F, ldw, ws, s) != cudaSuccess) return cuda_failed();
   GatedSched sc;
   cudaError_t e;
   if (solo) {
@@ -804,11 +943,11 @@ rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, co
                    &sc, &grid);
     if (e == cudaSuccess)
       e = stage_k == 128 ? launch_overlapped(gated_linear_kernel<128>, grid, kThreads,
-                                             PairRingT<kHalfRows, 128>::kSmemBytes, s, tm_x, tm_w,
-                                             sc, o)
+                                             GatedRing<128>::kSmemBytes, s, tm_x, tm_w, tm_h,
+                                             tm_kept, sc, o)
                          : launch_overlapped(gated_linear_kernel<64>, grid, kThreads,
-                                             PairRingT<kHalfRows, 64>::kSmemBytes, s, tm_x, tm_w,
-                                             sc, o);
+                                             GatedRing<64>::kSmemBytes, s, tm_x, tm_w, tm_h,
+                                             tm_kept, sc, o);
   }
   return e == cudaSuccess ? RLK_OK : cuda_failed();
 }
@@ -862,9 +1001,13 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
   if (ensure_attrs(dev.device) != cudaSuccess) return cuda_failed();
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Operands in = operands_of(p, X, W, ws);
-  CUtensorMap tm_x, tm_w;
+  uint16_t* G = reinterpret_cast<uint16_t*>(ws);
+  const bool up_vec = block_vec(G + F, p.ldG, 2);
+  CUtensorMap tm_x, tm_w, tm_gate = {}, tm_up = {};
   if (keep == RLK_KEEP_NONE && (!encode_x(&tm_x, p, in.x, M, K, kHalfRows) ||
-                                !encode_w(&tm_w, p, in.w, K, F, kGateCols, 1)))
+                                !encode_w(&tm_w, p, in.w, K, F, kGateCols, 1) ||
+                                !encode_store_2d(&tm_gate, G, 2, F, M, p.ldG) ||
+                                (up_vec && !encode_store_2d(&tm_up, G + F, 2, F, M, p.ldG))))
     return RLK_ERR_CUDA;
   if (stage(p, x_used, w_used, X, M, K, ldx, W, F, ldw, ws, s) != cudaSuccess) return cuda_failed();
 
@@ -876,9 +1019,9 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
   o.lddh = lddh;
   o.dh_fp32 = dh_dtype == RLK_FP32;
   o.dh_vec = block_vec(dH, lddh, dtype_bytes(dh_dtype));
-  o.G = reinterpret_cast<uint16_t*>(ws);
+  o.G = G;
   o.ldG = p.ldG;
-  o.up_vec = block_vec(o.G + F, p.ldG, 2);
+  o.up_vec = up_vec;
   int* counter = reinterpret_cast<int*>(ws + p.off_ctr);
   cudaError_t e;
   if (keep == RLK_KEEP_NONE) {
@@ -888,11 +1031,11 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
     e = pair_sched(M, K, F, stage_k, dev.sm_count / 2, counter, s, &sc, &grid);
     if (e == cudaSuccess)
       e = stage_k == 128 ? launch_overlapped(gated_grad_kernel<128>, grid, kThreads,
-                                             PairRingT<kHalfRows, 128>::kSmemBytes, s, tm_x, tm_w,
-                                             sc, o)
+                                             GatedRing<128>::kSmemBytes, s, tm_x, tm_w, tm_gate,
+                                             tm_up, sc, o)
                          : launch_overlapped(gated_grad_kernel<64>, grid, kThreads,
-                                             PairRingT<kHalfRows, 64>::kSmemBytes, s, tm_x, tm_w,
-                                             sc, o);
+                                             GatedRing<64>::kSmemBytes, s, tm_x, tm_w, tm_gate,
+                                             tm_up, sc, o);
   } else {
     const int Fp = (int)(ceil_div(F, kInt8Block) * kInt8Block);
     const auto launch = [&](auto q8, auto d32, auto v) {

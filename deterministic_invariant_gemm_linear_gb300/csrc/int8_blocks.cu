@@ -56,7 +56,11 @@ __global__ void __launch_bounds__(kRowThreads)
         continue;
       const uint32_t e = int8_exponent(most);
       const float inverse = int8_inverse(e);
-      uint2 w = make_uint2(int8_word(v[k], inverse), int8_word(v[k] + 4, inverse));
+      uint2 w;
+      if (int8_holds(most, inverse))
+        w = make_uint2(int8_word(v[k], inverse, true), int8_word(v[k] + 4, inverse, true));
+      else
+        w = make_uint2(int8_word(v[k], inverse, false), int8_word(v[k] + 4, inverse, false));
       if (e == 255u) w = make_uint2(0u, 0u);
       *reinterpret_cast<uint2*>(q + r * ldq + c) = w;
       if ((c & (kInt8Block - 1)) == 0) exponents[r * lde + c / kInt8Block] = (uint8_t)e;

@@ -32,27 +32,25 @@ __device__ __forceinline__ float int8_inverse(uint32_t e) {
 }
 __device__ __forceinline__ float int8_step(uint32_t e) { return __uint_as_float(e << 23); }
 
-// Four x / step as bytes, rounded to nearest even and held to -127 .. 127.  x / step + 1.5 2^23 is
-// rounded to a whole number by the addition (the product is exact), whose low byte it is: one
-// fused operation where a conversion would run at a quarter of the rate.  |x / step| is below
-// 128, so only +-128 has to be held, which is rare and shows as a byte of 0x80.
-__device__ __forceinline__ uint32_t int8_word(const float* x, float inverse) {
+// Whether a block with this largest magnitude has values that round to +-128, to be held to +-127
+// (|x / step| is below 128, so no others are out of range).  Rare: a call for one branch a block.
+__device__ __forceinline__ bool int8_holds(float most, float inverse) {
+  return __fmul_rn(most, inverse) >= 127.5f;
+}
+
+// Four x / step as bytes, rounded to nearest even, held to -127 .. 127 if `hold`.
+// x / step + 1.5 2^23 is rounded to a whole number by the addition (the product is exact), whose low
+// byte it is: one fused operation where a conversion would run at a quarter of the rate.
+__device__ __forceinline__ uint32_t int8_word(const float* x, float inverse, bool hold) {
   constexpr float kOffset = 12582912.f;
-  float y[4];
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = __fmaf_rn(x[i], inverse, kOffset);
-  const auto bytes = [&]() {
-    return __byte_perm(__byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040),
-                       __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040), 0x5410);
-  };
-  uint32_t w = bytes();
-  const uint32_t t = w ^ 0x80808080u;
-  if ((t - 0x01010101u) & ~t & 0x80808080u) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = fminf(fmaxf(y[i], kOffset - 127.f), kOffset + 127.f);
-    w = bytes();
+  for (int i = 0; i < 4; ++i) {
+    float y = __fmaf_rn(x[i], inverse, kOffset);
+    if (hold) y = fminf(fmaxf(y, kOffset - 127.f), kOffset + 127.f);
+    w[i] = __float_as_uint(y);
   }
-  return w;
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
 
 // Four values of a word as FP32: q + 2^23 + 128 built by bytes (q with its sign bit flipped is

@@ -42,6 +42,12 @@ bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t
                     uint64_t planes, uint64_t ld, uint64_t plane_stride, uint32_t box_inner,
                     uint32_t box_outer, uint32_t box_planes);
 
+// Map of a row-major matrix that epilogues store in boxes of 32 columns and 32 rows, whose box rows
+// (32 elements of esize bytes: 32, 64 or 128) lie swizzled over as many bytes in shared memory.
+// Base on 16 bytes, pitch a multiple of 16 bytes.
+bool encode_store_2d(CUtensorMap* map, void* base, int esize, uint64_t cols, uint64_t rows,
+                     uint64_t ld);
+
 // Launches `kernel` with programmatic stream serialisation: it may begin while
 // the previous kernel in the stream is finishing, and must call griddep_wait()
 // (rlk_device.cuh) before it touches global memory that kernel may use.

@@ -31,8 +31,9 @@ constexpr int kMaxStages = 11;                        // barrier slots; the ring
 // its kBHalf rows of the right-operand tile (half of the tile's 2 kBHalf
 // columns), kK reduction columns each (64: 16 KiB apiece for 256-wide tiles, 7
 // stages; 128: 32 KiB apiece, 3 stages), in two areas: left-operand blocks of all
-// stages first, then the right-operand blocks.
-template <int kBHalf_, int kK_ = kBK>
+// stages first, then the right-operand blocks.  kReserve bytes of shared memory after the
+// stages are left to the epilogue.
+template <int kBHalf_, int kK_ = kBK, int kReserve = 0>
 struct PairRingT {
   static constexpr int kBHalf = kBHalf_;
   static constexpr int kK = kK_;                                    // reduction elements per stage
@@ -40,17 +41,21 @@ struct PairRingT {
   static constexpr int kABytes = kHalfRows * kK * 2;               // 16 or 32 KiB
   static constexpr int kBBytes = kBHalf * kK * 2;                  // 8 - 32 KiB
   static constexpr int kStages =
-      (kSmemLimit - 1024 - kBarrierBlockBytes) / (kABytes + kBBytes) < kMaxStages
-          ? (kSmemLimit - 1024 - kBarrierBlockBytes) / (kABytes + kBBytes)
+      (kSmemLimit - 1024 - kBarrierBlockBytes - kReserve) / (kABytes + kBBytes) < kMaxStages
+          ? (kSmemLimit - 1024 - kBarrierBlockBytes - kReserve) / (kABytes + kBBytes)
           : kMaxStages;                                             // 7
   // Bytes rank 0's full barrier counts per stage (both CTAs' copies).
   static constexpr uint32_t kTxBytes = 2u * (kABytes + kBBytes);
-  static constexpr int kSmemBytes = 1024 + kBarrierBlockBytes + kStages * (kABytes + kBBytes);
+  static constexpr int kSmemBytes =
+      1024 + kBarrierBlockBytes + kStages * (kABytes + kBBytes) + kReserve;
   static __device__ __forceinline__ uint32_t a_stage(uint32_t ring, int s) {
     return ring + s * kABytes;
   }
   static __device__ __forceinline__ uint32_t b_stage(uint32_t ring, int s) {
     return ring + kStages * kABytes + s * kBBytes;
+  }
+  static __device__ __forceinline__ uint32_t reserve(uint32_t ring) {   // 1024-byte aligned
+    return ring + kStages * (kABytes + kBBytes);
   }
   static_assert(kSmemBytes <= kSmemLimit, "exceeds the 227 KiB per-CTA shared memory limit");
   // One CTA per SM: a second resident CTA could not get TMEM columns.
