@@ -248,10 +248,14 @@ def _on(device):
 
 
 def _used_by(stream, tensors):
-    """Marks the memory of CUDA tensors as in use by a stream that it was not allocated on."""
+    """Marks the memory of CUDA tensors (in tuples too) as in use by a stream that it was not
+    allocated on."""
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(stream)
+        if isinstance(t, torch.Tensor):
+            if t.is_cuda:
+                t.record_stream(stream)
+        elif isinstance(t, (tuple, list)):
+            _used_by(stream, t)
 
 
 def _streamed(call):
@@ -287,10 +291,30 @@ def _matrix(t: torch.Tensor, name: str):
     return t, ld if rows > 1 or ld > cols else cols
 
 
+def _in_place(t, ld) -> bool:
+    """Whether the kernels read a BF16 matrix in place (16-byte base, pitch of whole 16 bytes)."""
+    return ld % 8 == 0 and t.data_ptr() % 16 == 0
+
+
 def _require_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("rlk operates on CUDA tensors only (no CPU fallback)")
+
+
+def _one_device(*ts):
+    """Refuses operands that are not CUDA tensors of one device."""
+    at = None
+    for t in ts:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError("rlk operates on CUDA tensors only (no CPU fallback)")
+        if at is None:
+            at = d
+        elif d != at:
+            raise ValueError("the operands of a call must be on one device")
 
 
 _DT = {torch.bfloat16: RLK_BF16, torch.float32: RLK_FP32}
@@ -1228,7 +1252,7 @@ def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, *, ou
     gives a row of zeros.  Forward only: use embedding_trainable for gradients.
     """
     _refuse_grad("embedding", weight)
-    _require_cuda(ids, weight)
+    _one_device(ids, weight)
     if weight.dtype not in _DT:
         raise TypeError("weight must be bfloat16 or float32")
     flat, step, N = _ids(ids)
@@ -1243,7 +1267,7 @@ def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, *, ou
 
 
 def _embedding_backward(grad, ids, V, scale, out, ld_out, accumulate, stream):
-    _require_cuda(grad, ids, out)
+    _one_device(grad, ids, out)
     if grad.dtype not in _DT:
         raise TypeError("grad must be bfloat16 or float32")
     if grad.shape[:-1] != ids.shape:
@@ -1295,7 +1319,7 @@ class _EmbeddingGrad(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, weight, ids, scale):
-        out = embedding(ids, weight.detach(), scale)
+        out = embedding(ids, weight, scale)          # (grad mode is off here)
         ctx.save_for_backward(ids)
         ctx.of = weight.size(0), weight.dtype, scale
         return out
@@ -1325,7 +1349,7 @@ def pack_int8(x: torch.Tensor, *, stream=None):
     floor(log2 max|x|) + 121) and hold x / 2^(e - 127) rounded to whole numbers -127 .. 127; what they
     stand for is exact in bf16.  A block with a NaN or an infinity reads back as NaN.
     """
-    _require_cuda(x)
+    _one_device(x)
     if x.dtype not in _DT:
         raise TypeError("x must be bfloat16 or float32")
     lead, K = x.shape[:-1], x.size(-1)
@@ -1361,7 +1385,7 @@ def _int8_rows(values: torch.Tensor):
 def unpack_int8(values: torch.Tensor, exponents: torch.Tensor, out_dtype=torch.bfloat16, *,
                 stream=None):
     """What pack_int8's blocks stand for: [..., K] in out_dtype (exact in bf16 and fp32)."""
-    _require_cuda(values, exponents)
+    _one_device(values, exponents)
     if values.dtype != torch.int8 or exponents.dtype != torch.uint8:
         raise TypeError("values must be int8 and exponents uint8")
     lead, K = values.shape[:-1], values.size(-1)
@@ -1392,7 +1416,7 @@ class _Gated:
     __slots__ = ("lead", "x", "ldx", "w", "ldw", "act", "M", "K", "F")
 
     def __init__(self, X, W, activation):
-        _require_cuda(X, W)
+        _one_device(X, W)
         if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
             raise TypeError("X and W must be bfloat16")
         if activation not in ACTIVATIONS:
@@ -1451,9 +1475,11 @@ def gated_linear(X: torch.Tensor, W: torch.Tensor, activation: str = "silu", out
             exponents = torch.empty((M, 2, blocks), dtype=torch.uint8, device=dev)
     lib_ = lib()
     with _on(dev):
-        n = lib_.rlk_gated_linear_workspace_size(_ptr(g.x), M, g.K, g.ldx, _ptr(g.w), F, g.ldw)
-        if n == 0:
-            raise RlkError(2, "rlk_gated_linear_workspace_size")
+        n = 256                          # all that operands read in place need
+        if not (_in_place(g.x, g.ldx) and _in_place(g.w, g.ldw)):
+            n = lib_.rlk_gated_linear_workspace_size(_ptr(g.x), M, g.K, g.ldx, _ptr(g.w), F, g.ldw)
+            if n == 0:
+                raise RlkError(2, "rlk_gated_linear_workspace_size")
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         _check(lib_.rlk_gated_linear(
             _ptr(g.x), M, g.K, g.ldx, _ptr(g.w), F, g.ldw, g.act, _ptr(H), _DT[out_dtype], F,
@@ -1479,7 +1505,7 @@ def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
     as the [rows, 2 F] view that the products read.
     """
     g = _Gated(X, W, activation)
-    _require_cuda(dH)
+    _one_device(dH, X)
     if dH.dtype not in _DT:
         raise TypeError("dH must be bfloat16 or float32")
     if dH.shape != (*g.lead, g.F):
@@ -1487,7 +1513,7 @@ def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
     d, ldd = _matrix(_flatten_rows(dH), "dH")
     M, K, F, dev = g.M, g.K, g.F, X.device
     keep, values, exponents = _kept_parts(kept, M, F)
-    _require_cuda(values, exponents)
+    _one_device(X, values, exponents)
     dX = torch.empty((M, K), dtype=out_dtype, device=dev) if grad_x else None
     dW = torch.empty((2 * F, K), dtype=out_dtype, device=dev) if grad_w else None
     lib_ = lib()
@@ -1523,12 +1549,12 @@ class _GatedLinearGrad(torch.autograd.Function):
     def forward(ctx, X, W, activation, checkpoint):
         ctx.of = activation, checkpoint, X.shape
         if checkpoint == "again":
-            H = gated_linear(X.detach(), W.detach(), activation)
+            H = gated_linear(X, W, activation)       # (grad mode is off here)
             ctx.save_for_backward(X, W)
             return H
-        H, kept = gated_linear(X.detach(), W.detach(), activation, keep=checkpoint)
+        H, kept = gated_linear(X, W, activation, keep=checkpoint)
         if checkpoint == "int8":             # X is read for dW alone
-            x = pack_int8(_flatten_rows(X.detach())) if ctx.needs_input_grad[1] else ()
+            x = pack_int8(_flatten_rows(X)) if ctx.needs_input_grad[1] else ()
             ctx.save_for_backward(W, *kept, *x)
         else:
             ctx.save_for_backward(X, W, kept)
@@ -1608,11 +1634,10 @@ class _DetLinearGrad(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, W, out_dtype, int8):
-        with torch.no_grad():
-            Y = det_linear(X.detach(), W.detach(), out_dtype)
-            held = (X,)
-            if int8:                             # X is read for dW alone
-                held = pack_int8(_flatten_rows(X.detach())) if ctx.needs_input_grad[1] else ()
+        Y = det_linear(X, W, out_dtype)              # (grad mode is off here)
+        held = (X,)
+        if int8:                                     # X is read for dW alone
+            held = pack_int8(_flatten_rows(X)) if ctx.needs_input_grad[1] else ()
         ctx.save_for_backward(W, *held)
         ctx.shape = X.shape
         return Y

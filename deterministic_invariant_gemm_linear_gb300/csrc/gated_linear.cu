@@ -734,6 +734,41 @@ cudaError_t allow_smem(Kernel* kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+template <int kARows, int kCols>
+constexpr int solo_smem() {
+  return SoloRing<kARows, 2 * kCols>::kSmemBytes;
+}
+template <int kARows>
+cudaError_t allow_solo() {
+  cudaError_t e = allow_smem(gated_linear_solo_kernel<kARows, 128>, solo_smem<kARows, 128>());
+  if (e == cudaSuccess)
+    e = allow_smem(gated_linear_solo_kernel<kARows, 64>, solo_smem<kARows, 64>());
+  if (e == cudaSuccess)
+    e = allow_smem(gated_linear_solo_kernel<kARows, 32>, solo_smem<kARows, 32>());
+  return e;
+}
+
+// Columns of g a tile of the one-CTA loop: 128, halved while twice the tiles still find an SM each,
+// so that more of them stream the weight and a tile's epilogue, which ends the call, is shorter.
+// Measured (us, 128 / 64 / 32 columns, L2 written over before): 17 x 2048 -> 5461 22.5 / 18.5 / 26.6,
+// 128 x 4096 -> 2000 32.8 / 26.6 / 24.6, 64 x 256 -> 1024 10.2 / 8.2 / 8.2, 1 x 4096 -> 16384 60 / 65 / 80.
+int solo_cols(int64_t F, int64_t sms) {
+  int w = 128;
+  while (w > 32 && 2 * ceil_div(F, w) <= sms) w /= 2;
+  return w;
+}
+
+template <int kARows>
+cudaError_t launch_solo(int w, int grid, cudaStream_t s, const CUtensorMap& x, const CUtensorMap& wm,
+                        const GatedSched& sc, const GatedOut& o) {
+  return w == 128 ? launch_overlapped(gated_linear_solo_kernel<kARows, 128>, grid, kThreads,
+                                      solo_smem<kARows, 128>(), s, x, wm, sc, o)
+         : w == 64 ? launch_overlapped(gated_linear_solo_kernel<kARows, 64>, grid, kThreads,
+                                       solo_smem<kARows, 64>(), s, x, wm, sc, o)
+                   : launch_overlapped(gated_linear_solo_kernel<kARows, 32>, grid, kThreads,
+                                       solo_smem<kARows, 32>(), s, x, wm, sc, o);
+}
+
 cudaError_t ensure_attrs(int dev) {
   std::lock_guard<std::mutex> lock(g_attr_mutex);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -745,10 +780,7 @@ cudaError_t ensure_attrs(int dev) {
       (e = allow_smem(gated_linear_kernel<128>, kWide)) != cudaSuccess ||
       (e = allow_smem(gated_grad_kernel<64>, kDeep)) != cudaSuccess ||
       (e = allow_smem(gated_grad_kernel<128>, kWide)) != cudaSuccess ||
-      (e = allow_smem(gated_linear_solo_kernel<32, 128>, SoloRing<32, 256>::kSmemBytes)) !=
-          cudaSuccess ||
-      (e = allow_smem(gated_linear_solo_kernel<128, 128>, SoloRing<128, 256>::kSmemBytes)) !=
-          cudaSuccess)
+      (e = allow_solo<32>()) != cudaSuccess || (e = allow_solo<128>()) != cudaSuccess)
     return e;
   g_attr_set[dev] = true;
   return cudaSuccess;
@@ -898,9 +930,10 @@ rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, co
   const Operands in = operands_of(p, X, W, ws);
   const bool solo = M <= kHalfRows;
   const int x_rows = M <= 32 ? 32 : kHalfRows;
+  const int cols = solo ? solo_cols(F, dev.sm_count) : kGateCols;      // a tile's, of g
   CUtensorMap tm_x, tm_w;
   if (!encode_x(&tm_x, p, in.x, M, K, x_rows) ||
-      !encode_w(&tm_w, p, in.w, K, F, kGateCols, solo ? 2 : 1))
+      !encode_w(&tm_w, p, in.w, K, F, cols, solo ? 2 : 1))
     return RLK_ERR_CUDA;
   GatedOut o;
   o.M = (int)M;
@@ -926,16 +959,14 @@ rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, co
   cudaError_t e;
   if (solo) {
     sc.order.rows = 1;
-    sc.order.cols = (int)ceil_div(F, kGateCols);
+    sc.order.cols = (int)ceil_div(F, cols);
     sc.order.band = 1;
     sc.counter = nullptr;
     sc.nkb = sc.nkb64 = (int)ceil_div(K, kBK);
-    sc.tile_rows = kBN;
+    sc.tile_rows = 2 * cols;
     const int grid = sc.order.cols < dev.sm_count ? sc.order.cols : dev.sm_count;
-    e = x_rows == 32 ? launch_overlapped(gated_linear_solo_kernel<32, 128>, grid, kThreads,
-                                         SoloRing<32, 256>::kSmemBytes, s, tm_x, tm_w, sc, o)
-                     : launch_overlapped(gated_linear_solo_kernel<128, 128>, grid, kThreads,
-                                         SoloRing<128, 256>::kSmemBytes, s, tm_x, tm_w, sc, o);
+    e = x_rows == 32 ? launch_solo<32>(cols, grid, s, tm_x, tm_w, sc, o)
+                     : launch_solo<128>(cols, grid, s, tm_x, tm_w, sc, o);
   } else {
     const int stage_k = M > kWideStageRows ? 128 : 64;
     int grid;
