@@ -26,6 +26,7 @@
 #include "rlk.h"
 #include "rlk_internal.h"
 #include "rlk_pipeline.cuh"
+#include "rlk_rows.cuh"
 
 namespace rlk {
 
@@ -60,94 +61,69 @@ struct GemmOut {
   int64_t ldc;       // elements
   int fp32;          // 1: FP32 output, 0: BF16
   int accum;         // 1: FP32 C += product (C read once, added after the full reduction)
-  int vec_bytes;     // widest vector store (16, 8 or 4 bytes) the base and pitch allow, or 0
+  int vec_bytes;     // widest vector (16 or 8 bytes) the base and pitch allow, or 0
 };
 
-// The widest vector store width (16, 8 or 4 bytes) that both the output's base
-// address and its row pitch are multiples of (a chunk starts at a column that is
-// a multiple of 32, so at a multiple of 64 bytes within its row), 0 for none.
+// The widest vector width (16 or 8 bytes) that both the output's base address and its row pitch
+// are multiples of (a chunk starts at a column that is a multiple of 32, so at a multiple of 64
+// bytes within its row), 0 for neither.
 inline int store_width(const void* C, int64_t ld, int64_t esize) {
-  for (int w = 16; w >= 4; w /= 2)
+  for (int w = 16; w >= 8; w /= 2)
     if (reinterpret_cast<uintptr_t>(C) % w == 0 && (ld * esize) % w == 0) return w;
   return 0;
 }
 
-__device__ __forceinline__ void store_chunk(const GemmOut& o, int row, int col0,
-                                            const uint32_t (&r)[32]) {
-  // the chunk's 32 columns (clipped to N) lie in row `row` of the M x ldc output
-  if (!RLK_STORE_OK(row >= 0 && row < o.M && col0 >= 0 &&
-                        (int64_t)min(col0 + 32, o.N) <= o.ldc,
-                    &g_err_det_gemm))
-    return;
-  // whole chunks go out as the widest vector stores the output allows (the same
-  // values and roundings as element stores); a row's ragged last chunk element-wise
-  const int w = col0 + 32 <= o.N ? o.vec_bytes : 0;
-  if (o.fp32) {
-    float* dst = static_cast<float*>(o.C) + (int64_t)row * o.ldc + col0;
-    if (o.accum) {
-      if (w == 16) {
+// C += product in the thread's own row: n (at most 32) columns from dst on, `w` bytes at a time.
+__device__ __forceinline__ void accum_chunk(float* dst, int n, int w, const uint32_t (&r)[32]) {
+  if (n == 32 && w == 16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float4 c = reinterpret_cast<const float4*>(dst)[i];
-          c.x = __fadd_rn(c.x, __uint_as_float(r[4 * i]));
-          c.y = __fadd_rn(c.y, __uint_as_float(r[4 * i + 1]));
-          c.z = __fadd_rn(c.z, __uint_as_float(r[4 * i + 2]));
-          c.w = __fadd_rn(c.w, __uint_as_float(r[4 * i + 3]));
-          reinterpret_cast<float4*>(dst)[i] = c;
-        }
-      } else if (w == 8) {
+    for (int i = 0; i < 8; ++i) {
+      float4 c = reinterpret_cast<const float4*>(dst)[i];
+      c.x = __fadd_rn(c.x, __uint_as_float(r[4 * i]));
+      c.y = __fadd_rn(c.y, __uint_as_float(r[4 * i + 1]));
+      c.z = __fadd_rn(c.z, __uint_as_float(r[4 * i + 2]));
+      c.w = __fadd_rn(c.w, __uint_as_float(r[4 * i + 3]));
+      reinterpret_cast<float4*>(dst)[i] = c;
+    }
+  } else if (n == 32 && w == 8) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 c = reinterpret_cast<const float2*>(dst)[i];
-          c.x = __fadd_rn(c.x, __uint_as_float(r[2 * i]));
-          c.y = __fadd_rn(c.y, __uint_as_float(r[2 * i + 1]));
-          reinterpret_cast<float2*>(dst)[i] = c;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (col0 + i < o.N) dst[i] = __fadd_rn(dst[i], __uint_as_float(r[i]));
-      }
-    } else if (w == 16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint4*>(dst)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-    } else if (w == 8) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        reinterpret_cast<uint2*>(dst)[i] = make_uint2(r[2 * i], r[2 * i + 1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col0 + i < o.N) dst[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 16; ++i) {
+      float2 c = reinterpret_cast<const float2*>(dst)[i];
+      c.x = __fadd_rn(c.x, __uint_as_float(r[2 * i]));
+      c.y = __fadd_rn(c.y, __uint_as_float(r[2 * i + 1]));
+      reinterpret_cast<float2*>(dst)[i] = c;
     }
   } else {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.C) + (int64_t)row * o.ldc + col0;
-    if (w != 0) {
-      uint32_t p[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        p[i] = *reinterpret_cast<uint32_t*>(&b);
-      }
-      if (w == 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(dst)[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-      } else if (w == 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<uint2*>(dst)[i] = make_uint2(p[2 * i], p[2 * i + 1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(dst)[i] = p[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col0 + i < o.N) dst[i] = __float2bfloat16_rn(__uint_as_float(r[i]));
-    }
+    for (int i = 0; i < 32; ++i)
+      if (i < n) dst[i] = __fadd_rn(dst[i], __uint_as_float(r[i]));
   }
+}
+
+// The 32 columns from col0 on (clipped to N) of the warp's rows row0 .. row0 + 31.  Whole chunks of
+// a 16-byte aligned output go out as 16-byte vectors from each row's thread; where the base, the
+// pitch or a row's ragged last chunk rules those out, the warp turns the block first and writes
+// whole runs (see store_block; the same values and roundings).  Measured (us, against the widest
+// vectors or elements that the pitch allowed from each row's thread): dB of 255 x 2048 x 10923 39
+// against 223 in BF16, 47 / 156 in FP32; 10922 columns 39 / 86; 3000 x 2500 x 2901 forward 61 / 131,
+// 2900 columns (8-byte vectors before) 61 / 67.
+__device__ __forceinline__ void store_warp(const GemmOut& o, int row0, int col0,
+                                           uint32_t (&r)[32]) {
+  const int n = min(32, o.N - col0);
+  if (!RLK_STORE_OK(row0 >= 0 && col0 >= 0 && (int64_t)col0 + n <= o.ldc, &g_err_det_gemm)) return;
+  if (o.accum) {
+    const int row = row0 + (int)(threadIdx.x & 31);
+    if (row < o.M)
+      accum_chunk(static_cast<float*>(o.C) + (int64_t)row * o.ldc + col0, n, o.vec_bytes, r);
+    return;
+  }
+  float x[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+  if (o.fp32)
+    store_block<true>(o.C, o.ldc, row0, o.M, col0, n, o.vec_bytes == 16, x);
+  else
+    store_block<false>(o.C, o.ldc, row0, o.M, col0, n, o.vec_bytes == 16, x);
 }
 
 // One 256 x kTileN output tile per CTA pair (2-SM loop): rank r stages rows
@@ -191,7 +167,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!epilogue_acquire(ps, acc, acc_phase, &g_err_det_gemm)) break;
       int m0, n0;
       sc.tile_coords(u, 0, m0, n0);
-      const int row = m0 + (int)ps.rank * kHalfRows + q * 32 + lane;
+      const int row0 = m0 + (int)ps.rank * kHalfRows + q * 32;
       const uint32_t taddr = tmem + acc * kAccCols + lane_off;
 #pragma unroll 1
       for (int c = 0; c < kTileN / 32; ++c) {
@@ -201,7 +177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         tmem_ld32(taddr + c * 32, r);
         tmem_wait_ld();
-        if (row < out.M) store_chunk(out, row, col0, r);
+        store_warp(out, row0, col0, r);
       }
       epilogue_release(ps, acc);
       acc ^= 1;
@@ -423,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const GemmOut& out = sc.second(u) ? out2 : out1;
       int m0, n0;
       sc.tile_coords(u, 0, m0, n0);
-      const int row = m0 + (int)ps.rank * kHalfRows + q * 32 + lane;
+      const int row0 = m0 + (int)ps.rank * kHalfRows + q * 32;
       const uint32_t taddr = tmem + acc * kAccCols + lane_off;
 #pragma unroll 1
       for (int c = 0; c < kBN / 32; ++c) {
@@ -433,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         tmem_ld32(taddr + c * 32, r);
         tmem_wait_ld();
-        if (row < out.M) store_chunk(out, row, col0, r);
+        store_warp(out, row0, col0, r);
       }
       epilogue_release(ps, acc);
       acc ^= 1;

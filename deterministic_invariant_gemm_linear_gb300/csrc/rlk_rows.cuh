@@ -130,6 +130,80 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int c, int gap, int 
   }
 }
 
+// ---- blocks of 32 x 32 in a warp's registers ----
+// An epilogue thread holds 32 columns of its own row.  Where a matrix allows 16-byte vectors it
+// writes (or reads) them itself, four neighbouring vectors of one row after another.  Else the
+// warp turns its 32 x 32 block by shuffles, so that a lane holds a column, and each row goes out
+// as one run of 32 elements: with an odd width every thread would write 32 single elements in a
+// row of its own, 32 sectors an instruction in place of two or three (the gated block of 2000 x
+// 2048 -> 5461: 140 us, turned 61, as for 5464).
+
+// Element i of lane l <- element (l mod n) of lane l - l mod n + i, n = 32 or 16.
+template <int n, class T>
+__device__ __forceinline__ void turn_block(T (&x)[n]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = n / 2; s >= 1; s >>= 1) {
+    const bool high = lane & s;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if (i & s) continue;
+      const T got = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i | s], s);
+      if (high)
+        x[i] = got;
+      else
+        x[i | s] = got;
+    }
+  }
+}
+
+// Columns c .. c + n - 1 (n <= 32) of the warp's rows r0 .. r0 + 31 below M; the whole warp takes part,
+// and x, the thread's row, is used up.  vec: whole rows of 32 are 16-byte vectors.  BF16 is turned
+// in pairs, columns i and i + 16 in one register: 32 shuffles in place of 80, and a store then
+// covers half a row of each half of the block.
+template <bool kFp32>
+__device__ __forceinline__ void store_block(void* base, int64_t ld, int r0, int M, int c, int n,
+                                            bool vec, float (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (vec && n == 32) {
+    if (r0 + lane >= M) return;
+    const int64_t at = (int64_t)(r0 + lane) * ld + c;
+    if constexpr (kFp32) {
+      float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+      uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        d[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                          pack_bf16(x[8 * i + 4], x[8 * i + 5]),
+                          pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+    }
+    return;
+  }
+  if constexpr (kFp32) {
+    turn_block(x);
+    float* d = static_cast<float*>(base) + (int64_t)r0 * ld + c + lane;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (r0 + i < M && lane < n) d[i * ld] = x[i];
+  } else {
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = pack_bf16(x[i], x[i + 16]);
+    turn_block(p);
+    const int r = r0 + (lane & 16), col = lane & 15;
+    uint16_t* d = static_cast<uint16_t*>(base) + (int64_t)r * ld + c + col;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (r + i < M && col < n) d[i * ld] = (uint16_t)p[i];
+      if (r + i < M && col + 16 < n) d[i * ld + 16] = (uint16_t)(p[i] >> 16);
+    }
+  }
+}
+
 // Eight consecutive columns a lane (c = those of RowLanes<8>, a whole warp on one row) of rows that
 // rule vectors out: the warp reads or writes whole runs of single elements, and the lanes'
 // eights change hands through 1 KB of shared memory a warp.  All lanes take part; `in` says
