@@ -1505,7 +1505,6 @@ def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
     as the [rows, 2 F] view that the products read.
     """
     g = _Gated(X, W, activation)
-    _one_device(dH, X)
     if dH.dtype not in _DT:
         raise TypeError("dH must be bfloat16 or float32")
     if dH.shape != (*g.lead, g.F):
@@ -1513,15 +1512,18 @@ def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
     d, ldd = _matrix(_flatten_rows(dH), "dH")
     M, K, F, dev = g.M, g.K, g.F, X.device
     keep, values, exponents = _kept_parts(kept, M, F)
-    _one_device(X, values, exponents)
+    _one_device(X, dH, values, exponents)
     dX = torch.empty((M, K), dtype=out_dtype, device=dev) if grad_x else None
     dW = torch.empty((2 * F, K), dtype=out_dtype, device=dev) if grad_w else None
     lib_ = lib()
     dt = _DT[out_dtype]
     with _on(dev):
-        n = lib_.rlk_gated_linear_backward_workspace_size(_ptr(g.x), M, K, g.ldx, _ptr(g.w), F, g.ldw)
-        if n == 0:
-            raise RlkError(2, "rlk_gated_linear_backward_workspace_size")
+        n = -(-(M * (-(-2 * F // 8) * 16)) // 256) * 256 + 256      # G and the unit counter
+        if not (_in_place(g.x, g.ldx) and _in_place(g.w, g.ldw)):
+            n = lib_.rlk_gated_linear_backward_workspace_size(_ptr(g.x), M, K, g.ldx, _ptr(g.w), F,
+                                                              g.ldw)
+            if n == 0:
+                raise RlkError(2, "rlk_gated_linear_backward_workspace_size")
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         _check(lib_.rlk_gated_linear_backward(
             _ptr(d), _DT[d.dtype], M, F, ldd, _ptr(g.x), K, g.ldx, _ptr(g.w), g.ldw, g.act, keep,

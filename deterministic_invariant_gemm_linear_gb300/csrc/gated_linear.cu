@@ -796,6 +796,22 @@ cudaError_t pair_sched(int64_t M, int64_t K, int64_t F, int stage_k, int64_t clu
   return cudaMemsetAsync(counter, 0, sizeof(int), s);
 }
 
+// Both products of a backward in one launch over both tile lists (the same bits), so that the one
+// with the shorter reduction fills the SM pairs that the few tiles of the long one leave idle.  Apart,
+// the long one has narrow tiles, which take 0.69 of a wide tile's time; so one launch pays where
+// the long one's 256 x 256 tiles fill at most half of the pairs and the other product takes
+// about half as long as one of them or more, counting 64-wide reduction blocks and six more for
+// a tile's store.  Measured (us for the whole backward from 8 bits, one launch / two; in brackets that
+// ratio): 255 x 4096 -> 11000 146 / 183 (0.53), 512 x 2048 -> 8192 119 / 106 (0.37), 255 x 2048 -> 5461
+// 90 / 73 (0.26), 1000 x 1024 -> 4096 64 / 54 (0.28).
+bool one_launch(int64_t M, int64_t K, int64_t F, int64_t pairs) {
+  const int64_t red_long = M > 2 * F ? M : 2 * F, red_short = M > 2 * F ? 2 * F : M;
+  const int64_t kb = ceil_div(K, kBN);
+  if (2 * ceil_div(red_short, kPairRows) * kb > pairs) return false;
+  const int64_t short_work = ceil_div(red_long, kPairRows) * kb * (ceil_div(red_short, kBK) + 6);
+  return 100 * short_work > 45 * pairs * ceil_div(red_long, kBK);
+}
+
 bool known_activation(int a) { return a == RLK_ACT_SILU || a == RLK_ACT_GELU_TANH; }
 
 rlk_status check_kept(int keep, const void* kept, const uint8_t* exponents) {
@@ -1014,11 +1030,8 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
   }
   if (e != cudaSuccess) return cuda_failed();
   // The products read G and the (possibly copied) operands, all TMA-ready: the counter is all the
-  // workspace they need, and every argument that they check was checked above.  Both wanted and the
-  // longer reduction's 256 x 256 tiles fill at most half of the SM pairs: one launch over both
-  // products' tiles, the linear-logp backward's rule (the same bits); else det_linear's.
-  const int64_t long_tiles = ceil_div(2 * F >= M ? M : 2 * F, kPairRows) * ceil_div(K, kBN);
-  if (dX && dW && 2 * long_tiles <= dev.sm_count / 2)
+  // workspace they need, and every argument that they check was checked above.
+  if (dX && dW && one_launch(M, K, F, dev.sm_count / 2))
     return launch_fwd_and_db(o.G, M, 2 * F, p.ldG, in.w, K, p.ldw, dX, dx_dtype, lddx, in.x, p.ldx,
                              dW, dw_dtype, lddw, counter, s);
   return rlk_det_linear_backward(o.G, RLK_BF16, M, 2 * F, p.ldG, in.x, K, p.ldx, in.w, p.ldw, dX,

@@ -14,7 +14,8 @@ ACTS = ["silu", "gelu_tanh"]
 # whole reductions and inner widths, fewer columns than a tile and several tiles
 SHAPES = [(1, 1, 1), (1, 64, 128), (2, 8, 31), (17, 65, 33), (31, 200, 300), (32, 128, 129), (33, 63, 127),
           (64, 256, 1024), (127, 100, 40), (128, 72, 257), (129, 64, 128), (200, 1000, 130), (256, 320, 96),
-          (257, 128, 385), (300, 65, 1000), (513, 192, 64)]
+          (257, 128, 385), (300, 65, 1000), (513, 192, 64),
+          (300, 4000, 600)]        # both products of the backward in one launch
 
 
 def operands(M, K, F, seed=0, loud=1.0):
