@@ -1505,6 +1505,8 @@ def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
     as the [rows, 2 F] view that the products read.
     """
     g = _Gated(X, W, activation)
+    if return_grad_projections and not (grad_x or grad_w):
+        raise ValueError("the projections' gradient is formed for dX or dW: ask for one of them")
     if dH.dtype not in _DT:
         raise TypeError("dH must be bfloat16 or float32")
     if dH.shape != (*g.lead, g.F):

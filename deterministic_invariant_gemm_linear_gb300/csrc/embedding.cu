@@ -305,6 +305,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 // ---------------------------------------------------------------- host side
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 constexpr int64_t kMaxTable = int64_t(1) << 30;    // ids of a gradient: a sorting CTA's last + 1 fits an int
+// Every sorting CTA reads all ids: 2^37 reads are about a second.  (2^20 rows of a table of 2^27.)
+constexpr int64_t kMaxSortReads = int64_t(1) << 37;
 
 // Most groups that the ids with more than kGroup of N rows can make: ceil(c / 64) <= 2 c / 65
 // for every c > 64.
@@ -316,7 +318,9 @@ struct EmbedPlan {
 };
 
 bool embed_plan(int64_t N, int64_t V, int64_t H, EmbedPlan* p) {
-  if (N < 0 || N >= kMaxExtent || V < 1 || V >= kMaxTable || H < 1 || H >= kMaxWidth) return false;
+  if (N < 0 || N >= kMaxExtent || V < 1 || V >= kMaxTable || H < 1 || H >= kMaxWidth ||
+      N * ceil_div(V, kSortIds) >= kMaxSortReads)
+    return false;
   p->groups = most_groups(N);
   p->ld_sums = ceil_div(H, 8) * 8;
   size_t off = align_up((size_t)(V + 1) * 4, 256);

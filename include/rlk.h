@@ -634,8 +634,8 @@ RLK_API rlk_status rlk_embedding(const int64_t* ids, int64_t ids_stride, int64_t
  *                (RLK_FP32 only) the sums are added to what is there and rows without any
  *                are left alone.  Must not overlap grad.
  *  workspace     >= rlk_embedding_backward_workspace_size(N, V, H) bytes, 256-byte aligned
- * 0 <= N < 2^31 - 256, 1 <= V < 2^30, 1 <= H < 2^20.  N == 0 writes zeros (accumulate: a
- * no-op).
+ * 0 <= N < 2^31 - 256, 1 <= V < 2^30, N * ceil(V / 1024) < 2^37, 1 <= H < 2^20.  N == 0
+ * writes zeros (accumulate: a no-op).
  */
 #define RLK_EMBED_GROUP 64
 RLK_API size_t rlk_embedding_backward_workspace_size(int64_t N, int64_t V, int64_t H);

@@ -15,7 +15,8 @@ ACTS = ["silu", "gelu_tanh"]
 SHAPES = [(1, 1, 1), (1, 64, 128), (2, 8, 31), (17, 65, 33), (31, 200, 300), (32, 128, 129), (33, 63, 127),
           (64, 256, 1024), (127, 100, 40), (128, 72, 257), (129, 64, 128), (200, 1000, 130), (256, 320, 96),
           (257, 128, 385), (300, 65, 1000), (513, 192, 64),
-          (300, 4000, 600)]        # both products of the backward in one launch
+          (300, 4000, 600),        # both products of the backward in one launch
+          (2600, 64, 7100)]        # tiles handed out from the workspace's counter
 
 
 def operands(M, K, F, seed=0, loud=1.0):
@@ -172,6 +173,13 @@ def test_any_layout(M):
         g3 = rlk.gated_linear_backward(d3, x3, w)
         assert g3[0].shape == x3.shape and bits_equal(g3[0].view(M, K), grads[0]) and bits_equal(g3[1], grads[1])
     assert bits_equal(rlk.gated_linear(x.t().contiguous().t(), w), h)
+    # one row without leading dimensions; a gradient that is one number
+    assert bits_equal(rlk.gated_linear(x[3], w), h[3])
+    alone = rlk.gated_linear_backward(d[3], x[3], w)
+    assert bits_equal(alone[0], grads[0][3]) and alone[1].shape == w.shape
+    ones = rlk.gated_linear_backward(torch.ones_like(d), x, w)
+    same = rlk.gated_linear_backward(torch.ones((), dtype=BF16, device=d.device).expand(M, F), x, w)
+    assert all(bits_equal(a, b) for a, b in zip(ones, same))
 
 
 def test_not_finite_numbers_stay_in_their_rows():
@@ -254,6 +262,8 @@ def test_empty_and_refusals():
                 (kept[0].float(), kept[1])):
         with pytest.raises(ValueError, match="kept"):
             rlk.gated_linear_backward(d, x, w, kept=bad)
+    with pytest.raises(ValueError, match="dX or dW"):
+        rlk.gated_linear_backward(d, x, w, grad_x=False, grad_w=False, return_grad_projections=True)
     with pytest.raises(ValueError, match="checkpoint"):
         rlk.gated_linear_trainable(x, w, checkpoint="bf16")
     with pytest.raises(RuntimeError, match="forward-only"):

@@ -188,9 +188,9 @@ def test_a_call_on_another_stream(name):
     assert rlk.device_error() == 0
 
 
-@pytest.mark.parametrize("M,K,F", [(1, 64, 128), (100, 200, 130), (300, 256, 1000), (2600, 128, 2100)])
+@pytest.mark.parametrize("M,K,F", [(1, 64, 128), (100, 200, 130), (300, 256, 1000), (2600, 64, 7100)])
 def test_captured_and_replayed(M, K, F):
-    """Two graphs of a whole step, replayed in turn with new inputs in their buffers (2600 rows: units
+    """Two graphs of a whole step, replayed in turn with new inputs in their buffers (the largest: tiles
     handed out from the workspace's counter)."""
     dev = cuda_or_skip()
     V = 700
@@ -392,6 +392,29 @@ def test_gated_guard_bands(M, K, F, dtype, wide):
         grads = rlk.gated_linear_backward(d, x, w, kept=parts, out_dtype=dtype)
         assert bits_equal(dx.contiguous(), grads[0]) and bits_equal(dw.contiguous(), grads[1])
         assert untouched(hpad, xpad, wpad)
+
+
+def test_operands_that_a_product_does_not_read_may_be_missing():
+    dev = cuda_or_skip()
+    g = torch.Generator(device=dev).manual_seed(3)
+    M, K, F = 40, 64, 96
+    x = torch.randn(M, K, device=dev, generator=g).bfloat16()
+    w = torch.randn(2 * F, K, device=dev, generator=g).bfloat16()
+    d = torch.randn(M, F, device=dev, generator=g).bfloat16()
+    kept = rlk.gated_linear(x, w, keep="int8")[1]
+    want = rlk.gated_linear_backward(d, x, w, kept=kept)
+    lib, stream = rlk.lib(), rlk._stream_ptr(None)
+    for with_x in (False, True):
+        b = Guarded(dev)
+        px, pw = (x.data_ptr(), None) if with_x else (None, w.data_ptr())
+        size = lib.rlk_gated_linear_backward_workspace_size(px, M, K, K, pw, F, K)
+        ws = b.take(size)
+        out = b.take(2 * (2 * F if with_x else M) * K, BF16, (2 * F if with_x else M, K))
+        dx, dw = (None, out.data_ptr()) if with_x else (out.data_ptr(), None)
+        assert lib.rlk_gated_linear_backward(ptr(d), 0, M, F, F, px, K, K, pw, K, 0, 2, ptr(kept[0]), ptr(kept[1]), dx, 0, K,
+                                             dw, 0, K, ptr(ws), size, stream) == 0
+        b.check()
+        assert bits_equal(out, want[1 if with_x else 0])
 
 
 def test_operands_on_one_device_only():

@@ -45,7 +45,7 @@ EGRAD = dict(ids=P, step=1, N=4, grad=P, gdt=0, H=8, ldg=8, scale=1.0, out=P, od
 
 @pytest.mark.parametrize("change,status", [
     (dict(N=-1), SHAPE), (dict(V=0), SHAPE), (dict(V=1 << 30), SHAPE), (dict(H=0), SHAPE), (dict(step=-1), SHAPE),
-    (dict(ldg=7), SHAPE), (dict(ldo=7), SHAPE), (dict(gdt=2), DTYPE), (dict(odt=2), DTYPE),
+    (dict(N=1 << 21, V=1 << 26), SHAPE), (dict(ldg=7), SHAPE), (dict(ldo=7), SHAPE), (dict(gdt=2), DTYPE), (dict(odt=2), DTYPE),
     (dict(odt=0, acc=1), DTYPE), (dict(scale=INF), VALUE), (dict(ids=None), NULL), (dict(grad=None), NULL),
     (dict(out=None), NULL), (dict(ids=HALF), ALIGN), (dict(grad=ODD), ALIGN), (dict(out=HALF), ALIGN),
     (dict(ws=None), WORKSPACE), (dict(ws=ctypes.c_void_p(0x10010)), WORKSPACE), (dict(n=100), WORKSPACE),
