@@ -287,6 +287,37 @@ def test_second_derivative_is_refused(name):
         grad.float().square().sum().backward()
 
 
+# ------------------------------------------------------------------ cliffs
+def median_us(call, reps=11):
+    times = []
+    for _ in range(3):
+        call()
+    for _ in range(reps):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        torch.cuda._sleep(100_000)            # the host's launches are not what is timed
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return sorted(times)[reps // 2]
+
+
+def test_odd_widths_stay_off_the_cliff():
+    """Ratios of times in one process: an odd width costs at most half as much again as an even one
+    (it took two to five times as much with single elements from each row's thread)."""
+    dev = cuda_or_skip()
+    g = torch.Generator(device=dev).manual_seed(9)
+    times = {}
+    for F in (5464, 5461):
+        x = torch.randn(2000, 2048, device=dev, generator=g).bfloat16()
+        w = torch.randn(2 * F, 2048, device=dev, generator=g).bfloat16()
+        d = torch.randn(2000, F, device=dev, generator=g).bfloat16()
+        times[F] = [median_us(lambda: rlk.gated_linear(x, w)), median_us(lambda: rlk.gated_linear_backward(d, x, w)),
+                    median_us(lambda: rlk.det_gemm_db(x[:255], d[:255])), median_us(lambda: rlk.det_linear(x, w[:F]))]
+    assert all(b <= 1.5 * a for a, b in zip(times[5464], times[5461])), times
+
+
 # ------------------------------------------------------------------ guard bands, through the C ABI
 def ptr(t):
     return None if t is None else t.data_ptr()
