@@ -152,8 +152,9 @@ struct GatedSched {
   }
 };
 
-// A block of 32 x 32 (see store_block) read: x is the thread's row, 0 past column n and past row M.  The turned loads
-// take the block's nearest element where there is none, so that none hangs on a branch.
+// A block of 32 x 32 (see store_block) read: x is the thread's row, 0 past column n and past row M.
+// The turned loads take the block's nearest element where there is none, so that none hangs on a
+// branch (with branches the 32 loads came one after another: G of 2000 x 5461 158 us, without 80).
 template <bool kFp32>
 __device__ __forceinline__ void load_block(const void* base, int64_t ld, int r0, int M, int c,
                                            int n, bool vec, float (&x)[32]) {
@@ -205,9 +206,9 @@ inline bool block_vec(const void* base, int64_t ld, int64_t esize) {
 // on; a slot is taken again once its last copy has been read.  The copies write whole rows of
 // 32, 64 or 128 bytes and end at the matrix's last row by themselves.  (Not at its last column: a
 // box that the width cuts is written in units of 16 bytes, so a run of fewer than 32 columns
-// goes out from the threads.)  With stores from
-// the threads, 16 bytes in each of 32 rows an instruction, the epilogue of a tile with FP32
-// projections kept took 9.9 us (4096 rows, K = 64 -> 16384).
+// goes out from the threads.)  Against stores from the threads, 16 bytes in each of 32 rows an
+// instruction, with FP32 projections kept: 4096 x 64 -> 16384 157 us for 267 (a tile's epilogue 5.8
+// for 9.9), 4096 x 4096 -> 16384 595 for 622.
 struct StoreSlots {
   uint32_t base;      // this warp's two slots, or 0 (no slots: stores from the threads)
   int turn = 0;
@@ -371,10 +372,14 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap*
     if (RLK_STORE_OK(f + n <= o.ldh, &g_err_gated_linear)) {
       if (kSlots && o.h_vec && n == 32) {
         const uint32_t slot = slots.take();
-        if (o.h_fp32)
-          put_fp32(slot, reinterpret_cast<const uint32_t(&)[32]>(h));
-        else
+        if (o.h_fp32) {
+          uint32_t bits[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) bits[i] = __float_as_uint(h[i]);
+          put_fp32(slot, bits);
+        } else {
           put_bf16(slot, h);
+        }
         slots.send(tm_h, f, r0);
       } else if (o.h_fp32) {
         store_block<true>(o.H, o.ldh, r0, o.M, f, n, o.h_vec, h);
@@ -389,6 +394,11 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap*
   }
 }
 
+// More than 128 rows.  Bound by the tensor cores: 4096 x 4096 -> 16384 545 us by itself (2.02 PFLOP/s, 1.05
+// of the measured product; 616 - 640 back to back, at the clock that the power cap leaves), 595
+// with FP32 projections kept, 566 with 8 bits.  The epilogue (3.8 us a tile, 5.8 and 7.0 with them kept)
+// hides behind a tile's MMAs from K of about 900, 1400 and 1700 on; below, it bounds the call: 4096 x 512 ->
+// 16384 118 us, where the products alone are 36.
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gated_linear_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -439,7 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pipe_teardown(tmem);
 }
 
-// At most 128 rows: the weight is streamed once, a CTA to a tile of kCols columns.
+// At most 128 rows: the weight is streamed once, a CTA to a tile of kCols columns (solo_cols).  Bound by
+// HBM: 1 x 4096 -> 16384 43 us a call, 0.92 of the measured copy; with few tiles by a CTA's own stream and
+// what comes before and after it (17 x 2048 -> 5461 17 us with a cold L2, 45 MB).
 template <int kARows, int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
     gated_linear_solo_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -509,7 +521,8 @@ __device__ __forceinline__ void slope_run(float (&d)[32], const uint32_t (&g)[32
   }
 }
 
-// G from projections formed again: the forward's loop, with another epilogue.
+// G from projections formed again: the forward's loop, with another epilogue.  Its 9.8 us a tile (dH is
+// read when its chunk's turn comes) hide behind the MMAs from K of about 2400 on.
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gated_grad_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -594,8 +607,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pipe_teardown(tmem);
 }
 
-// G from kept projections, eight columns a thread: one pass at memory speed.  kVec: dH and both
-// halves of G's rows allow 16-byte vectors; else they pass through shared memory (RowStage).
+// G from kept projections, eight columns a thread: one pass over 14 bytes a column in FP32, 8 in 8 bits,
+// bound by HBM: 4096 x 16384 from FP32 131 - 135 us (7.0 TB/s), 2000 x 5464 from 8 bits 19 - 21.  kVec: dH
+// and both halves of G's rows allow 16-byte vectors; else they pass through shared memory (RowStage):
+// 2000 x 5461 39 us, 50 with single elements for all operands.
 template <bool kInt8, bool kDFp32, int kAct, bool kVec>
 __global__ void __launch_bounds__(kRowThreads)
     gated_grad_kept_kernel(const void* __restrict__ kept, const uint8_t* __restrict__ exponents,
