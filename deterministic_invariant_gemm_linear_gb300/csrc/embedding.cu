@@ -13,9 +13,11 @@
 //    its warps, each over its own stretch of the rows, count its ids and then place their rows
 //    (equal ids of a warp's 32 rows are ranked by match_any).  N ids are read by V / 1024 CTAs
 //    from L2, which for N rows of H elements of d is less than reading d.
-//  * embed_groups_kernel: ids with more than 64 rows (a padding or a common token can have most
-//    of them) are cut into groups of 64 that any CTA can add; their sums wait in the workspace.
-//  * embed_rows_kernel: every table row: zeros, its rows' sum, or its groups' sum.
+//  * embed_rows_kernel: every table row.  Most are zeros; an id of at most 64 rows is summed by the
+//    threads of its table row.  Ids with more (a padding or a common token can have most of the
+//    rows) are cut into groups of 64 for the launch's first blocks; the block that finds all of
+//    an id's groups summed (a count says so, the sums lie in the workspace) adds them, in their
+//    order, and writes the table row.  No block waits for another.
 #include <math.h>
 
 #include <mutex>
@@ -68,12 +70,16 @@ constexpr uint16_t kNoKey = 0xffff;
 inline int sort_smem(int64_t N) { return kSortCounts + (N <= kSortKeys ? 2 * (int)align_up(N, 32) : 0); }
 constexpr int kGroup = RLK_EMBED_GROUP;
 
+// First group of an id with more than kGroup rows, from the place of its first row: c rows make
+// ceil(c / 64) <= 2 c / 65 groups for every c > 64, so no two ids share one, N rows have at most
+// 2 N / 65, and nobody has to count them.
+__host__ __device__ inline int64_t first_group(int64_t place) { return 2 * place / (kGroup + 1); }
+
 struct Order {
   int* start;        // [V + 1]: the rows of id v are rows[start[v] .. start[v + 1] - 1]
   int* rows;         // [N], ascending within an id
-  int* group_base;   // [V]: first group of an id with more than kGroup rows
-  int2* groups;      // {first place in rows, number of rows}
-  int* group_count;
+  int4* groups;      // {first place in rows, number of rows (0: none), first group of the id, id}
+  int* summed;       // [groups, column blocks]: groups summed, counted at an id's first group
   float* sums;       // [groups, ld_sums]
   int64_t ld_sums;
 };
@@ -108,7 +114,7 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 // its keys in shared memory, and two over the 32 warps' counts), 6 for 255 rows.
 __global__ void __launch_bounds__(kSortIds, 1)
     embed_sort_kernel(const int64_t* __restrict__ ids, int64_t ids_stride, int N, int V,
-                      Order o, int max_groups) {
+                      Order o, int max_groups, int col_blocks) {
   extern __shared__ int count[];      // [kSortWarps][kSortIds], then the keys of at most kSortKeys rows
   __shared__ int warp_sums[32];
   __shared__ int2 heavy[kSortIds];    // {id - lo, first group}
@@ -146,11 +152,7 @@ __global__ void __launch_bounds__(kSortIds, 1)
   if (lo + t < V && RLK_STORE_OK(lo + t < V, &g_err_embedding)) {
     o.start[lo + t] = at;
     if (lo + t == V - 1) o.start[V] = at + rows;
-    if (rows > kGroup) {
-      const int base = atomicAdd(o.group_count, (rows + kGroup - 1) / kGroup);
-      o.group_base[lo + t] = base;
-      heavy[atomicAdd(&n_heavy, 1)] = make_int2(t, base);
-    }
+    if (rows > kGroup) heavy[atomicAdd(&n_heavy, 1)] = make_int2(t, (int)first_group(at));
   }
   const int first = at;
 #pragma unroll 8
@@ -183,7 +185,15 @@ __global__ void __launch_bounds__(kSortIds, 1)
     if (own && rank == 0) mine[key] += __popc(same);
     __syncwarp();
   }
-  // the groups of the ids with many rows: `first` of an id is what its thread computed
+  // the groups: those from this CTA's places on are its to clear (the last CTA's reach to the end),
+  // and to fill for its ids with many rows; `first` of an id is what its thread computed
+  const int clear_to =
+      lo + kSortIds >= V ? max_groups : (int)first_group((int64_t)before + total);
+  for (int g = (int)first_group(before) + t; g < clear_to; g += kSortIds)
+    if (RLK_STORE_OK(g < max_groups, &g_err_embedding)) {
+      o.groups[g] = make_int4(0, 0, 0, 0);
+      for (int k = 0; k < col_blocks; ++k) o.summed[(int64_t)g * col_blocks + k] = 0;
+    }
   __syncthreads();
   int* first_of = count;              // reused: every place was taken above
   int* rows_of = count + kSortIds;
@@ -195,7 +205,8 @@ __global__ void __launch_bounds__(kSortIds, 1)
     const int f = first_of[k], n = rows_of[k];
     for (int g = t; g * kGroup < n; g += kSortIds)
       if (RLK_STORE_OK(base + g < max_groups, &g_err_embedding))
-        o.groups[base + g] = make_int2(f + g * kGroup, min(kGroup, n - g * kGroup));
+        o.groups[base + g] =
+            make_int4(f + g * kGroup, min(kGroup, n - g * kGroup), base, lo + k);
   }
 }
 
@@ -228,43 +239,123 @@ __device__ __forceinline__ void add_rows(const void* __restrict__ d, int64_t ldd
   }
 }
 
-// Latency of 64 rows' loads, 16 at a time: some 100 groups of 16384 x 4096 13 us (38 with four at a time).
-template <bool kDFp32, int kRun>
-__global__ void __launch_bounds__(kRowThreads, 2)
-    embed_groups_kernel(const void* __restrict__ d, int64_t ldd, int H, Order o, int max_groups,
-                        RowLanes<kRun> lanes) {
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  const int n = min(*o.group_count, max_groups);
-  const int gap = lanes.gap();
-  for (int g = (int)blockIdx.x * lanes.rows() + lanes.row(); g < n;
-       g += (int)gridDim.x * lanes.rows()) {
-    const int2 what = o.groups[g];
-    for (int c = (int)blockIdx.y * lanes.step() + lanes.col(); c < H;
-         c += (int)gridDim.y * lanes.step()) {
-      float acc[8];
-      add_rows<kDFp32, kRun, kRun == 1 ? 4 : kDFp32 ? 8 : 16>(d, ldd, o.rows, what.x, what.y, c, gap, H, acc);
-      if (RLK_STORE_OK(g < max_groups && min(c + run_at<kRun>(7, gap) + 1, H) <= o.ld_sums, &g_err_embedding))
-        store8<true, kRun>(o.sums, g * o.ld_sums, c, gap, H, acc);
+// Sums of groups, which other blocks of this launch wrote.
+template <int kRun>
+__device__ __forceinline__ void load_sums(const float* s, int c, int gap, int H, float (&x)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8 / kRun; ++q) {
+    const int k = c + q * gap;
+    float* y = x + q * kRun;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) y[j] = 0.f;
+    if (k >= H) continue;
+    if constexpr (kRun == 1) {
+      y[0] = __ldcg(s + k);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRun; j += 4) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(s + k + j));
+        y[j] = a.x; y[j + 1] = a.y; y[j + 2] = a.z; y[j + 3] = a.w;
+      }
+    }
+  }
+}
+
+struct TableOut {
+  void* dw;
+  int64_t ldw;
+  float scale;
+  int H, V;
+};
+
+// A table row's eight columns from their sum.
+template <bool kOutFp32, bool kAccumulate, int kRun>
+__device__ __forceinline__ void write_row(const TableOut& out, int64_t v, int c, int gap,
+                                          float (&acc)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = __fmul_rn(acc[i], out.scale);
+  if (kAccumulate) {
+    const float* p = static_cast<const float*>(out.dw) + v * out.ldw;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + run_at<kRun>(i, gap) < out.H)
+        acc[i] = __fadd_rn(p[c + run_at<kRun>(i, gap)], acc[i]);
+  }
+  if (RLK_STORE_OK(v < out.V && min(c + run_at<kRun>(7, gap) + 1, out.H) <= out.ldw,
+                   &g_err_embedding))
+    store8<kOutFp32, kRun, true>(out.dw, v * out.ldw, c, gap, out.H, acc);
+}
+
+// The groups, by blocks of column steps: block b of group_blocks takes column step b / across and every
+// across-th round of groups, most of them empty.  Latency (64 rows' loads, eight at a time), under the
+// table's zeros.
+template <bool kDFp32, bool kOutFp32, bool kAccumulate, int kRun>
+__device__ __forceinline__ void sum_groups(const void* __restrict__ d, int64_t ldd, const Order& o,
+                                           int max_groups, int across, int col_blocks,
+                                           const TableOut& out, const RowLanes<kRun>& lanes) {
+  __shared__ bool last[kRowThreads / 4];
+  const int gap = lanes.gap(), row = lanes.row();
+  const int by = (int)blockIdx.x / across, bx = (int)blockIdx.x - by * across;
+  const int c = by * lanes.step() + lanes.col();
+  for (int g0 = bx * lanes.rows(); g0 < max_groups; g0 += across * lanes.rows()) {
+    const int g = g0 + row;
+    const int4 what = g < max_groups ? o.groups[g] : make_int4(0, 0, 0, 0);
+    const bool in = what.y > 0;
+    if (!__syncthreads_or(in)) continue;
+    float acc[8];
+    if (in && c < out.H) {
+      add_rows<kDFp32, kRun, kRun == 1 ? 2 : kDFp32 ? 4 : 8>(d, ldd, o.rows, what.x, what.y, c, gap,
+                                                             out.H, acc);
+      if (RLK_STORE_OK(g < max_groups && min(c + run_at<kRun>(7, gap) + 1, out.H) <= o.ld_sums,
+                       &g_err_embedding))
+        store8<true, kRun>(o.sums, g * o.ld_sums, c, gap, out.H, acc);
+    }
+    __threadfence();
+    __syncthreads();
+    int groups = 0;
+    if (in) groups = (o.start[what.w + 1] - o.start[what.w] + kGroup - 1) / kGroup;
+    if (in && lanes.col() == 0)
+      last[row] = atomicAdd(o.summed + (int64_t)what.z * col_blocks + by, 1) == groups - 1;
+    __syncthreads();
+    if (in && last[row] && c < out.H) {
+      __threadfence();
+      const float* s = o.sums + (int64_t)what.z * o.ld_sums;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < groups; ++k) {
+        float x[8];
+        load_sums<kRun>(s + k * o.ld_sums, c, gap, out.H, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], x[i]);
+      }
+      write_row<kOutFp32, kAccumulate, kRun>(out, what.w, c, gap, acc);
     }
   }
 }
 
 // Threads of a row take `turns` (at most kRowsInTurn) consecutive table rows, most of them rows of
 // zeros: how many rows of d each has is read for all of them at once, and the zeros wait for
-// nothing.  Bound by HBM: 151936 x 4096 BF16 from 16384 rows 213 us (1.27 GB, 6.0 TB/s; 377 with a block a
-// row), 32003 x 2048 FP32 40 us (6.6 TB/s).
+// nothing.  Written past the caches (nothing reads a table's gradient soon: 47 against 51 us for a lookup and
+// gradient of 32003 x 2048 FP32).  Bound by HBM: 151936 x 4096 BF16 from 16384 rows 220 us (1.32 GB, 6.0 TB/s;
+// 377 with a block a row, and 13 more for the groups in a launch of their own), that FP32 table 40 (6.6 TB/s).
 constexpr int kRowsInTurn = 16;
 
 template <bool kDFp32, bool kOutFp32, bool kAccumulate, int kRun>
 __global__ void __launch_bounds__(kRowThreads, 4)
-    embed_rows_kernel(const void* __restrict__ d, int64_t ldd, int H, int V, Order o, float scale,
-                      void* __restrict__ dw, int64_t ldw, int turns, RowLanes<kRun> lanes) {
+    embed_rows_kernel(const void* __restrict__ d, int64_t ldd, Order o, int max_groups,
+                      int group_blocks, int across, TableOut out, int turns, RowLanes<kRun> lanes) {
   __shared__ int start[kRowThreads / 4 * kRowsInTurn + 1];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
+  if ((int)blockIdx.x < group_blocks) {
+    sum_groups<kDFp32, kOutFp32, kAccumulate, kRun>(d, ldd, o, max_groups, across,
+                                                    group_blocks / across, out, lanes);
+    return;
+  }
+  const int V = out.V, H = out.H;
   const int per_block = lanes.rows() * turns;
-  const int64_t first = (int64_t)blockIdx.x * per_block;
+  const int64_t first = (int64_t)(blockIdx.x - group_blocks) * per_block;
   for (int i = threadIdx.x; i <= per_block; i += kRowThreads)
     start[i] = __ldg(o.start + (first + i < V ? first + i : V));
   __syncthreads();
@@ -275,36 +366,11 @@ __global__ void __launch_bounds__(kRowThreads, 4)
     const int64_t v = first + mine;
     if (v >= V) break;
     const int at = start[mine], n = start[mine + 1] - at;
-    if (kAccumulate && n == 0) continue;
+    if (n > kGroup || (kAccumulate && n == 0)) continue;
     for (int c = lanes.col(); c < H; c += lanes.step()) {
       float acc[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-      if (n > 0) {
-        if (n <= kGroup) {
-          add_rows<kDFp32, kRun, kRun == 1 ? 2 : 4>(d, ldd, o.rows, at, n, c, gap, H, acc);
-        } else {
-          const int groups = (n + kGroup - 1) / kGroup;
-          const float* s = o.sums + (int64_t)__ldg(o.group_base + v) * o.ld_sums;
-#pragma unroll 4
-          for (int g = 0; g < groups; ++g) {
-            float x[8];
-            load8<true, kRun>(s, g * o.ld_sums, c, gap, H, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], x[i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = __fmul_rn(acc[i], scale);
-      }
-      if (kAccumulate) {
-        const float* p = static_cast<const float*>(dw) + v * ldw;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + run_at<kRun>(i, gap) < H) acc[i] = __fadd_rn(p[c + run_at<kRun>(i, gap)], acc[i]);
-      }
-      if (RLK_STORE_OK(v < V && min(c + run_at<kRun>(7, gap) + 1, H) <= ldw, &g_err_embedding))
-        store8<kOutFp32, kRun>(dw, v * ldw, c, gap, H, acc);
+      add_rows<kDFp32, kRun, kRun == 1 ? 2 : 4>(d, ldd, o.rows, at, n, c, gap, H, acc);
+      write_row<kOutFp32, kAccumulate, kRun>(out, v, c, gap, acc);
     }
   }
 }
@@ -315,30 +381,27 @@ constexpr int64_t kMaxTable = int64_t(1) << 30;    // ids of a gradient: a sorti
 // Every sorting CTA reads all ids: 2^37 reads are about a second.  (2^20 rows of a table of 2^27.)
 constexpr int64_t kMaxSortReads = int64_t(1) << 37;
 
-// Most groups that the ids with more than kGroup of N rows can make: ceil(c / 64) <= 2 c / 65
-// for every c > 64.
-inline int64_t most_groups(int64_t N) { return 2 * N / (kGroup + 1); }
-
 struct EmbedPlan {
   int64_t groups = 0, ld_sums = 0;
-  size_t off_base = 0, off_rows = 0, off_groups = 0, off_count = 0, off_sums = 0, total = 0;
+  size_t off_rows = 0, off_groups = 0, off_summed = 0, off_sums = 0, total = 0;
 };
+
+// Column steps of a pass: at most 256 threads of eight columns a row (at least four threads).
+inline int64_t column_steps(int64_t H) { return ceil_div(H, 8 * kRowThreads); }
 
 bool embed_plan(int64_t N, int64_t V, int64_t H, EmbedPlan* p) {
   if (N < 0 || N >= kMaxExtent || V < 1 || V >= kMaxTable || H < 1 || H >= kMaxWidth ||
       N * ceil_div(V, kSortIds) >= kMaxSortReads)
     return false;
-  p->groups = most_groups(N);
+  p->groups = first_group(N);
   p->ld_sums = ceil_div(H, 8) * 8;
   size_t off = align_up((size_t)(V + 1) * 4, 256);
-  p->off_base = off;
-  off = align_up(off + (size_t)V * 4, 256);
   p->off_rows = off;
   off = align_up(off + (size_t)N * 4, 256);
   p->off_groups = off;
-  off = align_up(off + (size_t)p->groups * 8, 256);
-  p->off_count = off;
-  off += 256;
+  off = align_up(off + (size_t)p->groups * 16, 256);
+  p->off_summed = off;
+  off = align_up(off + (size_t)p->groups * column_steps(H) * 4, 256);
   p->off_sums = off;
   p->total = align_up(off + (size_t)p->groups * p->ld_sums * 4, 256);
   return true;
@@ -469,18 +532,14 @@ rlk_status rlk_embedding_backward(const int64_t* ids, int64_t ids_stride, int64_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Order o;
   o.start = reinterpret_cast<int*>(ws);
-  o.group_base = reinterpret_cast<int*>(ws + p.off_base);
   o.rows = reinterpret_cast<int*>(ws + p.off_rows);
-  o.groups = reinterpret_cast<int2*>(ws + p.off_groups);
-  o.group_count = reinterpret_cast<int*>(ws + p.off_count);
+  o.groups = reinterpret_cast<int4*>(ws + p.off_groups);
+  o.summed = reinterpret_cast<int*>(ws + p.off_summed);
   o.sums = reinterpret_cast<float*>(ws + p.off_sums);
   o.ld_sums = p.ld_sums;
-  const bool heavy = N > kGroup;       // fewer rows cannot make an id of many
-  if (heavy && cudaMemsetAsync(o.group_count, 0, sizeof(int), s) != cudaSuccess)
-    return cuda_failed();
   if (launch_overlapped(embed_sort_kernel, dim3((unsigned)ceil_div(V, kSortIds)), kSortIds,
                         sort_smem(N), s, ids, ids_stride, (int)N, (int)V, o,
-                        (int)p.groups) != cudaSuccess)
+                        (int)p.groups, (int)column_steps(H)) != cudaSuccess)
     return cuda_failed();
   const int run = embed_run(H, grad, grad_dtype, ld_grad, grad_weight, grad_weight_dtype,
                             ld_grad_weight);
@@ -489,29 +548,25 @@ rlk_status rlk_embedding_backward(const int64_t* ids, int64_t ids_stride, int64_
       constexpr bool kD = decltype(d32)::value, kO = decltype(o32)::value;
       constexpr int kRun = decltype(r)::value;
       const RowLanes<kRun> lanes = row_lanes<kRun>(H);
-      if (heavy) {
-        // groups by columns: four blocks an SM, or all there can be
-        const int64_t col_blocks = ceil_div(H, lanes.step());
-        int64_t gx = ceil_div(4 * (int64_t)dev.sm_count, col_blocks);
-        const int64_t all = ceil_div(p.groups, lanes.rows());
-        gx = gx < all ? gx : all;
-        const cudaError_t err = launch_overlapped(
-            embed_groups_kernel<kD, kRun>, dim3((unsigned)(gx < 1 ? 1 : gx), (unsigned)col_blocks),
-            kRowThreads, 0, s, grad, ld_grad, (int)H, o, (int)p.groups, lanes);
-        if (err != cudaSuccess) return err;
-      }
+      // the groups' blocks: four an SM, or all there can be
+      const int64_t col_blocks = ceil_div(H, lanes.step());     // column_steps(H)
+      int64_t across = ceil_div(4 * (int64_t)dev.sm_count, col_blocks);
+      const int64_t all = N > kGroup ? ceil_div(p.groups, lanes.rows()) : 0;
+      if (across > all) across = all;
       // 16 table rows in turn a row of threads, fewer where that leaves under 16 blocks an SM
       int turns = kRowsInTurn;
       while (turns > 1 && ceil_div(V, lanes.rows() * turns) < 16 * dev.sm_count) turns /= 2;
-      const dim3 grid((unsigned)ceil_div(V, lanes.rows() * turns));
+      const int64_t group_blocks = across * col_blocks;
+      const dim3 grid((unsigned)(group_blocks + ceil_div(V, lanes.rows() * turns)));
+      const TableOut out = {grad_weight, ld_grad_weight, scale, (int)H, (int)V};
       if constexpr (kO)
         if (accumulate)
           return launch_overlapped(embed_rows_kernel<kD, true, true, kRun>, grid, kRowThreads, 0, s,
-                                   grad, ld_grad, (int)H, (int)V, o, scale, grad_weight,
-                                   ld_grad_weight, turns, lanes);
+                                   grad, ld_grad, o, (int)p.groups, (int)group_blocks, (int)across,
+                                   out, turns, lanes);
       return launch_overlapped(embed_rows_kernel<kD, kO, false, kRun>, grid, kRowThreads, 0, s,
-                               grad, ld_grad, (int)H, (int)V, o, scale, grad_weight,
-                               ld_grad_weight, turns, lanes);
+                               grad, ld_grad, o, (int)p.groups, (int)group_blocks, (int)across, out,
+                               turns, lanes);
     });
   });
   return e == cudaSuccess ? RLK_OK : cuda_failed();

@@ -16,7 +16,8 @@ __device__ unsigned int g_err_int8 = 0;
 
 namespace {
 
-// kRowsAThread rows a thread, their loads issued together.  Rows that rule vectors out (kVec false)
+// kRowsAThread rows a thread, their loads issued together (16384 x 4096 BF16, us with 1, 2, 3 and 4: packing
+// 41.6, 37.1, 35.7, 42.3, unpacking 41.1, 36.1, 44.6, 50.1).  Rows that rule vectors out (kVec false)
 // pass through shared memory (RowStage).  Packing is bound by instructions as much as by HBM.
 constexpr int kRowsAThread = 2;
 

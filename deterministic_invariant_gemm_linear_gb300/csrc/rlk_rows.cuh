@@ -100,8 +100,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Stores x to the eight columns from c on (those before column n).
-template <bool kFp32, int kRun>
+template <bool kStream, class T>
+__device__ __forceinline__ void put(T* p, T v) {
+  if constexpr (kStream)
+    __stcs(p, v);
+  else
+    *p = v;
+}
+
+// Stores x to the eight columns from c on (those before column n).  kStream: nothing reads them soon.
+template <bool kFp32, int kRun, bool kStream = false>
 __device__ __forceinline__ void store8(void* p, int64_t at, int c, int gap, int n,
                                        const float (&x)[8]) {
 #pragma unroll
@@ -117,15 +125,17 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int c, int gap, int 
     } else if constexpr (kFp32) {
 #pragma unroll
       for (int j = 0; j < kRun; j += 4)
-        *reinterpret_cast<float4*>(static_cast<float*>(p) + at + k + j) =
-            make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        put<kStream>(reinterpret_cast<float4*>(static_cast<float*>(p) + at + k + j),
+                     make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]));
     } else {
       uint16_t* d = static_cast<uint16_t*>(p) + at + k;
       if constexpr (kRun == 8)
-        *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                                  pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        put<kStream>(reinterpret_cast<uint4*>(d),
+                     make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])));
       else
-        *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+        put<kStream>(reinterpret_cast<uint2*>(d),
+                     make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])));
     }
   }
 }

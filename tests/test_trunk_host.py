@@ -56,14 +56,22 @@ def test_embedding_backward(lib, change, status):
 
 def test_embedding_workspace(lib):
     size = lib.rlk_embedding_backward_workspace_size
-    # offsets, first groups, rows, groups and their sums: an id of c > 64 rows makes ceil(c / 64)
+    # offsets, rows, groups, counts of them, their sums: an id of c > 64 rows makes ceil(c / 64)
     for N, V, H in ((1, 1, 1), (64, 10, 8), (65, 10, 9), (16384, 151936, 4096)):
         groups = 2 * N // 65
-        assert size(N, V, H) == up(4 * (V + 1)) + up(4 * V) + up(4 * N) + up(8 * groups) + 256 + \
-            up(groups * up(H, 8) * 4)
+        assert size(N, V, H) == up(4 * (V + 1)) + up(4 * N) + up(16 * groups) + \
+            up(groups * -(-H // 2048) * 4) + up(groups * up(H, 8) * 4)
         worst = max((N // c) * -(-c // 64) for c in range(65, min(N, 400) + 1)) if N > 64 else 0
         assert worst <= groups
     assert size(-1, 10, 8) == 0 and size(4, 0, 8) == 0 and size(4, 10, 0) == 0 and size(4, 1 << 30, 8) == 0
+
+
+def test_first_groups_leave_room():
+    """An id of c > 64 rows from place p on has its ceil(c / 64) groups from 2 p // 65 on: before the
+    next id's, whatever p."""
+    for c in list(range(65, 2000)) + [10 ** 4, 10 ** 5 + 1, 2 ** 20, 2 ** 30 + 7]:
+        for p in (0, 1, 31, 32, 33, 64, 65, 1000, 2 ** 30):
+            assert 2 * p // 65 + -(-c // 64) <= 2 * (p + c) // 65
 
 
 PACK = dict(x=P, dt=0, rows=4, cols=40, ldx=40, q=P, ldq=64, e=P, lde=2, stream=None)
