@@ -105,8 +105,8 @@ __device__ __forceinline__ void accum_chunk(float* dst, int n, int w, const uint
 // pitch or a row's ragged last chunk rules those out, the warp turns the block first and writes
 // whole runs (see store_block; the same values and roundings).  Measured (us, against the widest
 // vectors or elements that the pitch allowed from each row's thread): dB of 255 x 2048 x 10923 39
-// against 223 in BF16, 47 / 156 in FP32; 10922 columns 39 / 86; 3000 x 2500 x 2901 forward 61 / 131,
-// 2900 columns (8-byte vectors before) 61 / 67.
+// against 223 in BF16, 47 / 156 in FP32; 10922 columns 39 / 86; 3000 x 2500 x 2901 forward 61 /
+// 131, 2900 columns (8-byte vectors before) 61 / 67.
 __device__ __forceinline__ void store_warp(const GemmOut& o, int row0, int col0,
                                            uint32_t (&r)[32]) {
   const int n = min(32, o.N - col0);

@@ -33,8 +33,8 @@ __device__ unsigned int g_err_embedding = 0;
 namespace {
 
 // ---------------------------------------------------------------- lookup
-// A row to the threads of row_lanes, each thread's loads of a row before its stores.  16384 x 5120 BF16: 41 us,
-// 335 MB moved of which common rows come from L2; one row 3.5 us, all of it latency.
+// A row to the threads of row_lanes, each thread's loads of a row before its stores.  16384 x 5120
+// BF16: 41 us, 335 MB moved of which common rows come from L2; one row 3.5 us, all of it latency.
 template <bool kWFp32, bool kOutFp32, int kRun>
 __global__ void __launch_bounds__(kRowThreads)
     embed_kernel(const int64_t* __restrict__ ids, int64_t ids_stride, int64_t N,
@@ -65,9 +65,12 @@ __global__ void __launch_bounds__(kRowThreads)
 constexpr int kSortIds = 1024;        // ids a CTA owns, one a thread
 constexpr int kSortWarps = kSortIds / 32;
 constexpr int kSortCounts = kSortWarps * kSortIds * 4;  // bytes: a count for each warp and id
-constexpr int kSortKeys = 32768;      // rows whose id - lo (kNoKey: another CTA's) waits in shared memory
+// rows whose id - lo (kNoKey: another CTA's) waits in shared memory
+constexpr int kSortKeys = 32768;
 constexpr uint16_t kNoKey = 0xffff;
-inline int sort_smem(int64_t N) { return kSortCounts + (N <= kSortKeys ? 2 * (int)align_up(N, 32) : 0); }
+inline int sort_smem(int64_t N) {
+  return kSortCounts + (N <= kSortKeys ? 2 * (int)align_up(N, 32) : 0);
+}
 constexpr int kGroup = RLK_EMBED_GROUP;
 
 // First group of an id with more than kGroup rows, from the place of its first row: c rows make
@@ -115,7 +118,7 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 __global__ void __launch_bounds__(kSortIds, 1)
     embed_sort_kernel(const int64_t* __restrict__ ids, int64_t ids_stride, int N, int V,
                       Order o, int max_groups, int col_blocks) {
-  extern __shared__ int count[];      // [kSortWarps][kSortIds], then the keys of at most kSortKeys rows
+  extern __shared__ int count[];      // [kSortWarps][kSortIds], then the keys of kSortKeys rows
   __shared__ int warp_sums[32];
   __shared__ int2 heavy[kSortIds];    // {id - lo, first group}
   __shared__ int n_heavy;
@@ -286,9 +289,9 @@ __device__ __forceinline__ void write_row(const TableOut& out, int64_t v, int c,
     store8<kOutFp32, kRun, true>(out.dw, v * out.ldw, c, gap, out.H, acc);
 }
 
-// The groups, by blocks of column steps: block b of group_blocks takes column step b / across and every
-// across-th round of groups, most of them empty.  Latency (64 rows' loads, eight at a time), under the
-// table's zeros.
+// The groups, by blocks of column steps: block b of group_blocks takes column step b / across and
+// every across-th round of groups, most of them empty.  Latency (64 rows' loads, eight at a time),
+// under the table's zeros.
 template <bool kDFp32, bool kOutFp32, bool kAccumulate, int kRun>
 __device__ __forceinline__ void sum_groups(const void* __restrict__ d, int64_t ldd, const Order& o,
                                            int max_groups, int across, int col_blocks,
@@ -336,9 +339,10 @@ __device__ __forceinline__ void sum_groups(const void* __restrict__ d, int64_t l
 
 // Threads of a row take `turns` (at most kRowsInTurn) consecutive table rows, most of them rows of
 // zeros: how many rows of d each has is read for all of them at once, and the zeros wait for
-// nothing.  Written past the caches (nothing reads a table's gradient soon: 47 against 51 us for a lookup and
-// gradient of 32003 x 2048 FP32).  Bound by HBM: 151936 x 4096 BF16 from 16384 rows 220 us (1.32 GB, 6.0 TB/s;
-// 377 with a block a row, and 13 more for the groups in a launch of their own), that FP32 table 40 (6.6 TB/s).
+// nothing.  Written past the caches (nothing reads a table's gradient soon: 47 against 51 us for a
+// lookup and gradient of 32003 x 2048 FP32).  Bound by HBM: 151936 x 4096 BF16 from 16384 rows 220
+// us (1.32 GB, 6.0 TB/s; 377 with a block a row, and 13 more for the groups in a launch of their
+// own), that FP32 table 40 (6.6 TB/s).
 constexpr int kRowsInTurn = 16;
 
 template <bool kDFp32, bool kOutFp32, bool kAccumulate, int kRun>
@@ -377,7 +381,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 
 // ---------------------------------------------------------------- host side
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
-constexpr int64_t kMaxTable = int64_t(1) << 30;    // ids of a gradient: a sorting CTA's last + 1 fits an int
+// ids of a gradient: a sorting CTA's last + 1 fits an int
+constexpr int64_t kMaxTable = int64_t(1) << 30;
 // Every sorting CTA reads all ids: 2^37 reads are about a second.  (2^20 rows of a table of 2^27.)
 constexpr int64_t kMaxSortReads = int64_t(1) << 37;
 
@@ -466,8 +471,8 @@ rlk_status rlk_embedding(const int64_t* ids, int64_t ids_stride, int64_t N, cons
   RLK_CALL_RANGE();
   if (!known_dtype(weight_dtype) || !known_dtype(out_dtype)) return RLK_ERR_DTYPE;
   if (N < 0 || N >= kMaxExtent || V < 1 || V >= kMaxExtent || H < 1 || H >= kMaxWidth ||
-      ids_stride < 0 || ids_stride >= kPitchLimit || ld_weight < H || ld_weight >= kPitchLimit || ld_out < H ||
-      ld_out >= kPitchLimit)
+      ids_stride < 0 || ids_stride >= kPitchLimit || ld_weight < H || ld_weight >= kPitchLimit ||
+      ld_out < H || ld_out >= kPitchLimit)
     return RLK_ERR_SHAPE;
   if (!isfinite(scale)) return RLK_ERR_VALUE;
   if (N == 0) return RLK_OK;
@@ -508,8 +513,8 @@ rlk_status rlk_embedding_backward(const int64_t* ids, int64_t ids_stride, int64_
       (accumulate && grad_weight_dtype != RLK_FP32))
     return RLK_ERR_DTYPE;
   EmbedPlan p;
-  if (!embed_plan(N, V, H, &p) || ids_stride < 0 || ids_stride >= kPitchLimit || ld_grad < H || ld_grad >= kPitchLimit ||
-      ld_grad_weight < H || ld_grad_weight >= kPitchLimit)
+  if (!embed_plan(N, V, H, &p) || ids_stride < 0 || ids_stride >= kPitchLimit || ld_grad < H ||
+      ld_grad >= kPitchLimit || ld_grad_weight < H || ld_grad_weight >= kPitchLimit)
     return RLK_ERR_SHAPE;
   if (!isfinite(scale)) return RLK_ERR_VALUE;
   if (N == 0 && accumulate) return RLK_OK;

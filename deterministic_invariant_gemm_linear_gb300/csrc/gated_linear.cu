@@ -132,8 +132,8 @@ struct GateUpBoth {
   }
 };
 
-// The 2-SM loop's ring, with room for the epilogue's store slots after it (3 stages of 128 reduction
-// elements, or 6 of 64).
+// The 2-SM loop's ring, with room for the epilogue's store slots after it (3 stages of 128
+// reduction elements, or 6 of 64).
 template <int kK>
 using GatedRing = PairRingT<kHalfRows, kK, kStoreBytes>;
 
@@ -281,7 +281,7 @@ struct GatedOut {
   int Fp;                // 32 ceil(F / 32)
 };
 
-// One projection's 32 columns from column f of rows r0 .. r0 + 31 as they are kept (plane 0: g, 1: u).
+// One projection's 32 columns from column f of rows r0 .. r0 + 31, kept (plane 0: g, 1: u).
 template <bool kSlots>
 __device__ __forceinline__ void keep_run(const GatedOut& o, const CUtensorMap* map,
                                          StoreSlots& slots, int r0, int f, int plane,
@@ -394,11 +394,11 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap*
   }
 }
 
-// More than 128 rows.  Bound by the tensor cores: 4096 x 4096 -> 16384 545 us by itself (2.02 PFLOP/s, 1.05
-// of the measured product; 616 - 640 back to back, at the clock that the power cap leaves), 595
-// with FP32 projections kept, 566 with 8 bits.  The epilogue (3.8 us a tile, 5.8 and 7.0 with them kept)
-// hides behind a tile's MMAs from K of about 900, 1400 and 1700 on; below, it bounds the call: 4096 x 512 ->
-// 16384 118 us, where the products alone are 36.
+// More than 128 rows.  Bound by the tensor cores: 4096 x 4096 -> 16384 545 us by itself (2.02
+// PFLOP/s, 1.05 of the measured product; 616 - 640 back to back, at the clock that the power cap
+// leaves), 595 with FP32 projections kept, 566 with 8 bits.  The epilogue (3.8 us a tile, 5.8 and
+// 7.0 with them kept) hides behind a tile's MMAs from K of about 900, 1400 and 1700 on; below, it
+// bounds the call: 4096 x 512 -> 16384 118 us, where the products alone are 36.
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gated_linear_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -449,9 +449,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pipe_teardown(tmem);
 }
 
-// At most 128 rows: the weight is streamed once, a CTA to a tile of kCols columns (solo_cols).  Bound by
-// HBM: 1 x 4096 -> 16384 43 us a call, 0.92 of the measured copy; with few tiles by a CTA's own stream and
-// what comes before and after it (17 x 2048 -> 5461 17 us with a cold L2, 45 MB).
+// At most 128 rows: the weight is streamed once, a CTA to a tile of kCols columns (solo_cols).
+// Bound by HBM: 1 x 4096 -> 16384 43 us a call, 0.92 of the measured copy; with few tiles by a
+// CTA's own stream and what comes before and after it (17 x 2048 -> 5461 17 us with a cold L2, 45
+// MB).
 template <int kARows, int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
     gated_linear_solo_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -521,8 +522,8 @@ __device__ __forceinline__ void slope_run(float (&d)[32], const uint32_t (&g)[32
   }
 }
 
-// G from projections formed again: the forward's loop, with another epilogue.  Its 9.8 us a tile (dH is
-// read when its chunk's turn comes) hide behind the MMAs from K of about 2400 on.
+// G from projections formed again: the forward's loop, with another epilogue.  Its 9.8 us a tile
+// (dH is read when its chunk's turn comes) hide behind the MMAs from K of about 2400 on.
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gated_grad_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -607,10 +608,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pipe_teardown(tmem);
 }
 
-// G from kept projections, eight columns a thread: one pass over 14 bytes a column in FP32, 8 in 8 bits,
-// bound by HBM: 4096 x 16384 from FP32 131 - 135 us (7.0 TB/s), 2000 x 5464 from 8 bits 19 - 21.  kVec: dH
-// and both halves of G's rows allow 16-byte vectors; else they pass through shared memory (RowStage):
-// 2000 x 5461 39 us, 50 with single elements for all operands.
+// G from kept projections, eight columns a thread: one pass over 14 bytes a column in FP32, 8 in 8
+// bits, bound by HBM: 4096 x 16384 from FP32 131 - 135 us (7.0 TB/s), 2000 x 5464 from 8 bits 19 -
+// 21.  kVec: dH and both halves of G's rows allow 16-byte vectors; else they pass through shared
+// memory (RowStage): 2000 x 5461 39 us, 50 with single elements for all operands.
 template <bool kInt8, bool kDFp32, int kAct, bool kVec>
 __global__ void __launch_bounds__(kRowThreads)
     gated_grad_kept_kernel(const void* __restrict__ kept, const uint8_t* __restrict__ exponents,
@@ -691,8 +692,9 @@ cudaError_t allow_solo() {
 
 // Columns of g a tile of the one-CTA loop: 128, halved while twice the tiles still find an SM each,
 // so that more of them stream the weight and a tile's epilogue, which ends the call, is shorter.
-// Measured (us, 128 / 64 / 32 columns, L2 written over before): 17 x 2048 -> 5461 22.5 / 18.5 / 26.6,
-// 128 x 4096 -> 2000 32.8 / 26.6 / 24.6, 64 x 256 -> 1024 10.2 / 8.2 / 8.2, 1 x 4096 -> 16384 60 / 65 / 80.
+// Measured (us, 128 / 64 / 32 columns, L2 written over before): 17 x 2048 -> 5461 22.5 / 18.5 /
+// 26.6, 128 x 4096 -> 2000 32.8 / 26.6 / 24.6, 64 x 256 -> 1024 10.2 / 8.2 / 8.2, 1 x 4096 -> 16384
+// 60 / 65 / 80.
 int solo_cols(int64_t F, int64_t sms) {
   int w = 128;
   while (w > 32 && 2 * ceil_div(F, w) <= sms) w /= 2;
@@ -700,8 +702,8 @@ int solo_cols(int64_t F, int64_t sms) {
 }
 
 template <int kARows>
-cudaError_t launch_solo(int w, int grid, cudaStream_t s, const CUtensorMap& x, const CUtensorMap& wm,
-                        const GatedSched& sc, const GatedOut& o) {
+cudaError_t launch_solo(int w, int grid, cudaStream_t s, const CUtensorMap& x,
+                        const CUtensorMap& wm, const GatedSched& sc, const GatedOut& o) {
   return w == 128 ? launch_overlapped(gated_linear_solo_kernel<kARows, 128>, grid, kThreads,
                                       solo_smem<kARows, 128>(), s, x, wm, sc, o)
          : w == 64 ? launch_overlapped(gated_linear_solo_kernel<kARows, 64>, grid, kThreads,
@@ -812,13 +814,13 @@ cudaError_t pair_sched(int64_t M, int64_t K, int64_t F, int stage_k, int64_t clu
 }
 
 // Both products of a backward in one launch over both tile lists (the same bits), so that the one
-// with the shorter reduction fills the SM pairs that the few tiles of the long one leave idle.  Apart,
-// the long one has narrow tiles, which take 0.69 of a wide tile's time; so one launch pays where
-// the long one's 256 x 256 tiles fill at most half of the pairs and the other product takes
-// about half as long as one of them or more, counting 64-wide reduction blocks and six more for
-// a tile's store.  Measured (us for the whole backward from 8 bits, one launch / two; in brackets that
-// ratio): 255 x 4096 -> 11000 146 / 183 (0.53), 512 x 2048 -> 8192 119 / 106 (0.37), 255 x 2048 -> 5461
-// 90 / 73 (0.26), 1000 x 1024 -> 4096 64 / 54 (0.28).
+// with the shorter reduction fills the SM pairs that the few tiles of the long one leave idle.
+// Apart, the long one has narrow tiles, which take 0.69 of a wide tile's time; so one launch pays
+// where the long one's 256 x 256 tiles fill at most half of the pairs and the other product takes
+// about half as long as one of them or more, counting 64-wide reduction blocks and six more for a
+// tile's store.  Measured (us for the whole backward from 8 bits, one launch / two; in brackets
+// that ratio): 255 x 4096 -> 11000 146 / 183 (0.53), 512 x 2048 -> 8192 119 / 106 (0.37), 255 x
+// 2048 -> 5461 90 / 73 (0.26), 1000 x 1024 -> 4096 64 / 54 (0.28).
 bool one_launch(int64_t M, int64_t K, int64_t F, int64_t pairs) {
   const int64_t red_long = M > 2 * F ? M : 2 * F, red_short = M > 2 * F ? 2 * F : M;
   const int64_t kb = ceil_div(K, kBN);
@@ -1031,7 +1033,8 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
       constexpr bool kVec = decltype(v)::value;
       const RowLanes<8> lanes = row_lanes<8>(F, kVec ? 2 : 5);
       const int64_t steps = ceil_div(F, lanes.step());
-      const dim3 grid((unsigned)ceil_div(M, lanes.rows()), (unsigned)(steps < 65535 ? steps : 65535));
+      const dim3 grid((unsigned)ceil_div(M, lanes.rows()),
+                      (unsigned)(steps < 65535 ? steps : 65535));
       return activation == RLK_ACT_SILU
                  ? launch_overlapped(gated_grad_kept_kernel<kQ, kD, RLK_ACT_SILU, kVec>, grid,
                                      kRowThreads, 0, s, kept, kept_exponents, Fp, o, lanes)

@@ -1,10 +1,9 @@
 // Activations in 8 bits and back (the block format of rlk_int8.cuh).
 //
 // A BF16 element to 8 bits moves 3.03 bytes (2 read, 1 written, an exponent byte per 32), back as
-// much.  16384 x 4096: packing 38 - 44 us (5.0 TB/s; two thirds of it instructions), unpacking 32 - 35
-// (6.1 TB/s).  A thread takes eight columns, so a block's 32 columns
-// lie in four neighbouring lanes: one 16-byte load a thread, the largest magnitude by two
-// shuffles, one 8-byte store.
+// much.  16384 x 4096: packing 38 - 44 us (5.0 TB/s; two thirds of it instructions), unpacking 32 -
+// 35 (6.1 TB/s).  A thread takes eight columns, so a block's 32 columns lie in four neighbouring
+// lanes: one 16-byte load a thread, the largest magnitude by two shuffles, one 8-byte store.
 #include "rlk.h"
 #include "rlk_int8.cuh"
 #include "rlk_internal.h"
@@ -16,9 +15,10 @@ __device__ unsigned int g_err_int8 = 0;
 
 namespace {
 
-// kRowsAThread rows a thread, their loads issued together (16384 x 4096 BF16, us with 1, 2, 3 and 4: packing
-// 41.6, 37.1, 35.7, 42.3, unpacking 41.1, 36.1, 44.6, 50.1).  Rows that rule vectors out (kVec false)
-// pass through shared memory (RowStage).  Packing is bound by instructions as much as by HBM.
+// kRowsAThread rows a thread, their loads issued together (16384 x 4096 BF16, us with 1, 2, 3 and
+// 4: packing 41.6, 37.1, 35.7, 42.3, unpacking 41.1, 36.1, 44.6, 50.1).  Rows that rule vectors out
+// (kVec false) pass through shared memory (RowStage).  Packing is bound by instructions as much as
+// by HBM.
 constexpr int kRowsAThread = 2;
 
 template <bool kFp32, bool kVec>
@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(kRowThreads)
       for (int i = 1; i < 8; ++i) most = max_magnitude(most, v[k][i]);
       most = max_magnitude(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = max_magnitude(most, __shfl_xor_sync(0xffffffffu, most, 2));
-      if (r >= rows || c >= wide || !RLK_STORE_OK(c + 8 <= ldq && c / kInt8Block < lde, &g_err_int8))
+      if (r >= rows || c >= wide ||
+          !RLK_STORE_OK(c + 8 <= ldq && c / kInt8Block < lde, &g_err_int8))
         continue;
       const uint32_t e = int8_exponent(most);
       const float inverse = int8_inverse(e);

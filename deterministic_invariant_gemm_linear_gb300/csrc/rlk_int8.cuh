@@ -38,9 +38,9 @@ __device__ __forceinline__ bool int8_holds(float most, float inverse) {
   return __fmul_rn(most, inverse) >= 127.5f;
 }
 
-// Four x / step as bytes, rounded to nearest even, held to -127 .. 127 if `hold`.
-// x / step + 1.5 2^23 is rounded to a whole number by the addition (the product is exact), whose low
-// byte it is: one fused operation where a conversion would run at a quarter of the rate.
+// Four x / step as bytes, rounded to nearest even, held to -127 .. 127 if `hold`. x / step + 1.5
+// 2^23 is rounded to a whole number by the addition (the product is exact), whose low byte it is:
+// one fused operation where a conversion would run at a quarter of the rate.
 __device__ __forceinline__ uint32_t int8_word(const float* x, float inverse, bool hold) {
   constexpr float kOffset = 12582912.f;
   uint32_t w[4];
@@ -64,7 +64,8 @@ __device__ __forceinline__ void int8_floats(uint32_t word, float step, float* x)
   }
 }
 
-// Eight values from column c (a multiple of 8) of a row of blocks as FP32; the row begins on 8 bytes.
+// Eight values from column c (a multiple of 8) of a row of blocks as FP32; the row begins on 8
+// bytes.
 __device__ __forceinline__ void load_int8(const int8_t* q, const uint8_t* exponents, int c,
                                           float (&x)[8]) {
   const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + c));

@@ -73,7 +73,8 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int c, int gap,
     } else if constexpr (kFp32) {
 #pragma unroll
       for (int j = 0; j < kRun; j += 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + k + j));
+        const float4 a =
+            __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + k + j));
         y[j] = a.x; y[j + 1] = a.y; y[j + 2] = a.z; y[j + 3] = a.w;
       }
     } else {
@@ -108,7 +109,8 @@ __device__ __forceinline__ void put(T* p, T v) {
     *p = v;
 }
 
-// Stores x to the eight columns from c on (those before column n).  kStream: nothing reads them soon.
+// Stores x to the eight columns from c on (those before column n).  kStream: nothing reads them
+// soon.
 template <bool kFp32, int kRun, bool kStream = false>
 __device__ __forceinline__ void store8(void* p, int64_t at, int c, int gap, int n,
                                        const float (&x)[8]) {
@@ -167,10 +169,10 @@ __device__ __forceinline__ void turn_block(T (&x)[n]) {
   }
 }
 
-// Columns c .. c + n - 1 (n <= 32) of the warp's rows r0 .. r0 + 31 below M; the whole warp takes part,
-// and x, the thread's row, is used up.  vec: whole rows of 32 are 16-byte vectors.  BF16 is turned
-// in pairs, columns i and i + 16 in one register: 32 shuffles in place of 80, and a store then
-// covers half a row of each half of the block.
+// Columns c .. c + n - 1 (n <= 32) of the warp's rows r0 .. r0 + 31 below M; the whole warp takes
+// part, and x, the thread's row, is used up.  vec: whole rows of 32 are 16-byte vectors.  BF16 is
+// turned in pairs, columns i and i + 16 in one register: 32 shuffles in place of 80, and a store
+// then covers half a row of each half of the block.
 template <bool kFp32>
 __device__ __forceinline__ void store_block(void* base, int64_t ld, int r0, int M, int c, int n,
                                             bool vec, float (&x)[32]) {
