@@ -34,8 +34,15 @@ __device__ unsigned int g_err_gated_linear = 0;
 namespace {
 
 constexpr int kGateCols = kBN / 2;     // columns of g (and of u) in a 256-wide accumulator
+// Eight epilogue warps, two to a quarter of the accumulator rows, each half of a tile's columns: one
+// warp a scheduler issues an instruction in four cycles.  Four warps / eight, us: forward of 2000 x
+// 512 -> 4000 19.4 / 18.7, with 8 bits kept 31.6 / 26.6, its backward with G from projections formed
+// again 87.6 / 77.0; 4096 x 1024 -> 4096 37.6 / 38.0, 56.4 / 50.3, 164 / 143; 2000 x 2048 -> 5464, whose
+// MMAs hide either, 51.7 / 52.4, 58.6 / 59.9, 180 / 175.
+constexpr int kEpilogueWarps = 8;
+constexpr int kGatedThreads = 64 + 32 * kEpilogueWarps;     // and the producer's and the MMAs' warp
 constexpr int kSlotBytes = 4096;       // a block of 32 x 32 FP32 on its way out (see StoreSlots)
-constexpr int kStoreBytes = 4 * 2 * kSlotBytes;     // the four epilogue warps' two slots each
+constexpr int kStoreBytes = kEpilogueWarps * kSlotBytes;
 
 // ---------------------------------------------------------------- the activation
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -200,25 +207,33 @@ inline bool block_vec(const void* base, int64_t ld, int64_t esize) {
   return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (ld * esize) % 16 == 0;
 }
 
-// Blocks of 32 rows and 32 columns on their way out by TMA.  A warp has two slots of 4 KB after the
-// ring's stages; each thread writes its row into one (16-byte pieces swizzled as the tensor map
-// says, so that no two lanes of a phase share a bank), lane 0 starts the copy and the warp goes
-// on; a slot is taken again once its last copy has been read.  The copies write whole rows of
-// 32, 64 or 128 bytes and end at the matrix's last row by themselves.  (Not at its last column: a
-// box that the width cuts is written in units of 16 bytes, so a run of fewer than 32 columns
-// goes out from the threads.)  Against stores from the threads, 16 bytes in each of 32 rows an
-// instruction, with FP32 projections kept: 4096 x 64 -> 16384 157 us for 267 (a tile's epilogue 5.8
-// for 9.9), 4096 x 4096 -> 16384 595 for 622.
+// Blocks of 32 rows and 32 columns on their way out by TMA.  A warp has 4 KB after the ring's stages:
+// room for one block of FP32, or for two of BF16 or bytes.  Each thread writes its row (16-byte
+// pieces swizzled as the tensor map says, so that no two lanes of a phase share a bank), lane 0
+// starts the copy and the warp goes on; the room is taken again once the copy has been read.  The
+// copies write whole rows of 32, 64 or 128 bytes and end at the matrix's last row by themselves.
+// (Not at its last column: a box that the width cuts is written in units of 16 bytes, so a run of
+// fewer than 32 columns goes out from the threads.)  Against stores from the threads, 16 bytes in
+// each of 32 rows an instruction (four epilogue warps, FP32 projections kept): 4096 x 64 -> 16384
+// 157 us for 267, 4096 x 4096 -> 16384 595 for 622.
 struct StoreSlots {
-  uint32_t base;      // this warp's two slots, or 0 (no slots: stores from the threads)
-  int turn = 0;
-  __device__ __forceinline__ explicit StoreSlots(uint32_t at) : base(at) {}
-  // The next slot, free to be written.
+  uint32_t base;             // this warp's 4 KB, or 0 (stores from the threads)
+  uint32_t at;               // where the next block is put
+  bool whole = false;        // the last block had all of it
+  __device__ __forceinline__ explicit StoreSlots(uint32_t b) : base(b), at(b) {}
+  // Room for a block of FP32 (kWhole), or of BF16 or bytes.
+  template <bool kWhole>
   __device__ __forceinline__ uint32_t take() {
-    if ((threadIdx.x & 31) == 0)
-      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    if ((threadIdx.x & 31) == 0) {
+      if (kWhole || whole)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      else
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    }
     __syncwarp();
-    return base + (turn & 1) * kSlotBytes;
+    at = kWhole || at != base ? base : base + kSlotBytes / 2;
+    whole = kWhole;
+    return at;
   }
   // Sends it to columns c .. c + 31 of rows r .. r + 31.
   __device__ __forceinline__ void send(const CUtensorMap* map, int c, int r) {
@@ -228,11 +243,10 @@ struct StoreSlots {
       asm volatile(
           "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
               reinterpret_cast<uint64_t>(map)),
-          "r"(base + (turn & 1) * kSlotBytes), "r"(c), "r"(r)
+          "r"(at), "r"(c), "r"(r)
           : "memory");
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-    ++turn;
   }
   // Every copy has been written (before the CTA gives up its shared memory).
   __device__ __forceinline__ void finish() {
@@ -292,7 +306,7 @@ __device__ __forceinline__ void keep_run(const GatedOut& o, const CUtensorMap* m
   const int64_t at = ((int64_t)row * 2 + plane) * o.Fp + f;
   if (o.keep == RLK_KEEP_FP32) {
     if constexpr (kSlots) {
-      put_fp32(slots.take(), z);
+      put_fp32(slots.take<true>(), z);
       slots.send(map, plane * o.Fp + f, r0);
     } else if (in) {
       uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(o.kept) + at);
@@ -329,7 +343,7 @@ __device__ __forceinline__ void keep_run(const GatedOut& o, const CUtensorMap* m
   for (int i = 0; i < 8; ++i)
     if (e == 255u) w[i] = 0u;
   if constexpr (kSlots) {
-    put_bytes(slots.take(), w);
+    put_bytes(slots.take<false>(), w);
     slots.send(map, plane * o.Fp + f, r0);
   } else if (in) {
     uint4* d = reinterpret_cast<uint4*>(static_cast<int8_t*>(o.kept) + at);
@@ -348,14 +362,17 @@ __device__ __forceinline__ void value_run(const uint32_t (&g)[32], const uint32_
 }
 
 // A tile's epilogue in one warp: accumulator columns [0, kCols) hold g and [kCols, 2 kCols) u of
-// columns f0 .. f0 + kCols - 1 of the warp's rows r0 .. r0 + 31.  kSlots: the warp has store slots.
+// columns f0 .. f0 + kCols - 1 of the warp's rows r0 .. r0 + 31, of which it takes half `half`.
+// kSlots: the warp has store slots.
 template <int kCols, bool kSlots>
 __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap* tm_h,
                                            const CUtensorMap* tm_kept, StoreSlots& slots,
-                                           uint32_t taddr, int r0, int f0) {
+                                           uint32_t taddr, int r0, int f0, int half) {
   if (r0 >= o.M) return;                    // uniform: depends on the warp's rows only
+  constexpr int kChunks = kCols / 32, kMine = (kChunks + 1) / 2;
+  const int end = half == 0 ? kMine : kChunks;
 #pragma unroll 1
-  for (int c = 0; c < kCols / 32; ++c) {
+  for (int c = half * kMine; c < end; ++c) {
     const int f = f0 + 32 * c;
     if (f >= o.F) break;                    // uniform: depends on the tile only
     uint32_t g[32], u[32];
@@ -371,20 +388,20 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap*
     const int n = min(32, o.F - f);
     if (RLK_STORE_OK(f + n <= o.ldh, &g_err_gated_linear)) {
       if (kSlots && o.h_vec && n == 32) {
-        const uint32_t slot = slots.take();
         if (o.h_fp32) {
+          const uint32_t slot = slots.take<true>();
           uint32_t bits[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) bits[i] = __float_as_uint(h[i]);
           put_fp32(slot, bits);
         } else {
-          put_bf16(slot, h);
+          put_bf16(slots.take<false>(), h);
         }
         slots.send(tm_h, f, r0);
       } else if (o.h_fp32) {
-        store_block<true>(o.H, o.ldh, r0, o.M, f, n, o.h_vec, h);
+        store_block<true>(o.H, o.ldh, r0, o.M, f, n, !kSlots && o.h_vec, h);
       } else {
-        store_block<false>(o.H, o.ldh, r0, o.M, f, n, o.h_vec, h);
+        store_block<false>(o.H, o.ldh, r0, o.M, f, n, !kSlots && o.h_vec, h);
       }
     }
     if (o.keep != RLK_KEEP_NONE) {
@@ -396,11 +413,11 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap*
 
 // More than 128 rows.  Bound by the tensor cores: 4096 x 4096 -> 16384 545 us by itself (2.02
 // PFLOP/s, 1.05 of the measured product; 616 - 640 back to back, at the clock that the power cap
-// leaves), 595 with FP32 projections kept, 566 with 8 bits.  The epilogue (3.8 us a tile, 5.8 and
-// 7.0 with them kept) hides behind a tile's MMAs from K of about 900, 1400 and 1700 on; below, it
-// bounds the call: 4096 x 512 -> 16384 118 us, where the products alone are 36.
+// leaves), 593 with FP32 projections kept, 568 with 8 bits.  The epilogue (3.4 us a tile, 5.0 and
+// 5.5 with them kept) hides behind a tile's MMAs from K of about 800, 1200 and 1300 on; below, it
+// bounds the call: 4096 x 512 -> 16384 107 us, where the products alone are 36.
 template <int kK>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatedThreads, 1)
     gated_linear_kernel(const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ CUtensorMap tm_w,
                         const __grid_constant__ CUtensorMap tm_h,
@@ -412,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_w);
   }
-  const uint32_t tmem = pipe_setup(ps);
+  const uint32_t tmem = pipe_setup<kEpilogueWarps>(ps);
   using TA = OperandTile<false, kHalfRows, kK>;
   using TB = GateUpHalf<kK>;
   using R = GatedRing<kK>;
@@ -427,9 +444,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                       &g_err_gated_linear);
     __syncwarp();
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;     // rows 32 q on, half of the columns
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-    StoreSlots slots(R::reserve(ps.stages) + q * 2 * kSlotBytes);
+    StoreSlots slots(R::reserve(ps.stages) + (warp - 2) * kSlotBytes);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int k = 0;; ++k) {
@@ -439,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int r0, b0;
       sc.tile_coords(u, 0, r0, b0);
       gated_tile<kGateCols, true>(o, &tm_h, &tm_kept, slots, tmem + acc * kAccCols + lane_off,
-                                  r0 + (int)ps.rank * kHalfRows + q * 32, b0 / 2);
+                                  r0 + (int)ps.rank * kHalfRows + q * 32, b0 / 2, half);
       epilogue_release(ps, acc);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -454,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // CTA's own stream and what comes before and after it (17 x 2048 -> 5461 17 us with a cold L2, 45
 // MB).
 template <int kARows, int kCols>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kGatedThreads, 1)
     gated_linear_solo_kernel(const __grid_constant__ CUtensorMap tm_x,
                              const __grid_constant__ CUtensorMap tm_w, GatedSched sc, GatedOut o) {
   extern __shared__ uint8_t smem_raw[];
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_w);
   }
-  const uint32_t tmem = solo_setup(ps);
+  const uint32_t tmem = solo_setup<kEpilogueWarps>(ps);
   using R = SoloRing<kARows, 2 * kCols>;
   using TA = OperandTile<false, kARows>;
   using TB = GateUpBoth<kCols>;
@@ -477,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           &g_err_gated_linear);
     __syncwarp();
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;     // rows 32 q on, half of the columns
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     StoreSlots slots(0);
     int acc = 0;
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int r0, b0;
       sc.tile_coords(u, 0, r0, b0);
       gated_tile<kCols, false>(o, nullptr, nullptr, slots, tmem + acc * kAccCols + lane_off, q * 32,
-                               b0 / 2);
+                               b0 / 2, half);
       solo_release(ps, acc);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -522,10 +539,10 @@ __device__ __forceinline__ void slope_run(float (&d)[32], const uint32_t (&g)[32
   }
 }
 
-// G from projections formed again: the forward's loop, with another epilogue.  Its 9.8 us a tile
-// (dH is read when its chunk's turn comes) hide behind the MMAs from K of about 2400 on.
+// G from projections formed again: the forward's loop, with another epilogue.  Its 5.4 us a tile
+// (dH is read when its chunk's turn comes) hide behind the MMAs from K of about 1300 on.
 template <int kK>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatedThreads, 1)
     gated_grad_kernel(const __grid_constant__ CUtensorMap tm_x,
                       const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_gate,
@@ -537,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_w);
   }
-  const uint32_t tmem = pipe_setup(ps);
+  const uint32_t tmem = pipe_setup<kEpilogueWarps>(ps);
   using TA = OperandTile<false, kHalfRows, kK>;
   using TB = GateUpHalf<kK>;
   using R = GatedRing<kK>;
@@ -552,9 +569,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                       &g_err_gated_linear);
     __syncwarp();
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;     // rows 32 q on, half of the columns
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-    StoreSlots slots(R::reserve(ps.stages) + q * 2 * kSlotBytes);
+    StoreSlots slots(R::reserve(ps.stages) + (warp - 2) * kSlotBytes);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int k = 0;; ++k) {
@@ -567,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int f0 = b0 / 2;
       const uint32_t taddr = tmem + acc * kAccCols + lane_off;
 #pragma unroll 1
-      for (int c = 0; c < kGateCols / 32; ++c) {
+      for (int c = half * (kGateCols / 64); c < (half + 1) * (kGateCols / 64); ++c) {
         const int f = f0 + 32 * c;
         if (f >= o.F || row0 >= o.M) break;     // uniform: depends on the tile and the warp only
         const int n = min(32, o.F - f);
@@ -587,16 +604,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           slope_run<RLK_ACT_GELU_TANH>(d, g, u, dg);
         if (!RLK_STORE_OK(o.F + f + n <= o.ldG, &g_err_gated_linear)) continue;
         if (n == 32) {
-          put_bf16(slots.take(), dg);
+          put_bf16(slots.take<false>(), dg);
           slots.send(&tm_gate, f, row0);
         } else {
-          store_block<false>(o.G, o.ldG, row0, o.M, f, n, true, dg);
+          store_block<false>(o.G, o.ldG, row0, o.M, f, n, false, dg);
         }
         if (o.up_vec && n == 32) {
-          put_bf16(slots.take(), d);
+          put_bf16(slots.take<false>(), d);
           slots.send(&tm_up, f, row0);
         } else {
-          store_block<false>(o.G + o.F, o.ldG, row0, o.M, f, n, o.up_vec, d);
+          store_block<false>(o.G + o.F, o.ldG, row0, o.M, f, n, false, d);
         }
       }
       epilogue_release(ps, acc);
@@ -704,11 +721,11 @@ int solo_cols(int64_t F, int64_t sms) {
 template <int kARows>
 cudaError_t launch_solo(int w, int grid, cudaStream_t s, const CUtensorMap& x,
                         const CUtensorMap& wm, const GatedSched& sc, const GatedOut& o) {
-  return w == 128 ? launch_overlapped(gated_linear_solo_kernel<kARows, 128>, grid, kThreads,
+  return w == 128 ? launch_overlapped(gated_linear_solo_kernel<kARows, 128>, grid, kGatedThreads,
                                       solo_smem<kARows, 128>(), s, x, wm, sc, o)
-         : w == 64 ? launch_overlapped(gated_linear_solo_kernel<kARows, 64>, grid, kThreads,
+         : w == 64 ? launch_overlapped(gated_linear_solo_kernel<kARows, 64>, grid, kGatedThreads,
                                        solo_smem<kARows, 64>(), s, x, wm, sc, o)
-                   : launch_overlapped(gated_linear_solo_kernel<kARows, 32>, grid, kThreads,
+                   : launch_overlapped(gated_linear_solo_kernel<kARows, 32>, grid, kGatedThreads,
                                        solo_smem<kARows, 32>(), s, x, wm, sc, o);
 }
 
@@ -932,10 +949,10 @@ rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t ldx, co
     e = pair_sched(M, K, F, stage_k, dev.sm_count / 2, reinterpret_cast<int*>(ws + p.off_ctr), s,
                    &sc, &grid);
     if (e == cudaSuccess)
-      e = stage_k == 128 ? launch_overlapped(gated_linear_kernel<128>, grid, kThreads,
+      e = stage_k == 128 ? launch_overlapped(gated_linear_kernel<128>, grid, kGatedThreads,
                                              GatedRing<128>::kSmemBytes, s, tm_x, tm_w, tm_h,
                                              tm_kept, sc, o)
-                         : launch_overlapped(gated_linear_kernel<64>, grid, kThreads,
+                         : launch_overlapped(gated_linear_kernel<64>, grid, kGatedThreads,
                                              GatedRing<64>::kSmemBytes, s, tm_x, tm_w, tm_h,
                                              tm_kept, sc, o);
   }
@@ -1020,10 +1037,10 @@ rlk_status rlk_gated_linear_backward(const void* dH, int dh_dtype, int64_t M, in
     int grid;
     e = pair_sched(M, K, F, stage_k, dev.sm_count / 2, counter, s, &sc, &grid);
     if (e == cudaSuccess)
-      e = stage_k == 128 ? launch_overlapped(gated_grad_kernel<128>, grid, kThreads,
+      e = stage_k == 128 ? launch_overlapped(gated_grad_kernel<128>, grid, kGatedThreads,
                                              GatedRing<128>::kSmemBytes, s, tm_x, tm_w, tm_gate,
                                              tm_up, sc, o)
-                         : launch_overlapped(gated_grad_kernel<64>, grid, kThreads,
+                         : launch_overlapped(gated_grad_kernel<64>, grid, kGatedThreads,
                                              GatedRing<64>::kSmemBytes, s, tm_x, tm_w, tm_gate,
                                              tm_up, sc, o);
   } else {

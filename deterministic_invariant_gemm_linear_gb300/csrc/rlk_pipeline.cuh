@@ -175,9 +175,11 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 // A cluster's first unit is its own index and bypasses the ring, so the first
 // tiles start without waiting on the counter.
 constexpr int kUnitSlots = 4;
-// Consumers of each slot: rank 0's producer, MMA issuer and 4 epilogue warps;
-// rank 1's producer and 4 epilogue warps.
-constexpr int kUnitConsumers = 2 + 4 + 1 + 4;
+// Consumers of each slot: rank 0's producer, MMA issuer and epilogue warps (4, or
+// as many as a kernel names); rank 1's producer and epilogue warps.
+__host__ __device__ constexpr int unit_consumers(int epilogue_warps) {
+  return 2 + 1 + 2 * epilogue_warps;
+}
 constexpr int kUnitDone = -1;      // no more units
 constexpr int kUnitAbort = -2;     // the CTA is winding down
 
@@ -225,6 +227,7 @@ __device__ __forceinline__ PipeSmem pipe_smem(uint8_t* raw) {
 // Barrier initialisation, collective TMEM allocation, then a cluster barrier
 // so that no CTA touches its peer's barriers before they exist; then the wait
 // for the previous kernel in the stream (programmatic dependent launch).
+template <int kEpilogueWarps = kEpilogueThreads / 32>
 __device__ __forceinline__ uint32_t pipe_setup(const PipeSmem& ps) {
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
@@ -234,12 +237,12 @@ __device__ __forceinline__ uint32_t pipe_setup(const PipeSmem& ps) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(ps.acc_full(b), 1);
-      mbar_init(ps.acc_empty(b), 2 * (kEpilogueThreads / 32));
+      mbar_init(ps.acc_empty(b), 2 * kEpilogueWarps);
     }
     mbar_init(smem_u32(&ps.bars->drained), 1);
     for (int k = 0; k < kUnitSlots; ++k) {
       mbar_init(ps.unit_full(k), 1);
-      mbar_init(ps.unit_empty(k), kUnitConsumers);
+      mbar_init(ps.unit_empty(k), unit_consumers(kEpilogueWarps));
     }
     ps.bars->abort_flag = 0;
     fence_mbar_init();

@@ -63,6 +63,7 @@ __device__ __forceinline__ int solo_unit(const Sched& sc, int k) {
 
 // Barriers, the 512-column TMEM allocation, then the wait for the previous
 // kernel in the stream (programmatic dependent launch).
+template <int kEpilogueWarps = kEpilogueThreads / 32>
 __device__ __forceinline__ uint32_t solo_setup(const PipeSmem& ps) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -71,7 +72,7 @@ __device__ __forceinline__ uint32_t solo_setup(const PipeSmem& ps) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(ps.acc_full(b), 1);
-      mbar_init(ps.acc_empty(b), kEpilogueThreads / 32);
+      mbar_init(ps.acc_empty(b), kEpilogueWarps);
     }
     mbar_init(smem_u32(&ps.bars->drained), 1);
     ps.bars->abort_flag = 0;
