@@ -14,6 +14,7 @@
 //                   empty / accumulator-full barriers (multicast).
 //   warps 2..5      epilogue on the CTA's own 128 accumulator rows; each warp
 //                   releases the accumulator on rank 0's barrier (8 arrivals).
+//                   A kernel may have more of them (pipe_setup's argument).
 // Compared with one CTA owning a 128 x 256 tile, each SM reads half the
 // right-operand bytes from shared memory per MMA for the same accumulator shape.
 #pragma once
