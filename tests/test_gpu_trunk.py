@@ -242,6 +242,50 @@ def test_captured_and_replayed(M, K, F):
     assert rlk.device_error() == 0
 
 
+@pytest.mark.parametrize("checkpoint", ["fp32", "int8", "again"])
+@pytest.mark.parametrize("n,K,F", [(1, 64, 96), (100, 72, 130), (300, 256, 500)])
+def test_captured_through_autograd(n, K, F, checkpoint):
+    """Forward and backward through autograd in one graph, replayed with new numbers in its buffers.
+    The graph has leaves of its own: a leaf that an eager graph still holds keeps that graph's stream."""
+    dev = cuda_or_skip()
+    V = 500
+
+    def inputs(seed):
+        g = torch.Generator(device=dev).manual_seed(seed)
+        return [torch.randint(-1, V, (n,), device=dev, generator=g),
+                torch.randn(V, K, device=dev, generator=g).bfloat16(),
+                (torch.randn(2 * F, K, device=dev, generator=g) / K ** 0.5).bfloat16(),
+                (torch.randn(K, F, device=dev, generator=g) / F ** 0.5).bfloat16(),
+                torch.randn(n, K, device=dev, generator=g).bfloat16()]
+
+    def step(ids, table, w_in, w_out, up):
+        leaves = [t.requires_grad_() for t in (table, w_in, w_out)]
+        x = rlk.embedding_trainable(ids, table, 1.5)
+        h = rlk.gated_linear_trainable(x, w_in, checkpoint=checkpoint)
+        y = rlk.det_linear_trainable(h, w_out, checkpoint="int8" if checkpoint == "int8" else None)
+        return [y.detach(), *torch.autograd.grad(y, leaves, up)]
+
+    a, b = inputs(5), inputs(6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [[t.clone() for t in step(*(t.clone() for t in i))] for i in (a, b)]
+    torch.cuda.current_stream().wait_stream(side)
+    own = [t.clone() for t in a]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*own)
+    for i, exp in ((b, want[1]), (a, want[0]), (b, want[1])):
+        with torch.no_grad():
+            for t, new in zip(own, i):
+                t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, exp):
+            assert bits_equal(x, y)
+    assert rlk.device_error() == 0
+
+
 def test_threads_on_their_own_streams():
     dev = cuda_or_skip()
     of = entries(dev)
