@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kSortIds, 1)
   for (int h = 0; h < n_heavy; ++h) {
     const int k = heavy[h].x, base = heavy[h].y;
     const int f = first_of[k], n = rows_of[k];
-    for (int g = t; g * kGroup < n; g += kSortIds)
+    const int groups = (n + kGroup - 1) / kGroup;    // a row past n may not fit an int, a group does
+    for (int g = t; g < groups; g += kSortIds)
       if (RLK_STORE_OK(base + g < max_groups, &g_err_embedding))
         o.groups[base + g] =
             make_int4(f + g * kGroup, min(kGroup, n - g * kGroup), base, lo + k);
