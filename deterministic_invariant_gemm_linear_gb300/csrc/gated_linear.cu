@@ -405,6 +405,12 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap*
       }
     }
     if (o.keep != RLK_KEEP_NONE) {
+      // Columns past F are kept as 0: the products there are 0 times X, NaN where X is not finite.
+      if (n < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i >= n) g[i] = u[i] = 0u;
+      }
       keep_run<kSlots>(o, tm_kept, slots, r0, f, 0, g);
       keep_run<kSlots>(o, tm_kept, slots, r0, f, 1, u);
     }
