@@ -46,6 +46,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import math
 import operator
 import os
 
@@ -1417,20 +1418,28 @@ class _Gated:
 
     __slots__ = ("lead", "x", "ldx", "w", "ldw", "act", "M", "K", "F")
 
-    def __init__(self, X, W, activation):
+    def __init__(self, X, W, activation, lead=None):
+        """lead: X's leading shape where X is None (nothing reads it)."""
         _one_device(X, W)
-        if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        if W.dtype != torch.bfloat16 or X is not None and X.dtype != torch.bfloat16:
             raise TypeError("X and W must be bfloat16")
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
         self.act = ACTIVATIONS[activation]
-        self.lead, self.K = X.shape[:-1], X.size(-1)
+        self.lead, self.K = (lead, W.size(-1)) if X is None else (X.shape[:-1], X.size(-1))
         if W.dim() != 2 or W.size(1) != self.K or W.size(0) % 2:
             raise ValueError("W must be [2 F, K]: F rows of the gate, then F rows of the other projection")
         self.F = W.size(0) // 2
-        self.x, self.ldx = _matrix(_flatten_rows(X), "X")
         self.w, self.ldw = _matrix(W, "W")
-        self.M = self.x.size(0)
+        if X is None:
+            self.x, self.ldx, self.M = None, self.unread(), math.prod(lead)
+        else:
+            self.x, self.ldx = _matrix(_flatten_rows(X), "X")
+            self.M = self.x.size(0)
+
+    def unread(self):
+        """The pitch of an operand that is passed as NULL: one that asks for no padded copy."""
+        return -(-self.K // 8) * 8
 
 
 def _kept_parts(kept, M: int, F: int):
@@ -1495,7 +1504,7 @@ def gated_linear(X: torch.Tensor, W: torch.Tensor, activation: str = "silu", out
 
 
 @_streamed
-def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
+def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor | None, W: torch.Tensor,
                           activation: str = "silu", *, kept=None, grad_x: bool = True,
                           grad_w: bool = True, out_dtype=torch.bfloat16,
                           return_grad_projections: bool = False, stream=None):
@@ -1504,9 +1513,13 @@ def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
     kept: what gated_linear(..., keep=) returned for these rows, or None to form the projections
     again (the same bits as keep="fp32").  dX and dW are det_linear_backward's products of the
     projections' gradient rounded to bf16; with return_grad_projections that is returned too,
-    as the [rows, 2 F] view that the products read.
+    as the [rows, 2 F] view that the products read.  X is read for dW and to form the projections
+    again: with kept and without grad_w it may be None.
     """
-    g = _Gated(X, W, activation)
+    read_x, read_w = grad_w or kept is None, grad_x or kept is None
+    if X is None and read_x:
+        raise ValueError("X is read for dW and, without kept, for the projections: it cannot be None")
+    g = _Gated(X, W, activation, dH.shape[:-1])
     if return_grad_projections and not (grad_x or grad_w):
         raise ValueError("the projections' gradient is formed for dX or dW: ask for one of them")
     if dH.dtype not in _DT:
@@ -1514,26 +1527,28 @@ def gated_linear_backward(dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor,
     if dH.shape != (*g.lead, g.F):
         raise ValueError("dH must be [..., F] with X's leading shape")
     d, ldd = _matrix(_flatten_rows(dH), "dH")
-    M, K, F, dev = g.M, g.K, g.F, X.device
+    M, K, F, dev = g.M, g.K, g.F, W.device
     keep, values, exponents = _kept_parts(kept, M, F)
-    _one_device(X, dH, values, exponents)
+    _one_device(W, dH, values, exponents)
+    # an operand that nothing reads is not passed, so that no copy of it is made room for
+    x, ldx = (g.x, g.ldx) if read_x else (None, g.unread())
+    w, ldw = (g.w, g.ldw) if read_w else (None, g.unread())
     dX = torch.empty((M, K), dtype=out_dtype, device=dev) if grad_x else None
     dW = torch.empty((2 * F, K), dtype=out_dtype, device=dev) if grad_w else None
     lib_ = lib()
     dt = _DT[out_dtype]
     with _on(dev):
         n = -(-(M * (-(-2 * F // 8) * 16)) // 256) * 256 + 256      # G and the unit counter
-        if not (_in_place(g.x, g.ldx) and _in_place(g.w, g.ldw)):
-            n = lib_.rlk_gated_linear_backward_workspace_size(_ptr(g.x), M, K, g.ldx, _ptr(g.w), F,
-                                                              g.ldw)
+        if not ((x is None or _in_place(x, ldx)) and (w is None or _in_place(w, ldw))):
+            n = lib_.rlk_gated_linear_backward_workspace_size(_ptr(x), M, K, ldx, _ptr(w), F, ldw)
             if n == 0:
                 raise RlkError(2, "rlk_gated_linear_backward_workspace_size")
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         _check(lib_.rlk_gated_linear_backward(
-            _ptr(d), _DT[d.dtype], M, F, ldd, _ptr(g.x), K, g.ldx, _ptr(g.w), g.ldw, g.act, keep,
+            _ptr(d), _DT[d.dtype], M, F, ldd, _ptr(x), K, ldx, _ptr(w), ldw, g.act, keep,
             _ptr(values), _ptr(exponents), _ptr(dX), dt, K, _ptr(dW), dt, K, _ptr(ws), n,
             _stream_ptr(stream)), "rlk_gated_linear_backward")
-    out = (None if dX is None else dX if X.dim() == 2 else dX.reshape(X.shape), dW)
+    out = (None if dX is None else dX if len(g.lead) == 1 else dX.reshape(*g.lead, K), dW)
     if return_grad_projections:
         ldG = -(-2 * F // 8) * 8
         out = out + (ws[:M * ldG * 2].view(torch.bfloat16).view(M, ldG)[:, :2 * F],)
@@ -1562,11 +1577,10 @@ class _GatedLinearGrad(torch.autograd.Function):
             ctx.save_for_backward(X, W)
             return H
         H, kept = gated_linear(X, W, activation, keep=checkpoint)
-        if checkpoint == "int8":             # X is read for dW alone
-            x = pack_int8(_flatten_rows(X)) if ctx.needs_input_grad[1] else ()
-            ctx.save_for_backward(W, *kept, *x)
-        else:
-            ctx.save_for_backward(X, W, kept)
+        x = ()                               # X is read for dW alone
+        if ctx.needs_input_grad[1]:
+            x = pack_int8(_flatten_rows(X)) if checkpoint == "int8" else (X,)
+        ctx.save_for_backward(W, *(kept if checkpoint == "int8" else (kept,)), *x)
         return H
 
     @staticmethod
@@ -1576,18 +1590,15 @@ class _GatedLinearGrad(torch.autograd.Function):
         want_x, want_w = ctx.needs_input_grad[:2]
         if not (want_x or want_w):
             return None, None, None, None
-        kept = None
         if checkpoint == "int8":
             W, values, exponents, *x = ctx.saved_tensors
             kept = values, exponents
-            if x:
-                X = unpack_int8(*x).view(shape)
-            else:                            # nothing reads it: its shape alone counts
-                X = torch.empty(shape, dtype=torch.bfloat16, device=W.device)
+            X = unpack_int8(*x).view(shape) if want_w else None
         elif checkpoint == "fp32":
-            X, W, kept = ctx.saved_tensors
+            W, kept, *x = ctx.saved_tensors
+            X = x[0] if want_w else None
         else:
-            X, W = ctx.saved_tensors
+            (X, W), kept = ctx.saved_tensors, None
         dX, dW = gated_linear_backward(dH, X, W, activation, kept=kept, grad_x=want_x, grad_w=want_w)
         return dX, dW, None, None
 
@@ -1599,8 +1610,8 @@ def gated_linear_trainable(X: torch.Tensor, W: torch.Tensor, activation: str = "
     checkpoint says what waits for the backward beside W: "fp32" X and both projections in FP32
     (8 F bytes a row), "int8" X and both projections in 8 bits (about K + 2 F bytes; the gradients
     are those of the stored values), "again" X alone (the projections are formed again, the same
-    bits as "fp32").  None: "fp32" up to KEEP_PROJECTIONS_BYTES, else "again".  Where nothing asks
-    for a gradient nothing is kept.
+    bits as "fp32").  None: "fp32" up to KEEP_PROJECTIONS_BYTES, else "again".  Where W needs no
+    gradient "fp32" and "int8" do not keep X; where nothing does nothing is kept.
     """
     if checkpoint not in CHECKPOINTS:
         raise ValueError('checkpoint must be None, "fp32", "int8" or "again"')

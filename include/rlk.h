@@ -727,7 +727,8 @@ RLK_API rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t
  *  workspace     >= rlk_gated_linear_backward_workspace_size(...) bytes, 256-byte aligned;
  *                begins with G, row pitch 8 ceil(2 F / 8)
  * X may be NULL when dW is NULL and keep is not RLK_KEEP_NONE; W may be NULL when dX is
- * NULL and keep is not RLK_KEEP_NONE.  M == 0 writes zeros to dW.
+ * NULL and keep is not RLK_KEEP_NONE.  An operand passed as NULL with a pitch that is a
+ * multiple of 8 needs no room in the workspace.  M == 0 writes zeros to dW.
  */
 RLK_API size_t rlk_gated_linear_backward_workspace_size(const void* X, int64_t M, int64_t K,
                                                         int64_t ldx, const void* W, int64_t F,
