@@ -838,18 +838,23 @@ cudaError_t pair_sched(int64_t M, int64_t K, int64_t F, int stage_k, int64_t clu
 
 // Both products of a backward in one launch over both tile lists (the same bits), so that the one
 // with the shorter reduction fills the SM pairs that the few tiles of the long one leave idle.
-// Apart, the long one has narrow tiles, which take 0.69 of a wide tile's time; so one launch pays
-// where the long one's 256 x 256 tiles fill at most half of the pairs and the other product takes
-// about half as long as one of them or more, counting 64-wide reduction blocks and six more for a
-// tile's store.  Measured (us for the whole backward from 8 bits, one launch / two; in brackets
-// that ratio): 255 x 4096 -> 11000 146 / 183 (0.53), 512 x 2048 -> 8192 119 / 106 (0.37), 255 x
-// 2048 -> 5461 90 / 73 (0.26), 1000 x 1024 -> 4096 64 / 54 (0.28).
+// Apart, the long one has narrow tiles, which take 0.69 of a wide tile's time, and its launch
+// overlaps the other's ends; so one launch pays where the long one's 256 x 256 tiles fill at most
+// half of the pairs, the other product takes about half as long as one of them or more, counting
+// 64-wide reduction blocks and six more for a tile's store, and has eight tiles a pair or more to
+// deal out. Measured (us for the whole backward from 8 bits, one launch / two; in brackets that
+// ratio and the tiles a pair): grad X the longer, 255 x 4096 -> 11000 153 / 190 (0.53, 18), 37 x
+// 6144 -> 4856 96 / 115 (0.55, 12), 100 x 9728 -> 2000 71 / 75 (1.02, 8.0), 500 x 4864 -> 2000 65
+// / 57 (0.89, 4.0), 512 x 2048 -> 8192 125 / 112 (0.37, 6.7), 42 x 1544 -> 14080 175 / 151 (0.16,
+// 10); grad W the longer, 22410 x 5120 -> 72 179 / 237 (0.59, 23), 27678 x 3840 -> 128 186 / 232
+// (0.50, 21), 10000 x 4096 -> 128 91 / 97 (0.54, 8.4), 2500 x 9728 -> 64 54 / 51 (1.00, 5.0),
+// 10000 x 2048 -> 512 105 / 88 (0.59, 4.2), 44416 x 1280 -> 80 260 / 221 (0.15, 11).
 bool one_launch(int64_t M, int64_t K, int64_t F, int64_t pairs) {
   const int64_t red_long = M > 2 * F ? M : 2 * F, red_short = M > 2 * F ? 2 * F : M;
   const int64_t kb = ceil_div(K, kBN);
-  if (2 * ceil_div(red_short, kPairRows) * kb > pairs) return false;
-  const int64_t short_work = ceil_div(red_long, kPairRows) * kb * (ceil_div(red_short, kBK) + 6);
-  return 100 * short_work > 45 * pairs * ceil_div(red_long, kBK);
+  const int64_t short_tiles = ceil_div(red_long, kPairRows) * kb;
+  if (2 * ceil_div(red_short, kPairRows) * kb > pairs || short_tiles < 8 * pairs) return false;
+  return 100 * short_tiles * (ceil_div(red_short, kBK) + 6) > 45 * pairs * ceil_div(red_long, kBK);
 }
 
 bool known_activation(int a) { return a == RLK_ACT_SILU || a == RLK_ACT_GELU_TANH; }
