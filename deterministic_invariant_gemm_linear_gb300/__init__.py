@@ -1249,7 +1249,7 @@ def _refuse_grad(what: str, a, b=None):
 @_streamed
 def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0, *, out_dtype=None,
               stream=None):
-    """scale * weight[ids], rounded once: [..., H] in out_dtype (weight's dtype by default).
+    """scale * weight[ids], formed in FP32: [..., H] in out_dtype (weight's dtype by default).
 
     ids [...] int64 (any strides), weight [V, H] bf16 or fp32.  An id outside [0, V) (padding)
     gives a row of zeros.  Forward only: use embedding_trainable for gradients.
@@ -1302,8 +1302,12 @@ def embedding_backward(grad: torch.Tensor, ids: torch.Tensor, V: int, scale: flo
 @_streamed
 def embedding_grad_accum_fp32_(grad_weight: torch.Tensor, grad: torch.Tensor, ids: torch.Tensor,
                                scale: float = 1.0, *, stream=None):
-    """In place: grad_weight (fp32 [V, H]) += embedding_backward(grad, ids, V, scale) in FP32; rows
-    that no id names are not touched (nor read), so a small batch costs its own rows only."""
+    """In place: grad_weight (fp32 [V, H]) += embedding_backward(grad, ids, V, scale) in FP32.
+
+    Rows that no id names are neither read nor written.  The sort and the look through the table's
+    offsets stay, whose time and workspace go with V: 64 rows into 151,936 x 4096 take 65 us, where
+    the whole gradient takes 337.
+    """
     if grad_weight.dtype != torch.float32:
         raise TypeError("grad_weight must be float32")
     if grad_weight.dim() != 2 or (grad_weight.size(1) > 1 and grad_weight.stride(1) != 1) or \
@@ -1462,11 +1466,13 @@ def _kept_parts(kept, M: int, F: int):
 @_streamed
 def gated_linear(X: torch.Tensor, W: torch.Tensor, activation: str = "silu", out_dtype=torch.bfloat16,
                  *, keep: str | None = None, stream=None):
-    """H [..., F] = act(X Wg^T) * (X Wu^T), rounded once, in one kernel.
+    """H [..., F] = act(X Wg^T) * (X Wu^T) in one kernel, in FP32 up to the rounding to out_dtype.
 
     X [..., K] bf16 (leading dims are rows), W [2 F, K] bf16: the F rows of Wg, then those of Wu.
     activation: "silu" or "gelu_tanh".  A row's bits depend on its own row of X alone, and the
-    projections have the bits of det_linear(X, W, torch.float32).
+    projections have the bits of det_linear(X, W, torch.float32).  An FP32 H is within
+    (3 |a| + 10) 2^-23 of act(g) u for those projections, relative, with act(g) = g sigmoid(a), and
+    0 where a is below -87.3.
     keep: also return them for gated_linear_backward, "fp32" as a float32 tensor [rows, 2, Fp] or
     "int8" as (values int8 [rows, 2, Fp], exponents uint8 [rows, 2, Fp / 32]) in pack_int8's
     blocks, Fp = F rounded up to 32.  Forward only: use gated_linear_trainable for gradients.
@@ -1606,6 +1612,10 @@ class _GatedLinearGrad(torch.autograd.Function):
 def gated_linear_trainable(X: torch.Tensor, W: torch.Tensor, activation: str = "silu", *,
                            checkpoint: str | None = None):
     """gated_linear(X, W, activation) differentiable with respect to X and W (BF16 gradients).
+
+    With every checkpoint, "fp32" too, the gradient of the projections is rounded to BF16, the type
+    that both products read: the gradients' relative error is about 0.0024 (root mean square), of
+    which their own rounding to BF16 is 0.0017.
 
     checkpoint says what waits for the backward beside W: "fp32" X and both projections in FP32
     (8 F bytes a row), "int8" X and both projections in 8 bits (about K + 2 F bytes; the gradients

@@ -13,11 +13,14 @@
 //    its warps, each over its own stretch of the rows, count its ids and then place their rows
 //    (equal ids of a warp's 32 rows are ranked by match_any).  N ids are read by V / 1024 CTAs
 //    from L2, which for N rows of H elements of d is less than reading d.
+//    Its cost, and that of looking through the offsets below, goes with V however few rows there
+//    are: one row added to 151936 x 4096 takes 60 us, 64 rows 65, 16384 rows 185.
 //  * embed_rows_kernel: every table row.  Most are zeros; an id of at most 64 rows is summed by the
 //    threads of its table row.  Ids with more (a padding or a common token can have most of the
 //    rows) are cut into groups of 64 for the launch's first blocks; the block that finds all of
 //    an id's groups summed (a count says so, the sums lie in the workspace) adds them, in their
-//    order, and writes the table row.  No block waits for another.
+//    order, and writes the table row.  No block waits for another.  Those sums are added one after
+//    another: 2^20 rows of 256 columns, half of them one id, take 1.84 ms, without that id 0.58.
 #include <math.h>
 
 #include <mutex>
@@ -384,7 +387,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 // ids of a gradient: a sorting CTA's last + 1 fits an int
 constexpr int64_t kMaxTable = int64_t(1) << 30;
-// Every sorting CTA reads all ids: 2^37 reads are about a second.  (2^20 rows of a table of 2^27.)
+// Every sorting CTA reads all ids: 2^37 reads are about a second with a CTA on every SM (2^20 rows
+// of a table of 2^27).  A small table has few of them: 2^24 rows of 1000 ids, one CTA, take 22 ms.
 constexpr int64_t kMaxSortReads = int64_t(1) << 37;
 
 struct EmbedPlan {

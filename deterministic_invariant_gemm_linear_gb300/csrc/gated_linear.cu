@@ -54,7 +54,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 constexpr float kTanhSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
 
-// s = sigmoid(a(g)) and s (1 - s), from e = exp(-|a|) so that neither overflows.
+// s = sigmoid(a(g)) and s (1 - s), from e = exp(-|a|) so that neither overflows.  In FP32: the
+// argument's roundings make e off by up to 3 |a| 2^-23, the two approximations and the products
+// add 2^-21 (2^-14 in all for a of -87, far below a BF16 result's half step); below the normal
+// numbers (a under -87.3) e and with it s are 0.
 template <int kAct>
 __device__ __forceinline__ void gate(float g, float& s, float& both) {
   float a = g;
@@ -419,9 +422,12 @@ __device__ __forceinline__ void gated_tile(const GatedOut& o, const CUtensorMap*
 
 // More than 128 rows.  Bound by the tensor cores: 4096 x 4096 -> 16384 545 us by itself (2.02
 // PFLOP/s, 1.05 of the measured product; 616 - 640 back to back, at the clock that the power cap
-// leaves), 593 with FP32 projections kept, 568 with 8 bits.  The epilogue (3.4 us a tile, 5.0 and
-// 5.5 with them kept) hides behind a tile's MMAs from K of about 800, 1200 and 1300 on; below, it
-// bounds the call: 4096 x 512 -> 16384 107 us, where the products alone are 36.
+// leaves), 593 - 606 with FP32 projections kept, 568 with 8 bits.  The epilogue takes 3.4 us a
+// tile (5.0 and 5.5 with them kept); at that rate a tile's MMAs take as long from K of about 690,
+// 1010 and 1120 on.  Below, the epilogue bounds the call, and for some way above neither hides the
+// other wholly: 4096 x K -> 16384 with K = 512 / 704 / 1024 / 1408 takes 109 / 125 / 160 / 204 us,
+// 169 / 188 / 217 / 261 with FP32 kept, 161 / 170 / 188 / 233 with 8 bits, where the products
+// alone at the measured rate are 72 / 98 / 143 / 197.
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatedThreads, 1)
     gated_linear_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -545,8 +551,10 @@ __device__ __forceinline__ void slope_run(float (&d)[32], const uint32_t (&g)[32
   }
 }
 
-// G from projections formed again: the forward's loop, with another epilogue.  Its 5.4 us a tile
-// (dH is read when its chunk's turn comes) hide behind the MMAs from K of about 1300 on.
+// G from projections formed again: the forward's loop, with another epilogue.  It takes 6.5 us a
+// tile (dH is read when its chunk's turn comes), as long as the MMAs at K of about 1320: 4096 x K
+// -> 16384 with K = 64 / 1024 / 1408 / 2048 takes 175 / 198 / 233 / 308 us, the products alone 9 /
+// 143 / 197 / 286.
 template <int kK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGatedThreads, 1)
     gated_grad_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -713,11 +721,14 @@ cudaError_t allow_solo() {
   return e;
 }
 
-// Columns of g a tile of the one-CTA loop: 128, halved while twice the tiles still find an SM each,
-// so that more of them stream the weight and a tile's epilogue, which ends the call, is shorter.
-// Measured (us, 128 / 64 / 32 columns, L2 written over before): 17 x 2048 -> 5461 22.5 / 18.5 /
-// 26.6, 128 x 4096 -> 2000 32.8 / 26.6 / 24.6, 64 x 256 -> 1024 10.2 / 8.2 / 8.2, 1 x 4096 -> 16384
-// 60 / 65 / 80.
+// Columns of g a tile of the one-CTA loop: 128, halved while twice the tiles still find an SM
+// each, so that more of them stream the weight and a tile's epilogue, which ends the call, is
+// shorter.  Measured (us, 128 / 64 / 32 columns, L2 written over before): 17 x 2048 -> 5461 22.5 /
+// 18.5 / 26.6, 128 x 4096 -> 2000 32.8 / 26.6 / 24.6, 64 x 256 -> 1024 10.2 / 8.2 / 8.2, 1 x 4096
+// -> 16384 60 / 65 / 80.  Past one wave of 128 columns, narrower tiles do no better (the step to a
+// second round, at 19584, is there with either): 1 x 4096 -> 19456 (152 tiles) / 19584 / 22016 /
+// 27648 / 28672 / 29568 with 128 columns 71 / 85 / 85 / 93 / 97 / 98, with 64 74 / 83 / 85 / 94 /
+// 95 / 107; 100 rows 73 / 91 / 93 / 100 / 102 / 102 and 72 / 87 / 89 / 94 / 96 / 113.
 int solo_cols(int64_t F, int64_t sms) {
   int w = 128;
   while (w > 32 && 2 * ceil_div(F, w) <= sms) w /= 2;

@@ -26,7 +26,7 @@ namespace rlk {
 // Dynamic shared memory: alignment slack, the barrier block, then the stage ring.
 constexpr int kSmemLimit = 232448;                    // 227 KiB per CTA
 constexpr int kBarrierBlockBytes = 1024;              // keeps the ring 1024-byte aligned
-constexpr int kMaxStages = 11;                        // barrier slots; the rings use at most 7
+constexpr int kMaxStages = 11;                        // barrier slots: the most a ring uses
 
 // The stage ring: each stage holds this CTA's 128 rows of the left operand and
 // its kBHalf rows of the right-operand tile (half of the tile's 2 kBHalf
@@ -44,7 +44,7 @@ struct PairRingT {
   static constexpr int kStages =
       (kSmemLimit - 1024 - kBarrierBlockBytes - kReserve) / (kABytes + kBBytes) < kMaxStages
           ? (kSmemLimit - 1024 - kBarrierBlockBytes - kReserve) / (kABytes + kBBytes)
-          : kMaxStages;                                             // 7
+          : kMaxStages;
   // Bytes rank 0's full barrier counts per stage (both CTAs' copies).
   static constexpr uint32_t kTxBytes = 2u * (kABytes + kBBytes);
   static constexpr int kSmemBytes =

@@ -1,9 +1,10 @@
-// One-CTA variant of the tcgen05 main loop, for linear-logp calls of at most
-// 128 rows.
+// One-CTA variant of the tcgen05 main loop, for calls of at most 128 rows
+// (linear-logp, distillation, the gated block).
 //
-// A CTA owns a whole unit: it stages its left-operand rows and the full 256-row
-// right-operand tile per reduction block, and issues tcgen05.mma.cta_group::1
-// (M=128, N=256, K=16) into one of two 256-column FP32 accumulators.  For a
+// A CTA owns a whole unit: it stages its left-operand rows and the full
+// right-operand tile (256 rows, or 128 or 64 in the gated block) per reduction
+// block, and issues tcgen05.mma.cta_group::1 (M=128, N=256, 128 or 64, K=16)
+// into one of two FP32 accumulators, 256 columns apart.  For a
 // call of few rows the 2-SM loop spends its MMAs on 256 padded rows per tile
 // and deals its units to SM pairs in waves; here a tile costs half the MMA time
 // per SM and every SM takes a unit of its own.  Each output element still sums
@@ -12,8 +13,9 @@
 // computed it (compared bit for bit on GB300 at 17, 300 and 1024 rows).
 //
 // Roles as in the 2-SM loop: warp 0 lane 0 TMA producer, warp 1 TMEM
-// allocation and (lane 0) MMA issue, warps 2..5 epilogue on the 128
-// accumulator rows.  Units are dealt round-robin (few rounds at these sizes).
+// allocation and (lane 0) MMA issue, warps 2..5 (the gated block: 2..9)
+// epilogue on the 128 accumulator rows.  Units are dealt round-robin (few
+// rounds at these sizes).
 #pragma once
 
 #include "rlk_pipeline.cuh"
@@ -22,8 +24,10 @@ namespace rlk {
 
 // Stage ring: kARows rows of the left operand (32 when every row of the call
 // lies in the first 32, else 128) and the right-operand tile (256 rows, or fewer
-// for outputs of few columns), 64 reduction columns each; left-operand blocks of all stages first, then the
-// right-operand blocks.  The MMA always reads 128 left rows: with the thin ring
+// for outputs of few columns), 64 reduction columns each; left-operand blocks of
+// all stages first, then the right-operand blocks.  4 stages of full and 6 of thin
+// rows with 256-row tiles, up to 11 with narrower ones.  The MMA always reads 128
+// left rows: with the thin ring
 // the rows past the 32 staged ones hold other data (the next stages' blocks),
 // which reaches only accumulator rows that nothing reads (row i of a product
 // depends on row i of the left operand alone).

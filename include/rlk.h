@@ -607,7 +607,7 @@ RLK_API rlk_status rlk_linear_distill_backward(
  * ===================================================================== */
 
 /*
- * out[r, :] = scale * weight[ids[r], :], rounded once.
+ * out[r, :] = scale * weight[ids[r], :], rounded to out_dtype.
  *  ids           int64, row r reads ids[r * ids_stride] (0: one id shared by every row);
  *                an id outside [0, V) gives a row of zeros (nothing is read for it)
  *  weight        [V, H] in weight_dtype (RLK_BF16 / RLK_FP32), row pitch ld_weight (>= H)
@@ -626,13 +626,14 @@ RLK_API rlk_status rlk_embedding(const int64_t* ids, int64_t ids_stride, int64_t
  *   grad_weight[v, :] = scale * sum over the rows r with ids[r] == v of d[r, :]
  * Ids outside [0, V) take no part.  The rows of an id are added in FP32 in ascending
  * order of r, RLK_EMBED_GROUP at a time, and those sums in ascending order; scale is
- * applied to the whole sum and the result rounded once.  A table row's bits depend on its
- * own rows of d alone, however the other ids lie.
+ * applied to the whole sum in FP32 and the result rounded to grad_weight_dtype.  A table
+ * row's bits depend on its own rows of d alone, however the other ids lie.
  *  grad          [N, H] in grad_dtype (RLK_BF16 / RLK_FP32), row pitch ld_grad (>= H)
  *  grad_weight   [V, H] in grad_weight_dtype, row pitch ld_grad_weight (>= H).  Every row
  *                is written (zeros where no row of d belongs to it); with accumulate != 0
  *                (RLK_FP32 only) the sums are added to what is there and rows without any
- *                are left alone.  Must not overlap grad.
+ *                are left alone: neither read nor written, but their offsets are looked
+ *                through, so time and workspace still go with V.  Must not overlap grad.
  *  workspace     >= rlk_embedding_backward_workspace_size(N, V, H) bytes, 256-byte aligned
  * 0 <= N < 2^31 - 256, 1 <= V < 2^30, N * ceil(V / 1024) < 2^37, 1 <= H < 2^20.  N == 0
  * writes zeros (accumulate: a no-op).
@@ -687,6 +688,8 @@ RLK_API rlk_status rlk_unpack_int8(const int8_t* q, int64_t rows, int64_t cols, 
  *   RLK_ACT_GELU_TANH  a(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3)
  *                      (GELU in its tanh form, g (1 + tanh(a / 2)) / 2)
  * g and u are the FP32 accumulators: the bits of rlk_det_linear_fwd with an FP32 output.
+ * act(g) u is computed in FP32, within (3 |a| + 10) 2^-23 of its value, relative; where a is
+ * below -87.3 (exp(a) below FP32's normal numbers) it is 0.  Then it is rounded to h_dtype.
  *  X             BF16 [M, K], row pitch ldx (>= K)
  *  W             BF16 [2 F, K], row pitch ldw (>= K): rows 0 .. F - 1 are Wg, the others Wu
  *  H             [M, F] in h_dtype (RLK_BF16 / RLK_FP32), row pitch ldh (>= F)
@@ -717,7 +720,8 @@ RLK_API rlk_status rlk_gated_linear(const void* X, int64_t M, int64_t K, int64_t
  * Backward of rlk_gated_linear for an upstream gradient d = dL/dH:
  *   G = [d u act'(g), d act(g)]   [M, 2 F],    dX = G . W,    dW = G^T . X
  * G is formed in FP32 from g and u and rounded to BF16 (nearest even), the type the two
- * products read (they are rlk_det_linear_dx and rlk_det_linear_dw of G).  g and u are
+ * products read (they are rlk_det_linear_dx and rlk_det_linear_dw of G): whatever is kept,
+ * both gradients carry that rounding, half a BF16 step of G, beside their own.  g and u are
  * formed again on the tensor cores (RLK_KEEP_NONE) or read from what the forward kept;
  * with RLK_KEEP_FP32 the bits are the same.  With RLK_KEEP_INT8 they are the stored
  * values, and X is commonly the stored values of rlk_unpack_int8 too.
